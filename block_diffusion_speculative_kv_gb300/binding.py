@@ -59,6 +59,12 @@ class Sampling(C.Structure):
     _fields_ = [("temperature", C.c_float), ("seed", C.c_uint64), ("row_offset", C.c_int64)]
 
 
+class PagesStruct(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("table", C.c_void_p),
+                ("table_ld", C.c_int), ("n_pages", C.c_int), ("page_size", C.c_int),
+                ("n_kv", C.c_int), ("head_dim", C.c_int), ("dtype", C.c_int)]
+
+
 def sampling_arg(sampling):
     """None, or (temperature, seed[, row_offset]) -> a Sampling pointer argument."""
     if sampling is None:
@@ -99,6 +105,16 @@ _SIGS = {
     "ddtree_accept": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "dflash_commit_accepted": (_i, [_i, _i, _i, _i, _i, _vp, C.c_longlong, _vp, _vp, _vp, _vp,
                                     _vp, _vp, _vp, _vp, _vp]),
+    "dflash_qk_norm_rope": (_i, [_i, _i, _i, _i, _i, _vp, _vp, C.c_float, C.c_float, _vp, _vp,
+                                 C.c_longlong, _vp, C.c_longlong, _vp, C.c_longlong, _vp,
+                                 C.c_longlong, _vp]),
+    "dflash_paged_append": (_i, [C.POINTER(PagesStruct), _i, _i, _vp, _vp, _vp, _vp, _vp,
+                                 C.c_longlong, C.c_float, _vp]),
+    "dflash_paged_attention_workspace_bytes": (_sz, [_i, _i, _i]),
+    "dflash_paged_attention": (_i, [C.POINTER(PagesStruct), _i, _i, _i, _vp, _vp, _i, _vp,
+                                    C.c_longlong, _vp, _i, _vp, C.c_longlong, _vp, _sz, _vp]),
+    "dflash_logits_sample_filtered": (_i, [_i, _i, C.c_longlong, _i, _vp, _vp, _vp, _vp, _vp,
+                                           _vp, _vp, _vp, _vp]),
     "dflash_linear_workspace_bytes": (_sz, [_i, _i, _i]),
     "dflash_linear_bf16": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "dflash_set_trace_hook": (None, [_vp, _vp]),
@@ -331,3 +347,163 @@ def tree_rope(x: torch.Tensor, n_heads: int, head_dim: int, theta: float, ctx_le
     _check(lib().dflash_tree_rope(n_req, B1 - 1, n_heads, head_dim, theta, _ptr(ctx_len),
                                   _ptr(depth), _ptr(x), x.stride(1), _dtype_code(x),
                                   _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The target's pass over a paged cache
+# ---------------------------------------------------------------------------
+
+def _rows(t: torch.Tensor, name: str):
+    """Pointer and row stride of a [rows, columns] view whose columns are adjacent."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected [rows, columns] with adjacent columns")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str):
+    """Pointer of a contiguous CUDA tensor of n elements of dtype (None passes)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {n} {dtype} elements")
+    return t.data_ptr()
+
+
+def _together(*tensors):
+    """All on one device, and that the current one (the library launches there)."""
+    devs = {t.device.index for t in tensors if t is not None and t.is_cuda}
+    if devs and devs != {torch.cuda.current_device()}:
+        raise ValueError("all tensors must be on the current CUDA device")
+
+
+class Pages:
+    """A paged KV cache of one layer: pools [n_pages, n_kv, page_size, head_dim]
+    and the page table [n_req, pages per request] (int32).  Keeps the tensors
+    alive; the table's entries may change between calls, its storage not."""
+
+    def __init__(self, pool_k: torch.Tensor, pool_v: torch.Tensor, table: torch.Tensor):
+        if pool_k.dim() != 4 or pool_k.shape != pool_v.shape or pool_k.dtype != pool_v.dtype:
+            raise ValueError("pools: expected two [n_pages, n_kv, page_size, head_dim] of one type")
+        if table.dim() != 2 or table.dtype != torch.int32:
+            raise ValueError("table: expected int32 [n_req, pages]")
+        if not (pool_k.is_contiguous() and pool_v.is_contiguous() and table.is_contiguous()):
+            raise ValueError("pools and table must be contiguous")
+        if not (pool_k.device == pool_v.device == table.device):
+            raise ValueError("pools and table must be on one device")
+        if not pool_k.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        self.pool_k, self.pool_v, self.table = pool_k, pool_v, table
+        n_pages, self.n_kv, page, self.head_dim = pool_k.shape
+        self.n_req = table.shape[0]
+        self.dtype = pool_k.dtype
+        self.struct = PagesStruct(pool_k.data_ptr(), pool_v.data_ptr(), table.data_ptr(),
+                                  table.shape[1], n_pages, page, self.n_kv, self.head_dim,
+                                  _dtype_code(pool_k))
+        self.ref = C.byref(self.struct)
+
+
+def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                 q_gain: Optional[torch.Tensor], k_gain: Optional[torch.Tensor], eps: float,
+                 theta: float, pos: Optional[torch.Tensor], head_dim: int,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 stream=None):
+    """Per-head RMSNorm (a gain of None: none) and rotation at pos (theta 0: none) of
+    q [rows, n_q*head_dim] and k [rows, n_kv*head_dim] (either may be None) into q_out
+    and k_out, or in place."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("expected q or k")
+    n = first.shape[0]
+    _together(q, k, q_gain, k_gain, pos, q_out, k_out)
+    heads, args = [], []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            heads.append(0)
+            args.append((None, 0, None, 0))
+            continue
+        out = x if out is None else out
+        if x.dtype != first.dtype or out.dtype != first.dtype or out.shape != x.shape:
+            raise ValueError(f"{name}_out must have {name}'s shape, and all one type")
+        if x.dim() != 2 or x.shape[0] != n or x.shape[1] % head_dim:
+            raise ValueError(f"{name}: expected [{n}, heads * {head_dim}]")
+        heads.append(x.shape[1] // head_dim)
+        args.append(_rows(x, name) + _rows(out, name + "_out"))
+    (qp, ql, qo, qol), (kp, kl, ko, kol) = args
+    _check(lib().dflash_qk_norm_rope(
+        n, heads[0], heads[1], head_dim, _dtype_code(first),
+        _vec(q_gain, head_dim, first.dtype, "q_gain"),
+        _vec(k_gain, head_dim, first.dtype, "k_gain"), eps, theta,
+        _vec(pos, n, torch.int32, "pos"), qp, ql, kp, kl, qo, qol, ko, kol, _stream(stream)))
+
+
+def paged_append(pages: Pages, k: torch.Tensor, v: torch.Tensor, row_off: torch.Tensor,
+                 pos0: torch.Tensor, theta: float = 0.0, pos: Optional[torch.Tensor] = None,
+                 stream=None):
+    """Keys (rotated at pos, or at their slot; theta 0: as they come) and values
+    [rows, n_kv*head_dim] into slots pos0[r] .. of each request's pages."""
+    n, width = k.shape[0], pages.n_kv * pages.head_dim
+    if k.dtype != pages.dtype or v.dtype != pages.dtype:
+        raise ValueError("k and v must have the pools' type")
+    if k.shape != v.shape or k.dim() != 2 or k.shape[1] != width:
+        raise ValueError(f"k and v: expected [rows, {width}]")
+    _together(pages.pool_k, k, v, row_off, pos0, pos)
+    kp, kl = _rows(k, "k")
+    vp, vl = _rows(v, "v")
+    if kl != vl:
+        raise ValueError("k and v must have one row stride")
+    _check(lib().dflash_paged_append(
+        pages.ref, pages.n_req, n, _vec(row_off, pages.n_req + 1, torch.int32, "row_off"),
+        _vec(pos0, pages.n_req, torch.int32, "pos0"), _vec(pos, n, torch.int32, "pos"), kp, vp, kl,
+        theta, _stream(stream)))
+
+
+def paged_attention_workspace_bytes(n_q: int, n_kv: int, head_dim: int) -> int:
+    return int(lib().dflash_paged_attention_workspace_bytes(n_q, n_kv, head_dim))
+
+
+def paged_attention(pages: Pages, q: torch.Tensor, row_off: torch.Tensor, pos0: torch.Tensor,
+                    max_rows: int, out: torch.Tensor, ws: torch.Tensor,
+                    mask: Optional[torch.Tensor] = None, stream=None):
+    """q, out [rows, n_q*head_dim] (bf16): request r's rows row_off[r] .. are its tokens
+    at slots pos0[r] .., causal, or by mask [rows, words] (int32 view of the bits over
+    the request's rows)."""
+    n, hd = q.shape[0], pages.head_dim
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape != q.shape:
+        raise ValueError("q and out: expected bf16 [rows, n_q * head_dim]")
+    if q.dim() != 2 or q.shape[1] % hd:
+        raise ValueError(f"q: expected [rows, heads * {hd}]")
+    if mask is not None and (mask.dim() != 2 or mask.shape[0] != n):
+        raise ValueError("mask: expected [rows, words]")
+    _together(pages.pool_k, q, row_off, pos0, out, ws, mask)
+    qp, ql = _rows(q, "q")
+    op, ol = _rows(out, "out")
+    _check(lib().dflash_paged_attention(
+        pages.ref, pages.n_req, n, q.shape[1] // hd,
+        _vec(row_off, pages.n_req + 1, torch.int32, "row_off"),
+        _vec(pos0, pages.n_req, torch.int32, "pos0"), max_rows, qp, ql,
+        None if mask is None else _vec(mask, mask.numel(), torch.int32, "mask"),
+        0 if mask is None else mask.shape[1], op, ol, _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def logits_sample_filtered(logits: torch.Tensor, u: torch.Tensor, tok: torch.Tensor,
+                           logp: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+                           top_k: Optional[torch.Tensor] = None,
+                           top_p: Optional[torch.Tensor] = None,
+                           min_p: Optional[torch.Tensor] = None, vocab: Optional[int] = None,
+                           stream=None):
+    """One token per row of logits [rows, ld] from u in [0, 1), under per-row temperature,
+    top_k, top_p and min_p (None: off); logp is its log-share of the kept mass."""
+    rows = logits.shape[0]
+    _together(logits, u, tok, logp, temperature, top_k, top_p, min_p)
+    lp, ld = _rows(logits, "logits")
+    f32 = torch.float32
+    _check(lib().dflash_logits_sample_filtered(
+        rows, logits.shape[1] if vocab is None else vocab, ld, _dtype_code(logits), lp,
+        _vec(temperature, rows, f32, "temperature"), _vec(top_k, rows, torch.int32, "top_k"),
+        _vec(top_p, rows, f32, "top_p"), _vec(min_p, rows, f32, "min_p"), _vec(u, rows, f32, "u"),
+        _vec(tok, rows, torch.int32, "tok"), _vec(logp, rows, f32, "logp"), _stream(stream)))

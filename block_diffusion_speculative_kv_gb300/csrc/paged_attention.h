@@ -1,0 +1,154 @@
+// Attention over a paged KV cache: parameters and work split shared by its
+// kernels (paged_attention.cu).
+#pragma once
+
+#include "paged.cuh"
+
+namespace dfl {
+
+struct PagedAttnParams {
+  PagedView pv;
+  int n_req, n_rows, G;            // G = query heads per KV head
+  const int32_t* row_off;
+  const int32_t* pos0;
+  const uint32_t* mask;
+  int mask_ld;
+  const __nv_bfloat16* q;
+  long long q_ld;
+  __nv_bfloat16* out;
+  long long out_ld;
+  float scale_log2;
+  // a tile split between CTAs: two slots of partial rows per CTA (its first
+  // tile and its last), unnormalised O and (max, sum) of each row, and one
+  // arrival counter per CTA for the tile that begins there and goes on
+  float* part_o;                   // [grid][2][rows][hd]
+  float2* part_ml;                 // [grid][2][rows]
+  int* arrive;                     // [grid]
+  int* status;
+};
+
+// One request of the flattened work.  Its n rows and G heads of a KV head make
+// n * G query rows (row = token * G + head), TR to a tile; tile j sees keys
+// 0 .. key_end(j) - 1, in steps of KS keys.
+struct PagedReq {
+  int row0, n, p0, cap;
+  bool masked;
+  __device__ __forceinline__ void load(const PagedAttnParams& p, int r) {
+    row0 = min(max(p.row_off[r], 0), p.n_rows);
+    n = min(max(p.row_off[r + 1], row0), p.n_rows) - row0;
+    cap = p.pv.table_ld << p.pv.page_shift;
+    p0 = min(max(p.pos0[r], 0), cap);
+    masked = p.mask != nullptr;
+  }
+  __device__ __forceinline__ int tiles(int G, int TR) const { return (n * G + TR - 1) / TR; }
+  __device__ __forceinline__ int key_end(int j, int G, int TR) const {
+    const int last = masked ? n - 1 : min(j * TR + TR - 1, n * G - 1) / G;
+    return min(p0 + last + 1, cap);
+  }
+  // steps of tiles [0, j1) of one KV head
+  __device__ __forceinline__ long long steps(int j1, int G, int TR, int KS) const {
+    if (masked) return (long long)j1 * ((key_end(0, G, TR) + KS - 1) / KS);
+    long long s = 0;
+    for (int j = 0; j < j1; ++j) s += (key_end(j, G, TR) + KS - 1) / KS;
+    return s;
+  }
+};
+
+// A CTA's place in the flattened work: requests, then KV heads, then query
+// tiles, then key steps.  The CTA's share is [begin, end) of `total` steps.
+struct PagedCursor {
+  int r, g, j;             // request, KV head, tile
+  int step, n_steps;       // next step of the tile, its steps
+  long long left;          // steps left to this CTA, this tile's included
+  PagedReq rq;
+};
+
+// Warp-collective: total steps of all requests, then the request holding step
+// `begin` and the steps before it.
+__device__ __forceinline__ long long paged_total(const PagedAttnParams& p, int TR, int KS, int lane) {
+  long long total = 0;
+  for (int r0 = 0; r0 < p.n_req; r0 += 32) {
+    long long s = 0;
+    if (r0 + lane < p.n_req) {
+      PagedReq q;
+      q.load(p, r0 + lane);
+      s = q.steps(q.tiles(p.G, TR), p.G, TR, KS) * p.pv.n_kv;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    total += s;
+  }
+  return total;
+}
+
+__device__ __forceinline__ void paged_seek(const PagedAttnParams& p, int TR, int KS, int lane,
+                                           long long begin, PagedCursor* c) {
+  long long before = 0;
+  for (int r0 = 0; r0 < p.n_req; r0 += 32) {
+    long long s = 0;
+    if (r0 + lane < p.n_req) {
+      PagedReq q;
+      q.load(p, r0 + lane);
+      s = q.steps(q.tiles(p.G, TR), p.G, TR, KS) * p.pv.n_kv;
+    }
+    long long inc = s;                                   // inclusive scan
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + inc > begin);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const long long excl = __shfl_sync(0xffffffffu, inc - s, l);
+      c->r = r0 + l;
+      c->rq.load(p, c->r);
+      const int nt = c->rq.tiles(p.G, TR);
+      const long long per_g = c->rq.steps(nt, p.G, TR, KS);
+      long long rem = begin - before - excl;
+      c->g = static_cast<int>(rem / per_g);
+      rem -= (long long)c->g * per_g;
+      int j = 0, ns;
+      while (true) {
+        ns = (c->rq.key_end(j, p.G, TR) + KS - 1) / KS;
+        if (rem < ns) break;
+        rem -= ns;
+        ++j;
+      }
+      c->j = j;
+      c->step = static_cast<int>(rem);
+      c->n_steps = ns;
+      return;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  c->r = p.n_req;
+}
+
+// To the next tile (the current one's steps are used up).
+__device__ __forceinline__ void paged_next(const PagedAttnParams& p, int TR, int KS, PagedCursor* c) {
+  if (++c->j >= c->rq.tiles(p.G, TR)) {
+    c->j = 0;
+    if (++c->g >= p.pv.n_kv) {
+      c->g = 0;
+      do {
+        if (++c->r >= p.n_req) return;
+        c->rq.load(p, c->r);
+      } while (c->rq.n == 0);
+    }
+  }
+  c->step = 0;
+  c->n_steps = (c->rq.key_end(c->j, p.G, TR) + KS - 1) / KS;
+}
+
+// Share of CTA c of `grid`: [total * c / grid, total * (c + 1) / grid).
+__device__ __forceinline__ long long paged_share(long long total, int c, int grid) {
+  return total / grid * c + min((long long)c, total % grid);
+}
+// The CTA whose share holds step s.
+__device__ __forceinline__ int paged_owner(long long total, long long s, int grid) {
+  const long long q = total / grid, m = total % grid;
+  return static_cast<int>(s < m * (q + 1) ? s / (q + 1) : m + (s - m * (q + 1)) / q);
+}
+
+}  // namespace dfl

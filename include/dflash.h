@@ -28,6 +28,9 @@
  * the drafter draws tokens at temperature T (vanilla DFlash), and
  * dflash_chain_tree lays the drafted block out as a chain in ddtree_build's
  * layout.  dflash_logits_topk / dflash_logits_sample run step a6 alone.
+ * The target's own side of a cycle over a paged cache is dflash_qk_norm_rope,
+ * dflash_paged_append, dflash_paged_attention and, after its LM head,
+ * dflash_logits_sample_filtered (the walk's target_tok).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -429,6 +432,131 @@ dflash_status dflash_tree_attention(int n_req, int n_q, int n_kv, int head_dim, 
 dflash_status dflash_tree_rope(int n_req, int B, int n_heads, int head_dim, float theta,
                                const int32_t* ctx_len, const int32_t* depth, void* x,
                                long long ld, int dtype, void* stream);
+
+/* A paged KV cache of one target layer, for the verification pass over
+ * requests whose contexts grow (the pages serve DFlash and DDTree from engines
+ * that keep the target's cache in pages; DFlash page, section 4).  Slot t of
+ * request r (its t-th token) lies in page table[r][t / page_size] at place
+ * t % page_size.  Pages belong to the caller, may lie in any order, and a table
+ * entry outside [0, n_pages) (say -1) is a page that is not there.
+ *   k, v   T [n_pages][n_kv][page_size][head_dim] (device), 16-byte aligned
+ *   table  int32 [n_req][table_ld] (device)
+ * Requires page_size a power of two in [16, 1024], head_dim 64 or 128,
+ * table_ld >= 1, n_pages >= 1; dtype DFLASH_BF16 or DFLASH_F32. */
+typedef struct dflash_pages {
+  void* k;
+  void* v;
+  const int32_t* table;
+  int table_ld;
+  int n_pages;
+  int page_size;
+  int n_kv;
+  int head_dim;
+  int dtype;
+} dflash_pages;
+
+/* Per-head RMSNorm of queries and keys and their position rotation, in one pass
+ * (the target of the pages' experiments normalises both per head before the
+ * rotate-half RoPE).  For every row i and every head x of its n_q query and
+ * n_kv key heads:
+ *   y   = x / sqrt(mean(x^2) + eps) * gain      (gain NULL: no norm, y = x)
+ *   out = RoPE(y, pos[i], theta)                (theta == 0: no rotation)
+ * in fp32, rounded once.  A row whose pos is negative is left as it is (the
+ * rows past a tree's last node); pos may be NULL when theta == 0.
+ *   q, k          T [n_rows] rows q_ld / k_ld elements apart, head h at column
+ *                 h * head_dim; q_out, k_out likewise.  q_out may be q and k_out
+ *                 may be k (in place, with the same row stride); other overlap
+ *                 is not allowed
+ *   q_gain/k_gain T [head_dim]
+ *   pos           int32 [n_rows] (device)
+ * n_q or n_kv may be 0 (its pointers are then not read).  head_dim 64 or 128;
+ * T = dtype.  Any stride of at least heads * head_dim elements; rows and
+ * buffers on 16-byte boundaries take the vector path.  Needs no workspace. */
+dflash_status dflash_qk_norm_rope(int n_rows, int n_q, int n_kv, int head_dim, int dtype,
+                                  const void* q_gain, const void* k_gain, float eps, float theta,
+                                  const int32_t* pos, const void* q, long long q_ld,
+                                  const void* k, long long k_ld, void* q_out,
+                                  long long q_out_ld, void* k_out, long long k_out_ld,
+                                  void* stream);
+
+/* New keys and values into a paged cache, the keys rotated on the way.  Global
+ * row row_off[r] + i of request r (i < row_off[r+1] - row_off[r]) goes to slot
+ * pos0[r] + i, its key rotated at pos[row], or at its slot where pos is NULL
+ * (theta == 0: stored as it comes, for keys dflash_qk_norm_rope has rotated).
+ *   row_off  int32 [n_req+1] (device), row_off[0] = 0, non-decreasing; rows at
+ *            or past row_off[n_req] are stored nowhere
+ *   pos0     int32 [n_req] (device)   pos  int32 [n_rows] (device) or NULL
+ *   k, v     T [n_rows] rows kv_ld elements apart, head g at column g*head_dim
+ * Not stored: a row with a negative pos, and a row whose slot has no page (past
+ * the table, or an entry outside [0, n_pages)).  No other slot is written.  Two
+ * rows of one call must not share a slot (requests that share a page may share
+ * only slots that neither writes).  n_rows may be 0.  Needs no workspace. */
+dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_rows,
+                                  const int32_t* row_off, const int32_t* pos0,
+                                  const int32_t* pos, const void* k, const void* v,
+                                  long long kv_ld, float theta, void* stream);
+
+/* Attention of new tokens over a paged cache (DDTree page, 3.4.5, over pages):
+ * the rows of request r, global rows row_off[r] .. row_off[r+1] - 1, are its
+ * tokens at slots pos0[r] .., whose keys and values the cache already holds
+ * (dflash_paged_append).  Row i of the request, head h reading KV head
+ * h / (n_q / n_kv), takes softmax(q . key / sqrt(head_dim)) over
+ *   mask NULL  slots t <= pos0[r] + i (causal: decoding, chains, prompt chunks)
+ *   mask       slots t < pos0[r], and slots pos0[r] + j with bit j of its mask
+ *              row set, j < row_off[r+1] - row_off[r]: a draft tree with the
+ *              mask ddtree_build writes, or any other pattern.  A row with no
+ *              bit set attends to the context alone.
+ * A row that sees no slot gets zeros.  Keys and values no row may see are not
+ * read into any result, whatever they hold.
+ *   q     bf16 [n_rows] rows q_ld elements apart, head h at column h*head_dim
+ *   mask  uint32 [n_rows][mask_ld] (device), bit j in word j / 32; mask_ld * 32
+ *         >= the most rows of a request (bits past it count as not set)
+ *   out   bf16 [n_rows] rows out_ld apart; rows at or past row_off[n_req] are
+ *         left as they are
+ * max_rows is a host bound on the rows of one request, used to choose the
+ * kernel; results do not depend on it being tight.  Sizes stay on the device,
+ * so a captured call serves contexts that grow.  The work (requests x KV heads
+ * x query tiles x key tiles) is split evenly over the SMs; a tile split between
+ * CTAs is joined in key order by the last of them, so results do not depend on
+ * timing.  A visible slot whose page is not there reads as zeros and records
+ * DFLASH_ERR_INVALID_ARG in the workspace status word.
+ * Requires DFLASH_BF16 pages, n_q a multiple of n_kv, strides that are
+ * multiples of 8 elements and 16-byte aligned q and out.  ws of
+ * dflash_paged_attention_workspace_bytes bytes, zeroed once
+ * (dflash_workspace_init) before the first call; every call leaves its counters
+ * at zero.  Calls sharing a workspace must not overlap. */
+size_t dflash_paged_attention_workspace_bytes(int n_q, int n_kv, int head_dim);
+dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n_rows, int n_q,
+                                     const int32_t* row_off, const int32_t* pos0, int max_rows,
+                                     const void* q, long long q_ld, const uint32_t* mask,
+                                     int mask_ld, void* out, long long out_ld, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* The target's token of every row, from given random numbers (DFlash page,
+ * 3.4.4: verification at temperature 1; DDTree page, 3.4.5: the walk's target
+ * choices).  Per row, over logits l and in this order:
+ *   temperature  w_v = exp((l_v - max l) / T); T <= 0 (or NaN): the best token
+ *   top_k        k > 0 keeps the k best tokens (logit desc, id asc)
+ *   top_p        p < 1 keeps, of those in that order, a token if the mass before
+ *                it is below p times theirs (the best always)
+ *   min_p        m > 0 keeps tokens with l_v - max l >= T ln(min(m, 1))
+ *   draw         the first kept token, by id, whose cumulated mass exceeds u
+ *                times the kept mass, u in [0, 1) (clamped)
+ *   tok  int32 [rows], logp fp32 [rows] (device) out: the token, and the log of
+ *        its share of the kept mass (0 for T <= 0)
+ *   temperature, top_p, min_p, u  fp32 [rows], top_k int32 [rows] (device); a
+ *        NULL parameter is off (temperature: 1), u is required
+ * A NaN logit counts as -inf; tokens at -inf are never drawn; where some are
+ * +inf they share the mass.  A row of -inf alone gives tok -1, logp -inf.
+ *   logits  [rows] of dtype, ld elements apart, vocab <= ld
+ * Masses are 64-bit sums of fp32 exponentials with 40 fractional bits, so
+ * results depend neither on timing nor on the other rows.  rows may be 0.
+ * Requires 1 <= vocab <= 2^22.  Needs no workspace. */
+dflash_status dflash_logits_sample_filtered(int rows, int vocab, long long ld, int dtype,
+                                            const void* logits, const float* temperature,
+                                            const int32_t* top_k, const float* top_p,
+                                            const float* min_p, const float* u, int32_t* tok,
+                                            float* logp, void* stream);
 
 /* The dense contraction every step above is built on, exposed on its own:
  * Y[M][N] = X[M][K] . W[N][K]^T with bf16 X and W and fp32 Y, on the tcgen05
