@@ -29,6 +29,10 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-rdc=true", "-Xcompiler", "-fPIC",
                      "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 
+# Compiled as whole programs: setmaxnreg (a register split between warpgroups)
+# is ignored under separate compilation.
+WHOLE_PROGRAM = {"paged_attention.cu"}
+
 
 def _nvcc() -> str:
     for cand in (shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
@@ -52,7 +56,9 @@ def _stale(target: str, deps) -> bool:
 def _compile(src: str, extra) -> str:
     obj = os.path.join(OBJDIR, os.path.basename(src)[:-3] + ".o")
     if _stale(obj, [src] + _headers()):
-        cmd = [_nvcc()] + NVCC_FLAGS + list(extra) + ["-c", src, "-o", obj]
+        flags = [f for f in NVCC_FLAGS
+                 if f != "-rdc=true" or os.path.basename(src) not in WHOLE_PROGRAM]
+        cmd = [_nvcc()] + flags + list(extra) + ["-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stderr}")

@@ -28,9 +28,11 @@
 
 #include <math_constants.h>
 
+#include "gemm.h"
 #include "kernels.h"
 #include "mma_sync.cuh"
 #include "paged_attention.h"
+#include "ptx.cuh"
 
 namespace dfl {
 
@@ -66,6 +68,12 @@ __device__ __forceinline__ bool not_finite8(const uint4& u) {
     return (w & 0x7F800000u) == 0x7F800000u || (w & 0x00007F80u) == 0x00007F80u;
   };
   return bad(u.x) || bad(u.y) || bad(u.z) || bad(u.w);
+}
+
+__device__ __forceinline__ uint32_t zero_not_finite(uint32_t w) {
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  if ((w & 0x00007F80u) == 0x00007F80u) w &= 0xFFFF0000u;
+  return w;
 }
 
 template <int HD>
@@ -375,7 +383,611 @@ void launch_small(const PagedAttnParams& p, int grid, cudaStream_t st) {
   launch_k(paged_attn_small_kernel<HD>, dim3(grid), dim3(kThreadsS), SmallSmem<HD>::kBytes, st, p);
 }
 
-constexpr int kMaxTileRows = 16;
+// ---------------------------------------------------------------------------
+// Many query rows (chains, trees, prompt chunks): tensor-core tiles.
+// ---------------------------------------------------------------------------
+// A tile is 256 query rows, two MMA tiles of 128, against steps of 128 keys:
+//   S_x = Q_x K_t^T   (x = 0, 1; accumulators S_0, S_1 in TMEM)
+//   O_x += P_x V_t    (P_x in TMEM over S_x's columns, as the A operand; O_x in TMEM)
+// Two softmax groups of four warps, one thread to a row, take turns with the
+// tensor cores: while group 0 turns S_0 into P_0, the cores run P_1 V and the
+// next S_1.  A tile of at most 128 rows is given to both groups, which take
+// every other key step each and join their halves at the end, so that the
+// alternation also holds for short chains.  Warp 8 loads (TMA, a ring of K and
+// V tiles that runs ahead over tile borders; a box is a page, or 128 keys of a
+// larger one), warp 9 issues the MMAs.  A row's O is rescaled only when its
+// maximum has risen by more than 8 (base-2 units) over the reference in use.
+// Every wait is bounded (2 s); on expiry the CTA records DFLASH_ERR_TIMEOUT,
+// lets its copies and MMAs land, frees TMEM and returns.
+constexpr int kRowsT = 256, kStepT = 128, kThreadsT = 384;
+// Registers: the launch's 168 for each of three warpgroups, of which the softmax
+// groups take 216 (a row of scores in registers) and the other one keeps 72:
+// 2 * 216 + 72 = 3 * 168.
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "register split");
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+struct PagedTcMaps {
+  CUtensorMap k, v;    // pools as [n_pages * n_kv * page_size][HD], box 64 x min(page_size, 128)
+};
+
+template <int HD>
+struct TcSmem {
+  static constexpr int kAtom = 128 * 128;                   // 64 columns of 128 rows
+  static constexpr int kTile = (HD / 64) * kAtom;           // 128 rows of bf16
+  static constexpr int kSlots = HD == 128 ? 5 : 8;
+  static constexpr int kRing = 2 * kTile;                   // after Q's two tiles
+  static constexpr int kBar = kRing + kSlots * kTile;
+  static constexpr int kBytes = 1024 + kBar + 2048;
+};
+
+// Bits of keys [b, b + 32) relative to the first new token: 1 = seen.
+__device__ __forceinline__ uint32_t seen_word(const uint32_t* mrow, int mask_ld, int b) {
+  if (b <= -32) return 0xFFFFFFFFu;                          // context
+  const int w = b >> 5, sh = b & 31;                         // floor: w = -1 for b in (-32, 0)
+  const uint32_t lo = w < 0 ? 0xFFFFFFFFu : (w < mask_ld ? __ldg(mrow + w) : 0u);
+  const uint32_t hi = w + 1 < mask_ld ? __ldg(mrow + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+// The low n bits (n clamped to [0, 32]).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreadsT, 1)
+paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnParams p) {
+  using S = TcSmem<HD>;
+  constexpr int R = S::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;                                        // [2][HD / 64][128][64] bf16
+  uint8_t* sKV = smem + S::kRing;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::kBar);
+  uint64_t* full = bar;                                      // [R] tile landed
+  uint64_t* empty = bar + R;                                 // [R] tile read
+  uint64_t* q_full = bar + 2 * R;
+  uint64_t* s_ready = q_full + 1;                            // [2]
+  uint64_t* p_ready = q_full + 3;                            // [2]
+  uint64_t* pv_done = q_full + 5;                            // [2]
+  uint64_t* drain = q_full + 7;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(q_full + 8);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile int* s_last = reinterpret_cast<volatile int*>(tslot + 2);    // [2]
+  // keys with a value that is not finite: [group][step % 4][word].  Group 1 may
+  // still read group 0's of step t when group 0 is at step t + 2, not later.
+  volatile uint32_t* odd_keys = tslot + 4;
+  float2* sMl = reinterpret_cast<float2*>(tslot + 36);       // [128]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < R; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    ptx::mbar_init(q_full, 8);
+    for (int x = 0; x < 2; ++x) {
+      ptx::mbar_init(&s_ready[x], 1);
+      ptx::mbar_init(&p_ready[x], 4);
+      ptx::mbar_init(&pv_done[x], 1);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(tslot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tbase = *tslot;
+  // S_x at column 128 x (P_x over it), O_x at 256 + 128 x
+
+  pdl_wait();
+  pdl_trigger();
+  const int grid = gridDim.x;
+  const long long total = paged_total(p, kRowsT, kStepT, lane);
+  const long long begin = paged_share(total, blockIdx.x, grid);
+  const long long end = paged_share(total, blockIdx.x + 1, grid);
+  PagedCursor c;
+  c.left = end - begin;
+  if (c.left > 0) paged_seek(p, kRowsT, kStepT, lane, begin, &c);
+
+  auto fail = [&]() {
+    if (!*abort) record_status(p.status, DFLASH_ERR_TIMEOUT);
+    *abort = 1;
+  };
+  // bounded waits; the loader and the issuer back off between polls, since they
+  // share schedulers with the softmax
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    return ptx::mbar_wait_bounded(b, parity, kTimeoutNs, abort);
+  };
+
+  if (warp >= 8) {
+  ptx::regs_dec<kRegsOther>();
+  if (warp == 8) {
+    // ---------------- loads ----------------
+    const int box = min(1 << p.pv.page_shift, 128);
+    const int nb = 128 / box;                                // boxes of a tile
+    const uint64_t pol = ptx::policy_evict_last();
+    if (lane == 0) {
+      ptx::prefetch_tmap(&maps.k);
+      ptx::prefetch_tmap(&maps.v);
+    }
+    const int nowhere = (p.pv.n_pages * p.pv.n_kv) << p.pv.page_shift;   // past the pool: zeros
+    uint32_t it = 0;                                         // tiles loaded
+    bool ok = true;
+    while (c.left > 0 && ok) {
+      const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
+      const int kend = c.rq.key_end(c.j, p.G, kRowsT);
+      const int32_t* table = p.pv.table + (size_t)c.r * p.pv.table_ld;
+      // this lane's box of step i: its first slot, and its page's table entry
+      // (asked for one step ahead; kend lies within the table)
+      auto slot_of = [&](int i) { return (c.step + i) * kStepT + lane * box; };
+      auto entry_of = [&](int i) {
+        const int t = slot_of(i);
+        return lane < nb && i < n && t < kend ? __ldg(table + (t >> p.pv.page_shift)) : -1;
+      };
+      int entry = entry_of(0);
+      for (int i = 0; i < n && ok; ++i) {
+        const int t = slot_of(i), page = entry;
+        entry = entry_of(i + 1);
+        const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.pv.n_pages);
+        if (!there && lane < nb && t < kend) record_status(p.status, DFLASH_ERR_INVALID_ARG);
+        const int y = there ? static_cast<int>(pool_row(p.pv, page, c.g, t)) : nowhere;
+        for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+          const int s = it % R;
+          ok = wait(&empty[s], (it / R & 1u) ^ 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], S::kTile);
+          __syncwarp();
+          if (lane < nb)
+            for (int h = 0; h < HD / 64; ++h)
+              ptx::tma_load_2d(sKV + s * S::kTile + h * S::kAtom + lane * box * 128,
+                               kv ? &maps.v : &maps.k, &full[s], 64 * h, y, pol);
+        }
+      }
+      c.left -= n;
+      if (c.left > 0) paged_next(p, kRowsT, kStepT, &c);
+    }
+    if (!ok && lane == 0) fail();
+    // every copy must land before the CTA exits
+    for (uint32_t s = 0; s < R; ++s) {
+      if (it <= s) break;
+      const uint32_t last = (it - 1 - s) / R;                // uses of slot s - 1
+      ptx::mbar_wait_bounded(&full[s], last & 1u, kTimeoutNs, nullptr);
+    }
+  } else if (warp == 9) {
+    // ---------------- MMA issue ----------------
+    if (lane == 0) {
+      const uint32_t aQ = ptx::smem_addr(sQ), aKV = ptx::smem_addr(sKV);
+      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
+      constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD) | (1u << 16);   // B transposed
+      uint32_t it = 0, unit = 0, np[2] = {0, 0};             // ring base, units, PV products of x
+      bool ok = true;
+      while (c.left > 0 && ok) {
+        const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
+        const int nt = min(c.rq.n * p.G - c.j * kRowsT, kRowsT) > 128 ? 2 : 1;
+        ok = wait(q_full, unit & 1u);
+        ptx::tc_fence_after();
+        const int jobs[2] = {nt == 2 ? n : (n + 1) / 2, nt == 2 ? n : n / 2};
+        auto issue_s = [&](int x, int i) {
+          const int t = nt == 2 ? i : 2 * i + x;
+          const uint32_t at = it + 2 * t, s = at % R;
+          if (!wait(&full[s], at / R & 1u)) return false;
+          ptx::tc_fence_after();
+          const uint32_t q0 = aQ + (nt == 2 ? x * S::kTile : 0), k0 = aKV + s * S::kTile;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * S::kAtom + (kk & 3) * 32;
+            ptx::mma_bf16((tbase + 128 * x), ptx::sw128_kmajor_desc(q0 + off), ptx::sw128_kmajor_desc(k0 + off),
+                          idesc_s, kk > 0 ? 1u : 0u);
+          }
+          ptx::mma_commit(&s_ready[x]);
+          if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
+          return true;
+        };
+        auto issue_pv = [&](int x, int i) {
+          const int t = nt == 2 ? i : 2 * i + x;
+          const uint32_t at = it + 2 * t + 1, s = at % R;
+          if (!wait(&p_ready[x], np[x] & 1u)) return false;
+          if (!wait(&full[s], at / R & 1u)) return false;
+          ptx::tc_fence_after();
+          const uint32_t v0 = aKV + s * S::kTile;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            ptx::mma_bf16_ta((tbase + 256 + 128 * x), (tbase + 128 * x) + j * 8, ptx::sw128_mnmajor_desc(v0 + j * 2048, S::kAtom, 1024),
+                             idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
+          ptx::mma_commit(&pv_done[x]);
+          if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
+          ++np[x];
+          return true;
+        };
+#pragma unroll
+        for (int x = 0; x < 2 && ok; ++x)
+          if (jobs[x] > 0) ok = issue_s(x, 0);
+        for (int i = 0; i < jobs[0] && ok; ++i)
+#pragma unroll
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (i < jobs[x]) ok = issue_pv(x, i);
+            if (ok && i + 1 < jobs[x]) ok = issue_s(x, i + 1);
+          }
+        it += 2 * n;
+        ++unit;
+        c.left -= n;
+        if (c.left > 0) paged_next(p, kRowsT, kStepT, &c);
+      }
+      if (!ok) fail();
+      // the MMAs already issued finish before TMEM is released
+      if (unit > 0 || !ok) {
+        ptx::mma_commit(drain);
+        ptx::mbar_wait_bounded(drain, 0u, kTimeoutNs, nullptr);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    ptx::regs_inc<kRegsSoftmax>();
+    // ---------------- softmax: group x = warp / 4, a row to a thread ----------------
+    const int x = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t aS = (tbase + 128 * x) + lane_off, aO = (tbase + 256 + 128 * x) + lane_off;
+    const float sc = p.scale_log2;
+    uint32_t it = 0, nj = 0;                                 // ring base, jobs of this group
+    bool ok = true;
+    while (c.left > 0) {
+      const PagedReq rq = c.rq;
+      const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
+      const int nG = rq.n * p.G, tile0 = c.j * kRowsT;
+      const int nt = min(nG - tile0, kRowsT) > 128 ? 2 : 1;
+      const int kend = rq.key_end(c.j, p.G, kRowsT);
+      const int rho0 = tile0 + (nt == 2 ? x * 128 : 0);      // first row of this group's MMA tile
+      const int rho = rho0 + row;
+      const bool live = rho < nG;
+      const int tok = live ? rho / p.G : 0, head = c.g * p.G + (live ? rho % p.G : 0);
+      const int jobs = nt == 2 ? n : (n + 1 - x) / 2;
+      // Q into shared memory: rows of 128 bytes, 128-byte swizzle
+      if (nt == 2 || x == 0) {
+        const __nv_bfloat16* src = p.q + (long long)(rq.row0 + tok) * p.q_ld + (long long)head * HD;
+        uint8_t* dst = sQ + x * S::kTile + row * 128;
+#pragma unroll
+        for (int ch = 0; ch < HD / 8; ++ch) {
+          const uint4 u = live ? __ldg(reinterpret_cast<const uint4*>(src + ch * 8)) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * S::kAtom + (((ch & 7) ^ (row & 7)) << 4)) = u;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_full);
+
+      // first slot past what the row sees (causal), the mask row, and the keys
+      // that every row of the warp, and of the whole tile, sees
+      const int lim = live ? (rq.masked ? kend : min(rq.p0 + tok + 1, kend)) : 0;
+      const uint32_t* mrow = rq.masked ? p.mask + (size_t)(rq.row0 + tok) * p.mask_ld : nullptr;
+      const int first = min(rho0 + (warp & 3) * 32, nG - 1) / p.G;
+      const int plain_w = rho0 + (warp & 3) * 32 >= nG ? 0 : min(rq.masked ? rq.p0 : rq.p0 + first + 1, kend);
+      const int plain_t = min(rq.masked ? rq.p0 : rq.p0 + tile0 / p.G + 1, kend);
+      const bool dead = rho0 + (warp & 3) * 32 >= nG;        // no live row in this warp
+      float m_ref = -CUDART_INF_F, l = 0.f;
+      // (after a wait has run out the loop only keeps the group's barriers company)
+      for (int i = 0; i < jobs; ++i, ++nj) {
+        const int t = nt == 2 ? i : 2 * i + x, key0 = (c.step + t) * kStepT;
+        volatile uint32_t* noted = odd_keys + 16 * (nt == 2 ? 0 : x) + 4 * (t & 3);
+        if (ok) ok = __all_sync(0xffffffffu, wait(&s_ready[x], nj & 1u));
+        const bool check = key0 + kStepT > plain_t && (nt == 1 || x == 0);   // group-uniform
+        uint32_t seen[4];
+        if (ok && !dead) {
+          ptx::tc_fence_after();
+          uint32_t u[4][32];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) ptx::tmem_ld_32x32(aS + 32 * b, u[b]);
+          ptx::tmem_wait_ld();
+          if (key0 + kStepT > plain_w) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const int k = key0 + 32 * b;
+              seen[b] = low_bits(lim - k);
+              if (rq.masked && seen[b]) seen[b] &= seen_word(mrow, p.mask_ld, k - rq.p0);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((seen[b] >> j) & 1u)) u[b][j] = 0xff800000u;
+            }
+          } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) seen[b] = 0xFFFFFFFFu;
+          }
+          float mx = -CUDART_INF_F;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              mx = fmaxf(fmaxf(mx, __uint_as_float(u[b][j])), __uint_as_float(u[b][j + 1]));
+          mx *= sc;
+          const bool raise = mx > m_ref + kLazy || (m_ref == -CUDART_INF_F && mx > m_ref);
+          if (__any_sync(0xffffffffu, raise)) {
+            const float m_new = raise ? mx : m_ref;
+            const float f = raise ? (m_ref == -CUDART_INF_F ? 0.f : ex2(m_ref - m_new)) : 1.f;
+            m_ref = m_new;
+            l *= f;
+            if (i > 0) {
+              // the products so far must be in O before it is scaled
+              ok = __all_sync(0xffffffffu, wait(&pv_done[x], (nj - 1) & 1u));
+              if (ok) {
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int b = 0; b < HD / 16; ++b) {
+                  float o[16];
+                  ptx::tmem_ld_32x16(aO + 16 * b, o);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) o[j] *= f;
+                  ptx::tmem_st_32x16(aO + 16 * b, o);
+                }
+                ptx::tmem_wait_st();
+              }
+            }
+          }
+          const float base = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+          const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
+          float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int b = 2 * h + (j >> 4), e = 2 * (j & 15);
+              const float2 y = __ffma2_rn(
+                  make_float2(__uint_as_float(u[b][e]), __uint_as_float(u[b][e + 1])), sc2, nb2);
+              const float2 w = make_float2(ex2(y.x), ex2(y.y));
+              rs[j & 1] = __fadd2_rn(rs[j & 1], w);
+              pk[j] = mmas::pack_bf16(w.x, w.y);
+            }
+            ptx::tmem_st_32x32(aS + 32 * h, pk);
+          }
+          l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+          ptx::tmem_wait_st();
+        }
+        bool odd = false;
+        if (check) {
+          // Some row may not see some key of this step: the values of keys past
+          // the tile's last one become zeros, and so do values that are not
+          // finite (their keys are noted, see below).
+          const uint32_t at = it + 2 * t + 1, s = at % R;
+          ok = __all_sync(0xffffffffu, ok && wait(&full[s], at / R & 1u));
+          if (ptx::named_bar_or(1 + x, 128, !ok)) ok = false;
+          bool mine = false;
+          if (ok) {
+            uint8_t* v = sKV + s * S::kTile + row * 128;     // this thread: one key
+            const bool past = key0 + row >= kend;
+#pragma unroll
+            for (int ch = 0; ch < HD / 8; ++ch) {
+              uint4* a = reinterpret_cast<uint4*>(v + (ch >> 3) * S::kAtom + ((ch & 7) << 4));
+              uint4 w = past ? make_uint4(0, 0, 0, 0) : *a;
+              const bool bad = not_finite8(w);
+              if (bad) {
+                mine = true;
+                w.x = zero_not_finite(w.x);
+                w.y = zero_not_finite(w.y);
+                w.z = zero_not_finite(w.z);
+                w.w = zero_not_finite(w.w);
+              }
+              if (past || bad) *a = w;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          const uint32_t keys = __ballot_sync(0xffffffffu, mine);
+          if (lane == 0) noted[warp & 3] = keys;
+          odd = ptx::named_bar_or(1 + x, 128, mine);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) ptx::mbar_arrive(&p_ready[x]);
+        if (nt == 2 && x == 1 && key0 + kStepT > plain_t) odd = true;   // group 0 noted them
+        if (odd && ok) {
+          // P V ran with zeros for the bad values: a row that sees such a key takes
+          // the value itself now (times any weight it is the same inf or NaN)
+          ok = __all_sync(0xffffffffu, wait(&pv_done[x], nj & 1u));
+          if (ok && !dead) {
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              uint32_t keys = noted[b];
+              while (keys) {                                 // warp-uniform
+                const int j = __ffs(keys) - 1;
+                keys &= keys - 1;
+                const int key = key0 + 32 * b + j, page = page_of(p.pv, c.r, key);
+                if (page < 0) continue;
+                const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.pv.v) +
+                                         pool_row(p.pv, page, c.g, key) * HD;
+                const bool see = (seen[b] >> j) & 1u;
+                for (int cb = 0; cb < HD / 32; ++cb) {
+                  uint32_t o[32];
+                  ptx::tmem_ld_32x32(aO + 32 * cb, o);
+                  ptx::tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    const float val = __bfloat162float(v[32 * cb + e]);
+                    if (see && !(fabsf(val) <= CUDART_MAX_NORMAL_F))
+                      o[e] = __float_as_uint(__uint_as_float(o[e]) + val);
+                  }
+                  ptx::tmem_st_32x32(aO + 32 * cb, o);
+                  ptx::tmem_wait_st();
+                }
+              }
+            }
+            ptx::tc_fence_before();
+          }
+        }
+      }
+      if (ok && jobs > 0) {
+        ok = __all_sync(0xffffffffu, wait(&pv_done[x], (nj - 1) & 1u));
+        if (ok) ptx::tc_fence_after();
+      }
+      if (ptx::named_bar_or(5, 256, !ok)) {
+        ok = false;
+        break;
+      }
+      // ---- the tile's rows ----
+      float M = m_ref, L = l, fa = 1.f, fb = 0.f;            // weights of the two halves
+      float* sB = reinterpret_cast<float*>(sQ);              // [128][HD], chunks of 4 swizzled
+      if (nt == 1) {
+        if (x == 1) {
+          sMl[row] = make_float2(m_ref, l);
+          if (jobs > 0) {
+#pragma unroll
+            for (int b = 0; b < HD / 32; ++b) {
+              uint32_t o[32];
+              ptx::tmem_ld_32x32(aO + 32 * b, o);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(sB + row * HD + 4 * ((8 * b + j) ^ (row & 7))) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+          }
+        }
+        ptx::named_bar_sync(5, 256);
+        if (x == 0) {
+          const float2 ml = sMl[row];
+          if (ml.y != 0.f) {
+            M = fmaxf(m_ref, ml.x);
+            fa = l != 0.f ? ex2(m_ref - M) : 0.f;
+            fb = ex2(ml.x - M);
+            L = fa * l + fb * ml.y;
+          }
+        }
+      }
+      const bool mine = nt == 2 || x == 0;                   // this group writes its rows
+      const long long unit0 = end - c.left - c.step;
+      const bool whole = n == c.n_steps;
+      const int c0 = whole ? 0 : paged_owner(total, unit0, grid);
+      const int c1 = whole ? 0 : paged_owner(total, unit0 + c.n_steps - 1, grid);
+      // partials: [slot][x][HD / 4][128 rows] of four columns, so that a warp's lanes
+      // are neighbours in memory
+      auto part_of = [&](int cc) { return ((size_t)cc * 2 + (cc == c0)) * 2 + x; };
+      const size_t slot = part_of(blockIdx.x);
+      __nv_bfloat16* dst = p.out + (long long)(rq.row0 + tok) * p.out_ld + (long long)head * HD;
+      auto put = [&](int b, const float (&o)[32], float inv) {    // 32 columns of the output row
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w4[e] = L == 0.f ? 0u : mmas::pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
+          *reinterpret_cast<uint4*>(dst + 32 * b + 8 * j) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+      };
+      if (mine && !dead) {
+#pragma unroll
+        for (int b = 0; b < HD / 32; ++b) {
+          uint32_t u[32];
+          ptx::tmem_ld_32x32(aO + 32 * b, u);
+          ptx::tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = fa == 0.f ? 0.f : __uint_as_float(u[j]) * fa;
+          if (fb != 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 v = *reinterpret_cast<const float4*>(sB + row * HD + 4 * ((8 * b + j) ^ (row & 7)));
+              o[4 * j] += fb * v.x;
+              o[4 * j + 1] += fb * v.y;
+              o[4 * j + 2] += fb * v.z;
+              o[4 * j + 3] += fb * v.w;
+            }
+          }
+          if (whole) {
+            if (live) put(b, o, 1.f / L);
+          } else if (live) {
+            float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + 8 * b) * 128 + row;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              __stcg(po + j * 128, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      if (!whole && mine) {
+        if (live) __stcg(p.part_ml + slot * 128 + row, make_float2(M, L));
+        __threadfence();
+        ptx::named_bar_sync(1 + x, 128);
+        if (row == 0) s_last[x] = atomicAdd(p.arrive + 2 * c0 + x, 1) == c1 - c0;
+        ptx::named_bar_sync(1 + x, 128);
+        if (s_last[x]) {
+          __threadfence();
+          if (row == 0) p.arrive[2 * c0 + x] = 0;            // for the next call
+          if (live) {
+            M = -CUDART_INF_F;
+#pragma unroll 4
+            for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_ml + part_of(cc) * 128 + row).x);
+            float o[HD] = {};
+            L = 0.f;
+            float2 ml = __ldcg(p.part_ml + part_of(c0) * 128 + row);
+            for (int cc = c0; cc <= c1; ++cc) {
+              const float2 now = ml;
+              if (cc < c1) ml = __ldcg(p.part_ml + part_of(cc + 1) * 128 + row);
+              const float f = now.y != 0.f ? ex2(now.x - M) : 0.f;
+              L += f * now.y;
+              const float4* src = reinterpret_cast<const float4*>(p.part_o) + part_of(cc) * (HD / 4) * 128 + row;
+#pragma unroll
+              for (int j = 0; j < HD / 4; ++j) {
+                const float4 v = __ldcg(src + j * 128);
+                if (now.y != 0.f) {
+                  o[4 * j] += f * v.x;
+                  o[4 * j + 1] += f * v.y;
+                  o[4 * j + 2] += f * v.z;
+                  o[4 * j + 3] += f * v.w;
+                }
+              }
+            }
+#pragma unroll
+            for (int b = 0; b < HD / 32; ++b) put(b, reinterpret_cast<float(&)[32]>(o[32 * b]), 1.f / L);
+          }
+        }
+      }
+      it += 2 * n;
+      c.left -= n;
+      if (c.left > 0) paged_next(p, kRowsT, kStepT, &c);
+      // the joined half lies where the next tile's queries go
+      ptx::named_bar_sync(5, 256);
+    }
+    if (!ok) fail();
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 9) {
+    __syncwarp();
+    ptx::tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int HD>
+dflash_status launch_tc(const PagedAttnParams& p, const dflash_pages& pages, int grid, cudaStream_t st) {
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    cudaFuncSetAttribute(paged_attn_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         TcSmem<HD>::kBytes);
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  PagedTcMaps maps;
+  const int rows = pages.n_pages * pages.n_kv * pages.page_size;
+  const int box = pages.page_size < 128 ? pages.page_size : 128;
+  if (!encode_kmajor_map(&maps.k, pages.k, rows, HD, HD, box) ||
+      !encode_kmajor_map(&maps.v, pages.v, rows, HD, HD, box))
+    return set_error(DFLASH_ERR_CUDA, "paged attention: cannot encode the TMA descriptors");
+  TraceScope ts("paged_attn_tc", st);
+  launch_k(paged_attn_tc_kernel<HD>, dim3(grid), dim3(kThreadsT), TcSmem<HD>::kBytes, st, maps, p);
+  return DFLASH_OK;
+}
+
+constexpr int kMaxTileRows = kRowsT;
 
 // Header, arrival counters, (max, sum) pairs, partial rows.
 struct PagedWs {
@@ -384,7 +996,7 @@ struct PagedWs {
 PagedWs paged_ws(int grid, int head_dim) {
   PagedWs w;
   w.arrive = 256;
-  w.ml = w.arrive + align_up((size_t)grid * sizeof(int), 256);
+  w.ml = w.arrive + align_up((size_t)grid * 2 * sizeof(int), 256);
   w.o = w.ml + align_up((size_t)grid * 2 * kMaxTileRows * sizeof(float2), 256);
   w.bytes = w.o + (size_t)grid * 2 * kMaxTileRows * head_dim * sizeof(float);
   return w;
@@ -451,7 +1063,12 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
   p.part_o = reinterpret_cast<float*>(b + w.o);
   p.status = reinterpret_cast<int*>(b);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  hd == 128 ? launch_small<128>(p, grid, st) : launch_small<64>(p, grid, st);
+  if ((long long)max_rows * p.G <= kRowsS) {
+    hd == 128 ? launch_small<128>(p, grid, st) : launch_small<64>(p, grid, st);
+  } else {
+    const dflash_status e = hd == 128 ? launch_tc<128>(p, *pages, grid, st) : launch_tc<64>(p, *pages, grid, st);
+    if (e) return e;
+  }
   return check_launch("paged attention");
 }
 

@@ -19,11 +19,11 @@ struct PagedAttnParams {
   long long out_ld;
   float scale_log2;
   // a tile split between CTAs: two slots of partial rows per CTA (its first
-  // tile and its last), unnormalised O and (max, sum) of each row, and one
-  // arrival counter per CTA for the tile that begins there and goes on
+  // tile and its last), unnormalised O and (max, sum) of each row, and arrival
+  // counters per CTA for the tile that begins there and goes on
   float* part_o;                   // [grid][2][rows][hd]
   float2* part_ml;                 // [grid][2][rows]
-  int* arrive;                     // [grid]
+  int* arrive;                     // [grid], or [grid][2] (halves of a tile)
   int* status;
 };
 
