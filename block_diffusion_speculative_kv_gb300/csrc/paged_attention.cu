@@ -91,13 +91,10 @@ __global__ void __launch_bounds__(kThreadsS, 1) paged_attn_small_kernel(const Pa
   pdl_wait();
   pdl_trigger();
   const int grid = gridDim.x;
-  const long long total = paged_total(p, kRowsS, kStepS, lane);
-  const long long begin = paged_share(total, blockIdx.x, grid);
-  const long long end = paged_share(total, blockIdx.x + 1, grid);
-  if (begin >= end) return;
+  long long total, end;                                  // all steps, and the end of this CTA's share
   PagedCursor c;
-  paged_seek(p, kRowsS, kStepS, lane, begin, &c);
-  c.left = end - begin;
+  paged_plan(p, kRowsS, kStepS, lane, &total, &end, &c);
+  if (c.left <= 0) return;
 
   const __nv_bfloat16* pool_k = static_cast<const __nv_bfloat16*>(p.pv.k);
   const __nv_bfloat16* pool_v = static_cast<const __nv_bfloat16*>(p.pv.v);
@@ -332,23 +329,31 @@ __global__ void __launch_bounds__(kThreadsS, 1) paged_attn_small_kernel(const Pa
         *reinterpret_cast<float4*>(po + x) = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
       if ((tid & 7) == 0) p.part_ml[slot * kRowsS + row] = make_float2(M, L);
       __threadfence();
+      mmas::cp_async_wait<0>();
       __syncthreads();
       if (tid == 0) *sLast = atomicAdd(p.arrive + c0, 1) == c1 - c0;
       __syncthreads();
       if (*sLast) {
         __threadfence();
         if (tid == 0) p.arrive[c0] = 0;                  // for the next call
+        // the pieces' (max, sum) first, all at once, into the idle ring
+        float2* sPart = reinterpret_cast<float2*>(smem);
+        const int parts = c1 - c0 + 1;
+        for (int i = tid; i < parts * kRowsS; i += kThreadsS) {
+          const int cc = c0 + i / kRowsS;
+          sPart[i] = __ldcg(p.part_ml + ((size_t)cc * 2 + (cc == c0)) * kRowsS + i % kRowsS);
+        }
+        __syncthreads();
         M = -CUDART_INF_F;
+        for (int i = 0; i < parts; ++i) M = fmaxf(M, sPart[i * kRowsS + row].x);
         L = 0.f;
 #pragma unroll
         for (int x = 0; x < kCols; ++x) acc[x] = 0.f;
-        for (int cc = c0; cc <= c1; ++cc)
-          M = fmaxf(M, __ldcg(p.part_ml + ((size_t)cc * 2 + (cc == c0)) * kRowsS + row).x);
-        for (int cc = c0; cc <= c1; ++cc) {
-          const size_t s2 = ((size_t)cc * 2 + (cc == c0)) * kRowsS + row;
-          const float2 ml = __ldcg(p.part_ml + s2);
-          if (ml.y == 0.f) continue;
-          const float f = ex2(ml.x - M);
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+          const float2 ml = sPart[i * kRowsS + row];
+          const size_t s2 = ((size_t)(c0 + i) * 2 + (i == 0)) * kRowsS + row;
+          const float f = ml.y == 0.f ? 0.f : ex2(ml.x - M);
           L += f * ml.y;
 #pragma unroll
           for (int x = 0; x < kCols; x += 4) {
@@ -449,10 +454,10 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   uint64_t* empty = bar + R;                                 // [R] tile read
   uint64_t* q_full = bar + 2 * R;
   uint64_t* s_ready = q_full + 1;                            // [2]
-  uint64_t* p_ready = q_full + 3;                            // [2]
-  uint64_t* pv_done = q_full + 5;                            // [2]
-  uint64_t* drain = q_full + 7;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(q_full + 8);
+  uint64_t* p_ready = q_full + 3;                            // [2][half]
+  uint64_t* pv_done = q_full + 7;                            // [2]
+  uint64_t* drain = q_full + 9;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(q_full + 10);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(tslot + 2);    // [2]
   // keys with a value that is not finite: [group][step % 4][word].  Group 1 may
@@ -469,7 +474,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     ptx::mbar_init(q_full, 8);
     for (int x = 0; x < 2; ++x) {
       ptx::mbar_init(&s_ready[x], 1);
-      ptx::mbar_init(&p_ready[x], 4);
+      ptx::mbar_init(&p_ready[2 * x], 4);
+      ptx::mbar_init(&p_ready[2 * x + 1], 4);
       ptx::mbar_init(&pv_done[x], 1);
     }
     ptx::mbar_init(drain, 1);
@@ -489,12 +495,9 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   pdl_wait();
   pdl_trigger();
   const int grid = gridDim.x;
-  const long long total = paged_total(p, kRowsT, kStepT, lane);
-  const long long begin = paged_share(total, blockIdx.x, grid);
-  const long long end = paged_share(total, blockIdx.x + 1, grid);
+  long long total, end;
   PagedCursor c;
-  c.left = end - begin;
-  if (c.left > 0) paged_seek(p, kRowsT, kStepT, lane, begin, &c);
+  paged_plan(p, kRowsT, kStepT, lane, &total, &end, &c);
 
   auto fail = [&]() {
     if (!*abort) record_status(p.status, DFLASH_ERR_TIMEOUT);
@@ -563,70 +566,84 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     }
   } else if (warp == 9) {
     // ---------------- MMA issue ----------------
-    if (lane == 0) {
-      const uint32_t aQ = ptx::smem_addr(sQ), aKV = ptx::smem_addr(sKV);
-      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
-      constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD) | (1u << 16);   // B transposed
-      uint32_t it = 0, unit = 0, np[2] = {0, 0};             // ring base, units, PV products of x
-      bool ok = true;
-      while (c.left > 0 && ok) {
-        const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
-        const int nt = min(c.rq.n * p.G - c.j * kRowsT, kRowsT) > 128 ? 2 : 1;
-        ok = wait(q_full, unit & 1u);
+    // The whole warp runs the loop, so that addresses and descriptors stay in
+    // uniform registers; one elected lane issues.  Descriptors differ by their
+    // address field alone: a constant is added to the tile's.
+    const bool elected = ptx::elect_one();
+    const uint64_t dq = ptx::sw128_kmajor_desc(ptx::smem_addr(sQ));
+    const uint64_t dk = ptx::sw128_kmajor_desc(ptx::smem_addr(sKV));
+    const uint64_t dv = ptx::sw128_mnmajor_desc(ptx::smem_addr(sKV), S::kAtom, 1024);
+    constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
+    constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD) | (1u << 16);   // B transposed
+    uint32_t it = 0, unit = 0, np[2] = {0, 0};               // ring base, units, PV products of x
+    bool ok = true;
+    while (c.left > 0 && ok) {
+      const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
+      const int nt = min(c.rq.n * p.G - c.j * kRowsT, kRowsT) > 128 ? 2 : 1;
+      ok = __all_sync(0xffffffffu, wait(q_full, unit & 1u));
+      ptx::tc_fence_after();
+      const int jobs0 = nt == 2 ? n : (n + 1) / 2, jobs1 = nt == 2 ? n : n / 2;
+      auto issue_s = [&](int x, int i) {
+        const uint32_t at = it + 2 * (nt == 2 ? i : 2 * i + x);
+        const uint32_t s = __shfl_sync(0xffffffffu, at % R, 0);
+        if (!__all_sync(0xffffffffu, wait(&full[s], at / R & 1u))) return false;
         ptx::tc_fence_after();
-        const int jobs[2] = {nt == 2 ? n : (n + 1) / 2, nt == 2 ? n : n / 2};
-        auto issue_s = [&](int x, int i) {
-          const int t = nt == 2 ? i : 2 * i + x;
-          const uint32_t at = it + 2 * t, s = at % R;
-          if (!wait(&full[s], at / R & 1u)) return false;
-          ptx::tc_fence_after();
-          const uint32_t q0 = aQ + (nt == 2 ? x * S::kTile : 0), k0 = aKV + s * S::kTile;
+        const uint64_t q0 = dq + (nt == 2 ? x * (S::kTile >> 4) : 0), k0 = dk + s * (S::kTile >> 4);
+        if (elected) {
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * S::kAtom + (kk & 3) * 32;
-            ptx::mma_bf16((tbase + 128 * x), ptx::sw128_kmajor_desc(q0 + off), ptx::sw128_kmajor_desc(k0 + off),
-                          idesc_s, kk > 0 ? 1u : 0u);
+            const uint32_t off = ((kk >> 2) * S::kAtom + (kk & 3) * 32) >> 4;
+            ptx::mma_bf16(tbase + 128 * x, q0 + off, k0 + off, idesc_s, kk > 0 ? 1u : 0u);
           }
           ptx::mma_commit(&s_ready[x]);
           if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
-          return true;
-        };
-        auto issue_pv = [&](int x, int i) {
-          const int t = nt == 2 ? i : 2 * i + x;
-          const uint32_t at = it + 2 * t + 1, s = at % R;
-          if (!wait(&p_ready[x], np[x] & 1u)) return false;
-          if (!wait(&full[s], at / R & 1u)) return false;
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_pv = [&](int x, int i) {
+        const uint32_t at = it + 2 * (nt == 2 ? i : 2 * i + x) + 1;
+        const uint32_t s = __shfl_sync(0xffffffffu, at % R, 0);
+        if (!__all_sync(0xffffffffu, wait(&full[s], at / R & 1u))) return false;
+        const uint64_t v0 = dv + s * (S::kTile >> 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {                        // P arrives in two halves
+          if (!__all_sync(0xffffffffu, wait(&p_ready[2 * x + h], np[x] & 1u))) return false;
           ptx::tc_fence_after();
-          const uint32_t v0 = aKV + s * S::kTile;
+          if (elected) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            ptx::mma_bf16_ta((tbase + 256 + 128 * x), (tbase + 128 * x) + j * 8, ptx::sw128_mnmajor_desc(v0 + j * 2048, S::kAtom, 1024),
-                             idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
-          ptx::mma_commit(&pv_done[x]);
-          if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
-          ++np[x];
-          return true;
-        };
-#pragma unroll
-        for (int x = 0; x < 2 && ok; ++x)
-          if (jobs[x] > 0) ok = issue_s(x, 0);
-        for (int i = 0; i < jobs[0] && ok; ++i)
-#pragma unroll
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (i < jobs[x]) ok = issue_pv(x, i);
-            if (ok && i + 1 < jobs[x]) ok = issue_s(x, i + 1);
+            for (int j = 4 * h; j < 4 * h + 4; ++j)
+              ptx::mma_bf16_ta(tbase + 256 + 128 * x, tbase + 128 * x + j * 8, v0 + j * (2048 >> 4),
+                               idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
+            if (h == 1) {
+              ptx::mma_commit(&pv_done[x]);
+              if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
+            }
           }
-        it += 2 * n;
-        ++unit;
-        c.left -= n;
-        if (c.left > 0) paged_next(p, kRowsT, kStepT, &c);
+          __syncwarp();
+        }
+        ++np[x];
+        return true;
+      };
+      if (ok) ok = issue_s(0, 0);
+      if (ok && jobs1 > 0) ok = issue_s(1, 0);
+      for (int i = 0; i < jobs0 && ok; ++i) {
+        ok = issue_pv(0, i);
+        if (ok && i + 1 < jobs0) ok = issue_s(0, i + 1);
+        if (ok && i < jobs1) ok = issue_pv(1, i);
+        if (ok && i + 1 < jobs1) ok = issue_s(1, i + 1);
       }
-      if (!ok) fail();
-      // the MMAs already issued finish before TMEM is released
-      if (unit > 0 || !ok) {
-        ptx::mma_commit(drain);
-        ptx::mbar_wait_bounded(drain, 0u, kTimeoutNs, nullptr);
-      }
+      it += 2 * n;
+      ++unit;
+      c.left -= n;
+      if (c.left > 0) paged_next(p, kRowsT, kStepT, &c);
+    }
+    if (!ok && lane == 0) fail();
+    // the MMAs already issued finish before TMEM is released
+    if (unit > 0 || !ok) {
+      if (elected) ptx::mma_commit(drain);
+      __syncwarp();
+      ptx::mbar_wait_bounded(drain, 0u, kTimeoutNs, nullptr);
     }
     __syncwarp();
   }
@@ -650,14 +667,20 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       const bool live = rho < nG;
       const int tok = live ? rho / p.G : 0, head = c.g * p.G + (live ? rho % p.G : 0);
       const int jobs = nt == 2 ? n : (n + 1 - x) / 2;
-      // Q into shared memory: rows of 128 bytes, 128-byte swizzle
+      // Q into shared memory (rows of 128 bytes, 128-byte swizzle): HD / 8 lanes
+      // read a row, whose address its own lane knows
       if (nt == 2 || x == 0) {
-        const __nv_bfloat16* src = p.q + (long long)(rq.row0 + tok) * p.q_ld + (long long)head * HD;
-        uint8_t* dst = sQ + x * S::kTile + row * 128;
-#pragma unroll
-        for (int ch = 0; ch < HD / 8; ++ch) {
-          const uint4 u = live ? __ldg(reinterpret_cast<const uint4*>(src + ch * 8)) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + (ch >> 3) * S::kAtom + (((ch & 7) ^ (row & 7)) << 4)) = u;
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(
+            p.q + (long long)(rq.row0 + tok) * p.q_ld + (long long)head * HD);
+        const unsigned on = __ballot_sync(0xffffffffu, live);
+        constexpr int kPer = 256 / HD;                       // rows of a round
+#pragma unroll 8
+        for (int r0 = 0; r0 < 32; r0 += kPer) {
+          const int rr = r0 + lane / (HD / 8), ch = lane % (HD / 8);
+          const uint4* src = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, mine, rr)) + ch;
+          const uint4 u = (on >> rr) & 1u ? __ldg(src) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sQ + x * S::kTile + (ch >> 3) * S::kAtom + ((warp & 3) * 32 + rr) * 128 +
+                                    (((ch & 7) ^ (rr & 7)) << 4)) = u;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -680,6 +703,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         if (ok) ok = __all_sync(0xffffffffu, wait(&s_ready[x], nj & 1u));
         const bool check = key0 + kStepT > plain_t && (nt == 1 || x == 0);   // group-uniform
         uint32_t seen[4];
+        const bool early = !check && !dead;                  // P goes out in two halves
         if (ok && !dead) {
           ptx::tc_fence_after();
           uint32_t u[4][32];
@@ -700,25 +724,26 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
 #pragma unroll
             for (int b = 0; b < 4; ++b) seen[b] = 0xFFFFFFFFu;
           }
-          float mx = -CUDART_INF_F;
+          float mx8[8];                                      // eight chains: latency
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int j = 0; j < 8; ++j) mx8[j] = __uint_as_float(u[0][j]);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2)
-              mx = fmaxf(fmaxf(mx, __uint_as_float(u[b][j])), __uint_as_float(u[b][j + 1]));
-          mx *= sc;
-          const bool raise = mx > m_ref + kLazy || (m_ref == -CUDART_INF_F && mx > m_ref);
+          for (int j = 4; j < 64; ++j)
+            mx8[j & 7] = fmaxf(fmaxf(mx8[j & 7], __uint_as_float(u[j >> 4][2 * (j & 15)])),
+                               __uint_as_float(u[j >> 4][2 * (j & 15) + 1]));
+          const float top = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                  fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * sc;
+          const bool raise = top > m_ref + kLazy || (m_ref == -CUDART_INF_F && top > m_ref);
           if (__any_sync(0xffffffffu, raise)) {
-            const float m_new = raise ? mx : m_ref;
-            const float f = raise ? (m_ref == -CUDART_INF_F ? 0.f : ex2(m_ref - m_new)) : 1.f;
-            m_ref = m_new;
+            const float f = raise ? (m_ref == -CUDART_INF_F ? 0.f : ex2(m_ref - top)) : 1.f;
+            if (raise) m_ref = top;
             l *= f;
             if (i > 0) {
               // the products so far must be in O before it is scaled
               ok = __all_sync(0xffffffffu, wait(&pv_done[x], (nj - 1) & 1u));
               if (ok) {
                 ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < HD / 16; ++b) {
                   float o[16];
                   ptx::tmem_ld_32x16(aO + 16 * b, o);
@@ -726,7 +751,6 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
                   for (int j = 0; j < 16; ++j) o[j] *= f;
                   ptx::tmem_st_32x16(aO + 16 * b, o);
                 }
-                ptx::tmem_wait_st();
               }
             }
           }
@@ -746,6 +770,13 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
               pk[j] = mmas::pack_bf16(w.x, w.y);
             }
             ptx::tmem_st_32x32(aS + 32 * h, pk);
+            if (h == 0 && early) {
+              // the first half of P may meet V while the second is formed
+              ptx::tmem_wait_st();
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0 && ok) ptx::mbar_arrive(&p_ready[2 * x]);
+            }
           }
           l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
           ptx::tmem_wait_st();
@@ -764,7 +795,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
             const bool past = key0 + row >= kend;
 #pragma unroll
             for (int ch = 0; ch < HD / 8; ++ch) {
-              uint4* a = reinterpret_cast<uint4*>(v + (ch >> 3) * S::kAtom + ((ch & 7) << 4));
+              // chunks in another order in every row: no bank conflicts
+              uint4* a = reinterpret_cast<uint4*>(v + (ch >> 3) * S::kAtom + (((ch & 7) ^ (row & 7)) << 4));
               uint4 w = past ? make_uint4(0, 0, 0, 0) : *a;
               const bool bad = not_finite8(w);
               if (bad) {
@@ -784,7 +816,10 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) ptx::mbar_arrive(&p_ready[x]);
+        if (lane == 0 && ok) {
+          if (!early) ptx::mbar_arrive(&p_ready[2 * x]);
+          ptx::mbar_arrive(&p_ready[2 * x + 1]);
+        }
         if (nt == 2 && x == 1 && key0 + kStepT > plain_t) odd = true;   // group 0 noted them
         if (odd && ok) {
           // P V ran with zeros for the bad values: a row that sees such a key takes
@@ -869,19 +904,39 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       // are neighbours in memory
       auto part_of = [&](int cc) { return ((size_t)cc * 2 + (cc == c0)) * 2 + x; };
       const size_t slot = part_of(blockIdx.x);
-      __nv_bfloat16* dst = p.out + (long long)(rq.row0 + tok) * p.out_ld + (long long)head * HD;
-      auto put = [&](int b, const float (&o)[32], float inv) {    // 32 columns of the output row
+      // The warp's 32 bf16 rows go out through shared memory, so that HD / 8
+      // lanes write a row together: in the group's part of Q, or, a lane each, in
+      // its row of the joined half, over columns that it has read.
+      uint8_t* stage = nt == 2 ? sQ + warp * (S::kTile / 4) : sQ + (warp & 3) * (S::kTile / 2);
+      const int stage_ld = nt == 2 ? HD * 2 : HD * 4;
+      auto put = [&](int b, const float (&o)[32], float inv) {    // 32 columns of the row
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t w4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w4[e] = L == 0.f ? 0u : mmas::pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
-          *reinterpret_cast<uint4*>(dst + 32 * b + 8 * j) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          *reinterpret_cast<uint4*>(stage + lane * stage_ld + (((4 * b + j) ^ (lane & 7)) << 4)) =
+              make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+      };
+      auto send = [&]() {
+        __syncwarp();
+        const unsigned long long mine_to = reinterpret_cast<unsigned long long>(
+            p.out + (long long)(rq.row0 + tok) * p.out_ld + (long long)head * HD);
+        const unsigned on = __ballot_sync(0xffffffffu, live);
+        constexpr int kPer = 256 / HD;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += kPer) {
+          const int rr = r0 + lane / (HD / 8), ch = lane % (HD / 8);
+          uint4* to = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, mine_to, rr)) + ch;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * stage_ld + ((ch ^ (rr & 7)) << 4));
+          if ((on >> rr) & 1u) *to = w;
         }
       };
       if (mine && !dead) {
-#pragma unroll
+        const float inv = 1.f / L;
+#pragma unroll 1
         for (int b = 0; b < HD / 32; ++b) {
           uint32_t u[32];
           ptx::tmem_ld_32x32(aO + 32 * b, u);
@@ -900,7 +955,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
             }
           }
           if (whole) {
-            if (live) put(b, o, 1.f / L);
+            put(b, o, inv);
           } else if (live) {
             float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + 8 * b) * 128 + row;
 #pragma unroll
@@ -908,6 +963,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
               __stcg(po + j * 128, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
           }
         }
+        if (whole) send();
       }
       ptx::tc_fence_before();
       if (!whole && mine) {
@@ -919,7 +975,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         if (s_last[x]) {
           __threadfence();
           if (row == 0) p.arrive[2 * c0 + x] = 0;            // for the next call
-          if (live) {
+          if (!dead) {
             M = -CUDART_INF_F;
 #pragma unroll 4
             for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_ml + part_of(cc) * 128 + row).x);
@@ -945,6 +1001,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
             }
 #pragma unroll
             for (int b = 0; b < HD / 32; ++b) put(b, reinterpret_cast<float(&)[32]>(o[32 * b]), 1.f / L);
+            send();
           }
         }
       }

@@ -63,35 +63,52 @@ struct PagedCursor {
   PagedReq rq;
 };
 
-// Warp-collective: total steps of all requests, then the request holding step
-// `begin` and the steps before it.
-__device__ __forceinline__ long long paged_total(const PagedAttnParams& p, int TR, int KS, int lane) {
+// a / b for a >= 0, b > 0; almost always within 32 bits, where it is quick.
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+// Share of CTA c of `grid`: [paged_share(c), paged_share(c + 1)).
+__device__ __forceinline__ long long paged_share(long long total, int c, int grid) {
+  const long long q = div_pos(total, grid);
+  return q * c + min((long long)c, total - q * grid);
+}
+// The CTA whose share holds step s.
+__device__ __forceinline__ int paged_owner(long long total, long long s, int grid) {
+  const long long q = div_pos(total, grid), m = total - q * grid;
+  return static_cast<int>(s < m * (q + 1) ? div_pos(s, q + 1) : m + div_pos(s - m * (q + 1), q));
+}
+
+// Warp-collective: all requests' steps, this CTA's share of them, and the place
+// where the share begins.
+__device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int TR, int KS, int lane,
+                                           long long* total_out, long long* end_out,
+                                           PagedCursor* c) {
+  const int grid = gridDim.x;
+  auto steps_of = [&](int r, PagedReq* q) {
+    if (r >= p.n_req) return 0ll;
+    q->load(p, r);
+    return q->steps(q->tiles(p.G, TR), p.G, TR, KS) * p.pv.n_kv;
+  };
+  PagedReq q;
+  const long long first = steps_of(lane, &q);              // of the first 32 requests
   long long total = 0;
   for (int r0 = 0; r0 < p.n_req; r0 += 32) {
-    long long s = 0;
-    if (r0 + lane < p.n_req) {
-      PagedReq q;
-      q.load(p, r0 + lane);
-      s = q.steps(q.tiles(p.G, TR), p.G, TR, KS) * p.pv.n_kv;
-    }
+    long long s = r0 == 0 ? first : steps_of(r0 + lane, &q);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     total += s;
   }
-  return total;
-}
-
-__device__ __forceinline__ void paged_seek(const PagedAttnParams& p, int TR, int KS, int lane,
-                                           long long begin, PagedCursor* c) {
+  const long long begin = paged_share(total, blockIdx.x, grid);
+  const long long end = paged_share(total, blockIdx.x + 1, grid);
+  *total_out = total;
+  *end_out = end;
+  c->left = end - begin;
+  if (c->left <= 0) return;
   long long before = 0;
   for (int r0 = 0; r0 < p.n_req; r0 += 32) {
-    long long s = 0;
-    if (r0 + lane < p.n_req) {
-      PagedReq q;
-      q.load(p, r0 + lane);
-      s = q.steps(q.tiles(p.G, TR), p.G, TR, KS) * p.pv.n_kv;
-    }
-    long long inc = s;                                   // inclusive scan
+    const long long s = r0 == 0 ? first : steps_of(r0 + lane, &q);
+    long long inc = s;                                     // inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long t = __shfl_up_sync(0xffffffffu, inc, o);
@@ -101,12 +118,11 @@ __device__ __forceinline__ void paged_seek(const PagedAttnParams& p, int TR, int
     if (past) {
       const int l = __ffs(past) - 1;
       const long long excl = __shfl_sync(0xffffffffu, inc - s, l);
+      const long long per_g = div_pos(__shfl_sync(0xffffffffu, s, l), p.pv.n_kv);
       c->r = r0 + l;
       c->rq.load(p, c->r);
-      const int nt = c->rq.tiles(p.G, TR);
-      const long long per_g = c->rq.steps(nt, p.G, TR, KS);
       long long rem = begin - before - excl;
-      c->g = static_cast<int>(rem / per_g);
+      c->g = static_cast<int>(div_pos(rem, per_g));
       rem -= (long long)c->g * per_g;
       int j = 0, ns;
       while (true) {
@@ -122,7 +138,6 @@ __device__ __forceinline__ void paged_seek(const PagedAttnParams& p, int TR, int
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  c->r = p.n_req;
 }
 
 // To the next tile (the current one's steps are used up).
@@ -139,16 +154,6 @@ __device__ __forceinline__ void paged_next(const PagedAttnParams& p, int TR, int
   }
   c->step = 0;
   c->n_steps = (c->rq.key_end(c->j, p.G, TR) + KS - 1) / KS;
-}
-
-// Share of CTA c of `grid`: [total * c / grid, total * (c + 1) / grid).
-__device__ __forceinline__ long long paged_share(long long total, int c, int grid) {
-  return total / grid * c + min((long long)c, total % grid);
-}
-// The CTA whose share holds step s.
-__device__ __forceinline__ int paged_owner(long long total, long long s, int grid) {
-  const long long q = total / grid, m = total % grid;
-  return static_cast<int>(s < m * (q + 1) ? s / (q + 1) : m + (s - m * (q + 1)) / q);
 }
 
 }  // namespace dfl
