@@ -27,6 +27,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "mma_sync.cuh"
 
 namespace dfl {
 
@@ -90,17 +91,6 @@ __device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) 
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote_addr(p, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t add_remote(uint32_t* p, uint32_t rank, uint32_t n) {
-  uint32_t v;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
-               : "=r"(v)
-               : "r"(remote_addr(p, rank)), "r"(n)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_remote(uint64_t* p, uint32_t rank, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote_addr(p, rank)), "l"(v) : "memory");
-}
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -134,9 +124,12 @@ struct Shared {
     };
     uint64_t list[kList];                // gathered tokens: (ordered logit, ~id)
   };
+  uint64_t* sorted;                      // kList more, where the slice was
   uint32_t list_n;
   uint32_t found[2];
   uint64_t found_cum;
+  double below;                          // T ln(min-p): what min-p keeps reaches max + this
+  float hi, lo;                          // log2(e) / T in two parts
 };
 
 // Sums (and maxima) over the cluster; every thread receives the result.  The
@@ -170,18 +163,30 @@ struct Reducer {
   }
 };
 
-// Weights of one row: exp((x - mx) / T) as a power of two, log2(e) / T in two
-// non-negative parts so that far tokens keep their relative precision and no
-// infinite distance meets a zero or a sign.  With mx = +inf, x - mx is NaN for
-// the tokens there, and fminf turns that into 0.
+// Weights of one row (mx finite): exp((x - mx) / T) as a power of two, log2(e) / T
+// in two parts so that far tokens keep their relative precision; the second part
+// is positive, so that an infinite distance never meets a zero or a sign.
 struct Weight {
   float mx, hi, lo;
   __device__ __forceinline__ float operator()(float x) const {
-    const float d = fminf(x - mx, 0.f);
+    const float d = x - mx;
     return ex2(fmaf(d, hi, d * lo));
   }
+  // two distances x - mx at once
+  __device__ __forceinline__ float2 at(float2 d) const {
+    const float2 y = __ffma2_rn(d, make_float2(hi, hi), __fmul2_rn(d, make_float2(lo, lo)));
+    return make_float2(ex2(y.x), ex2(y.y));
+  }
+  __device__ __forceinline__ float2 dist(float a, float b) const {
+    return __fadd2_rn(make_float2(a, b), make_float2(-mx, -mx));
+  }
 };
-__device__ __forceinline__ uint64_t fix(float w) { return __float2ull_rn(w * kOne); }
+// w 2^40, w in [0, 8], rounded: in two 32-bit conversions (64-bit ones are slow).
+__device__ __forceinline__ uint64_t fix(float w) {
+  const uint32_t h = __float2uint_rz(w * 1048576.f);                     // 2^20 steps
+  const uint32_t l = __float2uint_rn(fmaf(-__uint2float_rn(h), 9.5367431640625e-7f, w) * kOne);
+  return ((uint64_t)h << 20) + l;
+}
 
 // The search runs over the ordered codes of the values (16 bits for bf16).
 template <typename T>
@@ -203,6 +208,12 @@ struct Chunk<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void clean() {                // NaN becomes -inf
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+    const __nv_bfloat162 none = __float2bfloat162_rn(-CUDART_INF_F);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = __hmax2(h[e], none);
+  }
   __device__ __forceinline__ float max() const {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
     const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
@@ -227,6 +238,14 @@ struct Chunk<float> {
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = a;
     reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void clean() {
+    float* h = &a.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = fmaxf(h[e], -CUDART_INF_F);
+    h = &b.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = fmaxf(h[e], -CUDART_INF_F);
   }
   __device__ __forceinline__ float max() const {
     return fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
@@ -253,9 +272,19 @@ struct Part {
       for (int e = 0; e < 8; ++e) t[e] = i + e < n ? data[i + e] : from_f32<T>(-CUDART_INF_F);
       c.load(t);
     }
+    if constexpr (!RES) c.clean();
     return c;
   }
-  // f(i, x) for every eight tokens of which one is at or above lo (x: NaN counts as -inf)
+  // f(i, x) for every eight tokens (all), or for those of which one is at or above lo
+  template <typename F>
+  __device__ __forceinline__ void all(F f) const {
+#pragma unroll 2
+    for (int i = (threadIdx.x & 31) * 8; i < n; i += 256) {
+      float x[8];
+      at(i).get(x);
+      f(i, x);
+    }
+  }
   template <typename F>
   __device__ __forceinline__ void each(float lo, F f) const {
     for (int i = (threadIdx.x & 31) * 8; i < n; i += 256) {
@@ -263,8 +292,6 @@ struct Part {
       if (!(c.max() >= lo)) continue;
       float x[8];
       c.get(x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaxf(x[e], -CUDART_INF_F);
       f(i, x);
     }
   }
@@ -301,26 +328,116 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, Shared* s, uint64_t* 
   return v;
 }
 
+// whole * f for f in [0, 1), rounded down; *rest: something was rounded away.
+// (Whole numbers throughout: FP64 is slow on this GPU.)
+__device__ __forceinline__ uint64_t share_of(uint64_t whole, float f, bool* rest) {
+  *rest = false;
+  if (!(f > 0.f)) return 0;
+  const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+  const uint64_t mant = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const int sh = 150 - static_cast<int>(e ? e : 1);        // f = mant * 2^-sh, 24 <= sh <= 149
+  const uint64_t lo = whole * mant, hi = __umul64hi(whole, mant);
+  if (sh >= 64) {
+    const int q = sh - 64;
+    *rest = lo != 0 || (q < 64 && (hi & ((1ull << q) - 1))) || (q >= 64 && hi);
+    return q < 64 ? hi >> q : 0;
+  }
+  *rest = (lo & ((1ull << sh) - 1)) != 0;
+  return (hi << (64 - sh)) | (lo >> sh);
+}
 // u of the whole, as the last mass that the token must pass.
-__device__ __forceinline__ uint64_t draw_target(float uf, uint64_t whole) {
-  const double u = uf > 0.f ? (uf < 1.f ? static_cast<double>(uf) : 1.0) : 0.0;
-  const uint64_t t = static_cast<uint64_t>(u * static_cast<double>(whole));
-  return t < whole ? t : whole - 1;
+__device__ __forceinline__ uint64_t draw_target(float u, uint64_t whole) {
+  if (u >= 1.f) return whole - 1;
+  bool rest;
+  return share_of(whole, u, &rest);
 }
-// ln of a token's share of the kept mass.
-__device__ __forceinline__ float log_share(float x, float mx, float temp, uint64_t whole) {
-  const double d = x == mx ? 0.0 : (static_cast<double>(x) - static_cast<double>(mx)) / static_cast<double>(temp);
-  return static_cast<float>(d - log(static_cast<double>(whole) * (1.0 / 1099511627776.0)));
-}
-// The mass that top-p asks for.
+// The mass that top-p (p < 1) asks for.
 __device__ __forceinline__ uint64_t mass_target(float p, uint64_t whole) {
-  const double want = static_cast<double>(p) * static_cast<double>(whole);
-  return want >= 1.0 ? static_cast<uint64_t>(ceil(want)) : 1;
+  bool rest;
+  const uint64_t t = share_of(whole, p, &rest);
+  return max(t + (rest ? 1 : 0), static_cast<uint64_t>(1));
 }
-// The least value that min-p keeps.
-__device__ __forceinline__ float min_p_value(float min_p, float mx, float temp) {
-  const double v = static_cast<double>(mx) + static_cast<double>(temp) * log(static_cast<double>(fminf(min_p, 1.f)));
-  return __double2float_ru(v);
+// ln of a token's share of the kept mass, which is m 2^e with m in [1, 2).
+__device__ __forceinline__ float log_share(float x, float mx, float temp, uint64_t whole) {
+  const int e = 63 - __clzll(whole);
+  const float m = static_cast<float>(whole << (63 - e)) * 1.0842021724855044e-19f;   // 2^-63
+  const float ln = fmaf(e - 40, 0.693145751953125f, fmaf(e - 40, 1.42860677e-6f, logf(m)));
+  return (x == mx ? 0.f : (x - mx) / temp) - ln;
+}
+
+// Sorts the n tokens of s->sorted (through s->list), descending; n <= kList.  Few are
+// placed by counting the greater ones (one pass, no barriers between), many by
+// a bitonic network.  Block-collective; the result is in s->list.
+__device__ __forceinline__ void sort_list(Shared* s, int n) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  if (n <= kThreads / 2) {
+    if (tid < n) {
+      const uint64_t key = s->sorted[tid];
+      int place = 0;
+      for (int i = 0; i < n; ++i) place += s->sorted[i] > key ? 1 : 0;
+      s->list[place] = key;                // the keys differ: ids do
+    }
+    __syncthreads();
+  } else {
+    int size = kThreads;
+    while (size < n) size <<= 1;
+    for (int i = tid; i < size; i += kThreads) s->list[i] = i < n ? s->sorted[i] : 0;
+    sort_desc(s->list, size);
+  }
+}
+
+// Top-k, top-p, min-p and the draw on the n gathered tokens in s->sorted.
+__device__ __noinline__ void draw_listed(const SampleParams& p, int row, Shared* s, int n, int k, float top_p,
+                                         float min_p, float uf, float temp, const Weight& w) {
+  constexpr int kRounds = kListK / kThreads;
+  const int tid = threadIdx.x;
+  sort_list(s, n);
+  auto value = [&](int i) { return from_ordered_bits(static_cast<uint32_t>(s->list[i] >> 32)); };
+  // weights in that order, and what top-k keeps
+  uint64_t wt[kRounds] = {}, before[kRounds] = {}, whole = 0;
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q)
+    if (q * kThreads < k) {
+      const int i = q * kThreads + tid;
+      uint64_t all;
+      wt[q] = i < k ? fix(w(value(i))) : 0;
+      before[q] = whole + block_scan(wt[q], s, &all) - wt[q];
+      whole += all;
+    }
+  // top-p and min-p: the kept tokens are a prefix, the best always among them
+  const uint64_t target = top_p < 1.f ? mass_target(top_p, whole) : ~0ull;
+  const float least = min_p > 0.f ? __double2float_ru(w.mx + s->below) : -CUDART_INF_F;
+  uint64_t kept = 0;
+  int kept_n = 0;
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q)
+    if (q * kThreads < k) {
+      const int i = q * kThreads + tid;
+      const bool keep = i < k && (i == 0 || before[q] < target) && value(i) >= least;
+      kept_n += __syncthreads_count(keep);
+      if (keep) s->sorted[i] = (s->list[i] << 32) | (s->list[i] >> 32);   // (~id, logit)
+    }
+  // by id; a draw is where the cumulated weight passes the goal
+  sort_list(s, kept_n);
+  uint64_t end[kRounds] = {}, one[kRounds] = {};
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q)
+    if (q * kThreads < kept_n) {
+      const int i = q * kThreads + tid;
+      uint64_t all;
+      one[q] = i < kept_n ? fix(w(from_ordered_bits(static_cast<uint32_t>(s->list[i])))) : 0;
+      end[q] = kept + block_scan(one[q], s, &all);
+      kept += all;
+    }
+  const uint64_t goal = draw_target(uf, kept);
+#pragma unroll
+  for (int q = 0; q < kRounds; ++q)
+    if (end[q] - one[q] <= goal && goal < end[q]) {
+      const uint64_t key = s->list[q * kThreads + tid];
+      p.tok[row] = static_cast<int>(~static_cast<uint32_t>(key >> 32));
+      p.logp[row] = log_share(from_ordered_bits(static_cast<uint32_t>(key)), w.mx, temp, kept);
+    }
 }
 
 template <typename T, bool RES>
@@ -347,20 +464,42 @@ sample_filtered_kernel(const SampleParams p) {
   const float min_p = p.min_p ? p.min_p[row] : 0.f;
   const float uf = p.u[row];
 
-  // the slice into shared memory, where each lane reads its own tokens only
-  float mine = -CUDART_INF_F;                              // this thread's best value
-  {
-    Part<T, false> g{part.data, part.id0, part.n, part.vec};
+  // the slice into shared memory (all of a lane's copies in flight at once), where
+  // each lane reads its own tokens only; and this thread's best value
+  float mine = -CUDART_INF_F;
+  if constexpr (RES) {
+    const Part<T, false> g{part.data, part.id0, part.n, part.vec};
     T* own = reinterpret_cast<T*>(smem) + (size_t)warp * p.part;
-#pragma unroll 4
     for (int i = lane * 8; i < part.n; i += 256) {
-      const Chunk<T> c = g.at(i);
-      if constexpr (RES) c.store(own + i);
-      mine = fmaxf(mine, c.max());
+      if (part.vec && i + 8 <= part.n) {
+        const uint32_t to = mmas::smem_u32(own + i);
+        mmas::cp_async16(to, part.data + i, true);
+        if constexpr (sizeof(T) == 4) mmas::cp_async16(to + 16, part.data + i + 4, true);
+      } else {
+        g.at(i).store(own + i);
+      }
     }
-    if constexpr (RES) part.data = own;
+    mmas::cp_async_commit();
+    mmas::cp_async_wait<0>();
+    part.data = own;
   }
-  if (tid == 0) sh.list_n = 0;
+  for (int i = lane * 8; i < part.n; i += 256) {
+    Chunk<T> c = part.at(i);
+    if constexpr (RES) {
+      c.clean();
+      c.store(const_cast<T*>(part.data) + i);
+    }
+    mine = fmaxf(mine, c.max());
+  }
+  if (tid == 0) {                          // (seen by all after the next block barrier)
+    sh.list_n = 0;
+    sh.sorted = reinterpret_cast<uint64_t*>(smem);
+    // log2(e) = 1.44269502 + 1.92596e-8: the quotient, rounded down, and its rest
+    const float hi = __fdiv_rd(1.4426950216293335f, temp);
+    sh.hi = fminf(fmaxf(hi, 1e-38f), 3e38f);               // (T = inf: all alike)
+    sh.lo = hi > 3e38f ? 1e-38f : fmaxf((fmaf(-hi, temp, 1.4426950216293335f) + 1.925963033500e-8f) / temp, 1e-38f);
+    if (temp > 0.f && min_p > 0.f) sh.below = static_cast<double>(temp) * log(static_cast<double>(fminf(min_p, 1.f)));
+  }
   Reducer red{&sh};
 
   // the row's best token, (value desc, id asc), and a value that k tokens reach
@@ -404,99 +543,42 @@ sample_filtered_kernel(const SampleParams p) {
     cluster_sync();                        // nobody leaves while its slots are read
     return;
   }
-  Weight w;
-  w.mx = mx;
-  const double c = 1.4426950408889634074 / static_cast<double>(temp);
-  w.hi = isinf(mx) ? 1.f : fminf(__double2float_rd(c), 3e38f);   // +inf takes everything, at any T
-  w.lo = isinf(mx) || c > 3e38 ? 1e-38f : fmaxf(static_cast<float>(c - static_cast<double>(w.hi)), 1e-38f);
+  const Weight w{mx, sh.hi, sh.lo};
 
-  if (listed) {
+  if (listed && !isinf(mx)) {
     const float from = C::value(0xFFFFFFFFu - static_cast<uint32_t>(reach_code));
     if (from > -CUDART_INF_F) {
       part.each(from, [&](int i, const float (&x)[8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (x[e] >= from) {
-            const uint32_t at = add_remote(&sh.list_n, 0, 1);
+            const uint32_t at = atomicAdd(&sh.list_n, 1u);
             if (at < kList)
-              st_remote(&sh.list[at], 0,
-                        ((uint64_t)ordered_bits(x[e]) << 32) | (uint32_t) ~(part.id0 + i + e));
+              sh.list[at] = ((uint64_t)ordered_bits(x[e]) << 32) | (uint32_t) ~(part.id0 + i + e);
           }
       });
       __syncwarp();
       cluster_sync();
-      const int n = static_cast<int>(ld_remote(&sh.list_n, 0));
+      uint32_t n = 0, n_mine = 0, n_before = 0;            // in all, of CTA `warp`, before it
+#pragma unroll
+      for (int r = 0; r < kCluster; ++r) {
+        const uint32_t c = ld_remote(&sh.list_n, r);
+        if (r < warp) n_before += c;
+        if (r == warp) n_mine = c;
+        n += c;
+      }
       if (n <= kList) {
+        static_assert(kWarps == kCluster, "a warp takes a CTA's list");
+        if (rank == 0)
+          for (uint32_t i = lane; i < n_mine; i += 32) sh.sorted[n_before + i] = ld_remote(&sh.list[i], warp);
         __syncwarp();
-        cluster_arrive();
-        if (rank != 0) return;             // (an exited CTA has arrived at every barrier)
-        int size = 32;
-        while (size < n) size <<= 1;
-        for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
-        sort_desc(sh.list, size);
-        // weights in that order; what top-k keeps, then top-p and min-p
-        const int rounds = (k + kThreads - 1) / kThreads;
-        auto value = [&](int i) { return from_ordered_bits(static_cast<uint32_t>(sh.list[i] >> 32)); };
-        uint64_t wt[kListK / kThreads] = {}, cum[kListK / kThreads] = {}, whole = 0;
-#pragma unroll
-        for (int q = 0; q < kListK / kThreads; ++q)
-          if (q < rounds) {
-            const int i = q * kThreads + tid;
-            uint64_t all;
-            wt[q] = i < k ? fix(w(value(i))) : 0;
-            cum[q] = whole + block_scan(wt[q], &sh, &all);
-            whole += all;
-          }
-        const uint64_t target = top_p < 1.f ? mass_target(top_p, whole) : ~0ull;
-        const float least = min_p > 0.f ? min_p_value(min_p, mx, temp) : -CUDART_INF_F;
-        // (the kept tokens are a prefix; the best is always among them)
-        uint64_t kept = 0;
-        uint32_t kept_n = 0;
-#pragma unroll
-        for (int q = 0; q < kListK / kThreads; ++q)
-          if (q < rounds) {
-            const int i = q * kThreads + tid;
-            const bool keep = i < k && (i == 0 || cum[q] - wt[q] < target) && value(i) >= least;
-            if (!keep) wt[q] = 0;
-            kept_n += __syncthreads_count(keep);
-            uint64_t all;
-            block_scan(wt[q], &sh, &all);
-            kept += all;
-          }
-        // by id: the weight travels as the place in the first order
-        __syncthreads();
-        uint64_t key[kListK / kThreads];
-        int n2 = 32;
-        while (n2 < static_cast<int>(kept_n)) n2 <<= 1;
-#pragma unroll
-        for (int q = 0; q < kListK / kThreads; ++q) {
-          const int i = q * kThreads + tid;
-          key[q] = i < static_cast<int>(kept_n) ? (sh.list[i] << 32) | (sh.list[i] >> 32) : 0;   // (~id, logit)
-        }
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < kListK / kThreads; ++q)
-          if (q * kThreads + tid < n2) sh.list[q * kThreads + tid] = key[q];
-        sort_desc(sh.list, n2);
-        const uint64_t goal = draw_target(uf, kept);
-        uint64_t run = 0;
-        for (int q = 0; q * kThreads < static_cast<int>(kept_n); ++q) {
-          const int i = q * kThreads + tid;
-          const float x = i < static_cast<int>(kept_n) ? from_ordered_bits(static_cast<uint32_t>(sh.list[i])) : 0.f;
-          const uint64_t one = i < static_cast<int>(kept_n) ? fix(w(x)) : 0;
-          uint64_t all;
-          const uint64_t end = run + block_scan(one, &sh, &all);
-          if (end - one <= goal && goal < end) {
-            p.tok[row] = static_cast<int>(~static_cast<uint32_t>(sh.list[i] >> 32));
-            p.logp[row] = log_share(x, mx, temp, kept);
-          }
-          run += all;
-        }
-        __syncwarp();
-        cluster_wait();                    // the others have read list_n
+        cluster_sync();                    // the lists are read: the other CTAs are done
+        if (rank != 0) return;
+        draw_listed(p, row, &sh, static_cast<int>(n), k, top_p, min_p, uf, temp, w);
         return;
       }
       // more tokens than the list holds (long ties): search
+      cluster_sync();                      // (the lists share their memory with the bins)
     }
   }
 
@@ -505,6 +587,9 @@ sample_filtered_kernel(const SampleParams p) {
   uint32_t m = 0;
   const uint32_t top_code = C::of(mx), floor_all = C::of(-CUDART_INF_F);
 
+  // the last search by mass leaves the mass of this thread's tokens above over_v
+  uint64_t over_sum = 0;
+  float over_v = CUDART_INF_F;
   struct Found {
     uint32_t code;
     uint64_t above, target;
@@ -522,7 +607,7 @@ sample_filtered_kernel(const SampleParams p) {
     const uint32_t lo0 = lo;
     const float lo0_v = C::value(lo);
     uint64_t target = k;
-    bool linear = !isinf(mx) && reach < 1e30f;
+    bool linear = reach < 1e30f;
     if (by_mass && !linear) {              // the whole in a pass of its own
       uint64_t whole = 0, none = 0;
       part.each(lo0_v, [&](int, const float (&x)[8]) {
@@ -545,32 +630,69 @@ sample_filtered_kernel(const SampleParams p) {
       __syncthreads();
       uint64_t sum = 0, none = 0;
       if (linear) {
-        // the mass above lo, and the bins, in one pass
-        part.each(by_mass ? lo0_v : fmaxf(lo_v, far_v), [&](int, const float (&x)[8]) {
-          float s8 = 0.f;
+        // the mass above lo, and the bins, in one pass; 2^23 + bin has the bin in its
+        // low bits (rounded down)
+        auto bin = [&](float d, bool in) {
+          const float at = __fmaf_rd(d, -scale, 8388608.f);
+          if (in && at < 8388608.f + (kBins - 1))
+            atomicAdd(&sh.hist[__float_as_uint(at) & (kBins - 1)], 1u);
+        };
+        if (by_mass && lo0 == floor_all) {
+          part.all([&](int, const float (&x)[8]) {
+            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (by_mass) s8 += x[e] > lo0_v ? w(x[e]) : 0.f;
-            const float at = (mx - x[e]) * scale;
-            if (at < kBins - 1.f && x[e] >= lo_v) atomicAdd(&sh.hist[static_cast<uint32_t>(at)], 1u);
-          }
-          if (by_mass) sum += fix(s8);
-        });
+            for (int e = 0; e < 8; e += 2) {
+              const float2 d = w.dist(x[e], x[e + 1]);
+              s2 = __fadd2_rn(s2, w.at(d));
+              bin(d.x, true);
+              bin(d.y, true);
+            }
+            sum += fix(s2.x + s2.y);
+          });
+        } else {
+          part.each(by_mass ? lo0_v : fmaxf(lo_v, far_v), [&](int, const float (&x)[8]) {
+            float s8 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (by_mass) s8 += x[e] > lo0_v ? w(x[e]) : 0.f;
+              bin(x[e] - mx, x[e] >= lo_v);
+            }
+            if (by_mass) sum += fix(s8);
+          });
+        }
       } else {
         part.each(lo_v, [&](int, const float (&x)[8]) {
-          float s8 = 0.f;
-          uint32_t n8 = 0;
+          uint32_t in = 0;                                 // the tokens of the bracket
+          if (by_mass) {
+            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (x[e] > hi_v) {
-              if (by_mass) s8 += w(x[e]);
-              else ++n8;
-            } else if (x[e] >= lo_v) {
-              atomicAdd(&sh.hist[(hi - C::of(x[e])) >> shift], 1u);
+            for (int e = 0; e < 8; e += 2) {
+              const float2 y = w.at(w.dist(x[e], x[e + 1]));
+              const bool a = x[e] > hi_v, b = x[e + 1] > hi_v;
+              s2 = __fadd2_rn(s2, make_float2(a ? y.x : 0.f, b ? y.y : 0.f));
+              if (!a && x[e] >= lo_v) in |= 1u << e;
+              if (!b && x[e + 1] >= lo_v) in |= 2u << e;
             }
+            sum += fix(s2.x + s2.y);
+          } else {
+            uint32_t n8 = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (x[e] > hi_v) ++n8;
+              else if (x[e] >= lo_v) in |= 1u << e;
+            }
+            sum += n8;
           }
-          sum += by_mass ? fix(s8) : n8;
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if ((in >> e) & 1u) atomicAdd(&sh.hist[(hi - C::of(x[e])) >> shift], 1u);
+          }
         });
+        if (by_mass) {
+          over_sum = sum;                                  // of this thread's tokens above hi_v
+          over_v = hi_v;
+        }
       }
       __syncthreads();
       red.both<false>(sum, none);                          // (all histograms are complete)
@@ -645,9 +767,9 @@ sample_filtered_kernel(const SampleParams p) {
       uint32_t nlo, nhi;
       if (linear) {
         // a little wider than the bins: the next level is exact about what lies above
-        const double bin = 1.0 / scale;
-        const float hv = __double2float_ru(mx - (b1 - 0.125) * bin);
-        const float lv = __double2float_rd(mx - (b2 + 1.125) * bin);
+        const float bin = 1.f / scale;
+        const float hv = __fsub_ru(mx, __fmul_rd(b1 - 0.25f, bin));
+        const float lv = __fsub_rd(mx, __fmul_ru(b2 + 1.25f, bin));
         nhi = max(min(hi, C::of(hv)), lo);
         nlo = b2 == kBins - 1 ? lo : min(max(lo, C::of(lv)), nhi);
         linear = false;
@@ -680,53 +802,88 @@ sample_filtered_kernel(const SampleParams p) {
     }
   };
 
-  if (k > 1 && k < p.vocab) {
-    const Found f = search(false, floor_all, 0, 32.f);
-    t = C::value(f.code);
-    if (t > -CUDART_INF_F) m = static_cast<uint32_t>(k - f.above);
-  }
-  if (top_p < 1.f) {
-    Found f{top_code, 0, 0};
-    const uint32_t floor_code = C::of(t);
-    const uint64_t extra = m ? m * fix(w(t)) : 0;
-    if (t < mx) {
-      // tokens further than `reach` below the best weigh less than 1 - p together
-      const float reach = fminf(mx - t, temp * logf(p.vocab / (1.f - fmaxf(top_p, 0.f))));
-      f = search(true, floor_code, extra, fmaxf(reach, 1e-30f));
-    } else {
-      f.target = mass_target(top_p, extra);                // top-k left ties at the best alone
-    }
-    if (f.code > floor_code || m) {
-      // how many of the ties at the border it takes
-      const uint64_t one = fix(w(C::value(f.code)));
-      uint64_t need = f.target > f.above && one ? (f.target - f.above + one - 1) / one : 1;
-      if (f.code == floor_code && need > m) need = m;
-      m = static_cast<uint32_t>(min(need, static_cast<uint64_t>(0xFFFFFFFFu)));
+  if (isinf(mx)) {
+    // the tokens at +inf share the mass: ties at the border, of which top-k takes
+    // the first k and top-p their share
+    uint64_t n = 0, none = 0;
+    part.each(mx, [&](int, const float (&x)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n += x[e] == mx ? 1 : 0;
+    });
+    __syncwarp();
+    red.both<false>(n, none);
+    if (k > 1) n = min(n, static_cast<uint64_t>(k));
+    if (top_p < 1.f) n = min(n, max(mass_target(top_p, n), static_cast<uint64_t>(1)));
+    t = mx;
+    m = static_cast<uint32_t>(n);
+  } else {
+    if (k > 1 && k < p.vocab) {
+      const Found f = search(false, floor_all, 0, 32.f);
       t = C::value(f.code);
+      if (t > -CUDART_INF_F) m = static_cast<uint32_t>(k - f.above);
+    }
+    if (top_p < 1.f) {
+      Found f{top_code, 0, 0};
+      const uint32_t floor_code = C::of(t);
+      const uint64_t extra = m ? m * fix(w(t)) : 0;
+      if (t < mx) {
+        // tokens further than `reach` below the best weigh less than 1 - p together
+        const float reach = fminf(mx - t, temp * logf(p.vocab / (1.f - fmaxf(top_p, 0.f))));
+        f = search(true, floor_code, extra, fmaxf(reach, 1e-30f));
+      } else {
+        f.target = mass_target(top_p, extra);              // top-k left ties at the best alone
+      }
+      if (f.code > floor_code || m) {
+        // how many of the ties at the border it takes
+        const uint64_t one = fix(w(C::value(f.code)));
+        uint64_t need = f.target > f.above && one ? (f.target - f.above + one - 1) / one : 1;
+        if (f.code == floor_code && need > m) need = m;
+        m = static_cast<uint32_t>(min(need, static_cast<uint64_t>(0xFFFFFFFFu)));
+        t = C::value(f.code);
+      }
+    }
+    if (min_p > 0.f) {
+      const float least = __double2float_ru(mx + sh.below);
+      if (least > t) {
+        t = nextafterf(least, -CUDART_INF_F);
+        m = 0;
+      }
     }
   }
-  if (min_p > 0.f) {
-    const float least = min_p_value(min_p, mx, temp);
-    if (least > t) {
-      t = nextafterf(least, -CUDART_INF_F);
-      m = 0;
-    }
-  }
+  // (the sum above over_v stands only if the border lies below it)
+  if (t > over_v) over_v = CUDART_INF_F;
+  if (over_v == CUDART_INF_F) over_sum = 0;
 
   // kept mass and ties of every part, in token order
-  const uint64_t one = m ? fix(w(t)) : 0;
-  uint64_t gt = 0;
+  const uint64_t one = m ? (isinf(mx) ? fix(1.f) : fix(w(t))) : 0;
+  uint64_t gt = over_sum;
   uint32_t ties = 0;
-  auto weigh = [&](const float (&x)[8], uint32_t& tie) {
-    float s = 0.f;
+  if (t == -CUDART_INF_F) {
+    part.all([&](int, const float (&x)[8]) {               // nothing was filtered
+      float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s += x[e] > t ? w(x[e]) : 0.f;
-      tie += x[e] == t ? 1 : 0;
-    }
-    return fix(s);
-  };
-  part.each(t, [&](int, const float (&x)[8]) { gt += weigh(x, ties); });
+      for (int e = 0; e < 8; e += 2) s2 = __fadd2_rn(s2, w.at(w.dist(x[e], x[e + 1])));
+      gt += fix(s2.x + s2.y);
+    });
+  } else {
+    part.each(t, [&](int, const float (&x)[8]) {
+      uint32_t in = 0;                                     // above the border, not yet summed
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (x[e] > t && x[e] <= over_v) in |= 1u << e;
+        if (x[e] == t) ++ties;
+      }
+      if (in) {
+        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 y = w.at(w.dist(x[e], x[e + 1]));
+          s2 = __fadd2_rn(s2, make_float2((in >> e) & 1u ? y.x : 0.f, (in >> e) & 2u ? y.y : 0.f));
+        }
+        gt += fix(s2.x + s2.y);
+      }
+    });
+  }
   __syncwarp();
   gt = warp_sum(gt);
   ties = __reduce_add_sync(0xffffffffu, ties);
@@ -777,9 +934,15 @@ sample_filtered_kernel(const SampleParams p) {
       uint64_t g = 0;
       if (i < part.n) {
         part.at(i).get(x);
+        float s[2] = {0.f, 0.f}, over[2] = {0.f, 0.f};     // (in pairs, as they were summed)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fmaxf(x[e], -CUDART_INF_F);
-        g = weigh(x, tie);
+        for (int e = 0; e < 8; ++e) {
+          const float y = x[e] > t ? w(x[e]) : 0.f;
+          if (x[e] > over_v) over[e & 1] += y;
+          else s[e & 1] += y;
+          tie += x[e] == t ? 1 : 0;
+        }
+        g = fix(s[0] + s[1]) + fix(over[0] + over[1]);
       }
       const uint64_t ig = warp_scan(g), it = warp_scan(tie);
       const bool past = cg + ig + kept_ties(ct + it) * one > goal;
@@ -787,15 +950,17 @@ sample_filtered_kernel(const SampleParams p) {
       if (any) {
         if (lane == __ffs(any) - 1) {
           const uint64_t g0 = cg + ig - g, t0 = ct + it - tie;
-          float s = 0.f, got = 0.f;
+          float s[2] = {0.f, 0.f}, over[2] = {0.f, 0.f}, got = 0.f;
           uint32_t seen = 0;
           int id = -1;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const bool above = x[e] > t, at = x[e] == t;
-            if (above) s += w(x[e]);
+            if (above && x[e] > over_v) over[e & 1] += w(x[e]);
+            else if (above) s[e & 1] += w(x[e]);
             if (at) ++seen;
-            if (id < 0 && (above || at) && g0 + fix(s) + kept_ties(t0 + seen) * one > goal) {
+            if (id < 0 && (above || at) &&
+                g0 + fix(s[0] + s[1]) + fix(over[0] + over[1]) + kept_ties(t0 + seen) * one > goal) {
               id = part.id0 + i + e;
               got = x[e];
             }
@@ -815,7 +980,7 @@ sample_filtered_kernel(const SampleParams p) {
 
 template <typename T>
 void launch_sample(const SampleParams& p, int rows, cudaStream_t st) {
-  const size_t slice = (size_t)kWarps * p.part * sizeof(T);
+  const size_t slice = (size_t)kWarps * p.part * sizeof(T), least = kList * sizeof(uint64_t);
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -825,9 +990,9 @@ void launch_sample(const SampleParams& p, int rows, cudaStream_t st) {
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   if (slice <= kMaxSlice)
-    launch_k(sample_filtered_kernel<T, true>, dim3(rows * kCluster), dim3(kThreads), slice, st, p);
+    launch_k(sample_filtered_kernel<T, true>, dim3(rows * kCluster), dim3(kThreads), slice < least ? least : slice, st, p);
   else
-    launch_k(sample_filtered_kernel<T, false>, dim3(rows * kCluster), dim3(kThreads), 0, st, p);
+    launch_k(sample_filtered_kernel<T, false>, dim3(rows * kCluster), dim3(kThreads), least, st, p);
 }
 
 }  // namespace
