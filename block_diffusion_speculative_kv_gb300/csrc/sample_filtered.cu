@@ -37,6 +37,7 @@ constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
 constexpr int kParts = kCluster * kWarps;          // contiguous parts of a row, one to a warp
 constexpr int kMaxSlice = 200 * 1024;              // resident slice bytes
 constexpr int kListK = 512, kList = 1024;          // largest k, and tokens, of the gathered list
+constexpr int kListPer = kList / kThreads;
 constexpr int kBins = 1024;                        // of a search level
 constexpr int kPer = kBins / kThreads;
 // A bin's weight bounds are widened by this much: exponents of up to 44 times a
@@ -91,18 +92,19 @@ __device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) 
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote_addr(p, rank)) : "memory");
   return v;
 }
+// Sum and maximum over a warp: hardware reductions of 32-bit parts (22-bit ones for
+// the sum, so that 32 of them do not overflow; v < 2^64 / 32).
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  const uint32_t a = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0x3FFFFFu);
+  const uint32_t b = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 22) & 0x3FFFFFu);
+  const uint32_t c = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 44));
+  return a + ((uint64_t)b << 22) + ((uint64_t)c << 44);
 }
 __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const uint64_t t = __shfl_xor_sync(0xffffffffu, v, o);
-    v = t > v ? t : v;
-  }
-  return v;
+  const uint32_t h = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
+  const uint32_t l =
+      __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == h ? static_cast<uint32_t>(v) : 0u);
+  return ((uint64_t)h << 32) | l;
 }
 __device__ __forceinline__ uint64_t warp_scan(uint64_t v) {   // inclusive
   const int lane = threadIdx.x & 31;
@@ -124,7 +126,7 @@ struct Shared {
     };
     uint64_t list[kList];                // gathered tokens: (ordered logit, ~id)
   };
-  uint64_t* sorted;                      // kList more, where the slice was
+  uint2 part[2][kWarps];
   uint32_t list_n;
   uint32_t found[2];
   uint64_t found_cum;
@@ -297,22 +299,6 @@ struct Part {
   }
 };
 
-// Bitonic sort of a[0 .. n), descending; n a power of two.  Block-collective.
-__device__ __forceinline__ void sort_desc(uint64_t* a, int n) {
-  for (int size = 2; size <= n; size <<= 1)
-    for (int d = size >> 1; d; d >>= 1) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int x = 2 * i - (i & (d - 1)), y = x + d;
-        const uint64_t p = a[x], q = a[y];
-        if ((p < q) == ((x & size) == 0)) {
-          a[x] = q;
-          a[y] = p;
-        }
-      }
-    }
-  __syncthreads();
-}
 // Inclusive prefix sum of one value per thread and round, in thread order.
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, Shared* s, uint64_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -365,78 +351,169 @@ __device__ __forceinline__ float log_share(float x, float mx, float temp, uint64
   return (x == mx ? 0.f : (x - mx) / temp) - ln;
 }
 
-// Sorts the n tokens of s->sorted (through s->list), descending; n <= kList.  Few are
-// placed by counting the greater ones (one pass, no barriers between), many by
-// a bitonic network.  Block-collective; the result is in s->list.
-__device__ __forceinline__ void sort_list(Shared* s, int n) {
-  const int tid = threadIdx.x;
+// Sum over the block of a mass of at most 2^40 per token, kListPer tokens a thread:
+// two 20-bit halves, so that 32-bit sums hold 1024 tokens.  Calls alternate `turn`.
+__device__ __forceinline__ uint64_t list_sum(uint32_t hi, uint32_t lo, Shared* s, int* turn) {
+  const int warp = threadIdx.x >> 5;
+  hi = __reduce_add_sync(0xffffffffu, hi);
+  lo = __reduce_add_sync(0xffffffffu, lo);
+  uint2* at = s->part[*turn];
+  if ((threadIdx.x & 31) == 0) at[warp] = make_uint2(hi, lo);
   __syncthreads();
-  if (n <= kThreads / 2) {
-    if (tid < n) {
-      const uint64_t key = s->sorted[tid];
-      int place = 0;
-      for (int i = 0; i < n; ++i) place += s->sorted[i] > key ? 1 : 0;
-      s->list[place] = key;                // the keys differ: ids do
-    }
-    __syncthreads();
-  } else {
-    int size = kThreads;
-    while (size < n) size <<= 1;
-    for (int i = tid; i < size; i += kThreads) s->list[i] = i < n ? s->sorted[i] : 0;
-    sort_desc(s->list, size);
+  uint32_t h = 0, l = 0;
+#pragma unroll
+  for (int x = 0; x < kWarps; ++x) {
+    h += at[x].x;
+    l += at[x].y;
+  }
+  *turn ^= 1;
+  return ((uint64_t)h << 20) + l;
+}
+
+// Top-k, top-p, min-p and the draw on the n <= kThreads / 2 gathered tokens in
+// s->list, of which k or more: a thread places its token among the others by
+// counting the greater ones, and sums run in that order.  Block-collective.
+__device__ __noinline__ void draw_sorted(const SampleParams& p, int row, Shared* s, int n, int k, float top_p,
+                                         float min_p, float uf, float temp, const Weight& w) {
+  const int tid = threadIdx.x;
+  const uint64_t key = tid < n ? s->list[tid] : 0;
+  const float x = from_ordered_bits(static_cast<uint32_t>(key >> 32));
+  const uint32_t id = ~static_cast<uint32_t>(key);
+  uint64_t* wt = s->list + kList / 2;
+  const uint64_t mine = tid < n ? fix(w(x)) : 0;
+  if (tid < n) wt[tid] = mine;
+  __syncthreads();
+  // the tokens before this one, and their mass; top-k keeps the first k
+  int place = 0;
+  uint64_t before = 0;
+  if (tid < n)
+    for (int i = 0; i < n; ++i)
+      if (s->list[i] > key) {
+        ++place;
+        before += wt[i];
+      }
+  bool keep = tid < n && place < k;
+  if (keep && place == k - 1) s->found_cum = before + mine;
+  __syncthreads();
+  const uint64_t target = top_p < 1.f ? mass_target(top_p, s->found_cum) : ~0ull;
+  const float least = min_p > 0.f ? __double2float_ru(w.mx + s->below) : -CUDART_INF_F;
+  keep = keep && (place == 0 || before < target) && x >= least;
+  // cumulated by id, over what is kept
+  wt[tid] = keep ? mine : 0;
+  __syncthreads();
+  uint64_t upto = 0, kept = 0;
+  for (int i = 0; i < n; ++i) {
+    const uint64_t m = wt[i];
+    kept += m;
+    if (static_cast<uint32_t>(s->list[i]) >= static_cast<uint32_t>(key)) upto += m;   // ~id: ids up to this one
+  }
+  const uint64_t goal = draw_target(uf, kept);
+  if (keep && upto - mine <= goal && goal < upto) {
+    p.tok[row] = static_cast<int>(id);
+    p.logp[row] = log_share(x, w.mx, temp, kept);
   }
 }
 
-// Top-k, top-p, min-p and the draw on the n gathered tokens in s->sorted.
-__device__ __noinline__ void draw_listed(const SampleParams& p, int row, Shared* s, int n, int k, float top_p,
-                                         float min_p, float uf, float temp, const Weight& w) {
-  constexpr int kRounds = kListK / kThreads;
+// The same for a longer list in s->list; block-collective.  The same border (t, m) as for a whole row, found by
+// halving the range of codes; a thread holds kListPer tokens.
+template <int SHIFT>
+__device__ __noinline__ void draw_halving(const SampleParams& p, int row, Shared* s, int n, int k, float top_p,
+                                         float min_p, float uf, float temp, float from, const Weight& w) {
   const int tid = threadIdx.x;
-  sort_list(s, n);
-  auto value = [&](int i) { return from_ordered_bits(static_cast<uint32_t>(s->list[i] >> 32)); };
-  // weights in that order, and what top-k keeps
-  uint64_t wt[kRounds] = {}, before[kRounds] = {}, whole = 0;
+  uint32_t code[kListPer], id[kListPer];                   // (code 0: no token)
+  uint64_t wt[kListPer];
+  int turn = 0;
 #pragma unroll
-  for (int q = 0; q < kRounds; ++q)
-    if (q * kThreads < k) {
-      const int i = q * kThreads + tid;
-      uint64_t all;
-      wt[q] = i < k ? fix(w(value(i))) : 0;
-      before[q] = whole + block_scan(wt[q], s, &all) - wt[q];
-      whole += all;
-    }
-  // top-p and min-p: the kept tokens are a prefix, the best always among them
-  const uint64_t target = top_p < 1.f ? mass_target(top_p, whole) : ~0ull;
-  const float least = min_p > 0.f ? __double2float_ru(w.mx + s->below) : -CUDART_INF_F;
-  uint64_t kept = 0;
-  int kept_n = 0;
+  for (int q = 0; q < kListPer; ++q) {
+    const int i = q * kThreads + tid;
+    const uint64_t key = i < n ? s->list[i] : 0;
+    code[q] = static_cast<uint32_t>(key >> 32) >> SHIFT;
+    id[q] = ~static_cast<uint32_t>(key);
+    wt[q] = i < n ? fix(w(from_ordered_bits(static_cast<uint32_t>(key >> 32)))) : 0;
+  }
+  // what satisfies f: how many, or their mass
+  auto count = [&](auto f) {
+    uint32_t c = 0;
 #pragma unroll
-  for (int q = 0; q < kRounds; ++q)
-    if (q * kThreads < k) {
-      const int i = q * kThreads + tid;
-      const bool keep = i < k && (i == 0 || before[q] < target) && value(i) >= least;
-      kept_n += __syncthreads_count(keep);
-      if (keep) s->sorted[i] = (s->list[i] << 32) | (s->list[i] >> 32);   // (~id, logit)
-    }
-  // by id; a draw is where the cumulated weight passes the goal
-  sort_list(s, kept_n);
-  uint64_t end[kRounds] = {}, one[kRounds] = {};
+    for (int q = 0; q < kListPer; ++q) c += code[q] && f(q) ? 1 : 0;
+    return static_cast<uint32_t>(list_sum(0, c, s, &turn));
+  };
+  auto mass = [&](auto f) {
+    uint32_t h = 0, l = 0;
 #pragma unroll
-  for (int q = 0; q < kRounds; ++q)
-    if (q * kThreads < kept_n) {
-      const int i = q * kThreads + tid;
-      uint64_t all;
-      one[q] = i < kept_n ? fix(w(from_ordered_bits(static_cast<uint32_t>(s->list[i])))) : 0;
-      end[q] = kept + block_scan(one[q], s, &all);
-      kept += all;
+    for (int q = 0; q < kListPer; ++q)
+      if (f(q)) {
+        h += static_cast<uint32_t>(wt[q] >> 20);
+        l += static_cast<uint32_t>(wt[q]) & 0xFFFFFu;
+      }
+    return list_sum(h, l, s, &turn);
+  };
+  const uint32_t top = ordered_bits(w.mx) >> SHIFT, floor = ordered_bits(from) >> SHIFT;
+  uint32_t t = floor, hi = top;
+  while (t < hi) {
+    const uint32_t mid = t + (hi - t + 1) / 2;
+    if (count([&](int q) { return code[q] >= mid; }) >= static_cast<uint32_t>(k)) t = mid;
+    else hi = mid - 1;
+  }
+  uint32_t m = k - count([&](int q) { return code[q] > t; });
+  if (top_p < 1.f) {
+    const uint64_t above = mass([&](int q) { return code[q] > t; });
+    const uint64_t one = fix(w(from_ordered_bits(t << SHIFT | (SHIFT && !(t >> 15) ? 0xFFFFu : 0u))));
+    const uint64_t target = mass_target(top_p, above + m * one);
+    if (target > above) {
+      if (one) m = static_cast<uint32_t>(min(static_cast<uint64_t>(m), (target - above + one - 1) / one));
+    } else {
+      hi = top;
+      while (t < hi) {
+        const uint32_t mid = t + (hi - t + 1) / 2;
+        if (mass([&](int q) { return code[q] >= mid; }) >= target) t = mid;
+        else hi = mid - 1;
+      }
+      const uint64_t over = mass([&](int q) { return code[q] > t; });
+      const uint64_t each = fix(w(from_ordered_bits(t << SHIFT | (SHIFT && !(t >> 15) ? 0xFFFFu : 0u))));
+      m = each ? static_cast<uint32_t>((target - over + each - 1) / each) : 1;
     }
+  }
+  if (min_p > 0.f) {
+    // (the least value that it keeps; between two codes it is the upper one's)
+    const float least = __double2float_ru(w.mx + s->below);
+    uint32_t c = ordered_bits(least) >> SHIFT;
+    if (from_ordered_bits(c << SHIFT | (SHIFT && !(c >> 15) ? 0xFFFFu : 0u)) < least) ++c;
+    if (c > t) {
+      t = c - 1;
+      m = 0;
+    }
+  }
+  // the first m ties, by id
+  uint32_t last = 0xFFFFFFFFu;
+  if (m < count([&](int q) { return code[q] == t; })) {
+    uint32_t lo = 0, up = p.vocab - 1;                     // the least id that m ties reach
+    while (m && lo < up) {
+      const uint32_t mid = lo + (up - lo) / 2;
+      if (count([&](int q) { return code[q] == t && id[q] <= mid; }) >= m) up = mid;
+      else lo = mid + 1;
+    }
+    last = lo;
+  }
+  bool keep[kListPer];
+#pragma unroll
+  for (int q = 0; q < kListPer; ++q)
+    keep[q] = code[q] && (code[q] > t || (m && code[q] == t && id[q] <= last));
+  // the draw: the least id whose cumulated mass passes the goal
+  const uint64_t kept = mass([&](int q) { return keep[q]; });
   const uint64_t goal = draw_target(uf, kept);
+  uint32_t lo = 0, up = p.vocab - 1;
+  while (lo < up) {
+    const uint32_t mid = lo + (up - lo) / 2;
+    if (mass([&](int q) { return keep[q] && id[q] <= mid; }) > goal) up = mid;
+    else lo = mid + 1;
+  }
 #pragma unroll
-  for (int q = 0; q < kRounds; ++q)
-    if (end[q] - one[q] <= goal && goal < end[q]) {
-      const uint64_t key = s->list[q * kThreads + tid];
-      p.tok[row] = static_cast<int>(~static_cast<uint32_t>(key >> 32));
-      p.logp[row] = log_share(from_ordered_bits(static_cast<uint32_t>(key)), w.mx, temp, kept);
+  for (int q = 0; q < kListPer; ++q)
+    if (keep[q] && id[q] == lo) {
+      p.tok[row] = static_cast<int>(lo);
+      const float x = from_ordered_bits(code[q] << SHIFT | (SHIFT && !(code[q] >> 15) ? 0xFFFFu : 0u));
+      p.logp[row] = log_share(x, w.mx, temp, kept);
     }
 }
 
@@ -493,7 +570,6 @@ sample_filtered_kernel(const SampleParams p) {
   }
   if (tid == 0) {                          // (seen by all after the next block barrier)
     sh.list_n = 0;
-    sh.sorted = reinterpret_cast<uint64_t*>(smem);
     // log2(e) = 1.44269502 + 1.92596e-8: the quotient, rounded down, and its rest
     const float hi = __fdiv_rd(1.4426950216293335f, temp);
     sh.hi = fminf(fmaxf(hi, 1e-38f), 3e38f);               // (T = inf: all alike)
@@ -502,6 +578,7 @@ sample_filtered_kernel(const SampleParams p) {
   }
   Reducer red{&sh};
 
+  const bool greedy = !(temp > 0.f) || k == 1;
   // the row's best token, (value desc, id asc), and a value that k tokens reach
   uint64_t best = 0;
   {
@@ -510,15 +587,15 @@ sample_filtered_kernel(const SampleParams p) {
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (mine == top && top > -CUDART_INF_F) {
       int id = 0x7FFFFFFF;
-      part.each(top, [&](int i, const float (&x)[8]) {
+      if (greedy)                                          // (nobody else asks which token it is)
+        part.each(top, [&](int i, const float (&x)[8]) {
 #pragma unroll
-        for (int e = 7; e >= 0; --e)
-          if (x[e] == top && part.id0 + i + e < id) id = part.id0 + i + e;
-      });
+          for (int e = 7; e >= 0; --e)
+            if (x[e] == top && part.id0 + i + e < id) id = part.id0 + i + e;
+        });
       best = ((uint64_t)ordered_bits(top) << 32) | (uint32_t)~id;
     }
   }
-  const bool greedy = !(temp > 0.f) || k == 1;
   const bool listed = !greedy && k > 1 && k <= kListK && k < p.vocab;
   uint64_t reach_code = 0;
   if (listed) {
@@ -569,12 +646,15 @@ sample_filtered_kernel(const SampleParams p) {
       }
       if (n <= kList) {
         static_assert(kWarps == kCluster, "a warp takes a CTA's list");
-        if (rank == 0)
-          for (uint32_t i = lane; i < n_mine; i += 32) sh.sorted[n_before + i] = ld_remote(&sh.list[i], warp);
+        // (CTA 0's own tokens lie in front; the others' follow)
+        if (rank == 0 && warp > 0)
+          for (uint32_t i = lane; i < n_mine; i += 32) sh.list[n_before + i] = ld_remote(&sh.list[i], warp);
         __syncwarp();
         cluster_sync();                    // the lists are read: the other CTAs are done
         if (rank != 0) return;
-        draw_listed(p, row, &sh, static_cast<int>(n), k, top_p, min_p, uf, temp, w);
+        __syncthreads();
+        if (n <= kThreads / 2) draw_sorted(p, row, &sh, static_cast<int>(n), k, top_p, min_p, uf, temp, w);
+        else draw_halving<C::kShift>(p, row, &sh, static_cast<int>(n), k, top_p, min_p, uf, temp, from, w);
         return;
       }
       // more tokens than the list holds (long ties): search
@@ -632,10 +712,11 @@ sample_filtered_kernel(const SampleParams p) {
       if (linear) {
         // the mass above lo, and the bins, in one pass; 2^23 + bin has the bin in its
         // low bits (rounded down)
+        const uint32_t hist0 = mmas::smem_u32(sh.hist) - 0x4B000000u * 4u;   // 2^23 is 0x4B000000
         auto bin = [&](float d, bool in) {
           const float at = __fmaf_rd(d, -scale, 8388608.f);
           if (in && at < 8388608.f + (kBins - 1))
-            atomicAdd(&sh.hist[__float_as_uint(at) & (kBins - 1)], 1u);
+            asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(hist0 + __float_as_uint(at) * 4) : "memory");
         };
         if (by_mass && lo0 == floor_all) {
           part.all([&](int, const float (&x)[8]) {
@@ -661,33 +742,30 @@ sample_filtered_kernel(const SampleParams p) {
           });
         }
       } else {
+        const uint32_t hist0 = mmas::smem_u32(sh.hist);
+        // (no branch per token: nearly every warp has one in the bracket)
+        auto bin = [&](float x) {
+          if (x >= lo_v && x <= hi_v)
+            asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(hist0 + (((hi - C::of(x)) >> shift) << 2))
+                         : "memory");
+        };
         part.each(lo_v, [&](int, const float (&x)[8]) {
-          uint32_t in = 0;                                 // the tokens of the bracket
           if (by_mass) {
             float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
               const float2 y = w.at(w.dist(x[e], x[e + 1]));
-              const bool a = x[e] > hi_v, b = x[e + 1] > hi_v;
-              s2 = __fadd2_rn(s2, make_float2(a ? y.x : 0.f, b ? y.y : 0.f));
-              if (!a && x[e] >= lo_v) in |= 1u << e;
-              if (!b && x[e + 1] >= lo_v) in |= 2u << e;
+              s2 = __fadd2_rn(s2, make_float2(x[e] > hi_v ? y.x : 0.f, x[e + 1] > hi_v ? y.y : 0.f));
             }
             sum += fix(s2.x + s2.y);
           } else {
             uint32_t n8 = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (x[e] > hi_v) ++n8;
-              else if (x[e] >= lo_v) in |= 1u << e;
-            }
+            for (int e = 0; e < 8; ++e) n8 += x[e] > hi_v ? 1 : 0;
             sum += n8;
           }
-          if (in) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if ((in >> e) & 1u) atomicAdd(&sh.hist[(hi - C::of(x[e])) >> shift], 1u);
-          }
+          for (int e = 0; e < 8; ++e) bin(x[e]);
         });
         if (by_mass) {
           over_sum = sum;                                  // of this thread's tokens above hi_v
@@ -980,7 +1058,7 @@ sample_filtered_kernel(const SampleParams p) {
 
 template <typename T>
 void launch_sample(const SampleParams& p, int rows, cudaStream_t st) {
-  const size_t slice = (size_t)kWarps * p.part * sizeof(T), least = kList * sizeof(uint64_t);
+  const size_t slice = (size_t)kWarps * p.part * sizeof(T);
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -990,9 +1068,9 @@ void launch_sample(const SampleParams& p, int rows, cudaStream_t st) {
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   if (slice <= kMaxSlice)
-    launch_k(sample_filtered_kernel<T, true>, dim3(rows * kCluster), dim3(kThreads), slice < least ? least : slice, st, p);
+    launch_k(sample_filtered_kernel<T, true>, dim3(rows * kCluster), dim3(kThreads), slice, st, p);
   else
-    launch_k(sample_filtered_kernel<T, false>, dim3(rows * kCluster), dim3(kThreads), least, st, p);
+    launch_k(sample_filtered_kernel<T, false>, dim3(rows * kCluster), dim3(kThreads), 0, st, p);
 }
 
 }  // namespace
