@@ -52,14 +52,16 @@ constexpr float kLazy = 8.f;   // a row's reference maximum may lag by this much
 // Four warps; a step is 64 keys, 16 to each warp, which loads them for itself
 // (cp.async, kStages deep) and keeps its own running softmax, so the main loop
 // has no block barrier.  The four states meet when the tile ends.
-constexpr int kRowsS = 16, kStepS = 64, kStagesS = 4, kThreadsS = 128;
+// Two CTAs share an SM: one streams while the other begins or ends a tile.
+constexpr int kRowsS = 16, kStepS = 64, kStagesS = 3, kThreadsS = 128, kPerSmS = 2;
+using GeoS = PagedGeo<kRowsS, kStepS, 4>;
 
 template <int HD>
 struct SmallSmem {
   static constexpr int kTile = 16 * HD * 2;                       // 16 keys of K or V
   static constexpr int kRing = 4 * kStagesS * 2 * kTile;
-  static constexpr int kO = 4 * 16 * HD * 4;
-  static constexpr int kBytes = kRing + kO + 4 * 16 * 8 + 16;
+  static constexpr int kBytes = kRing + 4 * 16 * 8 + 16;
+  static_assert(4 * 16 * HD * 4 <= kRing, "the warps' states meet in the idle ring");
 };
 
 // Any element of a 16-byte chunk of bf16 that is infinite or NaN.
@@ -77,35 +79,35 @@ __device__ __forceinline__ uint32_t zero_not_finite(uint32_t w) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kThreadsS, 1) paged_attn_small_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(const PagedAttnParams p) {
   using S = SmallSmem<HD>;
   constexpr int kCh = HD / 8;                 // 16-byte chunks per key
   constexpr int kNt = HD / 8;                 // output column tiles of 8
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ring = smem + warp * (kStagesS * 2 * S::kTile);
-  float* sO = reinterpret_cast<float*>(smem + S::kRing);               // [4][16][HD]
-  float2* sMl = reinterpret_cast<float2*>(smem + S::kRing + S::kO);    // [4][16]
+  float* sO = reinterpret_cast<float*>(smem);                          // [4][16][HD], in the ring
+  float2* sMl = reinterpret_cast<float2*>(smem + S::kRing);            // [4][16]
   int* sLast = reinterpret_cast<int*>(sMl + 64);
 
   pdl_wait();
   pdl_trigger();
-  const int grid = gridDim.x;
-  long long total, end;                                  // all steps, and the end of this CTA's share
+  long long total, end;                                  // the line, and the end of this CTA's share
   PagedCursor c;
-  paged_plan(p, kRowsS, kStepS, lane, &total, &end, &c);
-  if (c.left <= 0) return;
+  paged_plan<GeoS>(p, lane, &total, &end, &c);
 
   const __nv_bfloat16* pool_k = static_cast<const __nv_bfloat16*>(p.pv.k);
   const __nv_bfloat16* pool_v = static_cast<const __nv_bfloat16*>(p.pv.v);
   const int ra = lane >> 2, cq = (lane & 3) * 2;    // fragment row (and + 8) and column pair
 
-  while (c.left > 0) {
+  for (PagedPiece pc; c.left > 0; paged_next<GeoS>(p, pc, &c)) {
+    pc = PagedPiece::of<GeoS>(c);
+    if (pc.n <= 0) continue;
     const PagedReq rq = c.rq;
     const int nG = rq.n * p.G, rho0 = c.j * kRowsS;
-    const int kend = rq.key_end(c.j, p.G, kRowsS);
-    const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
-    const int k0 = c.step * kStepS + warp * 16;     // this warp's first key of the piece
+    const int kend = rq.key_end<GeoS>(c.j, p.G);
+    const int n = pc.n;
+    const int k0 = pc.first * kStepS + warp * 16;   // this warp's first key of the piece
     const int head0 = c.g * p.G;
 
     auto load = [&](int i) {
@@ -276,6 +278,8 @@ __global__ void __launch_bounds__(kThreadsS, 1) paged_attn_small_kernel(const Pa
     }
 
     // the four warps' states
+    mmas::cp_async_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -316,12 +320,11 @@ __global__ void __launch_bounds__(kThreadsS, 1) paged_attn_small_kernel(const Pa
         *reinterpret_cast<uint4*>(dst + x) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
       }
     };
-    const long long at = end - c.left, unit0 = at - c.step;
-    if (n == c.n_steps) {
+    if (n == pc.all) {
       write();
     } else {
-      const int c0 = paged_owner(total, unit0, grid);
-      const int c1 = paged_owner(total, unit0 + c.n_steps - 1, grid);
+      int c0, c1;
+      paged_owners<GeoS>(total, end - c.left - c.at, pc.all, &c0, &c1);
       const size_t slot = (size_t)blockIdx.x * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0);
       float* po = p.part_o + (slot * kRowsS + row) * HD + col0;
 #pragma unroll
@@ -329,7 +332,6 @@ __global__ void __launch_bounds__(kThreadsS, 1) paged_attn_small_kernel(const Pa
         *reinterpret_cast<float4*>(po + x) = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
       if ((tid & 7) == 0) p.part_ml[slot * kRowsS + row] = make_float2(M, L);
       __threadfence();
-      mmas::cp_async_wait<0>();
       __syncthreads();
       if (tid == 0) *sLast = atomicAdd(p.arrive + c0, 1) == c1 - c0;
       __syncthreads();
@@ -367,15 +369,12 @@ __global__ void __launch_bounds__(kThreadsS, 1) paged_attn_small_kernel(const Pa
         write();
       }
     }
-    c.left -= n;
-    mmas::cp_async_wait<0>();
-    __syncthreads();                                     // sO and the ring are free again
-    if (c.left > 0) paged_next(p, kRowsS, kStepS, &c);
+    __syncthreads();                                     // the ring is free again
   }
 }
 
 template <int HD>
-void launch_small(const PagedAttnParams& p, int grid, cudaStream_t st) {
+void launch_small(const PagedAttnParams& p, cudaStream_t st) {
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -385,45 +384,54 @@ void launch_small(const PagedAttnParams& p, int grid, cudaStream_t st) {
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   TraceScope ts("paged_attn_small", st);
-  launch_k(paged_attn_small_kernel<HD>, dim3(grid), dim3(kThreadsS), SmallSmem<HD>::kBytes, st, p);
+  launch_k(paged_attn_small_kernel<HD>, dim3(num_sms() * kPerSmS), dim3(kThreadsS), SmallSmem<HD>::kBytes, st, p);
 }
 
 // ---------------------------------------------------------------------------
 // Many query rows (chains, trees, prompt chunks): tensor-core tiles.
 // ---------------------------------------------------------------------------
-// A tile is 256 query rows, two MMA tiles of 128, against steps of 128 keys:
-//   S_x = Q_x K_t^T   (x = 0, 1; accumulators S_0, S_1 in TMEM)
+// A tile is NG MMA tiles of 128 query rows, against steps of 128 keys:
+//   S_x = Q_x K_t^T   (x < NG; accumulators S_x in TMEM)
 //   O_x += P_x V_t    (P_x in TMEM over S_x's columns, as the A operand; O_x in TMEM)
-// Two softmax groups of four warps, one thread to a row, take turns with the
-// tensor cores: while group 0 turns S_0 into P_0, the cores run P_1 V and the
-// next S_1.  A tile of at most 128 rows is given to both groups, which take
-// every other key step each and join their halves at the end, so that the
-// alternation also holds for short chains.  Warp 8 loads (TMA, a ring of K and
-// V tiles that runs ahead over tile borders; a box is a page, or 128 keys of a
-// larger one), warp 9 issues the MMAs.  A row's O is rescaled only when its
-// maximum has risen by more than 8 (base-2 units) over the reference in use.
-// Every wait is bounded (2 s); on expiry the CTA records DFLASH_ERR_TIMEOUT,
-// lets its copies and MMAs land, frees TMEM and returns.
-constexpr int kRowsT = 256, kStepT = 128, kThreadsT = 384;
-// Registers: the launch's 168 for each of three warpgroups, of which the softmax
-// groups take 216 (a row of scores in registers) and the other one keeps 72:
-// 2 * 216 + 72 = 3 * 168.
+// NG = 2 (prompt chunks, trees): two softmax groups of four warps, one thread to
+// a row, take turns with the tensor cores: while group 0 turns S_0 into P_0, the
+// cores run P_1 V and the next S_1, and both MMA tiles share K and V.  A tile of
+// at most 128 rows is given to both groups, which take every other key step each
+// and join their halves at the end.  NG = 1 (chains): one group and half the
+// shared memory and TMEM, so that two CTAs share an SM: memory bounds these
+// tiles, and one CTA streams while the other begins or ends a tile.
+// Warp 4 NG loads (TMA, a ring of K and V tiles that runs ahead over tile borders;
+// a box is a page, or a slot of a larger one), the next one issues the MMAs.  A
+// row's O is rescaled only when its maximum has risen by more than 8 (base-2
+// units) over the reference in use.  Every wait is bounded (2 s); on expiry the CTA
+// records DFLASH_ERR_TIMEOUT, lets its copies and MMAs land, frees TMEM and returns.
+constexpr int kStepT = 128;
+// Registers with NG = 2: the launch's 168 for each of three warpgroups, of which
+// the softmax groups take 216 (a row of scores in registers) and the other one
+// keeps 72: 2 * 216 + 72 = 3 * 168.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "register split");
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 struct PagedTcMaps {
-  CUtensorMap k, v;    // pools as [n_pages * n_kv * page_size][HD], box 64 x min(page_size, 128)
+  CUtensorMap k, v;    // pools as [n_pages * n_kv * page_size][HD], box 64 x min(page_size, slot)
 };
 
-template <int HD>
-struct TcSmem {
-  static constexpr int kAtom = 128 * 128;                   // 64 columns of 128 rows
-  static constexpr int kTile = (HD / 64) * kAtom;           // 128 rows of bf16
+template <int HD, int NG>
+struct Tc {
+  static constexpr int kRows = 128 * NG, kThreads = NG == 2 ? 384 : 192, kPerSm = NG == 2 ? 1 : 2;
+  using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 4 : 3>;
+  static constexpr int kAtomQ = 128 * 128;                  // 64 columns of 128 rows of Q
+  static constexpr int kTileQ = (HD / 64) * kAtomQ;
+  static constexpr int kKeys = NG == 2 ? 128 : 64;          // of a ring slot
+  static constexpr int kPer = kStepT / kKeys;               // slots of a step's K, or V
+  static constexpr int kAtom = kKeys * 128, kSlot = (HD / 64) * kAtom;
   static constexpr int kSlots = HD == 128 ? 5 : 8;
-  static constexpr int kRing = 2 * kTile;                   // after Q's two tiles
-  static constexpr int kBar = kRing + kSlots * kTile;
-  static constexpr int kBytes = 1024 + kBar + 2048;
+  static constexpr int kRing = NG * kTileQ;                 // after Q
+  static constexpr int kBar = kRing + kSlots * kSlot;
+  static constexpr int kBytes = kBar + (NG == 2 ? 2048 : 1024);
+  static constexpr int kTmem = 256 * NG;                    // S_x at 128 x (P_x over it), then O_x
+  static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // Bits of keys [b, b + 32) relative to the first new token: 1 = seen.
@@ -439,23 +447,36 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kThreadsT, 1)
+// Whether a value among eight is infinite or NaN: x * 0 is NaN for those, and
+// sticks in the sum.
+__device__ __forceinline__ void gather_bad(__nv_bfloat162& acc, const uint4& u) {
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc = __hfma2(h[e], zero, acc);
+}
+
+template <int HD, int NG>
+__global__ void __launch_bounds__(Tc<HD, NG>::kThreads, Tc<HD, NG>::kPerSm)
 paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnParams p) {
-  using S = TcSmem<HD>;
-  constexpr int R = S::kSlots;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem;                                        // [2][HD / 64][128][64] bf16
-  uint8_t* sKV = smem + S::kRing;
+  using S = Tc<HD, NG>;
+  using Geo = typename S::Geo;
+  constexpr int R = S::kSlots, kPer = S::kPer;
+  extern __shared__ __align__(1024) uint8_t smem_tc[];
+  uint8_t* smem = smem_tc;
+  if (ptx::smem_addr(smem) & 1023) {                         // (the swizzle counts on it)
+    record_status(p.status, DFLASH_ERR_UNSUPPORTED);
+    return;
+  }
+  uint8_t* sQ = smem;                                        // [NG][HD / 64][128][64] bf16
+  uint8_t* sKV = smem + S::kRing;                            // slots of [HD / 64][kKeys][64]
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::kBar);
   uint64_t* full = bar;                                      // [R] tile landed
   uint64_t* empty = bar + R;                                 // [R] tile read
   uint64_t* q_full = bar + 2 * R;
-  uint64_t* s_ready = q_full + 1;                            // [2]
-  uint64_t* p_ready = q_full + 3;                            // [2][half]
-  uint64_t* pv_done = q_full + 7;                            // [2]
+  uint64_t* s_ready = q_full + 1;                            // [NG]
+  uint64_t* p_ready = q_full + 3;                            // [NG][half]
+  uint64_t* pv_done = q_full + 7;                            // [NG]
   uint64_t* drain = q_full + 9;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(q_full + 10);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
@@ -463,7 +484,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   // keys with a value that is not finite: [group][step % 4][word].  Group 1 may
   // still read group 0's of step t when group 0 is at step t + 2, not later.
   volatile uint32_t* odd_keys = tslot + 4;
-  float2* sMl = reinterpret_cast<float2*>(tslot + 36);       // [128]
+  float2* sMl = reinterpret_cast<float2*>(tslot + 36);       // [128] (NG = 2)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -471,8 +492,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
-    ptx::mbar_init(q_full, 8);
-    for (int x = 0; x < 2; ++x) {
+    ptx::mbar_init(q_full, 4 * NG);
+    for (int x = 0; x < NG; ++x) {
       ptx::mbar_init(&s_ready[x], 1);
       ptx::mbar_init(&p_ready[2 * x], 4);
       ptx::mbar_init(&p_ready[2 * x + 1], 4);
@@ -482,22 +503,22 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     *abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 9) {
-    ptx::tmem_alloc(tslot, 512);
+  constexpr int kLoad = 4 * NG, kIssue = 4 * NG + 1;         // warps
+  if (warp == kIssue) {
+    ptx::tmem_alloc(tslot, S::kTmem);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tbase = *tslot;
-  // S_x at column 128 x (P_x over it), O_x at 256 + 128 x
+  const uint32_t tbase_o = tbase + 128 * NG;                 // O_x at 128 x from here
 
   pdl_wait();
   pdl_trigger();
-  const int grid = gridDim.x;
   long long total, end;
   PagedCursor c;
-  paged_plan(p, kRowsT, kStepT, lane, &total, &end, &c);
+  paged_plan<Geo>(p, lane, &total, &end, &c);
 
   auto fail = [&]() {
     if (!*abort) record_status(p.status, DFLASH_ERR_TIMEOUT);
@@ -509,12 +530,13 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     return ptx::mbar_wait_bounded(b, parity, kTimeoutNs, abort);
   };
 
-  if (warp >= 8) {
-  ptx::regs_dec<kRegsOther>();
-  if (warp == 8) {
+  if (warp >= kLoad) {
+  if constexpr (NG == 2) ptx::regs_dec<kRegsOther>();
+  if (warp == kLoad) {
     // ---------------- loads ----------------
-    const int box = min(1 << p.pv.page_shift, 128);
-    const int nb = 128 / box;                                // boxes of a tile
+    const int box = min(1 << p.pv.page_shift, S::kKeys);
+    const int nb = kStepT / box;                             // boxes of a step's K, or V
+    const int per_slot = S::kKeys / box;
     const uint64_t pol = ptx::policy_evict_last();
     if (lane == 0) {
       ptx::prefetch_tmap(&maps.k);
@@ -523,13 +545,14 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     const int nowhere = (p.pv.n_pages * p.pv.n_kv) << p.pv.page_shift;   // past the pool: zeros
     uint32_t it = 0;                                         // tiles loaded
     bool ok = true;
-    while (c.left > 0 && ok) {
-      const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
-      const int kend = c.rq.key_end(c.j, p.G, kRowsT);
+    for (PagedPiece pc; c.left > 0 && ok; paged_next<Geo>(p, pc, &c)) {
+      pc = PagedPiece::of<Geo>(c);
+      if (pc.n <= 0) continue;
+      const int n = pc.n, kend = c.rq.key_end<Geo>(c.j, p.G);
       const int32_t* table = p.pv.table + (size_t)c.r * p.pv.table_ld;
       // this lane's box of step i: its first slot, and its page's table entry
       // (asked for one step ahead; kend lies within the table)
-      auto slot_of = [&](int i) { return (c.step + i) * kStepT + lane * box; };
+      auto slot_of = [&](int i) { return (pc.first + i) * kStepT + lane * box; };
       auto entry_of = [&](int i) {
         const int t = slot_of(i);
         return lane < nb && i < n && t < kend ? __ldg(table + (t >> p.pv.page_shift)) : -1;
@@ -541,21 +564,20 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.pv.n_pages);
         if (!there && lane < nb && t < kend) record_status(p.status, DFLASH_ERR_INVALID_ARG);
         const int y = there ? static_cast<int>(pool_row(p.pv, page, c.g, t)) : nowhere;
-        for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
-          const int s = it % R;
+        for (int kv = 0; kv < 2 * kPer && ok; ++kv, ++it) {   // K's slots, then V's
+          const int s = it % R, part = kv % kPer;
           ok = wait(&empty[s], (it / R & 1u) ^ 1u);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], S::kTile);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], S::kSlot);
           __syncwarp();
-          if (lane < nb)
+          const int b = lane - part * per_slot;              // this lane's box in the slot
+          if (b >= 0 && b < per_slot)
             for (int h = 0; h < HD / 64; ++h)
-              ptx::tma_load_2d(sKV + s * S::kTile + h * S::kAtom + lane * box * 128,
-                               kv ? &maps.v : &maps.k, &full[s], 64 * h, y, pol);
+              ptx::tma_load_2d(sKV + s * S::kSlot + h * S::kAtom + b * box * 128,
+                               kv >= kPer ? &maps.v : &maps.k, &full[s], 64 * h, y, pol);
         }
       }
-      c.left -= n;
-      if (c.left > 0) paged_next(p, kRowsT, kStepT, &c);
     }
     if (!ok && lane == 0) fail();
     // every copy must land before the CTA exits
@@ -564,7 +586,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       const uint32_t last = (it - 1 - s) / R;                // uses of slot s - 1
       ptx::mbar_wait_bounded(&full[s], last & 1u, kTimeoutNs, nullptr);
     }
-  } else if (warp == 9) {
+  } else if (warp == kIssue) {
     // ---------------- MMA issue ----------------
     // The whole warp runs the loop, so that addresses and descriptors stay in
     // uniform registers; one elected lane issues.  Descriptors differ by their
@@ -573,52 +595,57 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     const uint64_t dq = ptx::sw128_kmajor_desc(ptx::smem_addr(sQ));
     const uint64_t dk = ptx::sw128_kmajor_desc(ptx::smem_addr(sKV));
     const uint64_t dv = ptx::sw128_mnmajor_desc(ptx::smem_addr(sKV), S::kAtom, 1024);
-    constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, 128);
+    constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, S::kKeys);
     constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD) | (1u << 16);   // B transposed
     uint32_t it = 0, unit = 0, np[2] = {0, 0};               // ring base, units, PV products of x
     bool ok = true;
-    while (c.left > 0 && ok) {
-      const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
-      const int nt = min(c.rq.n * p.G - c.j * kRowsT, kRowsT) > 128 ? 2 : 1;
+    for (PagedPiece pc; c.left > 0 && ok; paged_next<Geo>(p, pc, &c)) {
+      pc = PagedPiece::of<Geo>(c);
+      if (pc.n <= 0) continue;
+      const int n = pc.n, nt = NG == 2 && min(c.rq.n * p.G - c.j * S::kRows, S::kRows) > 128 ? 2 : 1;
       ok = __all_sync(0xffffffffu, wait(q_full, unit & 1u));
       ptx::tc_fence_after();
-      const int jobs0 = nt == 2 ? n : (n + 1) / 2, jobs1 = nt == 2 ? n : n / 2;
+      const int jobs0 = NG == 1 || nt == 2 ? n : (n + 1) / 2, jobs1 = NG == 1 ? 0 : (nt == 2 ? n : n / 2);
+      // group x's i-th job is step step_of(x, i); ring slots of a step: K's, V's
+      auto step_of = [&](int x, int i) { return NG == 1 || nt == 2 ? i : 2 * i + x; };
       auto issue_s = [&](int x, int i) {
-        const uint32_t at = it + 2 * (nt == 2 ? i : 2 * i + x);
-        const uint32_t s = __shfl_sync(0xffffffffu, at % R, 0);
-        if (!__all_sync(0xffffffffu, wait(&full[s], at / R & 1u))) return false;
-        ptx::tc_fence_after();
-        const uint64_t q0 = dq + (nt == 2 ? x * (S::kTile >> 4) : 0), k0 = dk + s * (S::kTile >> 4);
-        if (elected) {
+        const uint64_t q0 = dq + (nt == 2 ? x * (S::kTileQ >> 4) : 0);
 #pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * S::kAtom + (kk & 3) * 32) >> 4;
-            ptx::mma_bf16(tbase + 128 * x, q0 + off, k0 + off, idesc_s, kk > 0 ? 1u : 0u);
+        for (int part = 0; part < kPer; ++part) {
+          const uint32_t at = it + 2 * kPer * step_of(x, i) + part;
+          const uint32_t s = __shfl_sync(0xffffffffu, at % R, 0);
+          if (!__all_sync(0xffffffffu, wait(&full[s], at / R & 1u))) return false;
+          ptx::tc_fence_after();
+          const uint64_t k0 = dk + s * (S::kSlot >> 4);
+          if (elected) {
+#pragma unroll
+            for (int kk = 0; kk < HD / 16; ++kk)
+              ptx::mma_bf16(tbase + 128 * x + part * S::kKeys,
+                            q0 + (((kk >> 2) * S::kAtomQ + (kk & 3) * 32) >> 4),
+                            k0 + (((kk >> 2) * S::kAtom + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+            if (part == kPer - 1) ptx::mma_commit(&s_ready[x]);
+            if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
           }
-          ptx::mma_commit(&s_ready[x]);
-          if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
+          __syncwarp();
         }
-        __syncwarp();
         return true;
       };
       auto issue_pv = [&](int x, int i) {
-        const uint32_t at = it + 2 * (nt == 2 ? i : 2 * i + x) + 1;
-        const uint32_t s = __shfl_sync(0xffffffffu, at % R, 0);
-        if (!__all_sync(0xffffffffu, wait(&full[s], at / R & 1u))) return false;
-        const uint64_t v0 = dv + s * (S::kTile >> 4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {                        // P arrives in two halves
+          const uint32_t at = it + 2 * kPer * step_of(x, i) + kPer + (kPer == 2 ? h : 0);
+          const uint32_t s = __shfl_sync(0xffffffffu, at % R, 0);
+          if ((h == 0 || kPer == 2) && !__all_sync(0xffffffffu, wait(&full[s], at / R & 1u))) return false;
           if (!__all_sync(0xffffffffu, wait(&p_ready[2 * x + h], np[x] & 1u))) return false;
           ptx::tc_fence_after();
+          const uint64_t v0 = dv + s * (S::kSlot >> 4);
           if (elected) {
 #pragma unroll
             for (int j = 4 * h; j < 4 * h + 4; ++j)
-              ptx::mma_bf16_ta(tbase + 256 + 128 * x, tbase + 128 * x + j * 8, v0 + j * (2048 >> 4),
-                               idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
-            if (h == 1) {
-              ptx::mma_commit(&pv_done[x]);
-              if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
-            }
+              ptx::mma_bf16_ta(tbase_o + 128 * x, tbase + 128 * x + j * 8,
+                               v0 + (j % (S::kKeys / 16)) * (2048 >> 4), idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
+            if (h == 1) ptx::mma_commit(&pv_done[x]);
+            if ((kPer == 2 || h == 1) && (nt == 1 || x == 1)) ptx::mma_commit(&empty[s]);
           }
           __syncwarp();
         }
@@ -633,10 +660,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         if (ok && i < jobs1) ok = issue_pv(1, i);
         if (ok && i + 1 < jobs1) ok = issue_s(1, i + 1);
       }
-      it += 2 * n;
+      it += 2 * kPer * n;
       ++unit;
-      c.left -= n;
-      if (c.left > 0) paged_next(p, kRowsT, kStepT, &c);
     }
     if (!ok && lane == 0) fail();
     // the MMAs already issued finish before TMEM is released
@@ -648,38 +673,39 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     __syncwarp();
   }
   } else {
-    ptx::regs_inc<kRegsSoftmax>();
+    if constexpr (NG == 2) ptx::regs_inc<kRegsSoftmax>();
     // ---------------- softmax: group x = warp / 4, a row to a thread ----------------
     const int x = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t aS = (tbase + 128 * x) + lane_off, aO = (tbase + 256 + 128 * x) + lane_off;
+    const uint32_t aS = tbase + 128 * x + lane_off, aO = tbase_o + 128 * x + lane_off;
     const float sc = p.scale_log2;
     uint32_t it = 0, nj = 0;                                 // ring base, jobs of this group
     bool ok = true;
-    while (c.left > 0) {
+    for (PagedPiece pc; c.left > 0; paged_next<Geo>(p, pc, &c)) {
+      pc = PagedPiece::of<Geo>(c);
+      if (pc.n <= 0) continue;
       const PagedReq rq = c.rq;
-      const int n = static_cast<int>(min((long long)(c.n_steps - c.step), c.left));
-      const int nG = rq.n * p.G, tile0 = c.j * kRowsT;
-      const int nt = min(nG - tile0, kRowsT) > 128 ? 2 : 1;
-      const int kend = rq.key_end(c.j, p.G, kRowsT);
+      const int n = pc.n, nG = rq.n * p.G, tile0 = c.j * S::kRows;
+      const int nt = NG == 2 && min(nG - tile0, S::kRows) > 128 ? 2 : 1;
+      const int kend = rq.key_end<Geo>(c.j, p.G);
       const int rho0 = tile0 + (nt == 2 ? x * 128 : 0);      // first row of this group's MMA tile
       const int rho = rho0 + row;
       const bool live = rho < nG;
       const int tok = live ? rho / p.G : 0, head = c.g * p.G + (live ? rho % p.G : 0);
-      const int jobs = nt == 2 ? n : (n + 1 - x) / 2;
+      const int jobs = NG == 1 || nt == 2 ? n : (n + 1 - x) / 2;
       // Q into shared memory (rows of 128 bytes, 128-byte swizzle): HD / 8 lanes
       // read a row, whose address its own lane knows
       if (nt == 2 || x == 0) {
         const unsigned long long mine = reinterpret_cast<unsigned long long>(
             p.q + (long long)(rq.row0 + tok) * p.q_ld + (long long)head * HD);
         const unsigned on = __ballot_sync(0xffffffffu, live);
-        constexpr int kPer = 256 / HD;                       // rows of a round
-#pragma unroll 8
-        for (int r0 = 0; r0 < 32; r0 += kPer) {
+        constexpr int kLines = 256 / HD;                     // rows of a round
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kLines) {
           const int rr = r0 + lane / (HD / 8), ch = lane % (HD / 8);
           const uint4* src = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, mine, rr)) + ch;
           const uint4 u = (on >> rr) & 1u ? __ldg(src) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(sQ + x * S::kTile + (ch >> 3) * S::kAtom + ((warp & 3) * 32 + rr) * 128 +
+          *reinterpret_cast<uint4*>(sQ + x * S::kTileQ + (ch >> 3) * S::kAtomQ + ((warp & 3) * 32 + rr) * 128 +
                                     (((ch & 7) ^ (rr & 7)) << 4)) = u;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -698,7 +724,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       float m_ref = -CUDART_INF_F, l = 0.f;
       // (after a wait has run out the loop only keeps the group's barriers company)
       for (int i = 0; i < jobs; ++i, ++nj) {
-        const int t = nt == 2 ? i : 2 * i + x, key0 = (c.step + t) * kStepT;
+        const int t = NG == 1 || nt == 2 ? i : 2 * i + x, key0 = (pc.first + t) * kStepT;
         volatile uint32_t* noted = odd_keys + 16 * (nt == 2 ? 0 : x) + 4 * (t & 3);
         if (ok) ok = __all_sync(0xffffffffu, wait(&s_ready[x], nj & 1u));
         const bool check = key0 + kStepT > plain_t && (nt == 1 || x == 0);   // group-uniform
@@ -706,31 +732,43 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         const bool early = !check && !dead;                  // P goes out in two halves
         if (ok && !dead) {
           ptx::tc_fence_after();
-          uint32_t u[4][32];
+          const bool cut = key0 + kStepT > plain_w;          // some key is hidden from some row
 #pragma unroll
-          for (int b = 0; b < 4; ++b) ptx::tmem_ld_32x32(aS + 32 * b, u[b]);
-          ptx::tmem_wait_ld();
-          if (key0 + kStepT > plain_w) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
+          for (int b = 0; b < 4; ++b) {
+            seen[b] = 0xFFFFFFFFu;
+            if (cut) {
               const int k = key0 + 32 * b;
               seen[b] = low_bits(lim - k);
               if (rq.masked && seen[b]) seen[b] &= seen_word(mrow, p.mask_ld, k - rq.p0);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((seen[b] >> j) & 1u)) u[b][j] = 0xff800000u;
             }
-          } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) seen[b] = 0xFFFFFFFFu;
           }
+          // The scores, 64 keys at a time where registers are short (they are then
+          // read twice), a whole row otherwise.
+          constexpr int kAt = NG == 2 ? 4 : 2;               // 32-key blocks held
+          uint32_t u[kAt][32];
+          auto load = [&](int b0) {
+#pragma unroll
+            for (int b = 0; b < kAt; ++b) ptx::tmem_ld_32x32(aS + 32 * (b0 + b), u[b]);
+            ptx::tmem_wait_ld();
+            if (cut) {
+#pragma unroll
+              for (int b = 0; b < kAt; ++b)
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((seen[b0 + b] >> j) & 1u)) u[b][j] = 0xff800000u;
+            }
+          };
           float mx8[8];                                      // eight chains: latency
 #pragma unroll
-          for (int j = 0; j < 8; ++j) mx8[j] = __uint_as_float(u[0][j]);
+          for (int j = 0; j < 8; ++j) mx8[j] = -CUDART_INF_F;
 #pragma unroll
-          for (int j = 4; j < 64; ++j)
-            mx8[j & 7] = fmaxf(fmaxf(mx8[j & 7], __uint_as_float(u[j >> 4][2 * (j & 15)])),
-                               __uint_as_float(u[j >> 4][2 * (j & 15) + 1]));
+          for (int b0 = 0; b0 < 4; b0 += kAt) {
+            load(b0);
+#pragma unroll
+            for (int j = 0; j < 16 * kAt; ++j)
+              mx8[j & 7] = fmaxf(fmaxf(mx8[j & 7], __uint_as_float(u[j >> 4][2 * (j & 15)])),
+                                 __uint_as_float(u[j >> 4][2 * (j & 15) + 1]));
+          }
           const float top = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                   fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * sc;
           const bool raise = top > m_ref + kLazy || (m_ref == -CUDART_INF_F && top > m_ref);
@@ -759,10 +797,13 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            // (P's first half lies over scores 0 .. 31, its second over 32 .. 63: the
+            // first half of the scores is in registers before either is written)
+            if (NG == 1) load(2 * h);
             uint32_t pk[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const int b = 2 * h + (j >> 4), e = 2 * (j & 15);
+              const int b = (2 * h) % kAt + (j >> 4), e = 2 * (j & 15);
               const float2 y = __ffma2_rn(
                   make_float2(__uint_as_float(u[b][e]), __uint_as_float(u[b][e + 1])), sc2, nb2);
               const float2 w = make_float2(ex2(y.x), ex2(y.y));
@@ -786,27 +827,40 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           // Some row may not see some key of this step: the values of keys past
           // the tile's last one become zeros, and so do values that are not
           // finite (their keys are noted, see below).
-          const uint32_t at = it + 2 * t + 1, s = at % R;
-          ok = __all_sync(0xffffffffu, ok && wait(&full[s], at / R & 1u));
+          const uint32_t v_at = it + 2 * kPer * t + kPer;
+          bool landed = true;
+          for (int part = 0; part < kPer && ok && landed; ++part)
+            landed = wait(&full[(v_at + part) % R], (v_at + part) / R & 1u);
+          ok = __all_sync(0xffffffffu, ok && landed);
           if (ptx::named_bar_or(1 + x, 128, !ok)) ok = false;
           bool mine = false;
           if (ok) {
-            uint8_t* v = sKV + s * S::kTile + row * 128;     // this thread: one key
-            const bool past = key0 + row >= kend;
+            // this thread: one key, whose 16-byte chunks it takes in another order
+            // than its neighbours (no bank conflicts)
+            const uint32_t s = (v_at + row / S::kKeys) % R;
+            uint8_t* v = sKV + s * S::kSlot + (row % S::kKeys) * 128;
+            auto chunk = [&](int ch) {
+              return reinterpret_cast<uint4*>(v + (ch >> 3) * S::kAtom + (((ch & 7) ^ (row & 7)) << 4));
+            };
+            if (key0 + row >= kend) {
 #pragma unroll
-            for (int ch = 0; ch < HD / 8; ++ch) {
-              // chunks in another order in every row: no bank conflicts
-              uint4* a = reinterpret_cast<uint4*>(v + (ch >> 3) * S::kAtom + (((ch & 7) ^ (row & 7)) << 4));
-              uint4 w = past ? make_uint4(0, 0, 0, 0) : *a;
-              const bool bad = not_finite8(w);
-              if (bad) {
-                mine = true;
-                w.x = zero_not_finite(w.x);
-                w.y = zero_not_finite(w.y);
-                w.z = zero_not_finite(w.z);
-                w.w = zero_not_finite(w.w);
+              for (int ch = 0; ch < HD / 8; ++ch) *chunk(ch) = make_uint4(0, 0, 0, 0);
+            } else {
+              __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
+#pragma unroll
+              for (int ch = 0; ch < HD / 8; ++ch) gather_bad(acc, *chunk(ch));
+              mine = __hisnan(acc.x) || __hisnan(acc.y);
+              if (mine) {
+#pragma unroll 1
+                for (int ch = 0; ch < HD / 8; ++ch) {
+                  uint4 w = *chunk(ch);
+                  w.x = zero_not_finite(w.x);
+                  w.y = zero_not_finite(w.y);
+                  w.z = zero_not_finite(w.z);
+                  w.w = zero_not_finite(w.w);
+                  *chunk(ch) = w;
+                }
               }
-              if (past || bad) *a = w;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
@@ -827,9 +881,10 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           ok = __all_sync(0xffffffffu, wait(&pv_done[x], nj & 1u));
           if (ok && !dead) {
             ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < 4; ++b) {
               uint32_t keys = noted[b];
+              const uint32_t sees = b == 0 ? seen[0] : b == 1 ? seen[1] : b == 2 ? seen[2] : seen[3];
               while (keys) {                                 // warp-uniform
                 const int j = __ffs(keys) - 1;
                 keys &= keys - 1;
@@ -837,7 +892,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
                 if (page < 0) continue;
                 const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.pv.v) +
                                          pool_row(p.pv, page, c.g, key) * HD;
-                const bool see = (seen[b] >> j) & 1u;
+                const bool see = (sees >> j) & 1u;
+#pragma unroll 1
                 for (int cb = 0; cb < HD / 32; ++cb) {
                   uint32_t o[32];
                   ptx::tmem_ld_32x32(aO + 32 * cb, o);
@@ -861,14 +917,14 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         ok = __all_sync(0xffffffffu, wait(&pv_done[x], (nj - 1) & 1u));
         if (ok) ptx::tc_fence_after();
       }
-      if (ptx::named_bar_or(5, 256, !ok)) {
+      if (ptx::named_bar_or(5, 128 * NG, !ok)) {
         ok = false;
         break;
       }
       // ---- the tile's rows ----
       float M = m_ref, L = l, fa = 1.f, fb = 0.f;            // weights of the two halves
       float* sB = reinterpret_cast<float*>(sQ);              // [128][HD], chunks of 4 swizzled
-      if (nt == 1) {
+      if (NG == 2 && nt == 1) {
         if (x == 1) {
           sMl[row] = make_float2(m_ref, l);
           if (jobs > 0) {
@@ -896,19 +952,18 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         }
       }
       const bool mine = nt == 2 || x == 0;                   // this group writes its rows
-      const long long unit0 = end - c.left - c.step;
-      const bool whole = n == c.n_steps;
-      const int c0 = whole ? 0 : paged_owner(total, unit0, grid);
-      const int c1 = whole ? 0 : paged_owner(total, unit0 + c.n_steps - 1, grid);
-      // partials: [slot][x][HD / 4][128 rows] of four columns, so that a warp's lanes
+      const bool whole = n == pc.all;
+      int c0 = 0, c1 = 0;
+      if (!whole) paged_owners<Geo>(total, end - c.left - c.at, pc.all, &c0, &c1);
+      // partials: [slot][NG][HD / 4][128 rows] of four columns, so that a warp's lanes
       // are neighbours in memory
-      auto part_of = [&](int cc) { return ((size_t)cc * 2 + (cc == c0)) * 2 + x; };
+      auto part_of = [&](int cc) { return ((size_t)cc * 2 + (cc == c0)) * NG + x; };
       const size_t slot = part_of(blockIdx.x);
       // The warp's 32 bf16 rows go out through shared memory, so that HD / 8
       // lanes write a row together: in the group's part of Q, or, a lane each, in
       // its row of the joined half, over columns that it has read.
-      uint8_t* stage = nt == 2 ? sQ + warp * (S::kTile / 4) : sQ + (warp & 3) * (S::kTile / 2);
-      const int stage_ld = nt == 2 ? HD * 2 : HD * 4;
+      uint8_t* stage = sQ + (NG == 2 && nt == 1 ? warp * (S::kTileQ / 2) : warp * (S::kTileQ / 4));
+      const int stage_ld = NG == 2 && nt == 1 ? HD * 4 : HD * 2;
       auto put = [&](int b, const float (&o)[32], float inv) {    // 32 columns of the row
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -925,9 +980,9 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         const unsigned long long mine_to = reinterpret_cast<unsigned long long>(
             p.out + (long long)(rq.row0 + tok) * p.out_ld + (long long)head * HD);
         const unsigned on = __ballot_sync(0xffffffffu, live);
-        constexpr int kPer = 256 / HD;
+        constexpr int kLines = 256 / HD;
 #pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += kPer) {
+        for (int r0 = 0; r0 < 32; r0 += kLines) {
           const int rr = r0 + lane / (HD / 8), ch = lane % (HD / 8);
           uint4* to = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, mine_to, rr)) + ch;
           const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * stage_ld + ((ch ^ (rr & 7)) << 4));
@@ -970,11 +1025,11 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         if (live) __stcg(p.part_ml + slot * 128 + row, make_float2(M, L));
         __threadfence();
         ptx::named_bar_sync(1 + x, 128);
-        if (row == 0) s_last[x] = atomicAdd(p.arrive + 2 * c0 + x, 1) == c1 - c0;
+        if (row == 0) s_last[x] = atomicAdd(p.arrive + NG * c0 + x, 1) == c1 - c0;
         ptx::named_bar_sync(1 + x, 128);
         if (s_last[x]) {
           __threadfence();
-          if (row == 0) p.arrive[2 * c0 + x] = 0;            // for the next call
+          if (row == 0) p.arrive[NG * c0 + x] = 0;            // for the next call
           if (!dead) {
             M = -CUDART_INF_F;
 #pragma unroll 4
@@ -1005,11 +1060,9 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           }
         }
       }
-      it += 2 * n;
-      c.left -= n;
-      if (c.left > 0) paged_next(p, kRowsT, kStepT, &c);
-      // the joined half lies where the next tile's queries go
-      ptx::named_bar_sync(5, 256);
+      it += 2 * kPer * n;
+      // the rows on their way out lie where the next tile's queries go
+      ptx::named_bar_sync(5, 128 * NG);
     }
     if (!ok) fail();
   }
@@ -1017,45 +1070,46 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 9) {
+  if (warp == kIssue) {
     __syncwarp();
-    ptx::tmem_dealloc(tbase, 512);
+    ptx::tmem_dealloc(tbase, S::kTmem);
   }
 }
 
-template <int HD>
-dflash_status launch_tc(const PagedAttnParams& p, const dflash_pages& pages, int grid, cudaStream_t st) {
+template <int HD, int NG>
+dflash_status launch_tc(const PagedAttnParams& p, const dflash_pages& pages, cudaStream_t st) {
+  using S = Tc<HD, NG>;
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    cudaFuncSetAttribute(paged_attn_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         TcSmem<HD>::kBytes);
+    cudaFuncSetAttribute(paged_attn_tc_kernel<HD, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   PagedTcMaps maps;
   const int rows = pages.n_pages * pages.n_kv * pages.page_size;
-  const int box = pages.page_size < 128 ? pages.page_size : 128;
+  const int box = pages.page_size < S::kKeys ? pages.page_size : S::kKeys;
   if (!encode_kmajor_map(&maps.k, pages.k, rows, HD, HD, box) ||
       !encode_kmajor_map(&maps.v, pages.v, rows, HD, HD, box))
     return set_error(DFLASH_ERR_CUDA, "paged attention: cannot encode the TMA descriptors");
   TraceScope ts("paged_attn_tc", st);
-  launch_k(paged_attn_tc_kernel<HD>, dim3(grid), dim3(kThreadsT), TcSmem<HD>::kBytes, st, maps, p);
+  launch_k(paged_attn_tc_kernel<HD, NG>, dim3(num_sms() * S::kPerSm), dim3(S::kThreads), S::kBytes, st, maps, p);
   return DFLASH_OK;
 }
-
-constexpr int kMaxTileRows = kRowsT;
 
 // Header, arrival counters, (max, sum) pairs, partial rows.
 struct PagedWs {
   size_t arrive, ml, o, bytes;
 };
-PagedWs paged_ws(int grid, int head_dim) {
+// Every kernel: two CTAs an SM at most, two counters an SM, and for each SM two
+// slots of 256 rows (or 2 x 2 of 128, or of 16).
+PagedWs paged_ws(int sms, int head_dim) {
   PagedWs w;
+  const size_t rows = (size_t)sms * 2 * 256;
   w.arrive = 256;
-  w.ml = w.arrive + align_up((size_t)grid * 2 * sizeof(int), 256);
-  w.o = w.ml + align_up((size_t)grid * 2 * kMaxTileRows * sizeof(float2), 256);
-  w.bytes = w.o + (size_t)grid * 2 * kMaxTileRows * head_dim * sizeof(float);
+  w.ml = w.arrive + align_up((size_t)sms * 2 * sizeof(int), 256);
+  w.o = w.ml + align_up(rows * sizeof(float2), 256);
+  w.bytes = w.o + rows * head_dim * sizeof(float);
   return w;
 }
 
@@ -1095,8 +1149,7 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
   DFL_REQUIRE(row_off && pos0 && q && out, "paged attention: null pointer argument");
   DFL_REQUIRE(((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0,
               "paged attention: q and out must be 16-byte aligned");
-  const int grid = num_sms();
-  const PagedWs w = paged_ws(grid, hd);
+  const PagedWs w = paged_ws(num_sms(), hd);
   if (!ws || ws_bytes < w.bytes)
     return set_error(DFLASH_ERR_WORKSPACE, "paged attention workspace needs %zu bytes, got %zu",
                      w.bytes, ws_bytes);
@@ -1120,12 +1173,17 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
   p.part_o = reinterpret_cast<float*>(b + w.o);
   p.status = reinterpret_cast<int*>(b);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if ((long long)max_rows * p.G <= kRowsS) {
-    hd == 128 ? launch_small<128>(p, grid, st) : launch_small<64>(p, grid, st);
-  } else {
-    const dflash_status e = hd == 128 ? launch_tc<128>(p, *pages, grid, st) : launch_tc<64>(p, *pages, grid, st);
-    if (e) return e;
-  }
+  // The smallest tile that takes all rows of a (request, KV head): keys and values
+  // are then read once.
+  const long long rows = (long long)max_rows * p.G;
+  dflash_status e = DFLASH_OK;
+  if (rows <= kRowsS)
+    hd == 128 ? launch_small<128>(p, st) : launch_small<64>(p, st);
+  else if (rows <= 128)
+    e = hd == 128 ? launch_tc<128, 1>(p, *pages, st) : launch_tc<64, 1>(p, *pages, st);
+  else
+    e = hd == 128 ? launch_tc<128, 2>(p, *pages, st) : launch_tc<64, 2>(p, *pages, st);
+  if (e) return e;
   return check_launch("paged attention");
 }
 

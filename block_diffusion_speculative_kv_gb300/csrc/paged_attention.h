@@ -27,6 +27,13 @@ struct PagedAttnParams {
   int* status;
 };
 
+// Geometry of a kernel's work: TR query rows to a tile, KS keys to a step, and TC,
+// what beginning and ending a tile costs, in steps (it only weighs the shares).
+template <int TR_, int KS_, int TC_>
+struct PagedGeo {
+  static constexpr int TR = TR_, KS = KS_, TC = TC_;
+};
+
 // One request of the flattened work.  Its n rows and G heads of a KV head make
 // n * G query rows (row = token * G + head), TR to a tile; tile j sees keys
 // 0 .. key_end(j) - 1, in steps of KS keys.
@@ -40,27 +47,52 @@ struct PagedReq {
     p0 = min(max(p.pos0[r], 0), cap);
     masked = p.mask != nullptr;
   }
-  __device__ __forceinline__ int tiles(int G, int TR) const { return (n * G + TR - 1) / TR; }
-  __device__ __forceinline__ int key_end(int j, int G, int TR) const {
-    const int last = masked ? n - 1 : min(j * TR + TR - 1, n * G - 1) / G;
+  template <typename Geo>
+  __device__ __forceinline__ int tiles(int G) const {
+    return (n * G + Geo::TR - 1) / Geo::TR;
+  }
+  template <typename Geo>
+  __device__ __forceinline__ int key_end(int j, int G) const {
+    const int last = masked ? n - 1 : min(j * Geo::TR + Geo::TR - 1, n * G - 1) / G;
     return min(p0 + last + 1, cap);
   }
-  // steps of tiles [0, j1) of one KV head
-  __device__ __forceinline__ long long steps(int j1, int G, int TR, int KS) const {
-    if (masked) return (long long)j1 * ((key_end(0, G, TR) + KS - 1) / KS);
+  // length of a tile, and of tiles [0, j1) of one KV head, on the line
+  template <typename Geo>
+  __device__ __forceinline__ int length(int j, int G) const {
+    return Geo::TC + (key_end<Geo>(j, G) + Geo::KS - 1) / Geo::KS;
+  }
+  template <typename Geo>
+  __device__ __forceinline__ long long lengths(int j1, int G) const {
+    if (masked) return (long long)j1 * length<Geo>(0, G);
     long long s = 0;
-    for (int j = 0; j < j1; ++j) s += (key_end(j, G, TR) + KS - 1) / KS;
+    for (int j = 0; j < j1; ++j) s += length<Geo>(j, G);
     return s;
   }
 };
 
-// A CTA's place in the flattened work: requests, then KV heads, then query
-// tiles, then key steps.  The CTA's share is [begin, end) of `total` steps.
+// A CTA's place on the line: requests, then KV heads, then query tiles, then, for
+// each tile, TC units of overhead and its key steps.  The CTA's share is one
+// stretch of the line.
 struct PagedCursor {
   int r, g, j;             // request, KV head, tile
-  int step, n_steps;       // next step of the tile, its steps
-  long long left;          // steps left to this CTA, this tile's included
+  int at, length;          // place in the tile, its length
+  long long left;          // what is left of the share
   PagedReq rq;
+};
+
+// The key steps of the cursor's tile that lie in the share: [first, first + n) of
+// `all`; they end `used` further on the line.
+struct PagedPiece {
+  int first, n, all, used;
+  template <typename Geo>
+  __device__ __forceinline__ static PagedPiece of(const PagedCursor& c) {
+    PagedPiece p;
+    p.used = static_cast<int>(min((long long)(c.length - c.at), c.left));
+    p.all = c.length - Geo::TC;
+    p.first = max(c.at - Geo::TC, 0);
+    p.n = max(c.at + p.used - Geo::TC, 0) - p.first;
+    return p;
+  }
 };
 
 // a / b for a >= 0, b > 0; almost always within 32 bits, where it is quick.
@@ -79,22 +111,22 @@ __device__ __forceinline__ int paged_owner(long long total, long long s, int gri
   return static_cast<int>(s < m * (q + 1) ? div_pos(s, q + 1) : m + div_pos(s - m * (q + 1), q));
 }
 
-// Warp-collective: all requests' steps, this CTA's share of them, and the place
+// Warp-collective: the line's length, the end of this CTA's share, and the place
 // where the share begins.
-__device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int TR, int KS, int lane,
-                                           long long* total_out, long long* end_out,
-                                           PagedCursor* c) {
+template <typename Geo>
+__device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, long long* total_out,
+                                           long long* end_out, PagedCursor* c) {
   const int grid = gridDim.x;
-  auto steps_of = [&](int r, PagedReq* q) {
+  auto length_of = [&](int r, PagedReq* q) {
     if (r >= p.n_req) return 0ll;
     q->load(p, r);
-    return q->steps(q->tiles(p.G, TR), p.G, TR, KS) * p.pv.n_kv;
+    return q->lengths<Geo>(q->tiles<Geo>(p.G), p.G) * p.pv.n_kv;
   };
   PagedReq q;
-  const long long first = steps_of(lane, &q);              // of the first 32 requests
+  const long long first = length_of(lane, &q);             // of the first 32 requests
   long long total = 0;
   for (int r0 = 0; r0 < p.n_req; r0 += 32) {
-    long long s = r0 == 0 ? first : steps_of(r0 + lane, &q);
+    long long s = r0 == 0 ? first : length_of(r0 + lane, &q);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     total += s;
@@ -107,7 +139,7 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int TR, int
   if (c->left <= 0) return;
   long long before = 0;
   for (int r0 = 0; r0 < p.n_req; r0 += 32) {
-    const long long s = r0 == 0 ? first : steps_of(r0 + lane, &q);
+    const long long s = r0 == 0 ? first : length_of(r0 + lane, &q);
     long long inc = s;                                     // inclusive scan
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -124,25 +156,28 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int TR, int
       long long rem = begin - before - excl;
       c->g = static_cast<int>(div_pos(rem, per_g));
       rem -= (long long)c->g * per_g;
-      int j = 0, ns;
+      int j = 0, len;
       while (true) {
-        ns = (c->rq.key_end(j, p.G, TR) + KS - 1) / KS;
-        if (rem < ns) break;
-        rem -= ns;
+        len = c->rq.length<Geo>(j, p.G);
+        if (rem < len) break;
+        rem -= len;
         ++j;
       }
       c->j = j;
-      c->step = static_cast<int>(rem);
-      c->n_steps = ns;
+      c->at = static_cast<int>(rem);
+      c->length = len;
       return;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
 }
 
-// To the next tile (the current one's steps are used up).
-__device__ __forceinline__ void paged_next(const PagedAttnParams& p, int TR, int KS, PagedCursor* c) {
-  if (++c->j >= c->rq.tiles(p.G, TR)) {
+// Past the piece, to the next tile.
+template <typename Geo>
+__device__ __forceinline__ void paged_next(const PagedAttnParams& p, const PagedPiece& pc, PagedCursor* c) {
+  c->left -= pc.used;
+  if (c->left <= 0) return;
+  if (++c->j >= c->rq.tiles<Geo>(p.G)) {
     c->j = 0;
     if (++c->g >= p.pv.n_kv) {
       c->g = 0;
@@ -152,8 +187,15 @@ __device__ __forceinline__ void paged_next(const PagedAttnParams& p, int TR, int
       } while (c->rq.n == 0);
     }
   }
-  c->step = 0;
-  c->n_steps = (c->rq.key_end(c->j, p.G, TR) + KS - 1) / KS;
+  c->at = 0;
+  c->length = c->rq.length<Geo>(c->j, p.G);
+}
+
+// The CTAs of a tile that begins at `tile0` on the line and has `all` steps.
+template <typename Geo>
+__device__ __forceinline__ void paged_owners(long long total, long long tile0, int all, int* c0, int* c1) {
+  *c0 = paged_owner(total, tile0 + Geo::TC, gridDim.x);
+  *c1 = paged_owner(total, tile0 + Geo::TC + all - 1, gridDim.x);
 }
 
 }  // namespace dfl

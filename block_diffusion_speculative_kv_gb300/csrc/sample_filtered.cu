@@ -788,6 +788,7 @@ sample_filtered_kernel(const SampleParams p) {
       }
       cluster_sync();
       // kPer bins to a thread, from the best on; upper and lower bounds of their measures
+      const float per_bin = -w.hi / scale;                 // (linear) log2 of a bin's fall
       uint64_t up[kPer], low[kPer], cu = 0, cl = 0;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
@@ -803,8 +804,8 @@ sample_filtered_kernel(const SampleParams p) {
           if (shift == 0 && !linear) {
             wu = wl = fix(w(C::value(hi - b)));
           } else if (linear) {
-            wu = fix(fminf(ex2(-(b / scale) * w.hi) * (1.f + kSlack), 1.f)) + 1;
-            wl = fix(ex2(-((b + 1) / scale) * w.hi) * (1.f - kSlack));
+            wu = fix(fminf(ex2(b * per_bin) * (1.f + kSlack), 1.f)) + 1;
+            wl = fix(ex2((b + 1) * per_bin) * (1.f - kSlack));
           } else {
             const uint32_t top = hi - (b << shift), span = (1u << shift) - 1;
             wu = fix(fminf(w(C::value(top)) * (1.f + kSlack), 1.f)) + 1;
