@@ -397,11 +397,14 @@ void launch_small(const PagedAttnParams& p, cudaStream_t st) {
 // a row, take turns with the tensor cores: while group 0 turns S_0 into P_0, the
 // cores run P_1 V and the next S_1, and both MMA tiles share K and V.  A tile of
 // at most 128 rows is given to both groups, which take every other key step each
-// and join their halves at the end.  NG = 1 (chains): one group and half the
-// shared memory and TMEM, so that two CTAs share an SM: memory bounds these
-// tiles, and one CTA streams while the other begins or ends a tile.
-// Warp 4 NG loads (TMA, a ring of K and V tiles that runs ahead over tile borders;
-// a box is a page, or a slot of a larger one), the next one issues the MMAs.  A
+// and join their halves at the end.  NG = 1 (chains): tiles of 64 rows, the first
+// half of an MMA tile (the other half multiplies whatever follows Q in shared
+// memory, and nobody reads it), with half an SM's shared memory and TMEM, so that
+// two CTAs share an SM: memory bounds these tiles, and one CTA streams while the
+// other begins or ends a tile.
+// After the softmax warps, one loads (TMA, a ring of K and V tiles that runs ahead
+// over tile borders; a box is a page, or a slot of a larger one), the next one
+// issues the MMAs.  A
 // row's O is rescaled only when its maximum has risen by more than 8 (base-2
 // units) over the reference in use.  Every wait is bounded (2 s); on expiry the CTA
 // records DFLASH_ERR_TIMEOUT, lets its copies and MMAs land, frees TMEM and returns.
@@ -419,14 +422,16 @@ struct PagedTcMaps {
 
 template <int HD, int NG>
 struct Tc {
-  static constexpr int kRows = 128 * NG, kThreads = NG == 2 ? 384 : 192, kPerSm = NG == 2 ? 1 : 2;
+  static constexpr int kGroup = NG == 2 ? 128 : 64;         // rows, and threads, of a softmax group
+  static constexpr int kRows = kGroup * NG, kWarps = kRows / 32;
+  static constexpr int kThreads = NG == 2 ? 384 : 128, kPerSm = NG == 2 ? 1 : 2;
   using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 4 : 3>;
-  static constexpr int kAtomQ = 128 * 128;                  // 64 columns of 128 rows of Q
+  static constexpr int kAtomQ = kGroup * 128;               // 64 columns of a group's rows of Q
   static constexpr int kTileQ = (HD / 64) * kAtomQ;
   static constexpr int kKeys = NG == 2 ? 128 : 64;          // of a ring slot
   static constexpr int kPer = kStepT / kKeys;               // slots of a step's K, or V
   static constexpr int kAtom = kKeys * 128, kSlot = (HD / 64) * kAtom;
-  static constexpr int kSlots = HD == 128 ? 5 : 8;
+  static constexpr int kSlots = HD == 64 ? 8 : NG == 2 ? 5 : 6;
   static constexpr int kRing = NG * kTileQ;                 // after Q
   static constexpr int kBar = kRing + kSlots * kSlot;
   static constexpr int kBytes = kBar + (NG == 2 ? 2048 : 1024);
@@ -492,18 +497,19 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
-    ptx::mbar_init(q_full, 4 * NG);
+    ptx::mbar_init(q_full, S::kWarps);
     for (int x = 0; x < NG; ++x) {
       ptx::mbar_init(&s_ready[x], 1);
-      ptx::mbar_init(&p_ready[2 * x], 4);
-      ptx::mbar_init(&p_ready[2 * x + 1], 4);
+      ptx::mbar_init(&p_ready[2 * x], S::kGroup / 32);
+      ptx::mbar_init(&p_ready[2 * x + 1], S::kGroup / 32);
       ptx::mbar_init(&pv_done[x], 1);
     }
     ptx::mbar_init(drain, 1);
     *abort = 0;
     ptx::fence_mbar_init();
   }
-  constexpr int kLoad = 4 * NG, kIssue = 4 * NG + 1;         // warps
+  constexpr int kLoad = S::kWarps, kIssue = S::kWarps + 1;    // warps
+  constexpr int GT = S::kGroup;
   if (warp == kIssue) {
     ptx::tmem_alloc(tslot, S::kTmem);
     ptx::tmem_relinquish();
@@ -598,67 +604,88 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(128, S::kKeys);
     constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HD) | (1u << 16);   // B transposed
     uint32_t it = 0, unit = 0, np[2] = {0, 0};               // ring base, units, PV products of x
+    uint32_t ks[kPer] = {}, vs[kPer] = {};                   // ring slots in use
     bool ok = true;
     for (PagedPiece pc; c.left > 0 && ok; paged_next<Geo>(p, pc, &c)) {
       pc = PagedPiece::of<Geo>(c);
       if (pc.n <= 0) continue;
       const int n = pc.n, nt = NG == 2 && min(c.rq.n * p.G - c.j * S::kRows, S::kRows) > 128 ? 2 : 1;
-      ok = __all_sync(0xffffffffu, wait(q_full, unit & 1u));
-      ptx::tc_fence_after();
+      auto all = [&](bool landed) { return __all_sync(0xffffffffu, landed); };
+      ok = all(wait(q_full, unit & 1u));
       const int jobs0 = NG == 1 || nt == 2 ? n : (n + 1) / 2, jobs1 = NG == 1 ? 0 : (nt == 2 ? n : n / 2);
-      // group x's i-th job is step step_of(x, i); ring slots of a step: K's, V's
+      // group x's i-th job is this step; ring slots of a step: K's, V's
       auto step_of = [&](int x, int i) { return NG == 1 || nt == 2 ? i : 2 * i + x; };
-      auto issue_s = [&](int x, int i) {
+      auto slot_at = [&](uint32_t at) { return __shfl_sync(0xffffffffu, at % R, 0); };
+      // Waits that the loads decide come before the one that the softmax decides, and
+      // between that one and the next scores there is nothing but MMAs.
+      auto landed = [&](uint32_t at) { return all(wait(&full[at % R], at / R & 1u)); };
+      auto scores = [&](int x, int i) {                      // one lane: S_x of job i
         const uint64_t q0 = dq + (nt == 2 ? x * (S::kTileQ >> 4) : 0);
 #pragma unroll
         for (int part = 0; part < kPer; ++part) {
-          const uint32_t at = it + 2 * kPer * step_of(x, i) + part;
-          const uint32_t s = __shfl_sync(0xffffffffu, at % R, 0);
-          if (!__all_sync(0xffffffffu, wait(&full[s], at / R & 1u))) return false;
-          ptx::tc_fence_after();
+          const uint32_t s = ks[part];
           const uint64_t k0 = dk + s * (S::kSlot >> 4);
-          if (elected) {
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk)
-              ptx::mma_bf16(tbase + 128 * x + part * S::kKeys,
-                            q0 + (((kk >> 2) * S::kAtomQ + (kk & 3) * 32) >> 4),
-                            k0 + (((kk >> 2) * S::kAtom + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
-            if (part == kPer - 1) ptx::mma_commit(&s_ready[x]);
-            if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
-          }
-          __syncwarp();
+          for (int kk = 0; kk < HD / 16; ++kk)
+            ptx::mma_bf16(tbase + 128 * x + part * S::kKeys,
+                          q0 + (((kk >> 2) * S::kAtomQ + (kk & 3) * 32) >> 4),
+                          k0 + (((kk >> 2) * S::kAtom + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+          if (part == kPer - 1) ptx::mma_commit(&s_ready[x]);
+          if (nt == 1 || x == 1) ptx::mma_commit(&empty[s]);
         }
-        return true;
       };
-      auto issue_pv = [&](int x, int i) {
+      auto wait_k = [&](int x, int i) {
+        const uint32_t at = it + 2 * kPer * step_of(x, i);
+        bool got = true;
+#pragma unroll
+        for (int part = 0; part < kPer; ++part) {
+          ks[part] = slot_at(at + part);
+          got = got && landed(at + part);
+        }
+        return got;
+      };
+      // job i of group x: P V, then the scores of job i + 1
+      auto turn = [&](int x, int i, bool more) {
+        const bool shared = nt == 2 && x == 1;               // group 0 has waited for these
+        const uint32_t at = it + 2 * kPer * step_of(x, i) + kPer;
+        if (!shared) {
+#pragma unroll
+          for (int part = 0; part < kPer; ++part) {
+            vs[part] = slot_at(at + part);
+            if (!landed(at + part)) return false;
+          }
+          if (more && !wait_k(x, i + 1)) return false;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {                        // P arrives in two halves
-          const uint32_t at = it + 2 * kPer * step_of(x, i) + kPer + (kPer == 2 ? h : 0);
-          const uint32_t s = __shfl_sync(0xffffffffu, at % R, 0);
-          if ((h == 0 || kPer == 2) && !__all_sync(0xffffffffu, wait(&full[s], at / R & 1u))) return false;
-          if (!__all_sync(0xffffffffu, wait(&p_ready[2 * x + h], np[x] & 1u))) return false;
+          if (!all(wait(&p_ready[2 * x + h], np[x] & 1u))) return false;
           ptx::tc_fence_after();
-          const uint64_t v0 = dv + s * (S::kSlot >> 4);
           if (elected) {
+            const uint32_t s = vs[kPer == 2 ? h : 0];
+            const uint64_t v0 = dv + s * (S::kSlot >> 4);
 #pragma unroll
             for (int j = 4 * h; j < 4 * h + 4; ++j)
               ptx::mma_bf16_ta(tbase_o + 128 * x, tbase + 128 * x + j * 8,
                                v0 + (j % (S::kKeys / 16)) * (2048 >> 4), idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
             if (h == 1) ptx::mma_commit(&pv_done[x]);
             if ((kPer == 2 || h == 1) && (nt == 1 || x == 1)) ptx::mma_commit(&empty[s]);
+            if (h == 1 && more) scores(x, i + 1);
           }
           __syncwarp();
         }
         ++np[x];
         return true;
       };
-      if (ok) ok = issue_s(0, 0);
-      if (ok && jobs1 > 0) ok = issue_s(1, 0);
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (x == 1 && jobs1 == 0) break;
+        if (nt == 1 || x == 0) ok = wait_k(x, 0);
+        ptx::tc_fence_after();
+        if (ok && elected) scores(x, 0);
+        __syncwarp();
+      }
       for (int i = 0; i < jobs0 && ok; ++i) {
-        ok = issue_pv(0, i);
-        if (ok && i + 1 < jobs0) ok = issue_s(0, i + 1);
-        if (ok && i < jobs1) ok = issue_pv(1, i);
-        if (ok && i + 1 < jobs1) ok = issue_s(1, i + 1);
+        ok = turn(0, i, i + 1 < jobs0);
+        if (ok && i < jobs1) ok = turn(1, i, i + 1 < jobs1);
       }
       it += 2 * kPer * n;
       ++unit;
@@ -675,8 +702,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   } else {
     if constexpr (NG == 2) ptx::regs_inc<kRegsSoftmax>();
     // ---------------- softmax: group x = warp / 4, a row to a thread ----------------
-    const int x = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int x = warp / (GT / 32), wg = warp % (GT / 32), row = wg * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
     const uint32_t aS = tbase + 128 * x + lane_off, aO = tbase_o + 128 * x + lane_off;
     const float sc = p.scale_log2;
     uint32_t it = 0, nj = 0;                                 // ring base, jobs of this group
@@ -688,7 +715,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       const int n = pc.n, nG = rq.n * p.G, tile0 = c.j * S::kRows;
       const int nt = NG == 2 && min(nG - tile0, S::kRows) > 128 ? 2 : 1;
       const int kend = rq.key_end<Geo>(c.j, p.G);
-      const int rho0 = tile0 + (nt == 2 ? x * 128 : 0);      // first row of this group's MMA tile
+      const int rho0 = tile0 + (nt == 2 ? x * GT : 0);       // first row of this group's MMA tile
       const int rho = rho0 + row;
       const bool live = rho < nG;
       const int tok = live ? rho / p.G : 0, head = c.g * p.G + (live ? rho % p.G : 0);
@@ -705,7 +732,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           const int rr = r0 + lane / (HD / 8), ch = lane % (HD / 8);
           const uint4* src = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, mine, rr)) + ch;
           const uint4 u = (on >> rr) & 1u ? __ldg(src) : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(sQ + x * S::kTileQ + (ch >> 3) * S::kAtomQ + ((warp & 3) * 32 + rr) * 128 +
+          *reinterpret_cast<uint4*>(sQ + x * S::kTileQ + (ch >> 3) * S::kAtomQ + (wg * 32 + rr) * 128 +
                                     (((ch & 7) ^ (rr & 7)) << 4)) = u;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -717,10 +744,10 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       // that every row of the warp, and of the whole tile, sees
       const int lim = live ? (rq.masked ? kend : min(rq.p0 + tok + 1, kend)) : 0;
       const uint32_t* mrow = rq.masked ? p.mask + (size_t)(rq.row0 + tok) * p.mask_ld : nullptr;
-      const int first = min(rho0 + (warp & 3) * 32, nG - 1) / p.G;
-      const int plain_w = rho0 + (warp & 3) * 32 >= nG ? 0 : min(rq.masked ? rq.p0 : rq.p0 + first + 1, kend);
+      const int first = min(rho0 + wg * 32, nG - 1) / p.G;
+      const int plain_w = rho0 + wg * 32 >= nG ? 0 : min(rq.masked ? rq.p0 : rq.p0 + first + 1, kend);
       const int plain_t = min(rq.masked ? rq.p0 : rq.p0 + tile0 / p.G + 1, kend);
-      const bool dead = rho0 + (warp & 3) * 32 >= nG;        // no live row in this warp
+      const bool dead = rho0 + wg * 32 >= nG;        // no live row in this warp
       float m_ref = -CUDART_INF_F, l = 0.f;
       // (after a wait has run out the loop only keeps the group's barriers company)
       for (int i = 0; i < jobs; ++i, ++nj) {
@@ -742,33 +769,24 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
               if (rq.masked && seen[b]) seen[b] &= seen_word(mrow, p.mask_ld, k - rq.p0);
             }
           }
-          // The scores, 64 keys at a time where registers are short (they are then
-          // read twice), a whole row otherwise.
-          constexpr int kAt = NG == 2 ? 4 : 2;               // 32-key blocks held
-          uint32_t u[kAt][32];
-          auto load = [&](int b0) {
+          uint32_t u[4][32];
 #pragma unroll
-            for (int b = 0; b < kAt; ++b) ptx::tmem_ld_32x32(aS + 32 * (b0 + b), u[b]);
-            ptx::tmem_wait_ld();
-            if (cut) {
+          for (int b = 0; b < 4; ++b) ptx::tmem_ld_32x32(aS + 32 * b, u[b]);
+          ptx::tmem_wait_ld();
+          if (cut) {
 #pragma unroll
-              for (int b = 0; b < kAt; ++b)
+            for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!((seen[b0 + b] >> j) & 1u)) u[b][j] = 0xff800000u;
-            }
-          };
+              for (int j = 0; j < 32; ++j)
+                if (!((seen[b] >> j) & 1u)) u[b][j] = 0xff800000u;
+          }
           float mx8[8];                                      // eight chains: latency
 #pragma unroll
-          for (int j = 0; j < 8; ++j) mx8[j] = -CUDART_INF_F;
+          for (int j = 0; j < 8; ++j) mx8[j] = __uint_as_float(u[0][j]);
 #pragma unroll
-          for (int b0 = 0; b0 < 4; b0 += kAt) {
-            load(b0);
-#pragma unroll
-            for (int j = 0; j < 16 * kAt; ++j)
-              mx8[j & 7] = fmaxf(fmaxf(mx8[j & 7], __uint_as_float(u[j >> 4][2 * (j & 15)])),
-                                 __uint_as_float(u[j >> 4][2 * (j & 15) + 1]));
-          }
+          for (int j = 4; j < 64; ++j)
+            mx8[j & 7] = fmaxf(fmaxf(mx8[j & 7], __uint_as_float(u[j >> 4][2 * (j & 15)])),
+                               __uint_as_float(u[j >> 4][2 * (j & 15) + 1]));
           const float top = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
                                   fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * sc;
           const bool raise = top > m_ref + kLazy || (m_ref == -CUDART_INF_F && top > m_ref);
@@ -797,13 +815,10 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            // (P's first half lies over scores 0 .. 31, its second over 32 .. 63: the
-            // first half of the scores is in registers before either is written)
-            if (NG == 1) load(2 * h);
             uint32_t pk[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const int b = (2 * h) % kAt + (j >> 4), e = 2 * (j & 15);
+              const int b = 2 * h + (j >> 4), e = 2 * (j & 15);
               const float2 y = __ffma2_rn(
                   make_float2(__uint_as_float(u[b][e]), __uint_as_float(u[b][e + 1])), sc2, nb2);
               const float2 w = make_float2(ex2(y.x), ex2(y.y));
@@ -832,41 +847,46 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           for (int part = 0; part < kPer && ok && landed; ++part)
             landed = wait(&full[(v_at + part) % R], (v_at + part) / R & 1u);
           ok = __all_sync(0xffffffffu, ok && landed);
-          if (ptx::named_bar_or(1 + x, 128, !ok)) ok = false;
-          bool mine = false;
-          if (ok) {
+          if (ptx::named_bar_or(1 + x, GT, !ok)) ok = false;
+#pragma unroll
+          for (int k0 = 0; k0 < kStepT; k0 += GT) {
             // this thread: one key, whose 16-byte chunks it takes in another order
             // than its neighbours (no bank conflicts)
-            const uint32_t s = (v_at + row / S::kKeys) % R;
-            uint8_t* v = sKV + s * S::kSlot + (row % S::kKeys) * 128;
-            auto chunk = [&](int ch) {
-              return reinterpret_cast<uint4*>(v + (ch >> 3) * S::kAtom + (((ch & 7) ^ (row & 7)) << 4));
-            };
-            if (key0 + row >= kend) {
+            const int key = k0 + row;
+            bool mine = false;
+            if (ok) {
+              const uint32_t s = (v_at + key / S::kKeys) % R;
+              uint8_t* v = sKV + s * S::kSlot + (key % S::kKeys) * 128;
+              auto chunk = [&](int ch) {
+                return reinterpret_cast<uint4*>(v + (ch >> 3) * S::kAtom + (((ch & 7) ^ (row & 7)) << 4));
+              };
+              if (key0 + key >= kend) {
 #pragma unroll
-              for (int ch = 0; ch < HD / 8; ++ch) *chunk(ch) = make_uint4(0, 0, 0, 0);
-            } else {
-              __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
+                for (int ch = 0; ch < HD / 8; ++ch) *chunk(ch) = make_uint4(0, 0, 0, 0);
+              } else {
+                __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
 #pragma unroll
-              for (int ch = 0; ch < HD / 8; ++ch) gather_bad(acc, *chunk(ch));
-              mine = __hisnan(acc.x) || __hisnan(acc.y);
-              if (mine) {
+                for (int ch = 0; ch < HD / 8; ++ch) gather_bad(acc, *chunk(ch));
+                mine = __hisnan(acc.x) || __hisnan(acc.y);
+                if (mine) {
 #pragma unroll 1
-                for (int ch = 0; ch < HD / 8; ++ch) {
-                  uint4 w = *chunk(ch);
-                  w.x = zero_not_finite(w.x);
-                  w.y = zero_not_finite(w.y);
-                  w.z = zero_not_finite(w.z);
-                  w.w = zero_not_finite(w.w);
-                  *chunk(ch) = w;
+                  for (int ch = 0; ch < HD / 8; ++ch) {
+                    uint4 w = *chunk(ch);
+                    w.x = zero_not_finite(w.x);
+                    w.y = zero_not_finite(w.y);
+                    w.z = zero_not_finite(w.z);
+                    w.w = zero_not_finite(w.w);
+                    *chunk(ch) = w;
+                  }
                 }
               }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            const uint32_t keys = __ballot_sync(0xffffffffu, mine);
+            if (lane == 0) noted[k0 / 32 + wg] = keys;
+            odd |= mine;
           }
-          const uint32_t keys = __ballot_sync(0xffffffffu, mine);
-          if (lane == 0) noted[warp & 3] = keys;
-          odd = ptx::named_bar_or(1 + x, 128, mine);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          odd = ptx::named_bar_or(1 + x, GT, odd);
         }
         ptx::tc_fence_before();
         __syncwarp();
@@ -917,7 +937,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         ok = __all_sync(0xffffffffu, wait(&pv_done[x], (nj - 1) & 1u));
         if (ok) ptx::tc_fence_after();
       }
-      if (ptx::named_bar_or(5, 128 * NG, !ok)) {
+      if (ptx::named_bar_or(5, GT * NG, !ok)) {
         ok = false;
         break;
       }
@@ -940,7 +960,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
             }
           }
         }
-        ptx::named_bar_sync(5, 256);
+        ptx::named_bar_sync(5, GT * NG);
         if (x == 0) {
           const float2 ml = sMl[row];
           if (ml.y != 0.f) {
@@ -955,15 +975,15 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       const bool whole = n == pc.all;
       int c0 = 0, c1 = 0;
       if (!whole) paged_owners<Geo>(total, end - c.left - c.at, pc.all, &c0, &c1);
-      // partials: [slot][NG][HD / 4][128 rows] of four columns, so that a warp's lanes
+      // partials: [slot][NG][HD / 4][GT rows] of four columns, so that a warp's lanes
       // are neighbours in memory
       auto part_of = [&](int cc) { return ((size_t)cc * 2 + (cc == c0)) * NG + x; };
       const size_t slot = part_of(blockIdx.x);
       // The warp's 32 bf16 rows go out through shared memory, so that HD / 8
       // lanes write a row together: in the group's part of Q, or, a lane each, in
       // its row of the joined half, over columns that it has read.
-      uint8_t* stage = sQ + (NG == 2 && nt == 1 ? warp * (S::kTileQ / 2) : warp * (S::kTileQ / 4));
       const int stage_ld = NG == 2 && nt == 1 ? HD * 4 : HD * 2;
+      uint8_t* stage = sQ + warp * 32 * stage_ld;
       auto put = [&](int b, const float (&o)[32], float inv) {    // 32 columns of the row
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1012,40 +1032,40 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           if (whole) {
             put(b, o, inv);
           } else if (live) {
-            float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + 8 * b) * 128 + row;
+            float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + 8 * b) * GT + row;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              __stcg(po + j * 128, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+              __stcg(po + j * GT, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
           }
         }
         if (whole) send();
       }
       ptx::tc_fence_before();
       if (!whole && mine) {
-        if (live) __stcg(p.part_ml + slot * 128 + row, make_float2(M, L));
+        if (live) __stcg(p.part_ml + slot * GT + row, make_float2(M, L));
         __threadfence();
-        ptx::named_bar_sync(1 + x, 128);
+        ptx::named_bar_sync(1 + x, GT);
         if (row == 0) s_last[x] = atomicAdd(p.arrive + NG * c0 + x, 1) == c1 - c0;
-        ptx::named_bar_sync(1 + x, 128);
+        ptx::named_bar_sync(1 + x, GT);
         if (s_last[x]) {
           __threadfence();
           if (row == 0) p.arrive[NG * c0 + x] = 0;            // for the next call
           if (!dead) {
             M = -CUDART_INF_F;
 #pragma unroll 4
-            for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_ml + part_of(cc) * 128 + row).x);
+            for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_ml + part_of(cc) * GT + row).x);
             float o[HD] = {};
             L = 0.f;
-            float2 ml = __ldcg(p.part_ml + part_of(c0) * 128 + row);
+            float2 ml = __ldcg(p.part_ml + part_of(c0) * GT + row);
             for (int cc = c0; cc <= c1; ++cc) {
               const float2 now = ml;
-              if (cc < c1) ml = __ldcg(p.part_ml + part_of(cc + 1) * 128 + row);
+              if (cc < c1) ml = __ldcg(p.part_ml + part_of(cc + 1) * GT + row);
               const float f = now.y != 0.f ? ex2(now.x - M) : 0.f;
               L += f * now.y;
-              const float4* src = reinterpret_cast<const float4*>(p.part_o) + part_of(cc) * (HD / 4) * 128 + row;
+              const float4* src = reinterpret_cast<const float4*>(p.part_o) + part_of(cc) * (HD / 4) * GT + row;
 #pragma unroll
               for (int j = 0; j < HD / 4; ++j) {
-                const float4 v = __ldcg(src + j * 128);
+                const float4 v = __ldcg(src + j * GT);
                 if (now.y != 0.f) {
                   o[4 * j] += f * v.x;
                   o[4 * j + 1] += f * v.y;
@@ -1062,7 +1082,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       }
       it += 2 * kPer * n;
       // the rows on their way out lie where the next tile's queries go
-      ptx::named_bar_sync(5, 128 * NG);
+      ptx::named_bar_sync(5, GT * NG);
     }
     if (!ok) fail();
   }
@@ -1179,7 +1199,7 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
   dflash_status e = DFLASH_OK;
   if (rows <= kRowsS)
     hd == 128 ? launch_small<128>(p, st) : launch_small<64>(p, st);
-  else if (rows <= 128)
+  else if (rows <= Tc<128, 1>::kRows)
     e = hd == 128 ? launch_tc<128, 1>(p, *pages, st) : launch_tc<64, 1>(p, *pages, st);
   else
     e = hd == 128 ? launch_tc<128, 2>(p, *pages, st) : launch_tc<64, 2>(p, *pages, st);
