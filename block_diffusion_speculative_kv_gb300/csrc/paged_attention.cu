@@ -54,14 +54,15 @@ constexpr float kLazy = 8.f;   // a row's reference maximum may lag by this much
 // has no block barrier.  The four states meet when the tile ends.
 // Two CTAs share an SM: one streams while the other begins or ends a tile.
 constexpr int kRowsS = 16, kStepS = 64, kStagesS = 3, kThreadsS = 128, kPerSmS = 2;
-using GeoS = PagedGeo<kRowsS, kStepS, 4>;
+using GeoS = PagedGeo<kRowsS, kStepS, 4, kRowsS>;
 
 template <int HD>
 struct SmallSmem {
   static constexpr int kTile = 16 * HD * 2;                       // 16 keys of K or V
   static constexpr int kRing = 4 * kStagesS * 2 * kTile;
   static constexpr int kBytes = kRing + 4 * 16 * 8 + 16;
-  static_assert(4 * 16 * HD * 4 <= kRing, "the warps' states meet in the idle ring");
+  static constexpr int kLd = HD + 8;                              // of a state's rows: no bank conflicts
+  static_assert(4 * 16 * kLd * 4 <= kRing, "the warps' states meet in the idle ring");
 };
 
 // Any element of a 16-byte chunk of bf16 that is infinite or NaN.
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ring = smem + warp * (kStagesS * 2 * S::kTile);
-  float* sO = reinterpret_cast<float*>(smem);                          // [4][16][HD], in the ring
+  float* sO = reinterpret_cast<float*>(smem);                          // [4][16][kLd], in the ring
   float2* sMl = reinterpret_cast<float2*>(smem + S::kRing);            // [4][16]
   int* sLast = reinterpret_cast<int*>(sMl + 64);
 
@@ -277,60 +278,65 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
       __syncwarp();   // the slot may be loaded again
     }
 
-    // the four warps' states
+    // the four warps' states, of the tile's live rows
+    const int live = min(kRowsS, nG - rho0);
     mmas::cp_async_wait<0>();
     __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      float* dst = sO + (warp * 16 + ra + 8 * h) * HD + cq;
+      if (ra + 8 * h >= live) continue;
+      float* dst = sO + (warp * 16 + ra + 8 * h) * S::kLd + cq;
 #pragma unroll
       for (int nt = 0; nt < kNt; ++nt)
         *reinterpret_cast<float2*>(dst + nt * 8) = make_float2(o[nt][2 * h], o[nt][2 * h + 1]);
       if ((lane & 3) == 0) sMl[warp * 16 + ra + 8 * h] = make_float2(m[h], l[h]);
     }
     __syncthreads();
-    constexpr int kCols = HD / 8;                        // thread: one row, kCols columns
-    const int row = tid >> 3, col0 = (tid & 7) * kCols;
-    float M = -CUDART_INF_F, L = 0.f, acc[kCols] = {};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, sMl[w * 16 + row].x);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float2 ml = sMl[w * 16 + row];
-      if (ml.y == 0.f) continue;                         // this warp saw nothing for the row
-      const float f = ex2(ml.x - M);
-      L += f * ml.y;
-#pragma unroll
-      for (int x = 0; x < kCols; ++x) acc[x] += f * sO[(w * 16 + row) * HD + col0 + x];
-    }
-    const int rho = rho0 + row;
-    auto write = [&]() {
-      if (rho >= nG) return;
+    // a thread takes four columns of a row: HD / 4 neighbours make a row
+    const int items = live * (HD / 4);
+    auto write = [&](int row, int col, const float4& v, float L) {
+      const int rho = rho0 + row;
       const float inv = 1.f / L;                         // a row that saw no key: zeros
-      __nv_bfloat16* dst = p.out + (long long)(rq.row0 + rho / p.G) * p.out_ld +
-                           (long long)(head0 + rho % p.G) * HD + col0;
-#pragma unroll
-      for (int x = 0; x < kCols; x += 8) {
-        uint32_t w4[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w4[e] = L == 0.f ? 0u : mmas::pack_bf16(acc[x + 2 * e] * inv, acc[x + 2 * e + 1] * inv);
-        *reinterpret_cast<uint4*>(dst + x) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-      }
+      *reinterpret_cast<uint2*>(p.out + (long long)(rq.row0 + rho / p.G) * p.out_ld +
+                                (long long)(head0 + rho % p.G) * HD + col) =
+          L == 0.f ? make_uint2(0, 0)
+                   : make_uint2(mmas::pack_bf16(v.x * inv, v.y * inv), mmas::pack_bf16(v.z * inv, v.w * inv));
     };
-    if (n == pc.all) {
-      write();
-    } else {
-      int c0, c1;
-      paged_owners<GeoS>(total, end - c.left - c.at, pc.all, &c0, &c1);
-      const size_t slot = (size_t)blockIdx.x * 2 + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0);
-      float* po = p.part_o + (slot * kRowsS + row) * HD + col0;
+    auto add = [](float4& a, float f, const float4& v) {
+      a.x += f * v.x;
+      a.y += f * v.y;
+      a.z += f * v.z;
+      a.w += f * v.w;
+    };
+    const bool whole = n == pc.all;
+    int c0 = 0, c1 = 0;
+    if (!whole) paged_owners<GeoS>(c, total, end - c.left - c.at, pc.all, &c0, &c1);
+    const int bid = blockIdx.x;
+    const size_t slot = (size_t)bid * 2 + (bid == c0 ? 1 : 0);
+    for (int i = tid; i < items; i += kThreadsS) {
+      const int row = i / (HD / 4), col = i % (HD / 4) * 4;
+      float M = -CUDART_INF_F, L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int x = 0; x < kCols; x += 4)
-        *reinterpret_cast<float4*>(po + x) = make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
-      if ((tid & 7) == 0) p.part_ml[slot * kRowsS + row] = make_float2(M, L);
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, sMl[w * 16 + row].x);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 ml = sMl[w * 16 + row];
+        if (ml.y == 0.f) continue;                       // this warp saw nothing for the row
+        const float f = ex2(ml.x - M);
+        L += f * ml.y;
+        add(acc, f, *reinterpret_cast<const float4*>(sO + (w * 16 + row) * S::kLd + col));
+      }
+      if (whole) {
+        write(row, col, acc, L);
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (slot * kRowsS + row) * HD + col) = acc;
+        if (col == 0) p.part_ml[slot * kRowsS + row] = make_float2(M, L);
+      }
+    }
+    if (!whole) {
       __threadfence();
       __syncthreads();
       if (tid == 0) *sLast = atomicAdd(p.arrive + c0, 1) == c1 - c0;
@@ -343,30 +349,35 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
         const int parts = c1 - c0 + 1;
         for (int i = tid; i < parts * kRowsS; i += kThreadsS) {
           const int cc = c0 + i / kRowsS;
-          sPart[i] = __ldcg(p.part_ml + ((size_t)cc * 2 + (cc == c0)) * kRowsS + i % kRowsS);
+          sPart[i] = i % kRowsS < live
+                         ? __ldcg(p.part_ml + ((size_t)cc * 2 + (cc == c0)) * kRowsS + i % kRowsS)
+                         : make_float2(-CUDART_INF_F, 0.f);
         }
         __syncthreads();
-        M = -CUDART_INF_F;
-        for (int i = 0; i < parts; ++i) M = fmaxf(M, sPart[i * kRowsS + row].x);
-        L = 0.f;
+        for (int i = tid; i < items; i += kThreadsS) {
+          const int row = i / (HD / 4), col = i % (HD / 4) * 4;
+          float M = -CUDART_INF_F, L = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < parts; ++k) M = fmaxf(M, sPart[k * kRowsS + row].x);
+          for (int k0 = 0; k0 < parts; k0 += 8) {        // eight loads in flight
+            float4 v[8];
 #pragma unroll
-        for (int x = 0; x < kCols; ++x) acc[x] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-          const float2 ml = sPart[i * kRowsS + row];
-          const size_t s2 = ((size_t)(c0 + i) * 2 + (i == 0)) * kRowsS + row;
-          const float f = ml.y == 0.f ? 0.f : ex2(ml.x - M);
-          L += f * ml.y;
+            for (int k = 0; k < 8; ++k) {
+              const int cc = c0 + min(k0 + k, parts - 1);
+              v[k] = __ldcg(reinterpret_cast<const float4*>(
+                  p.part_o + (((size_t)cc * 2 + (cc == c0)) * kRowsS + row) * HD + col));
+            }
 #pragma unroll
-          for (int x = 0; x < kCols; x += 4) {
-            const float4 v4 = __ldcg(reinterpret_cast<const float4*>(p.part_o + s2 * HD + col0 + x));
-            acc[x] += f * v4.x;
-            acc[x + 1] += f * v4.y;
-            acc[x + 2] += f * v4.z;
-            acc[x + 3] += f * v4.w;
+            for (int k = 0; k < 8; ++k) {
+              const float2 ml = sPart[min(k0 + k, parts - 1) * kRowsS + row];
+              if (k0 + k >= parts || ml.y == 0.f) continue;
+              const float f = ex2(ml.x - M);
+              L += f * ml.y;
+              add(acc, f, v[k]);
+            }
           }
+          write(row, col, acc, L);
         }
-        write();
       }
     }
     __syncthreads();                                     // the ring is free again
@@ -425,7 +436,7 @@ struct Tc {
   static constexpr int kGroup = NG == 2 ? 128 : 64;         // rows, and threads, of a softmax group
   static constexpr int kRows = kGroup * NG, kWarps = kRows / 32;
   static constexpr int kThreads = NG == 2 ? 384 : 128, kPerSm = NG == 2 ? 1 : 2;
-  using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 4 : 3>;
+  using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 8 : 3, 128>;
   static constexpr int kAtomQ = kGroup * 128;               // 64 columns of a group's rows of Q
   static constexpr int kTileQ = (HD / 64) * kAtomQ;
   static constexpr int kKeys = NG == 2 ? 128 : 64;          // of a ring slot
@@ -749,6 +760,40 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       const int plain_t = min(rq.masked ? rq.p0 : rq.p0 + tile0 / p.G + 1, kend);
       const bool dead = rho0 + wg * 32 >= nG;        // no live row in this warp
       float m_ref = -CUDART_INF_F, l = 0.f;
+      // A step's P V ran with zeros for values that are not finite.  Once it is done
+      // (the next scores are, or pv_done), a row that sees such a key takes the value
+      // itself: times any weight it is the same inf or NaN.
+      int late = -1;                                         // first key of that step, or none
+      volatile uint32_t* late_note = odd_keys;
+      uint32_t late_seen[4];
+      auto repair = [&]() {
+        if (late < 0 || dead) return;
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          uint32_t keys = late_note[b];
+          const uint32_t sees = b == 0 ? late_seen[0] : b == 1 ? late_seen[1] : b == 2 ? late_seen[2] : late_seen[3];
+          while (keys) {                                     // warp-uniform
+            const int j = __ffs(keys) - 1;
+            keys &= keys - 1;
+            const int key = late + 32 * b + j, page = page_of(p.pv, c.r, key);
+            if (page < 0) continue;
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.pv.v) + pool_row(p.pv, page, c.g, key) * HD;
+            const bool see = (sees >> j) & 1u;
+#pragma unroll 1
+            for (int cb = 0; cb < HD / 16; ++cb) {
+              float o[16];
+              ptx::tmem_ld_32x16(aO + 16 * cb, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float val = __bfloat162float(v[16 * cb + e]);
+                if (see && !(fabsf(val) <= CUDART_MAX_NORMAL_F)) o[e] += val;
+              }
+              ptx::tmem_st_32x16(aO + 16 * cb, o);
+              ptx::tmem_wait_st();
+            }
+          }
+        }
+      };
       // (after a wait has run out the loop only keeps the group's barriers company)
       for (int i = 0; i < jobs; ++i, ++nj) {
         const int t = NG == 1 || nt == 2 ? i : 2 * i + x, key0 = (pc.first + t) * kStepT;
@@ -759,6 +804,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         const bool early = !check && !dead;                  // P goes out in two halves
         if (ok && !dead) {
           ptx::tc_fence_after();
+          if (late >= 0) repair();
           const bool cut = key0 + kStepT > plain_w;          // some key is hidden from some row
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
@@ -894,48 +940,18 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           if (!early) ptx::mbar_arrive(&p_ready[2 * x]);
           ptx::mbar_arrive(&p_ready[2 * x + 1]);
         }
-        if (nt == 2 && x == 1 && key0 + kStepT > plain_t) odd = true;   // group 0 noted them
-        if (odd && ok) {
-          // P V ran with zeros for the bad values: a row that sees such a key takes
-          // the value itself now (times any weight it is the same inf or NaN)
-          ok = __all_sync(0xffffffffu, wait(&pv_done[x], nj & 1u));
-          if (ok && !dead) {
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-              uint32_t keys = noted[b];
-              const uint32_t sees = b == 0 ? seen[0] : b == 1 ? seen[1] : b == 2 ? seen[2] : seen[3];
-              while (keys) {                                 // warp-uniform
-                const int j = __ffs(keys) - 1;
-                keys &= keys - 1;
-                const int key = key0 + 32 * b + j, page = page_of(p.pv, c.r, key);
-                if (page < 0) continue;
-                const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.pv.v) +
-                                         pool_row(p.pv, page, c.g, key) * HD;
-                const bool see = (sees >> j) & 1u;
-#pragma unroll 1
-                for (int cb = 0; cb < HD / 32; ++cb) {
-                  uint32_t o[32];
-                  ptx::tmem_ld_32x32(aO + 32 * cb, o);
-                  ptx::tmem_wait_ld();
+        // (group 0 noted them for both)
+        late = odd || (nt == 2 && x == 1 && key0 + kStepT > plain_t) ? key0 : -1;
+        if (late >= 0) {
+          late_note = noted;
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    const float val = __bfloat162float(v[32 * cb + e]);
-                    if (see && !(fabsf(val) <= CUDART_MAX_NORMAL_F))
-                      o[e] = __float_as_uint(__uint_as_float(o[e]) + val);
-                  }
-                  ptx::tmem_st_32x32(aO + 32 * cb, o);
-                  ptx::tmem_wait_st();
-                }
-              }
-            }
-            ptx::tc_fence_before();
-          }
+          for (int b = 0; b < 4; ++b) late_seen[b] = seen[b];
         }
       }
       if (ok && jobs > 0) {
         ok = __all_sync(0xffffffffu, wait(&pv_done[x], (nj - 1) & 1u));
         if (ok) ptx::tc_fence_after();
+        if (ok) repair();
       }
       if (ptx::named_bar_or(5, GT * NG, !ok)) {
         ok = false;
@@ -974,7 +990,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       const bool mine = nt == 2 || x == 0;                   // this group writes its rows
       const bool whole = n == pc.all;
       int c0 = 0, c1 = 0;
-      if (!whole) paged_owners<Geo>(total, end - c.left - c.at, pc.all, &c0, &c1);
+      if (!whole) paged_owners<Geo>(c, total, end - c.left - c.at, pc.all, &c0, &c1);
       // partials: [slot][NG][HD / 4][GT rows] of four columns, so that a warp's lanes
       // are neighbours in memory
       auto part_of = [&](int cc) { return ((size_t)cc * 2 + (cc == c0)) * NG + x; };

@@ -27,11 +27,15 @@ struct PagedAttnParams {
   int* status;
 };
 
-// Geometry of a kernel's work: TR query rows to a tile, KS keys to a step, and TC,
-// what beginning and ending a tile costs, in steps (it only weighs the shares).
-template <int TR_, int KS_, int TC_>
+// Geometry of a kernel's work: TR query rows to a tile, KS keys to a step.  What a
+// tile weighs when the work is shared out: TC for its beginning and end, and for
+// each step 1, or 2 where the tile has more than HALF rows.
+template <int TR_, int KS_, int TC_, int HALF_>
 struct PagedGeo {
-  static constexpr int TR = TR_, KS = KS_, TC = TC_;
+  static constexpr int TR = TR_, KS = KS_, TC = TC_, HALF = HALF_;
+  // Shares are whole multiples of the largest weight: every CTA between the first
+  // and the last of a tile then holds a step of it.
+  static constexpr int UNIT = HALF_ < TR_ ? 2 : 1;
 };
 
 // One request of the flattened work.  Its n rows and G heads of a KV head make
@@ -56,14 +60,18 @@ struct PagedReq {
     const int last = masked ? n - 1 : min(j * Geo::TR + Geo::TR - 1, n * G - 1) / G;
     return min(p0 + last + 1, cap);
   }
+  template <typename Geo>
+  __device__ __forceinline__ int weight(int j, int G) const {
+    return min(n * G - j * Geo::TR, Geo::TR) > Geo::HALF ? 2 : 1;
+  }
   // length of a tile, and of tiles [0, j1) of one KV head, on the line
   template <typename Geo>
   __device__ __forceinline__ int length(int j, int G) const {
-    return Geo::TC + (key_end<Geo>(j, G) + Geo::KS - 1) / Geo::KS;
+    return Geo::TC + (key_end<Geo>(j, G) + Geo::KS - 1) / Geo::KS * weight<Geo>(j, G);
   }
   template <typename Geo>
   __device__ __forceinline__ long long lengths(int j1, int G) const {
-    if (masked) return (long long)j1 * length<Geo>(0, G);
+    if (masked && j1 > 0) return (long long)(j1 - 1) * length<Geo>(0, G) + length<Geo>(j1 - 1, G);
     long long s = 0;
     for (int j = 0; j < j1; ++j) s += length<Geo>(j, G);
     return s;
@@ -72,10 +80,10 @@ struct PagedReq {
 
 // A CTA's place on the line: requests, then KV heads, then query tiles, then, for
 // each tile, TC units of overhead and its key steps.  The CTA's share is one
-// stretch of the line.
+// stretch of the line; a step is its whose stretch holds the step's beginning.
 struct PagedCursor {
   int r, g, j;             // request, KV head, tile
-  int at, length;          // place in the tile, its length
+  int at, length, weight;  // place in the tile, its length, a step's weight
   long long left;          // what is left of the share
   PagedReq rq;
 };
@@ -88,9 +96,10 @@ struct PagedPiece {
   __device__ __forceinline__ static PagedPiece of(const PagedCursor& c) {
     PagedPiece p;
     p.used = static_cast<int>(min((long long)(c.length - c.at), c.left));
-    p.all = c.length - Geo::TC;
-    p.first = max(c.at - Geo::TC, 0);
-    p.n = max(c.at + p.used - Geo::TC, 0) - p.first;
+    auto steps = [&](int at) { return at <= Geo::TC ? 0 : (at - Geo::TC + c.weight - 1) / c.weight; };
+    p.all = steps(c.length);
+    p.first = steps(c.at);
+    p.n = steps(c.at + p.used) - p.first;
     return p;
   }
 };
@@ -101,13 +110,16 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {
   return a / b;
 }
 // Share of CTA c of `grid`: [paged_share(c), paged_share(c + 1)).
+template <typename Geo>
 __device__ __forceinline__ long long paged_share(long long total, int c, int grid) {
-  const long long q = div_pos(total, grid);
-  return q * c + min((long long)c, total - q * grid);
+  const long long units = (total + Geo::UNIT - 1) / Geo::UNIT, q = div_pos(units, grid);
+  return min((q * c + min((long long)c, units - q * grid)) * Geo::UNIT, total);
 }
-// The CTA whose share holds step s.
+// The CTA whose share holds place s of the line.
+template <typename Geo>
 __device__ __forceinline__ int paged_owner(long long total, long long s, int grid) {
-  const long long q = div_pos(total, grid), m = total - q * grid;
+  const long long units = (total + Geo::UNIT - 1) / Geo::UNIT, q = div_pos(units, grid), m = units - q * grid;
+  s /= Geo::UNIT;
   return static_cast<int>(s < m * (q + 1) ? div_pos(s, q + 1) : m + div_pos(s - m * (q + 1), q));
 }
 
@@ -122,7 +134,7 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, l
     q->load(p, r);
     return q->lengths<Geo>(q->tiles<Geo>(p.G), p.G) * p.pv.n_kv;
   };
-  PagedReq q;
+  PagedReq q = {};
   const long long first = length_of(lane, &q);             // of the first 32 requests
   long long total = 0;
   for (int r0 = 0; r0 < p.n_req; r0 += 32) {
@@ -131,8 +143,8 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, l
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     total += s;
   }
-  const long long begin = paged_share(total, blockIdx.x, grid);
-  const long long end = paged_share(total, blockIdx.x + 1, grid);
+  const long long begin = paged_share<Geo>(total, blockIdx.x, grid);
+  const long long end = paged_share<Geo>(total, blockIdx.x + 1, grid);
   *total_out = total;
   *end_out = end;
   c->left = end - begin;
@@ -152,7 +164,16 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, l
       const long long excl = __shfl_sync(0xffffffffu, inc - s, l);
       const long long per_g = div_pos(__shfl_sync(0xffffffffu, s, l), p.pv.n_kv);
       c->r = r0 + l;
-      c->rq.load(p, c->r);
+      if (r0 == 0 && p.n_req <= 32) {                      // (q is still of these requests)
+        c->rq = q;
+        c->rq.row0 = __shfl_sync(0xffffffffu, q.row0, l);
+        c->rq.n = __shfl_sync(0xffffffffu, q.n, l);
+        c->rq.p0 = __shfl_sync(0xffffffffu, q.p0, l);
+        c->rq.cap = p.pv.table_ld << p.pv.page_shift;
+        c->rq.masked = p.mask != nullptr;
+      } else {
+        c->rq.load(p, c->r);
+      }
       long long rem = begin - before - excl;
       c->g = static_cast<int>(div_pos(rem, per_g));
       rem -= (long long)c->g * per_g;
@@ -166,6 +187,7 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, l
       c->j = j;
       c->at = static_cast<int>(rem);
       c->length = len;
+      c->weight = c->rq.weight<Geo>(j, p.G);
       return;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
@@ -189,13 +211,15 @@ __device__ __forceinline__ void paged_next(const PagedAttnParams& p, const Paged
   }
   c->at = 0;
   c->length = c->rq.length<Geo>(c->j, p.G);
+  c->weight = c->rq.weight<Geo>(c->j, p.G);
 }
 
-// The CTAs of a tile that begins at `tile0` on the line and has `all` steps.
+// The CTAs that hold the steps of the cursor's tile, which begins at `tile0`.
 template <typename Geo>
-__device__ __forceinline__ void paged_owners(long long total, long long tile0, int all, int* c0, int* c1) {
-  *c0 = paged_owner(total, tile0 + Geo::TC, gridDim.x);
-  *c1 = paged_owner(total, tile0 + Geo::TC + all - 1, gridDim.x);
+__device__ __forceinline__ void paged_owners(const PagedCursor& c, long long total, long long tile0, int all,
+                                             int* c0, int* c1) {
+  *c0 = paged_owner<Geo>(total, tile0 + Geo::TC, gridDim.x);
+  *c1 = paged_owner<Geo>(total, tile0 + Geo::TC + (long long)(all - 1) * c.weight, gridDim.x);
 }
 
 }  // namespace dfl
