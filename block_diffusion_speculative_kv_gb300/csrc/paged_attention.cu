@@ -436,7 +436,7 @@ struct Tc {
   static constexpr int kGroup = NG == 2 ? 128 : 64;         // rows, and threads, of a softmax group
   static constexpr int kRows = kGroup * NG, kWarps = kRows / 32;
   static constexpr int kThreads = NG == 2 ? 384 : 128, kPerSm = NG == 2 ? 1 : 2;
-  using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 8 : 3, 128>;
+  using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 12 : 3, 128>;
   static constexpr int kAtomQ = kGroup * 128;               // 64 columns of a group's rows of Q
   static constexpr int kTileQ = (HD / 64) * kAtomQ;
   static constexpr int kKeys = NG == 2 ? 128 : 64;          // of a ring slot
@@ -1017,7 +1017,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
             p.out + (long long)(rq.row0 + tok) * p.out_ld + (long long)head * HD);
         const unsigned on = __ballot_sync(0xffffffffu, live);
         constexpr int kLines = 256 / HD;
-#pragma unroll 4
+#pragma unroll 8
         for (int r0 = 0; r0 < 32; r0 += kLines) {
           const int rr = r0 + lane / (HD / 8), ch = lane % (HD / 8);
           uint4* to = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, mine_to, rr)) + ch;
@@ -1027,7 +1027,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       };
       if (mine && !dead) {
         const float inv = 1.f / L;
-#pragma unroll 1
+#pragma unroll 2
         for (int b = 0; b < HD / 32; ++b) {
           uint32_t u[32];
           ptx::tmem_ld_32x32(aO + 32 * b, u);

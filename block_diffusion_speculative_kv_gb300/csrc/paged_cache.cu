@@ -9,8 +9,14 @@
 // (latency, for the rows of one decoding step).  A thread holds 8 elements of
 // the first half of a head and their partners of the second, two 16-byte loads
 // (bf16), so hd / 16 lanes share a head and the sum of squares is a shuffle
-// over them.  A row's cosines and sines (64-bit angles, rope_cs) are formed
-// once by the CTA and shared by all its heads, while the loads are in flight.
+// over them.  It asks for all its heads of a batch of rows before it works on
+// the first: one head at a time left HBM half idle.  A batch's cosines and sines
+// are formed once by the CTA, while the loads are in flight.  Angles are whole
+// numbers: a frequency is kept as turns per position, a 64-bit fraction, so p f_i
+// modulo a turn is one 64-bit product whose overflow is the reduction (off by
+// p 2^-64 turns and the frequency's 53 bits).
+#include <cmath>
+
 #include "kernels.h"
 #include "paged.cuh"
 
@@ -39,185 +45,327 @@ dflash_status check_pages(const dflash_pages* p, const char* what, PagedView* ou
 
 namespace {
 
-// Eight consecutive elements as fp32; VEC: the address is 16-byte aligned.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (VEC && sizeof(T) == 2) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else if constexpr (VEC) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32<T>(p[i]);
+// Rotary frequencies theta^(-2i/head_dim) in turns, times 2^64.
+struct RopeTurns {
+  uint64_t f[64];
+};
+RopeTurns rope_turns(float theta, int head_dim) {
+  const RopeFreqs fr = rope_freqs(theta, head_dim);
+  RopeTurns t{};
+  for (int i = 0; i < head_dim / 2; ++i)
+  {
+    const double turns = fr.f[i] / 6.283185307179586476925;
+    t.f[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));   // whole turns are none
   }
+  return t;
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-  if constexpr (VEC && sizeof(T) == 2) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else if constexpr (VEC) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = from_f32<T>(x[i]);
-  }
+// (cos, sin) at a position >= 0.
+__device__ __forceinline__ float2 turn_cs(int pos, uint64_t f) {
+  const uint64_t a = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * f;
+  // signed half turns in [-1, 1)
+  const float x = static_cast<float>(static_cast<int32_t>(a >> 32)) * 4.656612873077392578125e-10f;   // 2^-31
+  float s, c;
+  sincospif(x, &s, &c);
+  return make_float2(c, s);
 }
 
-__device__ __forceinline__ void rotate8(float (&a)[8], float (&b)[8], const float2* cs) {
+// Eight consecutive elements as they lie in memory.  VEC: 16-byte aligned.
+template <typename T>
+struct Eight {
+  uint4 u[sizeof(T) / 2];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 c = cs[i];
-    const float x = a[i], y = b[i];
-    a[i] = x * c.x - y * c.y;
-    b[i] = y * c.x + x * c.y;
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+      T* t = reinterpret_cast<T*>(u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = p[i];
+    }
   }
+  template <bool VEC>
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+    } else {
+      const T* t = reinterpret_cast<const T*>(u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = t[i];
+    }
+  }
+  // as four pairs, for the packed fp32 instructions
+  __device__ __forceinline__ void get(float2 (&x)[4]) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    } else {
+      const float2* t = reinterpret_cast<const float2*>(u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = t[i];
+    }
+  }
+  __device__ __forceinline__ void set(const float2 (&x)[4]) {
+    if constexpr (sizeof(T) == 2) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[i].x, x[i].y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      float2* t = reinterpret_cast<float2*>(u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = x[i];
+    }
+  }
+};
+
+// The cosines and sines of a row, laid out so that the lanes of a head read 16-byte
+// pieces (two cosines, two sines) next to one another: entry i belongs to lane i / 8.
+template <int HD>
+struct Turns {
+  float4 v[4][HD / 16];
+  __device__ __forceinline__ void put(int i, float2 c) {
+    float* p = reinterpret_cast<float*>(&v[(i & 7) >> 1][i >> 3]) + (i & 1);
+    p[0] = c.x;
+    p[2] = c.y;
+  }
+  __device__ __forceinline__ void rotate(float2 (&a)[4], float2 (&b)[4], int sub) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 c = v[j][sub];
+      const float2 cc = make_float2(c.x, c.y), ss = make_float2(c.z, c.w), ms = make_float2(-c.z, -c.w);
+      const float2 x = a[j];
+      a[j] = __ffma2_rn(x, cc, __fmul2_rn(b[j], ms));
+      b[j] = __ffma2_rn(b[j], cc, __fmul2_rn(x, ss));
+    }
+  }
+};
+
+// i / n for 0 <= i < 2^31 / n, with m = divide_by(n).
+struct DivideBy {
+  uint32_t n, m;
+  __device__ __forceinline__ int operator()(int i) const {
+    return n == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), m));
+  }
+};
+DivideBy divide_by(int n) {
+  return DivideBy{static_cast<uint32_t>(n), static_cast<uint32_t>(((1ull << 32) + n - 1) / n)};
 }
+
+constexpr int kThreads = 256;
+// Rows of a CTA: several where there are enough of them to fill the SMs, one
+// otherwise, for latency.  Measured with 32 + 8 heads of 128, bf16: norm and rotation
+// of 512 rows 5.0 us one to a CTA and 7.2 us eight to a CTA, of 1024 rows 8.2 and
+// 7.2, of 8197 rows 58.7 and 30.0 (5.6 TB/s); the append of 8 heads 3.2 and 3.8, 4.7
+// and 4.0, 24.8 and 14.9.
+constexpr int kNormRows = 8, kAppendRows = 8;
 
 struct NormRopeParams {
-  int n_q, n_kv;
+  int n_rows, n_q, n_kv;
+  DivideBy by_q, by_kv;
   const void *q_gain, *k_gain;
   float eps;
   int rotate;
-  RopeFreqs fr;
+  RopeTurns fr;
   const int32_t* pos;
   const void *q, *k;
   void *q_out, *k_out;
   long long q_ld, k_ld, q_out_ld, k_out_ld;
 };
 
-// One CTA per row.  Lanes of a head: HD / 16, so a warp's shuffle groups never
-// straddle heads; the block is a whole number of warps and idle lanes take part
-// in the shuffles.
-template <typename T, int HD, bool VEC>
-__global__ void qk_norm_rope_kernel(const NormRopeParams p) {
-  constexpr int kLanes = HD / 16, kHalf = HD / 2;
-  __shared__ float2 cs[kHalf];
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const int sub = tid % kLanes, heads = p.n_q + p.n_kv;
+// ROWS rows to a CTA, queries then keys; an item is a row's head, HD / 16 lanes to it
+// (a warp's shuffle groups never straddle items, and lanes without one take part in
+// the shuffles).
+template <typename T, int HD, bool VEC, int ROWS>
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const NormRopeParams p) {
+  constexpr int kLanes = HD / 16, kHalf = HD / 2, kItems = kThreads / kLanes;
+  constexpr int kBatch = 2;
+  __shared__ Turns<HD> cs[ROWS];
+  __shared__ int pos[ROWS];
+  const int row0 = blockIdx.x * ROWS, tid = threadIdx.x, sub = tid % kLanes;
+  const int rows = min(ROWS, p.n_rows - row0);
   pdl_wait();
   pdl_trigger();
-  const int pos = p.pos ? p.pos[row] : 0;
-  if (pos < 0) return;
-  for (int h0 = 0; h0 < heads; h0 += blockDim.x / kLanes) {
-    const int h = h0 + tid / kLanes;
-    const bool live = h < heads, is_q = h < p.n_q;
-    const T* src = nullptr;
-    T* dst = nullptr;
-    if (live) {
-      const long long col = (long long)(is_q ? h : h - p.n_q) * HD + 8 * sub;
-      src = static_cast<const T*>(is_q ? p.q : p.k) + row * (is_q ? p.q_ld : p.k_ld) + col;
-      dst = static_cast<T*>(is_q ? p.q_out : p.k_out) + row * (is_q ? p.q_out_ld : p.k_out_ld) + col;
-    }
-    float a[8] = {}, b[8] = {};
-    if (live) {
-      load8<T, VEC>(src, a);
-      load8<T, VEC>(src + kHalf, b);
-    }
-    if (h0 == 0 && p.rotate) {
-      for (int i = tid; i < kHalf; i += blockDim.x) cs[i] = rope_cs(pos, i, p.fr);
-      __syncthreads();
-    }
-    const T* gain = static_cast<const T*>(is_q ? p.q_gain : p.k_gain);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-    for (int off = kLanes / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (!live) continue;
+  bool turned = false;
+  auto part = [&](int heads, DivideBy by_heads, const void* in, long long ld, void* out, long long out_ld,
+                  const void* gain) {
+    const int items = rows * heads;
+    if (items == 0) return;                                // block-uniform
+    Eight<T> g[2] = {};
     if (gain) {
-      const float inv = 1.f / sqrtf(ss * (1.f / HD) + p.eps);
+      g[0].template load<VEC>(static_cast<const T*>(gain) + 8 * sub);
+      g[1].template load<VEC>(static_cast<const T*>(gain) + kHalf + 8 * sub);
+    }
+    for (int i0 = 0; i0 < items; i0 += kBatch * kItems) {  // block-uniform
+      Eight<T> a[kBatch], b[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] *= inv * to_f32<T>(gain[8 * sub + i]);
-        b[i] *= inv * to_f32<T>(gain[kHalf + 8 * sub + i]);
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kItems + tid / kLanes, r = by_heads(i);
+        if (i >= items) continue;
+        const T* src = static_cast<const T*>(in) + (row0 + r) * ld + (i - r * heads) * HD + 8 * sub;
+        a[k].template load<VEC>(src);
+        b[k].template load<VEC>(src + kHalf);
+      }
+      if (!turned) {
+        turned = true;
+        for (int i = tid; i < ROWS * kHalf; i += kThreads) {
+          const int r = i / kHalf, at = r < rows && p.pos ? p.pos[row0 + r] : 0;
+          if (i % kHalf == 0) pos[r] = at;
+          if (p.rotate) cs[r].put(i % kHalf, turn_cs(at, p.fr.f[i % kHalf]));
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kItems + tid / kLanes, r = by_heads(i);
+        const bool live = i < items && pos[r] >= 0;
+        float2 x[4] = {}, y[4] = {};
+        if (live) {
+          a[k].get(x);
+          b[k].get(y);
+        }
+        if (gain) {                                        // block-uniform
+          float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(x[j], x[j], __ffma2_rn(y[j], y[j], s2));
+          float ss = s2.x + s2.y;
+#pragma unroll
+          for (int off = kLanes / 2; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          const float inv = rsqrtf(ss * (1.f / HD) + p.eps);
+          const float2 inv2 = make_float2(inv, inv);
+          float2 gx[4], gy[4];
+          g[0].get(gx);
+          g[1].get(gy);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] = __fmul2_rn(__fmul2_rn(x[j], inv2), gx[j]);
+            y[j] = __fmul2_rn(__fmul2_rn(y[j], inv2), gy[j]);
+          }
+        }
+        if (!live) continue;
+        if (p.rotate) cs[r].rotate(x, y, sub);
+        a[k].set(x);
+        b[k].set(y);
+        T* dst = static_cast<T*>(out) + (row0 + r) * out_ld + (i - r * heads) * HD + 8 * sub;
+        a[k].template store<VEC>(dst);
+        b[k].template store<VEC>(dst + kHalf);
       }
     }
-    if (p.rotate) rotate8(a, b, cs + 8 * sub);
-    store8<T, VEC>(dst, a);
-    store8<T, VEC>(dst + kHalf, b);
-  }
+  };
+  // (a single row's queries and keys go to two CTAs, at once)
+  if (ROWS > 1 || blockIdx.y == 0) part(p.n_q, p.by_q, p.q, p.q_ld, p.q_out, p.q_out_ld, p.q_gain);
+  if (ROWS > 1 || blockIdx.y == 1) part(p.n_kv, p.by_kv, p.k, p.k_ld, p.k_out, p.k_out_ld, p.k_gain);
 }
 
 struct AppendParams {
   PagedView pv;
   int n_req, n_rows;
+  DivideBy by_heads;
   const int32_t *row_off, *pos0, *pos;
   const void *k, *v;
   long long kv_ld;
   int rotate;
-  RopeFreqs fr;
+  RopeTurns fr;
 };
 
-// One CTA per row: K's heads, then V's, HD / 16 lanes each.
-template <typename T, int HD, bool VEC>
-__global__ void paged_append_kernel(const AppendParams p) {
-  constexpr int kLanes = HD / 16, kHalf = HD / 2;
-  __shared__ float2 cs[kHalf];
-  const int row = blockIdx.x, tid = threadIdx.x, sub = tid % kLanes;
+// ROWS rows to a CTA, whose places in the pool its warps find first; an item is a
+// row's K head or V head.
+template <typename T, int HD, bool VEC, int ROWS>
+__global__ void __launch_bounds__(kThreads, 3) paged_append_kernel(const AppendParams p) {
+  constexpr int kLanes = HD / 16, kHalf = HD / 2, kItems = kThreads / kLanes;
+  constexpr int kBatch = 2;
+  __shared__ Turns<HD> cs[ROWS];
+  __shared__ long long place[ROWS];                        // pool row of KV head 0, or -1
+  __shared__ int position[ROWS];
+  const int row0 = blockIdx.x * ROWS, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = tid % kLanes;
+  const int heads = 2 * p.pv.n_kv, items = min(ROWS, p.n_rows - row0) * heads;
   pdl_wait();
   pdl_trigger();
-  const int req = request_of(p.row_off, p.n_req, row, tid & 31);
-  if (req >= p.n_req || row < p.row_off[req]) return;
-  const int slot = p.pos0[req] + (row - p.row_off[req]);
-  const int pos = p.pos ? p.pos[row] : slot;
-  if (pos < 0) return;
-  const int page = page_of(p.pv, req, slot);
-  if (page < 0) return;
-  for (int h0 = 0; h0 < 2 * p.pv.n_kv; h0 += blockDim.x / kLanes) {
-    const int h = h0 + tid / kLanes;
-    const bool live = h < 2 * p.pv.n_kv, is_k = h < p.pv.n_kv;
-    const int g = is_k ? h : h - p.pv.n_kv;
-    float a[8] = {}, b[8] = {};
-    if (live) {
-      const T* src = static_cast<const T*>(is_k ? p.k : p.v) + row * p.kv_ld + (long long)g * HD + 8 * sub;
-      load8<T, VEC>(src, a);
-      load8<T, VEC>(src + kHalf, b);
+  auto load = [&](int i, Eight<T>& a, Eight<T>& b) {
+    const int r = p.by_heads(i), h = i - r * heads;
+    const bool is_k = h < p.pv.n_kv;
+    const T* src = static_cast<const T*>(is_k ? p.k : p.v) + (row0 + r) * p.kv_ld +
+                   (long long)(is_k ? h : h - p.pv.n_kv) * HD + 8 * sub;
+    a.template load<VEC>(src);
+    b.template load<VEC>(src + kHalf);
+  };
+  for (int i0 = 0; i0 < items; i0 += kBatch * kItems) {    // block-uniform
+    Eight<T> a[kBatch], b[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kItems + tid / kLanes;
+      if (i < items) load(i, a[k], b[k]);
     }
-    if (h0 == 0 && p.rotate) {
-      for (int i = tid; i < kHalf; i += blockDim.x) cs[i] = rope_cs(pos, i, p.fr);
+    if (i0 == 0) {
+      for (int r = warp; r < ROWS; r += kThreads / 32) {
+        const int row = row0 + r;
+        long long at = -1;
+        int pos = 0;
+        if (row < p.n_rows) {
+          const int req = request_of(p.row_off, p.n_req, row, lane);
+          if (req < p.n_req && row >= p.row_off[req]) {
+            const int slot = p.pos0[req] + (row - p.row_off[req]);
+            pos = p.pos ? p.pos[row] : slot;
+            const int page = pos < 0 ? -1 : page_of(p.pv, req, slot);
+            if (page >= 0) at = pool_row(p.pv, page, 0, slot);
+          }
+        }
+        if (lane == 0) {
+          place[r] = at;
+          position[r] = pos;
+        }
+      }
       __syncthreads();
+      if (p.rotate) {
+        for (int i = tid; i < ROWS * kHalf; i += kThreads)
+          cs[i / kHalf].put(i % kHalf, turn_cs(position[i / kHalf], p.fr.f[i % kHalf]));
+        __syncthreads();
+      }
     }
-    if (!live) continue;
-    if (is_k && p.rotate) rotate8(a, b, cs + 8 * sub);
-    T* dst = static_cast<T*>(is_k ? p.pv.k : p.pv.v) + pool_row(p.pv, page, g, slot) * HD + 8 * sub;
-    store8<T, true>(dst, a);
-    store8<T, true>(dst + kHalf, b);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kItems + tid / kLanes, r = p.by_heads(i), h = i - r * heads;
+      if (i >= items || place[r] < 0) continue;
+      const bool is_k = h < p.pv.n_kv;
+      if (is_k && p.rotate) {
+        float2 x[4], y[4];
+        a[k].get(x);
+        b[k].get(y);
+        cs[r].rotate(x, y, sub);
+        a[k].set(x);
+        b[k].set(y);
+      }
+      const long long row = place[r] + ((long long)(is_k ? h : h - p.pv.n_kv) << p.pv.page_shift);
+      T* dst = static_cast<T*>(is_k ? p.pv.k : p.pv.v) + row * HD + 8 * sub;
+      a[k].template store<true>(dst);
+      b[k].template store<true>(dst + kHalf);
+    }
   }
 }
 
-template <typename T, int HD>
-void launch_norm_rope(const NormRopeParams& p, int n_rows, bool vec, cudaStream_t st) {
-  const int lanes = (p.n_q + p.n_kv) * (HD / 16);
-  const int threads = lanes < 512 ? (lanes + 31) / 32 * 32 : 512;
-  if (vec)
-    launch_k(qk_norm_rope_kernel<T, HD, true>, dim3(n_rows), dim3(threads), 0, st, p);
+bool many(int rows) { return rows >= 6 * num_sms(); }
+
+template <typename T, int HD, bool VEC>
+void launch_norm_rope(const NormRopeParams& p, cudaStream_t st) {
+  if (many(p.n_rows))
+    launch_k(qk_norm_rope_kernel<T, HD, VEC, kNormRows>, dim3((p.n_rows + kNormRows - 1) / kNormRows),
+             dim3(kThreads), 0, st, p);
   else
-    launch_k(qk_norm_rope_kernel<T, HD, false>, dim3(n_rows), dim3(threads), 0, st, p);
+    launch_k(qk_norm_rope_kernel<T, HD, VEC, 1>, dim3(p.n_rows, 2), dim3(kThreads), 0, st, p);
 }
 
-template <typename T, int HD>
-void launch_append(const AppendParams& p, bool vec, cudaStream_t st) {
-  const int lanes = 2 * p.pv.n_kv * (HD / 16);
-  const int threads = lanes < 512 ? (lanes + 31) / 32 * 32 : 512;
-  if (vec)
-    launch_k(paged_append_kernel<T, HD, true>, dim3(p.n_rows), dim3(threads), 0, st, p);
+template <typename T, int HD, bool VEC>
+void launch_append(const AppendParams& p, cudaStream_t st) {
+  if (many(p.n_rows))
+    launch_k(paged_append_kernel<T, HD, VEC, kAppendRows>, dim3((p.n_rows + kAppendRows - 1) / kAppendRows),
+             dim3(kThreads), 0, st, p);
   else
-    launch_k(paged_append_kernel<T, HD, false>, dim3(p.n_rows), dim3(threads), 0, st, p);
+    launch_k(paged_append_kernel<T, HD, VEC, 1>, dim3(p.n_rows), dim3(kThreads), 0, st, p);
 }
 
 bool aligned16(const void* p, long long ld_bytes) {
@@ -253,13 +401,16 @@ dflash_status dflash_qk_norm_rope(int n_rows, int n_q, int n_kv, int head_dim, i
                   (n_kv == 0 || k != k_out || k_ld == k_out_ld),
               "qk norm rope: in place needs the same row stride");
   NormRopeParams p{};
+  p.n_rows = n_rows;
+  p.by_q = divide_by(n_q > 0 ? n_q : 1);
+  p.by_kv = divide_by(n_kv > 0 ? n_kv : 1);
   p.n_q = n_q;
   p.n_kv = n_kv;
   p.q_gain = q_gain;
   p.k_gain = k_gain;
   p.eps = eps;
   p.rotate = theta > 0.f;
-  if (p.rotate) p.fr = rope_freqs(theta, head_dim);
+  if (p.rotate) p.fr = rope_turns(theta, head_dim);
   p.pos = pos;
   p.q = q;
   p.k = k;
@@ -270,17 +421,20 @@ dflash_status dflash_qk_norm_rope(int n_rows, int n_q, int n_kv, int head_dim, i
   p.q_out_ld = q_out_ld;
   p.k_out_ld = k_out_ld;
   const long long es = dtype == DFLASH_F32 ? 4 : 2;
-  const bool vec = (n_q == 0 || (aligned16(q, q_ld * es) && aligned16(q_out, q_out_ld * es))) &&
+  const bool vec = aligned16(q_gain, 0) && aligned16(k_gain, 0) &&
+                   (n_q == 0 || (aligned16(q, q_ld * es) && aligned16(q_out, q_out_ld * es))) &&
                    (n_kv == 0 || (aligned16(k, k_ld * es) && aligned16(k_out, k_out_ld * es)));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     TraceScope ts("qk_norm_rope", st);
-    if (dtype == DFLASH_BF16)
-      head_dim == 128 ? launch_norm_rope<__nv_bfloat16, 128>(p, n_rows, vec, st)
-                      : launch_norm_rope<__nv_bfloat16, 64>(p, n_rows, vec, st);
-    else
-      head_dim == 128 ? launch_norm_rope<float, 128>(p, n_rows, vec, st)
-                      : launch_norm_rope<float, 64>(p, n_rows, vec, st);
+    auto go = [&](auto t) {
+      using T = decltype(t);
+      if (head_dim == 128)
+        vec ? launch_norm_rope<T, 128, true>(p, st) : launch_norm_rope<T, 128, false>(p, st);
+      else
+        vec ? launch_norm_rope<T, 64, true>(p, st) : launch_norm_rope<T, 64, false>(p, st);
+    };
+    dtype == DFLASH_BF16 ? go(__nv_bfloat16()) : go(float());
   }
   return check_launch("qk norm rope");
 }
@@ -300,6 +454,7 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
   DFL_REQUIRE(row_off && pos0 && k && v, "paged append: null pointer argument");
   p.n_req = n_req;
   p.n_rows = n_rows;
+  p.by_heads = divide_by(2 * pages->n_kv);
   p.row_off = row_off;
   p.pos0 = pos0;
   p.pos = pos;
@@ -307,18 +462,20 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
   p.v = v;
   p.kv_ld = kv_ld;
   p.rotate = theta > 0.f;
-  if (p.rotate) p.fr = rope_freqs(theta, pages->head_dim);
+  if (p.rotate) p.fr = rope_turns(theta, pages->head_dim);
   const long long es = pages->dtype == DFLASH_F32 ? 4 : 2;
   const bool vec = aligned16(k, kv_ld * es) && aligned16(v, kv_ld * es);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     TraceScope ts("paged_append", st);
-    if (pages->dtype == DFLASH_BF16)
-      pages->head_dim == 128 ? launch_append<__nv_bfloat16, 128>(p, vec, st)
-                             : launch_append<__nv_bfloat16, 64>(p, vec, st);
-    else
-      pages->head_dim == 128 ? launch_append<float, 128>(p, vec, st)
-                             : launch_append<float, 64>(p, vec, st);
+    auto go = [&](auto t) {
+      using T = decltype(t);
+      if (pages->head_dim == 128)
+        vec ? launch_append<T, 128, true>(p, st) : launch_append<T, 128, false>(p, st);
+      else
+        vec ? launch_append<T, 64, true>(p, st) : launch_append<T, 64, false>(p, st);
+    };
+    pages->dtype == DFLASH_BF16 ? go(__nv_bfloat16()) : go(float());
   }
   return check_launch("paged append");
 }

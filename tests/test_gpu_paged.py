@@ -66,6 +66,7 @@ def _rope_tol(ref, src, hd, dtype):
     (1, 32, 8, 128, BF, 0), (33, 14, 2, 64, BF, 0), (5, 5, 1, 128, F32, 0), (70, 64, 8, 64, F32, 0),
     (9, 3, 2, 128, BF, 5),        # rows off 16-byte boundaries
     (257, 32, 8, 128, BF, 0), (4, 100, 30, 128, BF, 8),      # more heads than one round of a CTA
+    (1501, 6, 2, 128, BF, 0), (1203, 3, 1, 64, F32, 0), (1000, 40, 7, 64, BF, 3),   # several rows to a CTA
 ])
 def test_norm_rope(rows, n_q, n_kv, hd, dtype, pad):
     rng = np.random.default_rng(rows + hd)
@@ -146,6 +147,8 @@ def _paged(rng, rows, ctx, n_kv, hd, page, dtype=BF, spare=3, wide=0):
     ([130, 2], [7, 1000], 3, 128, 1024, BF, THETA, 1),      # rows off 16-byte boundaries
     ([2] * 70, list(range(70)), 1, 64, 16, BF, THETA, 0),   # more requests than a warp
     ([7], [2], 40, 128, 16, BF, THETA, 0),                  # more heads than one round of a CTA
+    ([900, 0, 303], [40, 7, 100], 2, 128, 32, BF, THETA, 0),    # several rows to a CTA
+    ([1, 1099], [0, 3], 3, 64, 16, F32, THETA, 1),
 ])
 def test_append(rows, ctx, n_kv, hd, page, dtype, theta, pad):
     rng = np.random.default_rng(len(rows) * 7 + hd)
