@@ -353,29 +353,47 @@ def tree_rope(x: torch.Tensor, n_heads: int, head_dim: int, theta: float, ctx_le
 # The target's pass over a paged cache
 # ---------------------------------------------------------------------------
 
+# The calls below serve single decoding steps, where the host's time counts too:
+# pointers go to ctypes as plain integers, and the current stream's handle is
+# asked for without building a Stream object (2.9 us against 0.1).
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(stream, device: int):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _together(*tensors) -> int:
+    """The current CUDA device (the library launches there), which holds all tensors."""
+    at = {t.get_device() for t in tensors if t is not None}
+    dev = at.pop()
+    if at or dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("expected CUDA tensors, all on the current device")
+    return dev
+
+
 def _rows(t: torch.Tensor, name: str):
     """Pointer and row stride of a [rows, columns] view whose columns are adjacent."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected [rows, columns] with adjacent columns")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected [rows, columns]")
+    (n, width), (ld, step) = t.shape, t.stride()
+    if width > 1 and step != 1:
+        raise ValueError(f"{name}: expected adjacent columns")
+    return t.data_ptr(), ld if n > 1 else max(ld, width)
 
 
 def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str):
-    """Pointer of a contiguous CUDA tensor of n elements of dtype (None passes)."""
+    """Pointer of a contiguous tensor of n elements of dtype (None passes)."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {n} {dtype} elements")
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {n} {dtype} elements")
     return t.data_ptr()
-
-
-def _together(*tensors):
-    """All on one device, and that the current one (the library launches there)."""
-    devs = {t.device.index for t in tensors if t is not None and t.is_cuda}
-    if devs and devs != {torch.cuda.current_device()}:
-        raise ValueError("all tensors must be on the current CUDA device")
 
 
 class Pages:
@@ -416,28 +434,28 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
     if first is None:
         raise ValueError("expected q or k")
     n = first.shape[0]
-    _together(q, k, q_gain, k_gain, pos, q_out, k_out)
-    heads, args = [], []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+    dev, dtype = _together(q, k, q_gain, k_gain, pos, q_out, k_out), first.dtype
+
+    def side(x, out, name):
         if x is None:
             if out is not None:
                 raise ValueError(f"{name}_out without {name}")
-            heads.append(0)
-            args.append((None, 0, None, 0))
-            continue
-        out = x if out is None else out
-        if x.dtype != first.dtype or out.dtype != first.dtype or out.shape != x.shape:
-            raise ValueError(f"{name}_out must have {name}'s shape, and all one type")
-        if x.dim() != 2 or x.shape[0] != n or x.shape[1] % head_dim:
-            raise ValueError(f"{name}: expected [{n}, heads * {head_dim}]")
-        heads.append(x.shape[1] // head_dim)
-        args.append(_rows(x, name) + _rows(out, name + "_out"))
-    (qp, ql, qo, qol), (kp, kl, ko, kol) = args
+            return 0, None, 0, None, 0
+        p, ld = _rows(x, name)
+        if x.dtype is not dtype or x.shape[0] != n or x.shape[1] % head_dim:
+            raise ValueError(f"{name}: expected [{n}, heads * {head_dim}], all of one type")
+        if out is None:
+            return x.shape[1] // head_dim, p, ld, p, ld
+        if out.dtype is not dtype or out.shape != x.shape:
+            raise ValueError(f"{name}_out must have {name}'s shape and type")
+        return (x.shape[1] // head_dim, p, ld) + _rows(out, name + "_out")
+
+    n_q, qp, ql, qo, qol = side(q, q_out, "q")
+    n_kv, kp, kl, ko, kol = side(k, k_out, "k")
     _check(lib().dflash_qk_norm_rope(
-        n, heads[0], heads[1], head_dim, _dtype_code(first),
-        _vec(q_gain, head_dim, first.dtype, "q_gain"),
-        _vec(k_gain, head_dim, first.dtype, "k_gain"), eps, theta,
-        _vec(pos, n, torch.int32, "pos"), qp, ql, kp, kl, qo, qol, ko, kol, _stream(stream)))
+        n, n_q, n_kv, head_dim, _dtype_code(first),
+        _vec(q_gain, head_dim, dtype, "q_gain"), _vec(k_gain, head_dim, dtype, "k_gain"), eps, theta,
+        _vec(pos, n, torch.int32, "pos"), qp, ql, kp, kl, qo, qol, ko, kol, _handle(stream, dev)))
 
 
 def paged_append(pages: Pages, k: torch.Tensor, v: torch.Tensor, row_off: torch.Tensor,
@@ -450,7 +468,7 @@ def paged_append(pages: Pages, k: torch.Tensor, v: torch.Tensor, row_off: torch.
         raise ValueError("k and v must have the pools' type")
     if k.shape != v.shape or k.dim() != 2 or k.shape[1] != width:
         raise ValueError(f"k and v: expected [rows, {width}]")
-    _together(pages.pool_k, k, v, row_off, pos0, pos)
+    dev = _together(pages.pool_k, k, v, row_off, pos0, pos)
     kp, kl = _rows(k, "k")
     vp, vl = _rows(v, "v")
     if kl != vl:
@@ -458,7 +476,7 @@ def paged_append(pages: Pages, k: torch.Tensor, v: torch.Tensor, row_off: torch.
     _check(lib().dflash_paged_append(
         pages.ref, pages.n_req, n, _vec(row_off, pages.n_req + 1, torch.int32, "row_off"),
         _vec(pos0, pages.n_req, torch.int32, "pos0"), _vec(pos, n, torch.int32, "pos"), kp, vp, kl,
-        theta, _stream(stream)))
+        theta, _handle(stream, dev)))
 
 
 def paged_attention_workspace_bytes(n_q: int, n_kv: int, head_dim: int) -> int:
@@ -478,7 +496,9 @@ def paged_attention(pages: Pages, q: torch.Tensor, row_off: torch.Tensor, pos0: 
         raise ValueError(f"q: expected [rows, heads * {hd}]")
     if mask is not None and (mask.dim() != 2 or mask.shape[0] != n):
         raise ValueError("mask: expected [rows, words]")
-    _together(pages.pool_k, q, row_off, pos0, out, ws, mask)
+    dev = _together(pages.pool_k, q, row_off, pos0, out, ws, mask)
+    if not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous tensor")
     qp, ql = _rows(q, "q")
     op, ol = _rows(out, "out")
     _check(lib().dflash_paged_attention(
@@ -486,8 +506,8 @@ def paged_attention(pages: Pages, q: torch.Tensor, row_off: torch.Tensor, pos0: 
         _vec(row_off, pages.n_req + 1, torch.int32, "row_off"),
         _vec(pos0, pages.n_req, torch.int32, "pos0"), max_rows, qp, ql,
         None if mask is None else _vec(mask, mask.numel(), torch.int32, "mask"),
-        0 if mask is None else mask.shape[1], op, ol, _ptr(ws), ws.numel() * ws.element_size(),
-        _stream(stream)))
+        0 if mask is None else mask.shape[1], op, ol, ws.data_ptr(), ws.nbytes,
+        _handle(stream, dev)))
 
 
 def logits_sample_filtered(logits: torch.Tensor, u: torch.Tensor, tok: torch.Tensor,
@@ -499,11 +519,11 @@ def logits_sample_filtered(logits: torch.Tensor, u: torch.Tensor, tok: torch.Ten
     """One token per row of logits [rows, ld] from u in [0, 1), under per-row temperature,
     top_k, top_p and min_p (None: off); logp is its log-share of the kept mass."""
     rows = logits.shape[0]
-    _together(logits, u, tok, logp, temperature, top_k, top_p, min_p)
+    dev = _together(logits, u, tok, logp, temperature, top_k, top_p, min_p)
     lp, ld = _rows(logits, "logits")
     f32 = torch.float32
     _check(lib().dflash_logits_sample_filtered(
         rows, logits.shape[1] if vocab is None else vocab, ld, _dtype_code(logits), lp,
         _vec(temperature, rows, f32, "temperature"), _vec(top_k, rows, torch.int32, "top_k"),
         _vec(top_p, rows, f32, "top_p"), _vec(min_p, rows, f32, "min_p"), _vec(u, rows, f32, "u"),
-        _vec(tok, rows, torch.int32, "tok"), _vec(logp, rows, f32, "logp"), _stream(stream)))
+        _vec(tok, rows, torch.int32, "tok"), _vec(logp, rows, f32, "logp"), _handle(stream, dev)))

@@ -49,11 +49,19 @@ namespace {
 struct RopeTurns {
   uint64_t f[64];
 };
-RopeTurns rope_turns(float theta, int head_dim) {
+// (kept from call to call: 64 powers cost the host as much as the launch)
+const RopeTurns& rope_turns(float theta, int head_dim) {
+  static thread_local struct {
+    float theta = 0.f;
+    int head_dim = 0;
+    RopeTurns t;
+  } last;
+  if (last.theta == theta && last.head_dim == head_dim) return last.t;
   const RopeFreqs fr = rope_freqs(theta, head_dim);
-  RopeTurns t{};
-  for (int i = 0; i < head_dim / 2; ++i)
-  {
+  RopeTurns& t = last.t;
+  last.theta = theta;
+  last.head_dim = head_dim;
+  for (int i = 0; i < head_dim / 2; ++i) {
     const double turns = fr.f[i] / 6.283185307179586476925;
     t.f[i] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));   // whole turns are none
   }
