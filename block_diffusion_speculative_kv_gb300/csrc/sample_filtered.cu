@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t ld_remote(const uint32_t* p, uint32_t rank) 
   return v;
 }
 // Sum and maximum over a warp: hardware reductions of 32-bit parts (22-bit ones for
-// the sum, so that 32 of them do not overflow; v < 2^64 / 32).
+// the sum, so that 32 of them do not overflow; the sum itself stays below 2^64).
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
   const uint32_t a = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0x3FFFFFu);
   const uint32_t b = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 22) & 0x3FFFFFu);
@@ -183,6 +183,24 @@ struct Weight {
     return __fadd2_rn(make_float2(a, b), make_float2(-mx, -mx));
   }
 };
+// Counts one at shared address a if lo <= x <= hi (no branch around it).
+__device__ __forceinline__ void count_if_in(uint32_t a, float x, float lo, float hi) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ge.f32 p, %1, %2;\n\t"
+      "setp.le.and.f32 p, %1, %3, p;\n\t"
+      "@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(a),
+      "f"(x), "f"(lo), "f"(hi)
+      : "memory");
+}
+__device__ __forceinline__ void count_if_below(uint32_t a, float x, float limit) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.lt.f32 p, %1, %2;\n\t"
+      "@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(a),
+      "f"(x), "f"(limit)
+      : "memory");
+}
 // w 2^40, w in [0, 8], rounded: in two 32-bit conversions (64-bit ones are slow).
 __device__ __forceinline__ uint64_t fix(float w) {
   const uint32_t h = __float2uint_rz(w * 1048576.f);                     // 2^20 steps
@@ -298,21 +316,6 @@ struct Part {
     }
   }
 };
-
-// Inclusive prefix sum of one value per thread and round, in thread order.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, Shared* s, uint64_t* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  v = warp_scan(v);
-  __syncthreads();
-  if (lane == 31) s->warp[0][warp] = v;
-  __syncthreads();
-  *total = 0;
-  for (int x = 0; x < kWarps; ++x) {
-    if (x < warp) v += s->warp[0][x];
-    *total += s->warp[0][x];
-  }
-  return v;
-}
 
 // whole * f for f in [0, 1), rounded down; *rest: something was rounded away.
 // (Whole numbers throughout: FP64 is slow on this GPU.)
@@ -715,8 +718,7 @@ sample_filtered_kernel(const SampleParams p) {
         const uint32_t hist0 = mmas::smem_u32(sh.hist) - 0x4B000000u * 4u;   // 2^23 is 0x4B000000
         auto bin = [&](float d, bool in) {
           const float at = __fmaf_rd(d, -scale, 8388608.f);
-          if (in && at < 8388608.f + (kBins - 1))
-            asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(hist0 + __float_as_uint(at) * 4) : "memory");
+          count_if_below(hist0 + __float_as_uint(at) * 4, in ? at : CUDART_INF_F, 8388608.f + (kBins - 1));
         };
         if (by_mass && lo0 == floor_all) {
           part.all([&](int, const float (&x)[8]) {
@@ -745,9 +747,7 @@ sample_filtered_kernel(const SampleParams p) {
         const uint32_t hist0 = mmas::smem_u32(sh.hist);
         // (no branch per token: nearly every warp has one in the bracket)
         auto bin = [&](float x) {
-          if (x >= lo_v && x <= hi_v)
-            asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(hist0 + (((hi - C::of(x)) >> shift) << 2))
-                         : "memory");
+          count_if_in(hist0 + (((hi - C::of(x)) >> shift) << 2), x, lo_v, hi_v);
         };
         part.each(lo_v, [&](int, const float (&x)[8]) {
           if (by_mass) {
@@ -817,26 +817,41 @@ sample_filtered_kernel(const SampleParams p) {
         cu += up[q];
         cl += low[q];
       }
-      uint64_t all, all_low;
+      // The first bin whose upper (lower) cumulated measure reaches the target (the
+      // sums' roundings may leave it a little beyond everything): only the warp that
+      // holds it looks closer.
+      const uint64_t wu_sum = warp_sum(cu), wl_sum = warp_sum(cl);
+      if (lane == 0) {
+        sh.warp[0][warp] = wu_sum;
+        sh.warp[1][warp] = wl_sum;
+      }
       if (tid == 0) {
         sh.found[0] = 0;
         sh.found[1] = kBins - 1;
         sh.found_cum = above;
       }
-      uint64_t at_u = block_scan(cu, &sh, &all) - cu + above;
-      uint64_t at_l = block_scan(cl, &sh, &all_low) - cl + above;
-      // the first bin whose upper (lower) cumulated measure reaches the target
-      // (the sums' roundings may leave it a little beyond everything)
-      const uint64_t goal = min(target, all + above);
+      __syncthreads();
+      const uint64_t tu = lane < kWarps ? sh.warp[0][lane] : 0, tl = lane < kWarps ? sh.warp[1][lane] : 0;
+      const uint64_t goal = min(target, warp_sum(tu) + above);
+      uint64_t at_u = warp_sum(lane < warp ? tu : 0) + above, at_l = warp_sum(lane < warp ? tl : 0) + above;
+      if (at_u < goal && goal <= at_u + wu_sum) {
+        at_u += warp_scan(cu) - cu;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        if (at_u < goal && goal <= at_u + up[q]) {
-          sh.found[0] = kPer * tid + q;
-          sh.found_cum = at_u;
+        for (int q = 0; q < kPer; ++q) {
+          if (at_u < goal && goal <= at_u + up[q]) {
+            sh.found[0] = kPer * tid + q;
+            sh.found_cum = at_u;
+          }
+          at_u += up[q];
         }
-        if (at_l < goal && goal <= at_l + low[q]) sh.found[1] = kPer * tid + q;
-        at_u += up[q];
-        at_l += low[q];
+      }
+      if (at_l < goal && goal <= at_l + wl_sum) {
+        at_l += warp_scan(cl) - cl;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          if (at_l < goal && goal <= at_l + low[q]) sh.found[1] = kPer * tid + q;
+          at_l += low[q];
+        }
       }
       __syncthreads();
       const uint32_t b1 = sh.found[0], b2 = max(sh.found[1], b1);
