@@ -1175,7 +1175,7 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
   DFL_REQUIRE(n_req >= 0 && n_rows >= 0 && max_rows >= 0, "paged attention: sizes must be >= 0");
   DFL_REQUIRE(n_q >= pages->n_kv && n_q % pages->n_kv == 0,
               "paged attention: n_q must be a multiple of n_kv");
-  DFL_REQUIRE((long long)n_rows * n_q < (1ll << 31), "paged attention: rows x heads exceed 2^31");
+  DFL_REQUIRE((long long)n_rows * n_q < (1ll << 30), "paged attention: rows x heads exceed 2^30");
   DFL_REQUIRE(q_ld >= (long long)n_q * hd && out_ld >= (long long)n_q * hd && q_ld % 8 == 0 &&
                   out_ld % 8 == 0,
               "paged attention: row strides too small or not multiples of 8");

@@ -124,74 +124,80 @@ __device__ __forceinline__ int paged_owner(long long total, long long s, int gri
 }
 
 // Warp-collective: the line's length, the end of this CTA's share, and the place
-// where the share begins.
+// where the share begins.  Each lane adds up a run of requests; the run that holds
+// the place is then searched by all lanes.
 template <typename Geo>
 __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, long long* total_out,
                                            long long* end_out, PagedCursor* c) {
-  const int grid = gridDim.x;
+  const int run = (p.n_req + 31) / 32;
   auto length_of = [&](int r, PagedReq* q) {
-    if (r >= p.n_req) return 0ll;
     q->load(p, r);
     return q->lengths<Geo>(q->tiles<Geo>(p.G), p.G) * p.pv.n_kv;
   };
-  PagedReq q = {};
-  const long long first = length_of(lane, &q);             // of the first 32 requests
-  long long total = 0;
-  for (int r0 = 0; r0 < p.n_req; r0 += 32) {
-    long long s = r0 == 0 ? first : length_of(r0 + lane, &q);
+  auto scan = [&](long long v) {                           // inclusive
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    total += s;
-  }
-  const long long begin = paged_share<Geo>(total, blockIdx.x, grid);
-  const long long end = paged_share<Geo>(total, blockIdx.x + 1, grid);
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
+    }
+    return v;
+  };
+  PagedReq q = {};
+  long long mine = 0;
+  const int last = min((lane + 1) * run, p.n_req);
+#pragma unroll 4
+  for (int r = lane * run; r < last; ++r) mine += length_of(r, &q);
+  long long upto = scan(mine);
+  const long long total = __shfl_sync(0xffffffffu, upto, 31);
+  const long long begin = paged_share<Geo>(total, blockIdx.x, gridDim.x);
+  const long long end = paged_share<Geo>(total, blockIdx.x + 1, gridDim.x);
   *total_out = total;
   *end_out = end;
   c->left = end - begin;
   if (c->left <= 0) return;
-  long long before = 0;
-  for (int r0 = 0; r0 < p.n_req; r0 += 32) {
-    const long long s = r0 == 0 ? first : length_of(r0 + lane, &q);
-    long long inc = s;                                     // inclusive scan
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + inc > begin);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      const long long excl = __shfl_sync(0xffffffffu, inc - s, l);
-      const long long per_g = div_pos(__shfl_sync(0xffffffffu, s, l), p.pv.n_kv);
-      c->r = r0 + l;
-      if (r0 == 0 && p.n_req <= 32) {                      // (q is still of these requests)
-        c->rq = q;
-        c->rq.row0 = __shfl_sync(0xffffffffu, q.row0, l);
-        c->rq.n = __shfl_sync(0xffffffffu, q.n, l);
-        c->rq.p0 = __shfl_sync(0xffffffffu, q.p0, l);
-        c->rq.cap = p.pv.table_ld << p.pv.page_shift;
-        c->rq.masked = p.mask != nullptr;
-      } else {
-        c->rq.load(p, c->r);
+  // the lane whose run holds the place, and what lies before that run
+  int l = __ffs(__ballot_sync(0xffffffffu, upto > begin)) - 1;
+  long long before = __shfl_sync(0xffffffffu, upto - mine, l), length = __shfl_sync(0xffffffffu, mine, l);
+  c->r = l;
+  if (run == 1) {                                          // (q is the lane's own request)
+    c->rq = q;
+    c->rq.row0 = __shfl_sync(0xffffffffu, q.row0, l);
+    c->rq.n = __shfl_sync(0xffffffffu, q.n, l);
+    c->rq.p0 = __shfl_sync(0xffffffffu, q.p0, l);
+    c->rq.cap = p.pv.table_ld << p.pv.page_shift;
+    c->rq.masked = p.mask != nullptr;
+  } else {
+    const int stop = min((l + 1) * run, p.n_req);
+    for (int r0 = l * run; r0 < stop; r0 += 32) {
+      mine = r0 + lane < stop ? length_of(r0 + lane, &q) : 0;
+      upto = scan(mine);
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
+      if (past) {
+        l = __ffs(past) - 1;
+        before += __shfl_sync(0xffffffffu, upto - mine, l);
+        length = __shfl_sync(0xffffffffu, mine, l);
+        c->r = r0 + l;
+        break;
       }
-      long long rem = begin - before - excl;
-      c->g = static_cast<int>(div_pos(rem, per_g));
-      rem -= (long long)c->g * per_g;
-      int j = 0, len;
-      while (true) {
-        len = c->rq.length<Geo>(j, p.G);
-        if (rem < len) break;
-        rem -= len;
-        ++j;
-      }
-      c->j = j;
-      c->at = static_cast<int>(rem);
-      c->length = len;
-      c->weight = c->rq.weight<Geo>(j, p.G);
-      return;
+      before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    before += __shfl_sync(0xffffffffu, inc, 31);
+    c->rq.load(p, c->r);
   }
+  const long long per_g = div_pos(length, p.pv.n_kv);
+  long long rem = begin - before;
+  c->g = static_cast<int>(div_pos(rem, per_g));
+  rem -= (long long)c->g * per_g;
+  int j = 0, len;
+  while (true) {
+    len = c->rq.length<Geo>(j, p.G);
+    if (rem < len) break;
+    rem -= len;
+    ++j;
+  }
+  c->j = j;
+  c->at = static_cast<int>(rem);
+  c->length = len;
+  c->weight = c->rq.weight<Geo>(j, p.G);
 }
 
 // Past the piece, to the next tile.

@@ -85,7 +85,7 @@ struct Eight {
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];   // (in place: not __ldg)
     } else {
       T* t = reinterpret_cast<T*>(u);
 #pragma unroll

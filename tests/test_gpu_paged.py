@@ -221,6 +221,9 @@ CASES = [
     ([1], [2047], 32, 8, 128, 16, False),
     ([1, 1, 1, 1, 1], [0, 15, 16, 63, 500], 8, 2, 128, 16, False),
     ([1] * 40, list(range(0, 400, 10)), 2, 2, 64, 32, False),   # more requests than a warp
+    ([1, 0, 1, 1, 0] * 61, list(range(305)), 2, 1, 64, 16, False),   # many to a lane, some without rows
+    ([0] * 40 + [20, 0, 70] + [0] * 30, list(range(73)), 4, 1, 64, 32, False),
+    ([3] * 1100, [5] * 1100, 2, 1, 64, 16, False),          # more than a warp of runs of 32
     ([1], [300], 16, 1, 128, 32, False),                    # 16 heads to a KV head
     ([1, 1], [77, 0], 40, 1, 64, 16, False),                # 40: several tiles for one token
     ([3, 0, 5], [10, 20, 0], 14, 2, 64, 16, False),         # 7 heads, and a request without rows
@@ -503,3 +506,57 @@ def test_verification_layer_over_pages(kind):
             # values' size (N(0, 1), at most 5) for each, on both sides
             assert np.max(np.abs(a - b)) <= 4 * 2.0 ** -8 * 5
             assert np.linalg.norm(a - b) <= 2.0 ** -6 * np.linalg.norm(b)
+
+
+@pytest.mark.parametrize("rows,tree", [([1, 2], False), ([16], False), ([70, 3], False), ([90], True)])
+def test_attention_maxima_that_climb(rows, tree):
+    """Scores up to a few hundred apart, the largest ones late: the running maximum
+    moves by little, by much and by more than a step may lag, in every kernel."""
+    d = _build(rows, [900, 400][:len(rows)], 8, 2, 128, 16, tree, seed=4)
+    d["q"] = d["q"] * 16
+    for r in range(len(rows)):
+        kv = d["ctx"][r] + rows[r]
+        for t in range(kv):
+            d["pk"][d["table"][r, t // 16], :, t % 16] *= 0.05 + (t / kv) ** 3
+    out, _ = _attend(d)
+    torch.cuda.synchronize()
+    _check(d, out)
+
+
+def test_pools_past_32_bit_offsets():
+    """Pages whose elements lie beyond 2^32 (9.8 GB pools)."""
+    rng = np.random.default_rng(31)
+    n_pages, n_kv, page, hd, n_q = 300_000, 8, 16, 128, 32
+    assert n_pages * n_kv * page * hd > 2 ** 32
+    pk = torch.empty(n_pages, n_kv, page, hd, dtype=BF, device=DEV)
+    pv = torch.empty_like(pk)
+    for rows, ctx in (([1, 2], [70, 31]), ([20], [60]), ([100], [40])):
+        need = [-(-(n + c) // page) for n, c in zip(rows, ctx)]
+        ids = rng.choice(np.arange(n_pages - 5000, n_pages), size=sum(need), replace=False).astype(np.int32)
+        table = np.full((len(rows), max(need)), -1, dtype=np.int32)
+        at = 0
+        for r, n in enumerate(need):
+            table[r, :n] = ids[at:at + n]
+            at += n
+        n = sum(rows)
+        small = (sum(need), n_kv, page, hd)
+        pk[ids.tolist()], pv[ids.tolist()] = _t(rng.normal(size=small)), _t(rng.normal(size=small))
+        off = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        k, v = (_t(rng.normal(size=(n, n_kv * hd))) for _ in range(2))
+        pages = bd.Pages(pk, pv, _i(table))
+        bd.paged_append(pages, k, v, _i(off), _i(ctx))
+        q, ws = _t(rng.normal(size=(n, n_q * hd))), _ws(n_q, n_kv, hd)
+        out = torch.empty_like(q)
+        bd.paged_attention(pages, q, _i(off), _i(ctx), max(rows), out, ws)
+        torch.cuda.synchronize()
+        assert bd.read_status(ws) == 0
+        # the same on pools of these pages alone
+        again = {int(p): i for i, p in enumerate(ids)}
+        own = np.vectorize(lambda p: again.get(int(p), -1))(table).astype(np.int32)
+        d = dict(pk=pk[ids.tolist()], pv=pv[ids.tolist()], table=own, off=off, ctx=ctx, q=q, mask=None, n_q=n_q, hd=hd,
+                 n_kv=n_kv, rows=rows)
+        for r in range(len(rows)):
+            for i in range(rows[r]):
+                t = ctx[r] + i
+                assert torch.equal(d["pv"][own[r, t // page], :, t % page].reshape(-1), v[off[r] + i])
+        _check(d, out)
