@@ -105,11 +105,11 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
     pc = PagedPiece::of<GeoS>(c);
     if (pc.n <= 0) continue;
     const PagedReq rq = c.rq;
-    const int nG = rq.n * p.G, rho0 = c.j * kRowsS;
-    const int kend = rq.key_end<GeoS>(c.j, p.G);
+    const int nG = rq.n * p.heads.G, rho0 = c.j * kRowsS;
+    const int kend = rq.key_end<GeoS>(c.j, p.heads);
     const int n = pc.n;
     const int k0 = pc.first * kStepS + warp * 16;   // this warp's first key of the piece
-    const int head0 = c.g * p.G;
+    const int head0 = c.g * p.heads.G;
 
     auto load = [&](int i) {
       const int t0 = k0 + i * kStepS;
@@ -139,10 +139,10 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
     for (int h = 0; h < 2; ++h) {
       const int rho = rho0 + ra + 8 * h;
       const bool live = rho < nG;
-      tok[h] = live ? rho / p.G : 0;
+      tok[h] = live ? p.heads.quot(rho) : 0;
       lim[h] = live ? min(rq.p0 + (rq.masked ? 0 : tok[h] + 1), kend) : 0;
       const __nv_bfloat16* row =
-          p.q + (long long)(rq.row0 + tok[h]) * p.q_ld + (long long)(head0 + (live ? rho % p.G : 0)) * HD;
+          p.q + (long long)(rq.row0 + tok[h]) * p.q_ld + (long long)(head0 + (live ? rho - tok[h] * p.heads.G : 0)) * HD;
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
 #pragma unroll
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
               live ? __ldg(reinterpret_cast<const uint32_t*>(row + kk * 16 + 8 * e + cq)) : 0u;
     }
     // keys below `plain` are seen by every row of the tile
-    const int plain = min(rq.masked ? rq.p0 : rq.p0 + rho0 / p.G + 1, kend);
+    const int plain = min(rq.masked ? rq.p0 : rq.p0 + p.heads.quot(rho0) + 1, kend);
 
     float o[kNt][4] = {};
     float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
@@ -297,10 +297,10 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
     // a thread takes four columns of a row: HD / 4 neighbours make a row
     const int items = live * (HD / 4);
     auto write = [&](int row, int col, const float4& v, float L) {
-      const int rho = rho0 + row;
+      const int rho = rho0 + row, to = p.heads.quot(rho);
       const float inv = 1.f / L;                         // a row that saw no key: zeros
-      *reinterpret_cast<uint2*>(p.out + (long long)(rq.row0 + rho / p.G) * p.out_ld +
-                                (long long)(head0 + rho % p.G) * HD + col) =
+      *reinterpret_cast<uint2*>(p.out + (long long)(rq.row0 + to) * p.out_ld +
+                                (long long)(head0 + rho - to * p.heads.G) * HD + col) =
           L == 0.f ? make_uint2(0, 0)
                    : make_uint2(mmas::pack_bf16(v.x * inv, v.y * inv), mmas::pack_bf16(v.z * inv, v.w * inv));
     };
@@ -565,7 +565,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     for (PagedPiece pc; c.left > 0 && ok; paged_next<Geo>(p, pc, &c)) {
       pc = PagedPiece::of<Geo>(c);
       if (pc.n <= 0) continue;
-      const int n = pc.n, kend = c.rq.key_end<Geo>(c.j, p.G);
+      const int n = pc.n, kend = c.rq.key_end<Geo>(c.j, p.heads);
       const int32_t* table = p.pv.table + (size_t)c.r * p.pv.table_ld;
       // this lane's box of step i: its first slot, and its page's table entry
       // (asked for one step ahead; kend lies within the table)
@@ -620,7 +620,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     for (PagedPiece pc; c.left > 0 && ok; paged_next<Geo>(p, pc, &c)) {
       pc = PagedPiece::of<Geo>(c);
       if (pc.n <= 0) continue;
-      const int n = pc.n, nt = NG == 2 && min(c.rq.n * p.G - c.j * S::kRows, S::kRows) > 128 ? 2 : 1;
+      const int n = pc.n, nt = NG == 2 && min(c.rq.n * p.heads.G - c.j * S::kRows, S::kRows) > 128 ? 2 : 1;
       auto all = [&](bool landed) { return __all_sync(0xffffffffu, landed); };
       ok = all(wait(q_full, unit & 1u));
       const int jobs0 = NG == 1 || nt == 2 ? n : (n + 1) / 2, jobs1 = NG == 1 ? 0 : (nt == 2 ? n : n / 2);
@@ -723,13 +723,13 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       pc = PagedPiece::of<Geo>(c);
       if (pc.n <= 0) continue;
       const PagedReq rq = c.rq;
-      const int n = pc.n, nG = rq.n * p.G, tile0 = c.j * S::kRows;
+      const int n = pc.n, nG = rq.n * p.heads.G, tile0 = c.j * S::kRows;
       const int nt = NG == 2 && min(nG - tile0, S::kRows) > 128 ? 2 : 1;
-      const int kend = rq.key_end<Geo>(c.j, p.G);
+      const int kend = rq.key_end<Geo>(c.j, p.heads);
       const int rho0 = tile0 + (nt == 2 ? x * GT : 0);       // first row of this group's MMA tile
       const int rho = rho0 + row;
       const bool live = rho < nG;
-      const int tok = live ? rho / p.G : 0, head = c.g * p.G + (live ? rho % p.G : 0);
+      const int tok = live ? p.heads.quot(rho) : 0, head = c.g * p.heads.G + (live ? rho - tok * p.heads.G : 0);
       const int jobs = NG == 1 || nt == 2 ? n : (n + 1 - x) / 2;
       // Q into shared memory (rows of 128 bytes, 128-byte swizzle): HD / 8 lanes
       // read a row, whose address its own lane knows
@@ -755,9 +755,9 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       // that every row of the warp, and of the whole tile, sees
       const int lim = live ? (rq.masked ? kend : min(rq.p0 + tok + 1, kend)) : 0;
       const uint32_t* mrow = rq.masked ? p.mask + (size_t)(rq.row0 + tok) * p.mask_ld : nullptr;
-      const int first = min(rho0 + wg * 32, nG - 1) / p.G;
+      const int first = p.heads.quot(min(rho0 + wg * 32, nG - 1));
       const int plain_w = rho0 + wg * 32 >= nG ? 0 : min(rq.masked ? rq.p0 : rq.p0 + first + 1, kend);
-      const int plain_t = min(rq.masked ? rq.p0 : rq.p0 + tile0 / p.G + 1, kend);
+      const int plain_t = min(rq.masked ? rq.p0 : rq.p0 + p.heads.quot(tile0) + 1, kend);
       const bool dead = rho0 + wg * 32 >= nG;        // no live row in this warp
       float m_ref = -CUDART_INF_F, l = 0.f;
       // A step's P V ran with zeros for values that are not finite.  Once it is done
@@ -1193,7 +1193,8 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
               "paged attention: the workspace must be 16-byte aligned");
   p.n_req = n_req;
   p.n_rows = n_rows;
-  p.G = n_q / pages->n_kv;
+  p.heads.G = n_q / pages->n_kv;
+  p.heads.m = static_cast<uint32_t>((1ull << 32) / p.heads.G);
   p.row_off = row_off;
   p.pos0 = pos0;
   p.mask = mask;
@@ -1211,7 +1212,7 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // The smallest tile that takes all rows of a (request, KV head): keys and values
   // are then read once.
-  const long long rows = (long long)max_rows * p.G;
+  const long long rows = (long long)max_rows * p.heads.G;
   dflash_status e = DFLASH_OK;
   if (rows <= kRowsS)
     hd == 128 ? launch_small<128>(p, st) : launch_small<64>(p, st);

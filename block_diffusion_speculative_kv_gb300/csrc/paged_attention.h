@@ -6,9 +6,21 @@
 
 namespace dfl {
 
+// Query heads per KV head, and division by them: the quotient by 2^32 / G rounded
+// down is exact or one too small.
+struct Heads {
+  int G;
+  uint32_t m;
+  __device__ __forceinline__ int quot(int x) const {
+    const int q = G == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), m));
+    return q + (x - q * G >= G ? 1 : 0);
+  }
+};
+
 struct PagedAttnParams {
   PagedView pv;
-  int n_req, n_rows, G;            // G = query heads per KV head
+  int n_req, n_rows;
+  Heads heads;
   const int32_t* row_off;
   const int32_t* pos0;
   const uint32_t* mask;
@@ -52,28 +64,28 @@ struct PagedReq {
     masked = p.mask != nullptr;
   }
   template <typename Geo>
-  __device__ __forceinline__ int tiles(int G) const {
-    return (n * G + Geo::TR - 1) / Geo::TR;
+  __device__ __forceinline__ int tiles(const Heads& h) const {
+    return (n * h.G + Geo::TR - 1) / Geo::TR;
   }
   template <typename Geo>
-  __device__ __forceinline__ int key_end(int j, int G) const {
-    const int last = masked ? n - 1 : min(j * Geo::TR + Geo::TR - 1, n * G - 1) / G;
+  __device__ __forceinline__ int key_end(int j, const Heads& h) const {
+    const int last = masked ? n - 1 : h.quot(min(j * Geo::TR + Geo::TR - 1, n * h.G - 1));
     return min(p0 + last + 1, cap);
   }
   template <typename Geo>
-  __device__ __forceinline__ int weight(int j, int G) const {
-    return min(n * G - j * Geo::TR, Geo::TR) > Geo::HALF ? 2 : 1;
+  __device__ __forceinline__ int weight(int j, const Heads& h) const {
+    return min(n * h.G - j * Geo::TR, Geo::TR) > Geo::HALF ? 2 : 1;
   }
   // length of a tile, and of tiles [0, j1) of one KV head, on the line
   template <typename Geo>
-  __device__ __forceinline__ int length(int j, int G) const {
-    return Geo::TC + (key_end<Geo>(j, G) + Geo::KS - 1) / Geo::KS * weight<Geo>(j, G);
+  __device__ __forceinline__ int length(int j, const Heads& h) const {
+    return Geo::TC + (key_end<Geo>(j, h) + Geo::KS - 1) / Geo::KS * weight<Geo>(j, h);
   }
   template <typename Geo>
-  __device__ __forceinline__ long long lengths(int j1, int G) const {
-    if (masked && j1 > 0) return (long long)(j1 - 1) * length<Geo>(0, G) + length<Geo>(j1 - 1, G);
+  __device__ __forceinline__ long long lengths(int j1, const Heads& h) const {
+    if (masked && j1 > 0) return (long long)(j1 - 1) * length<Geo>(0, h) + length<Geo>(j1 - 1, h);
     long long s = 0;
-    for (int j = 0; j < j1; ++j) s += length<Geo>(j, G);
+    for (int j = 0; j < j1; ++j) s += length<Geo>(j, h);
     return s;
   }
 };
@@ -132,7 +144,7 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, l
   const int run = (p.n_req + 31) / 32;
   auto length_of = [&](int r, PagedReq* q) {
     q->load(p, r);
-    return q->lengths<Geo>(q->tiles<Geo>(p.G), p.G) * p.pv.n_kv;
+    return q->lengths<Geo>(q->tiles<Geo>(p.heads), p.heads) * p.pv.n_kv;
   };
   auto scan = [&](long long v) {                           // inclusive
 #pragma unroll
@@ -189,7 +201,7 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, l
   rem -= (long long)c->g * per_g;
   int j = 0, len;
   while (true) {
-    len = c->rq.length<Geo>(j, p.G);
+    len = c->rq.length<Geo>(j, p.heads);
     if (rem < len) break;
     rem -= len;
     ++j;
@@ -197,7 +209,7 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, l
   c->j = j;
   c->at = static_cast<int>(rem);
   c->length = len;
-  c->weight = c->rq.weight<Geo>(j, p.G);
+  c->weight = c->rq.weight<Geo>(j, p.heads);
 }
 
 // Past the piece, to the next tile.
@@ -205,7 +217,7 @@ template <typename Geo>
 __device__ __forceinline__ void paged_next(const PagedAttnParams& p, const PagedPiece& pc, PagedCursor* c) {
   c->left -= pc.used;
   if (c->left <= 0) return;
-  if (++c->j >= c->rq.tiles<Geo>(p.G)) {
+  if (++c->j >= c->rq.tiles<Geo>(p.heads)) {
     c->j = 0;
     if (++c->g >= p.pv.n_kv) {
       c->g = 0;
@@ -216,8 +228,8 @@ __device__ __forceinline__ void paged_next(const PagedAttnParams& p, const Paged
     }
   }
   c->at = 0;
-  c->length = c->rq.length<Geo>(c->j, p.G);
-  c->weight = c->rq.weight<Geo>(c->j, p.G);
+  c->length = c->rq.length<Geo>(c->j, p.heads);
+  c->weight = c->rq.weight<Geo>(c->j, p.heads);
 }
 
 // The CTAs that hold the steps of the cursor's tile, which begins at `tile0`.
