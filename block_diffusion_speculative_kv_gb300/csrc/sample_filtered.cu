@@ -12,18 +12,25 @@
 // min-p gives t outright.  The draw is the first kept token, by id, whose
 // cumulated mass passes u times the kept mass.
 //
-// One cluster of 8 CTAs per row: each CTA keeps its slice of the row in shared
-// memory (rows too long for that are read again from global memory), so HBM
+// One cluster of 2, 4 or 8 CTAs per row: each CTA keeps its slice of the row in
+// shared memory (rows too long for that are read again from global memory), so HBM
 // sees the logits once.  Counts and masses are whole numbers (a mass has 40
 // fractional bits), so their sums over lanes, warps and CTAs do not depend on
 // the order and every pass agrees with every other.
 //
-// Two ways from there.  A small top-k (2 .. 512): the r-th best of a CTA's
-// per-thread maxima, r = ceil(k / 8), is a value that r of its tokens reach, so
-// k tokens of the row reach the least of the eight; the few tokens that do are
-// gathered in one CTA, sorted, and everything else happens on that list.
+// Two ways from there.  A small top-k (2 .. 512): the r-th best of a CTA's share of
+// 2048 maxima over parts of the row, r = ceil(k / CTAs), is a value that r of its
+// tokens reach, so k tokens of the row reach the least of the CTAs'; the few tokens
+// that do are gathered in one CTA, ordered, and everything else happens on that list.
 // Otherwise t is searched over the whole row by counting its tokens in bins
-// (search() below).
+// (search() below), with one exponential per token for the whole mass and one for the
+// mass above the border's surroundings.
+//
+// Neither bandwidth nor any unit bounds it, but the chain of block and cluster
+// barriers between the steps of a row, of which an SM holds four CTAs: 480 rows of
+// 151936 bf16 logits take 48 us greedy (6.3 waves of clusters; their bytes alone
+// 21.5), 80 without filters, 92 with top-k 50, 250 with top-p 0.9 and 131 with
+// filters of every kind mixed; one fp32 row with top-k 50 takes 13.7, greedy 5.5.
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -33,17 +40,21 @@ namespace dfl {
 
 namespace {
 
-constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32;
-constexpr int kParts = kCluster * kWarps;          // contiguous parts of a row, one to a warp
-constexpr int kMaxSlice = 200 * 1024;              // resident slice bytes
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxima = 8 * kThreads;              // parts of a row whose maxima are compared
+constexpr int kMaxSlice = 196 * 1024;              // resident slice bytes
+constexpr int kManySlice = 52 * 1024;              // of several CTAs to an SM
 constexpr int kListK = 512, kList = 1024;          // largest k, and tokens, of the gathered list
 constexpr int kListPer = kList / kThreads;
 constexpr int kBins = 1024;                        // of a search level
-constexpr int kPer = kBins / kThreads;
+constexpr int kNearRow = 8192;                     // tokens kept near the border, of a row
 // A bin's weight bounds are widened by this much: exponents of up to 44 times a
 // few roundings of 2^-24 stay below 2^-15.
 constexpr float kSlack = 1e-4f;
 constexpr float kOne = 1099511627776.f;            // 2^40
+// More than the mass of all tokens that fit into near[].
+constexpr uint64_t kTooMany = 1ull << 54;
+static_assert(kNearRow < 1 << 14, "see above");
 
 struct SampleParams {
   int vocab, part;          // part: elements of a warp's part, a multiple of 8
@@ -120,22 +131,22 @@ struct Shared {
   uint64_t warp[2][kWarps];
   uint64_t xch[2][2];                    // exchanged between the CTAs, two in turn
   union {
-    struct {
-      uint32_t hist[kBins];              // this CTA's counts
-      uint32_t tot[kBins / kCluster];    // the cluster's, of this CTA's share of the bins
-    };
+    uint32_t hist[kBins];                // this CTA's counts
     uint64_t list[kList];                // gathered tokens: (ordered logit, ~id)
   };
   uint2 part[2][kWarps];
   uint32_t list_n;
   uint32_t found[2];
-  uint64_t found_cum;
+  uint64_t found_cum, before[2];
+  uint64_t share[2];                     // measures of this CTA's share of the bins
+  uint32_t near_n[kWarps];               // a warp's tokens near the border
   double below;                          // T ln(min-p): what min-p keeps reaches max + this
   float hi, lo;                          // log2(e) / T in two parts
 };
 
-// Sums (and maxima) over the cluster; every thread receives the result.  The
-// exchange slots alternate, so one cluster barrier per reduction is enough.
+// Sums (and maxima) over the cluster of CL CTAs; every thread receives the result.
+// The exchange slots alternate, so one cluster barrier per reduction is enough.
+template <int CL>
 struct Reducer {
   Shared* s;
   int buf = 0;
@@ -159,8 +170,8 @@ struct Reducer {
       }
     }
     cluster_sync();
-    a = op(lane < kCluster ? ld_remote(&s->xch[buf][0], lane) : 0);
-    b = op(lane < kCluster ? ld_remote(&s->xch[buf][1], lane) : 0);
+    a = op(lane < CL ? ld_remote(&s->xch[buf][0], lane) : 0);
+    b = op(lane < CL ? ld_remote(&s->xch[buf][1], lane) : 0);
     buf ^= 1;
   }
 };
@@ -227,6 +238,10 @@ template <>
 struct Chunk<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void gather(const __nv_bfloat16* p, int n) {   // n of them
+    auto one = [&](int e) -> uint32_t { return e < n ? __bfloat16_as_ushort(p[e]) : 0xFF80u; };
+    u = make_uint4(one(0) | one(1) << 16, one(2) | one(3) << 16, one(4) | one(5) << 16, one(6) | one(7) << 16);
+  }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
   __device__ __forceinline__ void clean() {                // NaN becomes -inf
     __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
@@ -254,6 +269,11 @@ struct Chunk<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void gather(const float* p, int n) {
+    auto one = [&](int e) { return e < n ? p[e] : -CUDART_INF_F; };
+    a = make_float4(one(0), one(1), one(2), one(3));
+    b = make_float4(one(4), one(5), one(6), one(7));
   }
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = a;
@@ -287,33 +307,54 @@ struct Part {
     if (RES || (vec && i + 8 <= n)) {
       c.load(data + i);
     } else {
-      alignas(16) T t[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = i + e < n ? data[i + e] : from_f32<T>(-CUDART_INF_F);
-      c.load(t);
+      c.gather(data + i, n - i);
     }
     if constexpr (!RES) c.clean();
     return c;
   }
+  __device__ __forceinline__ float one(int i) const {      // (not a NaN)
+    return to_f32(data[i]);
+  }
+  // g(i, chunk) for every eight tokens; from global memory the next two rounds are
+  // asked for ahead
+  template <typename G>
+  __device__ __forceinline__ void chunks(G g) const {
+    int i = (threadIdx.x & 31) * 8;
+    if constexpr (RES) {
+#pragma unroll 2
+      for (; i < n; i += 256) g(i, at(i));
+    } else {
+      Chunk<T> c[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) c[q] = at(min(i + q * 256, n));
+      for (; i < n; i += 512) {
+        Chunk<T> d[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) d[q] = at(min(i + (q + 2) * 256, n));
+        g(i, c[0]);
+        if (i + 256 < n) g(i + 256, c[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) c[q] = d[q];
+      }
+    }
+  }
   // f(i, x) for every eight tokens (all), or for those of which one is at or above lo
   template <typename F>
   __device__ __forceinline__ void all(F f) const {
-#pragma unroll 2
-    for (int i = (threadIdx.x & 31) * 8; i < n; i += 256) {
-      float x[8];
-      at(i).get(x);
-      f(i, x);
-    }
-  }
-  template <typename F>
-  __device__ __forceinline__ void each(float lo, F f) const {
-    for (int i = (threadIdx.x & 31) * 8; i < n; i += 256) {
-      const Chunk<T> c = at(i);
-      if (!(c.max() >= lo)) continue;
+    chunks([&](int i, const Chunk<T>& c) {
       float x[8];
       c.get(x);
       f(i, x);
-    }
+    });
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(float lo, F f) const {
+    chunks([&](int i, const Chunk<T>& c) {
+      if (!(c.max() >= lo)) return;
+      float x[8];
+      c.get(x);
+      f(i, x);
+    });
   }
 };
 
@@ -389,12 +430,14 @@ __device__ __noinline__ void draw_sorted(const SampleParams& p, int row, Shared*
   // the tokens before this one, and their mass; top-k keeps the first k
   int place = 0;
   uint64_t before = 0;
-  if (tid < n)
+  if (tid < n) {
+#pragma unroll 4
     for (int i = 0; i < n; ++i)
       if (s->list[i] > key) {
         ++place;
         before += wt[i];
       }
+  }
   bool keep = tid < n && place < k;
   if (keep && place == k - 1) s->found_cum = before + mine;
   __syncthreads();
@@ -404,7 +447,9 @@ __device__ __noinline__ void draw_sorted(const SampleParams& p, int row, Shared*
   // cumulated by id, over what is kept
   wt[tid] = keep ? mine : 0;
   __syncthreads();
+  if (tid >= n) return;
   uint64_t upto = 0, kept = 0;
+#pragma unroll 4
   for (int i = 0; i < n; ++i) {
     const uint64_t m = wt[i];
     kept += m;
@@ -417,8 +462,11 @@ __device__ __noinline__ void draw_sorted(const SampleParams& p, int row, Shared*
   }
 }
 
-// The same for a longer list in s->list; block-collective.  The same border (t, m) as for a whole row, found by
-// halving the range of codes; a thread holds kListPer tokens.
+// The same for a longer list in s->list; block-collective.  The border (t, m) as for a
+// whole row, found by halving the range of codes; a thread holds kListPer tokens.
+// (Counting costs n per token, halving some 50 block sums whatever n: 480 rows with
+// top-k 50, about 70 tokens, 97 us counted and 114 halved; with top-k 400, about 450,
+// 165 and 129.  The border between them is what half a block's threads hold.)
 template <int SHIFT>
 __device__ __noinline__ void draw_halving(const SampleParams& p, int row, Shared* s, int n, int k, float top_p,
                                          float min_p, float uf, float temp, float from, const Weight& w) {
@@ -520,14 +568,18 @@ __device__ __noinline__ void draw_halving(const SampleParams& p, int row, Shared
     }
 }
 
-template <typename T, bool RES>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
+template <typename T, bool RES, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads, 4)
 sample_filtered_kernel(const SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
   using C = Codes<T>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = static_cast<int>(cluster_rank()), row = blockIdx.x / kCluster;
+  constexpr int kNear = kNearRow / (CL * kWarps);          // of a warp
+  float* near = reinterpret_cast<float*>(smem) + warp * kNear;
+  T* slice = reinterpret_cast<T*>(smem + kWarps * kNear * sizeof(float));
+  const int rank = static_cast<int>(cluster_rank());
+  const int row = blockIdx.x / CL;
   pdl_wait();
   pdl_trigger();
 
@@ -546,10 +598,18 @@ sample_filtered_kernel(const SampleParams p) {
 
   // the slice into shared memory (all of a lane's copies in flight at once), where
   // each lane reads its own tokens only; and this thread's best value
-  float mine = -CUDART_INF_F;
+  constexpr int kMine = kMaxima / (CL * kThreads);
+  float mine[kMine];
+  int where[kMine];                        // its first chunk
+#pragma unroll
+  for (int q = 0; q < kMine; ++q) mine[q] = -CUDART_INF_F, where[q] = 0;
+  auto take = [&](int q, float v, int i) {
+    where[q] = v > mine[q] ? i : where[q];
+    mine[q] = fmaxf(mine[q], v);
+  };
   if constexpr (RES) {
     const Part<T, false> g{part.data, part.id0, part.n, part.vec};
-    T* own = reinterpret_cast<T*>(smem) + (size_t)warp * p.part;
+    T* own = slice + (size_t)warp * p.part;
     for (int i = lane * 8; i < part.n; i += 256) {
       if (part.vec && i + 8 <= part.n) {
         const uint32_t to = mmas::smem_u32(own + i);
@@ -563,13 +623,21 @@ sample_filtered_kernel(const SampleParams p) {
     mmas::cp_async_wait<0>();
     part.data = own;
   }
-  for (int i = lane * 8; i < part.n; i += 256) {
-    Chunk<T> c = part.at(i);
-    if constexpr (RES) {
-      c.clean();
-      c.store(const_cast<T*>(part.data) + i);
+  constexpr int kAhead = RES || kMine > 4 ? kMine : 4;     // rounds asked for at once
+  for (int i = lane * 8; i < part.n; i += 256 * kAhead) {
+    Chunk<T> c[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (!RES || i + q * 256 < part.n) c[q] = part.at(min(i + q * 256, part.n));
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      if constexpr (RES) {
+        if (i + q * 256 >= part.n) continue;
+        c[q].clean();
+        c[q].store(const_cast<T*>(part.data) + i + q * 256);
+      }
+      take(q % kMine, c[q].max(), i + q * 256);
     }
-    mine = fmaxf(mine, c.max());
   }
   if (tid == 0) {                          // (seen by all after the next block barrier)
     sh.list_n = 0;
@@ -579,40 +647,59 @@ sample_filtered_kernel(const SampleParams p) {
     sh.lo = hi > 3e38f ? 1e-38f : fmaxf((fmaf(-hi, temp, 1.4426950216293335f) + 1.925963033500e-8f) / temp, 1e-38f);
     if (temp > 0.f && min_p > 0.f) sh.below = static_cast<double>(temp) * log(static_cast<double>(fminf(min_p, 1.f)));
   }
-  Reducer red{&sh};
+  Reducer<CL> red{&sh};
 
   const bool greedy = !(temp > 0.f) || k == 1;
   // the row's best token, (value desc, id asc), and a value that k tokens reach
   uint64_t best = 0;
   {
-    float top = mine;
+    float top = mine[0];
+#pragma unroll
+    for (int q = 1; q < kMine; ++q) top = fmaxf(top, mine[q]);
+    const float here = top;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (mine == top && top > -CUDART_INF_F) {
+    if (here == top && top > -CUDART_INF_F) {
       int id = 0x7FFFFFFF;
-      if (greedy)                                          // (nobody else asks which token it is)
-        part.each(top, [&](int i, const float (&x)[8]) {
+      if (greedy) {                                        // (nobody else asks which token it is)
+        int i = part.n;
 #pragma unroll
-          for (int e = 7; e >= 0; --e)
-            if (x[e] == top && part.id0 + i + e < id) id = part.id0 + i + e;
-        });
+        for (int q = 0; q < kMine; ++q) i = mine[q] == top ? min(i, where[q]) : i;
+        float x[8];
+        part.at(i).get(x);
+#pragma unroll
+        for (int e = 7; e >= 0; --e)
+          if (x[e] == top) id = part.id0 + i + e;
+      }
       best = ((uint64_t)ordered_bits(top) << 32) | (uint32_t)~id;
     }
   }
   const bool listed = !greedy && k > 1 && k <= kListK && k < p.vocab;
   uint64_t reach_code = 0;
   if (listed) {
-    const int r = (k + kCluster - 1) / kCluster;
-    const uint32_t code = C::of(mine);
-    uint32_t lo = 0, hi = C::of(CUDART_INF_F);
+    const uint32_t r = (k + CL - 1) / CL;
+    uint32_t code[kMine];                                  // (16 bits are enough)
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) code[q] = ordered_bits(mine[q]) >> 16;
+    uint32_t lo = 0, hi = ordered_bits(CUDART_INF_F) >> 16;
+    int turn = 0;
     while (lo < hi) {                                      // block-uniform
       const uint32_t mid = lo + (hi - lo + 1) / 2;
-      if (__syncthreads_count(code >= mid) >= r) lo = mid;
+      uint32_t n;
+      if constexpr (kMine == 1) {
+        n = __syncthreads_count(code[0] >= mid);
+      } else {
+        uint32_t c = 0;
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) c += code[q] >= mid ? 1 : 0;
+        n = static_cast<uint32_t>(list_sum(0, c, &sh, &turn));
+      }
+      if (n >= r) lo = mid;
       else hi = mid - 1;
     }
-    reach_code = 0xFFFFFFFFull - lo;                       // the least of the eight, as a maximum
+    reach_code = 0xFFFFull - lo;                           // the least of the CTAs', as a maximum
   }
-  red.both<true>(best, reach_code);
+  red.template both<true>(best, reach_code);
   const float mx = best ? from_ordered_bits(static_cast<uint32_t>(best >> 32)) : -CUDART_INF_F;
   const int best_id = static_cast<int>(~static_cast<uint32_t>(best));
   if (mx == -CUDART_INF_F || greedy) {
@@ -626,7 +713,7 @@ sample_filtered_kernel(const SampleParams p) {
   const Weight w{mx, sh.hi, sh.lo};
 
   if (listed && !isinf(mx)) {
-    const float from = C::value(0xFFFFFFFFu - static_cast<uint32_t>(reach_code));
+    const float from = from_ordered_bits((0xFFFFu - static_cast<uint32_t>(reach_code)) << 16);
     if (from > -CUDART_INF_F) {
       part.each(from, [&](int i, const float (&x)[8]) {
 #pragma unroll
@@ -641,14 +728,14 @@ sample_filtered_kernel(const SampleParams p) {
       cluster_sync();
       uint32_t n = 0, n_mine = 0, n_before = 0;            // in all, of CTA `warp`, before it
 #pragma unroll
-      for (int r = 0; r < kCluster; ++r) {
+      for (int r = 0; r < CL; ++r) {
         const uint32_t c = ld_remote(&sh.list_n, r);
         if (r < warp) n_before += c;
         if (r == warp) n_mine = c;
         n += c;
       }
       if (n <= kList) {
-        static_assert(kWarps == kCluster, "a warp takes a CTA's list");
+        static_assert(CL <= kWarps, "a warp takes a CTA's list");
         // (CTA 0's own tokens lie in front; the others' follow)
         if (rank == 0 && warp > 0)
           for (uint32_t i = lane; i < n_mine; i += 32) sh.list[n_before + i] = ld_remote(&sh.list[i], warp);
@@ -670,9 +757,11 @@ sample_filtered_kernel(const SampleParams p) {
   uint32_t m = 0;
   const uint32_t top_code = C::of(mx), floor_all = C::of(-CUDART_INF_F);
 
-  // the last search by mass leaves the mass of this thread's tokens above over_v
+  // A search by mass leaves the mass of this thread's tokens above over_v, and (close)
+  // the tokens between over_v and somewhat below the border in near[].
   uint64_t over_sum = 0;
   float over_v = CUDART_INF_F;
+  bool close = false;
   struct Found {
     uint32_t code;
     uint64_t above, target;
@@ -681,16 +770,20 @@ sample_filtered_kernel(const SampleParams p) {
   // the target, and the measure strictly above it.  The target is k, or, by mass,
   // top_p of the mass above `lo` (and `extra` more, which lies at lo; if that is
   // needed the answer is lo).  Each level counts the bracket's tokens in kBins
-  // bins (first by distance from the best, up to `reach`, which spreads them
-  // evenly; then by code) and takes the exact measure above the bracket.  A bin's
-  // mass lies between its count times its lightest and its heaviest weight, so a
-  // few bins, often one, remain.  Bins of one code settle it.
+  // bins, first by distance from the best, up to `reach`, which spreads them
+  // evenly, then by code.  By mass, a bin of the first level is taken at its middle's
+  // weight; the bin that this points to and its neighbours make the next bracket,
+  // whose tokens are few and are kept, and the masses above it and in it are then
+  // summed exactly.  Should the border not lie there (or a warp's tokens not fit),
+  // everything runs again with bounds: a bin's mass lies between its count times its
+  // lightest and its heaviest weight, so a few bins remain.  Bins of one code settle it.
   auto search = [&](bool by_mass, uint32_t lo, uint64_t extra, float reach) {
     uint32_t hi = top_code;
     const uint32_t lo0 = lo;
     const float lo0_v = C::value(lo);
     uint64_t target = k;
-    bool linear = reach < 1e30f;
+    bool linear = reach < 1e30f, guess = by_mass && linear;
+    close = false;
     if (by_mass && !linear) {              // the whole in a pass of its own
       uint64_t whole = 0, none = 0;
       part.each(lo0_v, [&](int, const float (&x)[8]) {
@@ -699,7 +792,7 @@ sample_filtered_kernel(const SampleParams p) {
         for (int e = 0; e < 8; ++e) s8 += x[e] > lo0_v ? w(x[e]) : 0.f;
         whole += fix(s8);
       });
-      red.both<false>(whole, none);
+      red.template both<false>(whole, none);
       target = mass_target(top_p, whole + extra);
       if (target > whole) return Found{lo, whole, target};
     }
@@ -710,12 +803,18 @@ sample_filtered_kernel(const SampleParams p) {
       const float scale = static_cast<float>(kBins - 1) / reach;
       const float far_v = mx - reach;                      // (linear) beyond: the last bin
       for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+      if (lane == 0) sh.near_n[warp] = close ? sh.near_n[warp] : 0;
       __syncthreads();
-      uint64_t sum = 0, none = 0;
+      uint64_t sum = 0, in_sum = 0;
+      const uint32_t hist_c = mmas::smem_u32(sh.hist);
+      // (no branch per token: nearly every warp has one in the bracket)
+      auto bin_code = [&](float x) {
+        count_if_in(hist_c + (((hi - C::of(x)) >> shift) << 2), x, lo_v, hi_v);
+      };
       if (linear) {
         // the mass above lo, and the bins, in one pass; 2^23 + bin has the bin in its
         // low bits (rounded down)
-        const uint32_t hist0 = mmas::smem_u32(sh.hist) - 0x4B000000u * 4u;   // 2^23 is 0x4B000000
+        const uint32_t hist0 = hist_c - 0x4B000000u * 4u;  // 2^23 is 0x4B000000
         auto bin = [&](float d, bool in) {
           const float at = __fmaf_rd(d, -scale, 8388608.f);
           count_if_below(hist0 + __float_as_uint(at) * 4, in ? at : CUDART_INF_F, 8388608.f + (kBins - 1));
@@ -743,13 +842,15 @@ sample_filtered_kernel(const SampleParams p) {
             if (by_mass) sum += fix(s8);
           });
         }
+      } else if (close) {
+        sum = over_sum;
+        for (uint32_t i = lane; i < sh.near_n[warp]; i += 32) {
+          const float x = near[i];
+          if (x > hi_v) sum += fix(w(x));
+          bin_code(x);
+        }
       } else {
-        const uint32_t hist0 = mmas::smem_u32(sh.hist);
-        // (no branch per token: nearly every warp has one in the bracket)
-        auto bin = [&](float x) {
-          count_if_in(hist0 + (((hi - C::of(x)) >> shift) << 2), x, lo_v, hi_v);
-        };
-        part.each(lo_v, [&](int, const float (&x)[8]) {
+        part.each(lo_v, [&](int i, const float (&x)[8]) {
           if (by_mass) {
             float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -764,36 +865,61 @@ sample_filtered_kernel(const SampleParams p) {
             for (int e = 0; e < 8; ++e) n8 += x[e] > hi_v ? 1 : 0;
             sum += n8;
           }
+          if (guess) {
+            uint32_t in = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) bin(x[e]);
+            for (int e = 0; e < 8; ++e)
+              if (x[e] >= lo_v && x[e] <= hi_v) in |= 1u << e;
+            for (; in; in &= in - 1) {
+              const float y = part.one(i + __ffs(in) - 1);
+              const uint32_t at = atomicAdd(&sh.near_n[warp], 1u);
+              if (at < kNear) near[at] = y;
+              in_sum += fix(w(y));
+              bin_code(y);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) bin_code(x[e]);
+          }
         });
         if (by_mass) {
           over_sum = sum;                                  // of this thread's tokens above hi_v
           over_v = hi_v;
         }
+        __syncwarp();
+        if (guess && lane == 0 && sh.near_n[warp] > kNear) in_sum += kTooMany;
       }
       __syncthreads();
-      red.both<false>(sum, none);                          // (all histograms are complete)
+      red.template both<false>(sum, in_sum);               // (all histograms are complete)
       if (linear && by_mass) {
         target = mass_target(top_p, sum + extra);
         if (target > sum) return Found{lo0, sum, target};
         sum = 0;                                           // nothing lies above the best
       }
-      const uint64_t above = sum;
-      if (tid < kBins / kCluster) {
-        uint32_t n = 0;
-#pragma unroll
-        for (int r = 0; r < kCluster; ++r) n += ld_remote(&sh.hist[rank * (kBins / kCluster) + tid], r);
-        sh.tot[tid] = n;
+      if (guess && !linear && !close) {
+        close = sum < target && target <= sum + in_sum && in_sum < kTooMany;
+        if (!close) {
+          guess = false;
+          linear = true;
+          lo = lo0;
+          hi = top_code;
+          continue;
+        }
       }
-      cluster_sync();
-      // kPer bins to a thread, from the best on; upper and lower bounds of their measures
+      const uint64_t above = sum;
+      // Every CTA takes a share of the bins, from the best on; upper and lower bounds
+      // (or the guess) of their measures
+      constexpr int kShare = kBins / CL, kPer = kShare > kThreads ? kShare / kThreads : 1;
       const float per_bin = -w.hi / scale;                 // (linear) log2 of a bin's fall
       uint64_t up[kPer], low[kPer], cu = 0, cl = 0;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        const uint32_t b = kPer * tid + q;
-        uint32_t n = ld_remote(&sh.tot[b % (kBins / kCluster)], b / (kBins / kCluster));
+        up[q] = low[q] = 0;
+        if (kPer * tid + q >= kShare) continue;
+        const uint32_t b = rank * kShare + kPer * tid + q;
+        uint32_t n = 0;
+#pragma unroll
+        for (int r = 0; r < CL; ++r) n += ld_remote(&sh.hist[b], r);
         uint64_t wu = 1, wl = 1;
         if (linear && b == kBins - 1) {
           // what the bins did not count: at most everything
@@ -803,6 +929,8 @@ sample_filtered_kernel(const SampleParams p) {
         } else if (by_mass && n) {
           if (shift == 0 && !linear) {
             wu = wl = fix(w(C::value(hi - b)));
+          } else if (linear && guess) {
+            wu = fix(b ? ex2((b + 0.5f) * per_bin) : 1.f);   // (the best lies at its bin's edge)
           } else if (linear) {
             wu = fix(fminf(ex2(b * per_bin) * (1.f + kSlack), 1.f)) + 1;
             wl = fix(ex2((b + 1) * per_bin) * (1.f - kSlack));
@@ -817,55 +945,70 @@ sample_filtered_kernel(const SampleParams p) {
         cu += up[q];
         cl += low[q];
       }
-      // The first bin whose upper (lower) cumulated measure reaches the target (the
-      // sums' roundings may leave it a little beyond everything): only the warp that
-      // holds it looks closer.
       const uint64_t wu_sum = warp_sum(cu), wl_sum = warp_sum(cl);
       if (lane == 0) {
         sh.warp[0][warp] = wu_sum;
         sh.warp[1][warp] = wl_sum;
       }
-      if (tid == 0) {
-        sh.found[0] = 0;
-        sh.found[1] = kBins - 1;
-        sh.found_cum = above;
-      }
       __syncthreads();
       const uint64_t tu = lane < kWarps ? sh.warp[0][lane] : 0, tl = lane < kWarps ? sh.warp[1][lane] : 0;
-      const uint64_t goal = min(target, warp_sum(tu) + above);
-      uint64_t at_u = warp_sum(lane < warp ? tu : 0) + above, at_l = warp_sum(lane < warp ? tl : 0) + above;
-      if (at_u < goal && goal <= at_u + wu_sum) {
-        at_u += warp_scan(cu) - cu;
+      const uint64_t share_u = warp_sum(tu), share_l = warp_sum(tl);
+      if (tid == 0) {
+        sh.share[0] = share_u;
+        sh.share[1] = share_l;
+      }
+      cluster_sync();
+      // The first bin whose upper (lower) cumulated measure reaches the target (the
+      // sums' roundings may leave it a little beyond everything): only the warp that
+      // holds it looks closer.
+      const uint64_t su = lane < CL ? ld_remote(&sh.share[0], lane) : 0;
+      const uint64_t sl = lane < CL ? ld_remote(&sh.share[1], lane) : 0;
+      const uint64_t goal = min(target, warp_sum(su) + above);
+      const uint64_t end_u = warp_scan(su) + above, end_l = warp_scan(sl) + above;
+      // the CTAs that hold them (none: 0, or everything)
+      const unsigned in_u = __ballot_sync(0xffffffffu, lane < CL && end_u - su < goal && goal <= end_u);
+      const unsigned in_l = __ballot_sync(0xffffffffu, lane < CL && end_l - sl < goal && goal <= end_l);
+      const int cta_u = __ffs(in_u) - 1, cta_l = __ffs(in_l) - 1;
+      if (cta_u == rank) {
+        uint64_t at = __shfl_sync(0xffffffffu, end_u - su, cta_u) + warp_sum(lane < warp ? tu : 0);
+        if (at < goal && goal <= at + wu_sum) {
+          at += warp_scan(cu) - cu;
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          if (at_u < goal && goal <= at_u + up[q]) {
-            sh.found[0] = kPer * tid + q;
-            sh.found_cum = at_u;
+          for (int q = 0; q < kPer; ++q) {
+            if (at < goal && goal <= at + up[q]) {
+              sh.found[0] = rank * kShare + kPer * tid + q;
+              sh.found_cum = at;
+            }
+            at += up[q];
           }
-          at_u += up[q];
         }
       }
-      if (at_l < goal && goal <= at_l + wl_sum) {
-        at_l += warp_scan(cl) - cl;
+      if (cta_l == rank) {
+        uint64_t at = __shfl_sync(0xffffffffu, end_l - sl, cta_l) + warp_sum(lane < warp ? tl : 0);
+        if (at < goal && goal <= at + wl_sum) {
+          at += warp_scan(cl) - cl;
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          if (at_l < goal && goal <= at_l + low[q]) sh.found[1] = kPer * tid + q;
-          at_l += low[q];
+          for (int q = 0; q < kPer; ++q) {
+            if (at < goal && goal <= at + low[q]) sh.found[1] = rank * kShare + kPer * tid + q;
+            at += low[q];
+          }
         }
       }
-      __syncthreads();
-      const uint32_t b1 = sh.found[0], b2 = max(sh.found[1], b1);
-      const uint64_t cum = sh.found_cum;
-      __syncthreads();
+      __syncwarp();
+      cluster_sync();
+      const uint32_t b1 = cta_u >= 0 ? ld_remote(&sh.found[0], cta_u) : 0;
+      const uint32_t b2 = max(cta_l >= 0 ? ld_remote(&sh.found[1], cta_l) : kBins - 1, b1);
+      const uint64_t cum = cta_u >= 0 ? ld_remote(&sh.found_cum, cta_u) : above;
       if (shift == 0 && !linear) return Found{hi - min(hi - lo, b1), cum, target};
       uint32_t nlo, nhi;
       if (linear) {
         // a little wider than the bins: the next level is exact about what lies above
-        const float bin = 1.f / scale;
-        const float hv = __fsub_ru(mx, __fmul_rd(b1 - 0.25f, bin));
-        const float lv = __fsub_rd(mx, __fmul_ru(b2 + 1.25f, bin));
+        const float bin = 1.f / scale, more = guess ? 0.75f : 0.25f;
+        const uint32_t last = guess ? b1 : b2;
+        const float hv = __fsub_ru(mx, __fmul_rd(fmaxf(b1 - more, -1.f), bin));
+        const float lv = __fsub_rd(mx, __fmul_ru(last + 1.f + more, bin));
         nhi = max(min(hi, C::of(hv)), lo);
-        nlo = b2 == kBins - 1 ? lo : min(max(lo, C::of(lv)), nhi);
+        nlo = last + (guess ? 1 : 0) >= kBins - 1 ? lo : min(max(lo, C::of(lv)), nhi);
         linear = false;
       } else {
         nhi = hi - min(hi - lo, b1 << shift);
@@ -886,7 +1029,7 @@ sample_filtered_kernel(const SampleParams p) {
               }
             ge += by_mass ? fix(s8) : n8;
           });
-          red.both<false>(ge, zero);
+          red.template both<false>(ge, zero);
           if (ge >= target) nlo = mid;
           else nhi = mid - 1;
         }
@@ -905,7 +1048,7 @@ sample_filtered_kernel(const SampleParams p) {
       for (int e = 0; e < 8; ++e) n += x[e] == mx ? 1 : 0;
     });
     __syncwarp();
-    red.both<false>(n, none);
+    red.template both<false>(n, none);
     if (k > 1) n = min(n, static_cast<uint64_t>(k));
     if (top_p < 1.f) n = min(n, max(mass_target(top_p, n), static_cast<uint64_t>(1)));
     t = mx;
@@ -946,7 +1089,10 @@ sample_filtered_kernel(const SampleParams p) {
   }
   // (the sum above over_v stands only if the border lies below it)
   if (t > over_v) over_v = CUDART_INF_F;
-  if (over_v == CUDART_INF_F) over_sum = 0;
+  if (over_v == CUDART_INF_F) {
+    over_sum = 0;
+    close = false;
+  }
 
   // kept mass and ties of every part, in token order
   const uint64_t one = m ? (isinf(mx) ? fix(1.f) : fix(w(t))) : 0;
@@ -959,6 +1105,12 @@ sample_filtered_kernel(const SampleParams p) {
       for (int e = 0; e < 8; e += 2) s2 = __fadd2_rn(s2, w.at(w.dist(x[e], x[e + 1])));
       gt += fix(s2.x + s2.y);
     });
+  } else if (close) {
+    for (uint32_t i = lane; i < sh.near_n[warp]; i += 32) {
+      const float x = near[i];
+      if (x > t) gt += fix(w(x));
+      if (x == t) ++ties;
+    }
   } else {
     part.each(t, [&](int, const float (&x)[8]) {
       uint32_t in = 0;                                     // above the border, not yet summed
@@ -999,7 +1151,7 @@ sample_filtered_kernel(const SampleParams p) {
   cluster_sync();
   uint64_t before_gt = 0, before_tie = 0, all_gt = 0, all_tie = 0;
 #pragma unroll
-  for (int r = 0; r < kCluster; ++r) {
+  for (int r = 0; r < CL; ++r) {
     const uint64_t a = ld_remote(&sh.xch[buf][0], r), b = ld_remote(&sh.xch[buf][1], r);
     all_gt += a;
     all_tie += b;
@@ -1016,77 +1168,137 @@ sample_filtered_kernel(const SampleParams p) {
   auto kept_ties = [&](uint64_t n) { return n < m ? n : static_cast<uint64_t>(m); };
   const uint64_t whole = all_gt + kept_ties(all_tie) * one;
   const uint64_t goal = draw_target(uf, whole);
-  // the part whose cumulated mass passes the goal
+  // The part whose cumulated mass passes the goal; all warps of its CTA look into it,
+  // each into some rounds of 256 tokens.
   const uint64_t cum = before_gt + kept_ties(before_tie) * one;
   const uint64_t part_end = before_gt + gt + kept_ties(before_tie + ties) * one;
-  if (cum <= goal && goal < part_end) {
-    uint64_t cg = before_gt, ct = before_tie;          // before this round
-    for (int i0 = 0; i0 < part.n; i0 += 256) {         // warp-uniform
-      const int i = i0 + lane * 8;
-      float x[8];
-      uint32_t tie = 0;
-      uint64_t g = 0;
-      if (i < part.n) {
-        part.at(i).get(x);
-        float s[2] = {0.f, 0.f}, over[2] = {0.f, 0.f};     // (in pairs, as they were summed)
+  if (tid == 0) sh.found[0] = kWarps;
+  __syncthreads();
+  if (lane == 0 && cum <= goal && goal < part_end) {
+    sh.found[0] = warp;
+    sh.before[0] = before_gt;
+    sh.before[1] = before_tie;
+  }
+  __syncthreads();
+  if (sh.found[0] < kWarps) {                              // block-uniform
+    const int owner = sh.found[0];
+    Part<T, RES> its = part;
+    its.id0 = (rank * kWarps + owner) * p.part;            // (holds a token: below vocab)
+    its.data = RES ? slice + (size_t)owner * p.part : src + its.id0;
+    its.n = min(p.part, p.vocab - its.id0);
+    const int rounds = (its.n + 255) / 256, r0 = rounds * warp / kWarps, r1 = rounds * (warp + 1) / kWarps;
+    auto chunk = [&](int i, float (&x)[8], uint64_t& g, uint32_t& tie) {
+      g = 0;
+      tie = 0;
+      if (i >= its.n) return;
+      its.at(i).get(x);
+      float s[2] = {0.f, 0.f}, over[2] = {0.f, 0.f};       // (in pairs, as they were summed)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float y = x[e] > t ? w(x[e]) : 0.f;
-          if (x[e] > over_v) over[e & 1] += y;
-          else s[e & 1] += y;
-          tie += x[e] == t ? 1 : 0;
-        }
-        g = fix(s[0] + s[1]) + fix(over[0] + over[1]);
+      for (int e = 0; e < 8; ++e) {
+        const float y = x[e] > t ? w(x[e]) : 0.f;
+        if (x[e] > over_v) over[e & 1] += y;
+        else if (close) g += fix(y);                       // (as these were)
+        else s[e & 1] += y;
+        tie += x[e] == t ? 1 : 0;
       }
-      const uint64_t ig = warp_scan(g), it = warp_scan(tie);
-      const bool past = cg + ig + kept_ties(ct + it) * one > goal;
-      const unsigned any = __ballot_sync(0xffffffffu, past);
-      if (any) {
-        if (lane == __ffs(any) - 1) {
-          const uint64_t g0 = cg + ig - g, t0 = ct + it - tie;
-          float s[2] = {0.f, 0.f}, over[2] = {0.f, 0.f}, got = 0.f;
-          uint32_t seen = 0;
-          int id = -1;
+      g += fix(s[0] + s[1]) + fix(over[0] + over[1]);
+    };
+    uint64_t sg = 0;
+    uint32_t st = 0, tie;
+    float x[8];
+    for (int r = r0; r < r1; ++r) {
+      uint64_t g;
+      chunk(r * 256 + lane * 8, x, g, tie);
+      sg += g;
+      st += tie;
+    }
+    sg = warp_sum(sg);
+    st = __reduce_add_sync(0xffffffffu, st);
+    if (lane == 0) {
+      sh.warp[0][warp] = sg;
+      sh.warp[1][warp] = st;
+    }
+    __syncthreads();
+    uint64_t cg = sh.before[0], ct = sh.before[1];         // before this warp's rounds
+    for (int x = 0; x < warp; ++x) {
+      cg += sh.warp[0][x];
+      ct += sh.warp[1][x];
+    }
+    if (cg + kept_ties(ct) * one <= goal && goal < cg + sg + kept_ties(ct + st) * one) {
+      for (int r = r0; r < r1; ++r) {                      // warp-uniform
+        const int i = r * 256 + lane * 8;
+        uint64_t g;
+        chunk(i, x, g, tie);
+        const uint64_t ig = warp_scan(g), it = warp_scan(tie);
+        const bool past = cg + ig + kept_ties(ct + it) * one > goal;
+        const unsigned any = __ballot_sync(0xffffffffu, past);
+        if (any) {
+          if (lane == __ffs(any) - 1) {
+            const uint64_t t0 = ct + it - tie;
+            uint64_t g0 = cg + ig - g;
+            float s[2] = {0.f, 0.f}, over[2] = {0.f, 0.f}, got = 0.f;
+            uint32_t seen = 0;
+            int id = -1;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const bool above = x[e] > t, at = x[e] == t;
-            if (above && x[e] > over_v) over[e & 1] += w(x[e]);
-            else if (above) s[e & 1] += w(x[e]);
-            if (at) ++seen;
-            if (id < 0 && (above || at) &&
-                g0 + fix(s[0] + s[1]) + fix(over[0] + over[1]) + kept_ties(t0 + seen) * one > goal) {
-              id = part.id0 + i + e;
-              got = x[e];
+            for (int e = 0; e < 8; ++e) {
+              const bool above = x[e] > t, at = x[e] == t;
+              if (above && x[e] > over_v) over[e & 1] += w(x[e]);
+              else if (above && close) g0 += fix(w(x[e]));
+              else if (above) s[e & 1] += w(x[e]);
+              if (at) ++seen;
+              if (id < 0 && (above || at) &&
+                  g0 + fix(s[0] + s[1]) + fix(over[0] + over[1]) + kept_ties(t0 + seen) * one > goal) {
+                id = its.id0 + i + e;
+                got = x[e];
+              }
             }
+            p.tok[row] = id;
+            p.logp[row] = log_share(got, mx, temp, whole);
           }
-          p.tok[row] = id;
-          p.logp[row] = log_share(got, mx, temp, whole);
+          break;
         }
-        break;
+        cg += __shfl_sync(0xffffffffu, ig, 31);
+        ct += __shfl_sync(0xffffffffu, it, 31);
       }
-      cg += __shfl_sync(0xffffffffu, ig, 31);
-      ct += __shfl_sync(0xffffffffu, it, 31);
     }
   }
   __syncwarp();
   cluster_wait();
 }
 
-template <typename T>
-void launch_sample(const SampleParams& p, int rows, cudaStream_t st) {
-  const size_t slice = (size_t)kWarps * p.part * sizeof(T);
+template <typename T, bool RES, int CL>
+void launch_cluster(SampleParams p, int rows, cudaStream_t st) {
+  p.part = ((p.vocab + CL * kWarps - 1) / (CL * kWarps) + 7) / 8 * 8;
+  const size_t near = kNearRow / CL * sizeof(float), slice = RES ? (size_t)kWarps * p.part * sizeof(T) : 0;
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !set[dev]) {
-    cudaFuncSetAttribute(sample_filtered_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         kMaxSlice);
+  if (RES && (dev < 0 || dev >= 64 || !set[dev])) {
+    cudaFuncSetAttribute(sample_filtered_kernel<T, RES, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         kMaxSlice + kWarps * 16 * sizeof(T) + near);
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  if (slice <= kMaxSlice)
-    launch_k(sample_filtered_kernel<T, true>, dim3(rows * kCluster), dim3(kThreads), slice, st, p);
+  launch_k(sample_filtered_kernel<T, RES, CL>, dim3(rows * CL), dim3(kThreads), near + slice, st, p);
+}
+
+template <typename T>
+void launch_sample(const SampleParams& p, int rows, cudaStream_t st) {
+  // Small clusters repeat less of a row's fixed work and leave room for more rows at
+  // once, large ones are sooner done with a row: once there is a CTA to every SM, the
+  // smallest cluster whose slices let several CTAs share an SM.  With top-p 0.9, bf16,
+  // clusters of 8 / 4 / 2, us: 400 rows of 8192 124 / 59 / 42, of 50000 156 / 89 / 76, of
+  // 100000 176 / 137 / 234, of 151936 211 / 212 / 312; 32 rows of 50000 25 / 24 / 30;
+  // one row of 151936 27 / 36 / 56.
+  auto slice = [&](int cl) { return ((long long)p.vocab * (int)sizeof(T) + cl - 1) / cl; };
+  auto fits = [&](int cl) { return (long long)rows * cl * 2 > num_sms() && slice(cl) <= kManySlice; };
+  if (slice(8) > kMaxSlice)
+    launch_cluster<T, false, 8>(p, rows, st);
+  else if (!fits(4))
+    launch_cluster<T, true, 8>(p, rows, st);
+  else if (!fits(2))
+    launch_cluster<T, true, 4>(p, rows, st);
   else
-    launch_k(sample_filtered_kernel<T, false>, dim3(rows * kCluster), dim3(kThreads), 0, st, p);
+    launch_cluster<T, true, 2>(p, rows, st);
 }
 
 }  // namespace
@@ -1109,7 +1321,6 @@ dflash_status dflash_logits_sample_filtered(int rows, int vocab, long long ld, i
   DFL_REQUIRE(logits && u && tok && logp, "sample filtered: null logits/u/tok/logp");
   SampleParams p{};
   p.vocab = vocab;
-  p.part = ((vocab + kParts - 1) / kParts + 7) / 8 * 8;
   p.ld = ld;
   p.logits = logits;
   p.temperature = temperature;

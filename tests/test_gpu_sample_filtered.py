@@ -229,3 +229,39 @@ def test_sampled_targets_walk_the_tree():
     for r in range(n_req):
         a, nodes, bon = odt.accept_walk(t[r], p[r], int(n_nodes[r]), picked.reshape(n_req, B + 1)[r], D)
         assert int(al[r]) == a and int(bonus[r]) == bon and np.array_equal(acc[r].cpu().numpy(), nodes)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,vocab", [(90, 1000), (45, 4099), (80, 24000), (40, 45001)])
+def test_sample_many_rows(n, vocab, dtype):
+    """Rows enough that two or four CTAs share one, every row with its own filters."""
+    rng = np.random.default_rng(n)
+    x = _logits(rng, n, vocab, dtype, scale=math.sqrt(2.0))
+    how = dict(temperature=rng.choice([0.0, 0.6, 1.0, 2.0], size=n), top_k=rng.choice([0, 0, 0, 1, 30, 300, 700], size=n),
+               top_p=rng.choice([1.0, 0.3, 0.8, 0.95], size=n), min_p=rng.choice([0.0, 0.0, 0.05], size=n))
+    _check(x, rng.random(n), how)
+
+
+@pytest.mark.parametrize("n", [6, 60])
+@pytest.mark.parametrize("steps", [1, 4, 64])
+def test_sample_logits_of_few_values(steps, n):
+    """Many tokens at each value (`steps` to a unit): more of them lie near a border
+    than are kept aside there, and the bins' middles misjudge their weights."""
+    rng = np.random.default_rng(steps)
+    vocab = 20011
+    x = torch.as_tensor((np.round(rng.normal(size=(n, vocab)) * steps) / steps).astype(np.float32)).to(DEV)
+    for how in (dict(top_p=0.9), dict(temperature=0.5, top_p=0.6), dict(top_k=5000, top_p=0.7), dict(temperature=3.0, top_p=0.3)):
+        _check(x, rng.random(n), {k: [v] * n for k, v in how.items()})
+
+
+@pytest.mark.parametrize("far", [3.0, 12.0, 40.0])
+def test_sample_mass_in_few_tokens(far):
+    """A handful of tokens holds the mass that top-p asks for, the rest lies far below."""
+    rng = np.random.default_rng(9)
+    n, vocab = 8, 30000
+    for dtype in (BF, F32):
+        x = _logits(rng, n, vocab, dtype, scale=0.5, fav=0.0)
+        for j in range(5):
+            x[torch.arange(n), torch.as_tensor(rng.integers(0, vocab, size=n))] = far + 0.25 * j
+        for p in (0.2, 0.5, 0.9, 0.999):
+            _check(x, rng.random(n), dict(top_p=[p] * n))
