@@ -358,6 +358,7 @@ def tree_rope(x: torch.Tensor, n_heads: int, head_dim: int, theta: float, ctx_le
 # asked for without building a Stream object (2.9 us against 0.1).
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _handle(stream, device: int):
@@ -370,21 +371,25 @@ def _handle(stream, device: int):
 
 def _together(*tensors) -> int:
     """The current CUDA device (the library launches there), which holds all tensors."""
-    at = {t.get_device() for t in tensors if t is not None}
-    dev = at.pop()
-    if at or dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError("expected CUDA tensors, all on the current device")
-    return dev
+    dev = next(t for t in tensors if t is not None).get_device()
+    if dev >= 0 and dev == _device():
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            return dev
+    raise ValueError("expected CUDA tensors, all on the current device")
 
 
 def _rows(t: torch.Tensor, name: str):
     """Pointer and row stride of a [rows, columns] view whose columns are adjacent."""
-    if t.dim() != 2:
+    by = t.stride()
+    if len(by) != 2:
         raise ValueError(f"{name}: expected [rows, columns]")
-    (n, width), (ld, step) = t.shape, t.stride()
-    if width > 1 and step != 1:
+    n, width = t.shape
+    if by[1] != 1 and width > 1:
         raise ValueError(f"{name}: expected adjacent columns")
-    return t.data_ptr(), ld if n > 1 else max(ld, width)
+    return t.data_ptr(), by[0] if n > 1 else max(by[0], width)
 
 
 def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str):
@@ -422,6 +427,25 @@ class Pages:
         self.ref = C.byref(self.struct)
 
 
+def _side(x, out, n: int, head_dim: int, dtype, name: str):
+    """Heads, and pointer and row stride of x and of out (None: in place)."""
+    if x is None:
+        if out is not None:
+            raise ValueError(f"{name}_out without {name}")
+        return 0, None, 0, None, 0
+    p, ld = _rows(x, name)
+    shape = x.shape
+    heads, rest = divmod(shape[1], head_dim)
+    if x.dtype is not dtype or shape[0] != n or rest:
+        raise ValueError(f"{name}: expected [{n}, heads * {head_dim}], all of one type")
+    if out is None:
+        return heads, p, ld, p, ld
+    if out.dtype is not dtype or out.shape != shape:
+        raise ValueError(f"{name}_out must have {name}'s shape and type")
+    po, ldo = _rows(out, name)
+    return heads, p, ld, po, ldo
+
+
 def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
                  q_gain: Optional[torch.Tensor], k_gain: Optional[torch.Tensor], eps: float,
                  theta: float, pos: Optional[torch.Tensor], head_dim: int,
@@ -436,22 +460,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
     n = first.shape[0]
     dev, dtype = _together(q, k, q_gain, k_gain, pos, q_out, k_out), first.dtype
 
-    def side(x, out, name):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"{name}_out without {name}")
-            return 0, None, 0, None, 0
-        p, ld = _rows(x, name)
-        if x.dtype is not dtype or x.shape[0] != n or x.shape[1] % head_dim:
-            raise ValueError(f"{name}: expected [{n}, heads * {head_dim}], all of one type")
-        if out is None:
-            return x.shape[1] // head_dim, p, ld, p, ld
-        if out.dtype is not dtype or out.shape != x.shape:
-            raise ValueError(f"{name}_out must have {name}'s shape and type")
-        return (x.shape[1] // head_dim, p, ld) + _rows(out, name + "_out")
-
-    n_q, qp, ql, qo, qol = side(q, q_out, "q")
-    n_kv, kp, kl, ko, kol = side(k, k_out, "k")
+    n_q, qp, ql, qo, qol = _side(q, q_out, n, head_dim, dtype, "q")
+    n_kv, kp, kl, ko, kol = _side(k, k_out, n, head_dim, dtype, "k")
     _check(lib().dflash_qk_norm_rope(
         n, n_q, n_kv, head_dim, _dtype_code(first),
         _vec(q_gain, head_dim, dtype, "q_gain"), _vec(k_gain, head_dim, dtype, "k_gain"), eps, theta,
