@@ -17,9 +17,9 @@
 // n * G query rows, TR to a tile.  All (request, KV head, tile) key ranges are
 // laid end to end in steps of KS keys, and every CTA takes an equal share of
 // that line, found on the device from row_off and pos0.  So ragged batches,
-// single long contexts and prompt chunks all fill the SMs, and a tile that a
-// share's border cuts is joined, in key order, by the last of its CTAs to
-// arrive (a counter, no waiting).
+// single long contexts and prompt chunks all fill the SMs.  A tile that shares'
+// borders cut is joined, in key order, by the last of its CTAs to arrive (a
+// counter, no waiting), or, where tiles fall into many parts, by a second kernel.
 //
 // Rows whose mask hides a key must not meet that key's value: 0 * NaN is not 0.
 // In steps where some row may not see some key, values that are not finite are
@@ -719,6 +719,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
     const float sc = p.scale_log2;
     uint32_t it = 0, nj = 0;                                 // ring base, jobs of this group
     bool ok = true;
+    if (p.cut && tid == 0) p.cut[blockIdx.x].c1 = -1;
     for (PagedPiece pc; c.left > 0; paged_next<Geo>(p, pc, &c)) {
       pc = PagedPiece::of<Geo>(c);
       if (pc.n <= 0) continue;
@@ -1059,40 +1060,45 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       ptx::tc_fence_before();
       if (!whole && mine) {
         if (live) __stcg(p.part_ml + slot * GT + row, make_float2(M, L));
-        __threadfence();
-        ptx::named_bar_sync(1 + x, GT);
-        if (row == 0) s_last[x] = atomicAdd(p.arrive + NG * c0 + x, 1) == c1 - c0;
-        ptx::named_bar_sync(1 + x, GT);
-        if (s_last[x]) {
+        if (p.cut) {
+          if (tid == 0 && c0 == static_cast<int>(blockIdx.x))   // its first piece
+            p.cut[c0] = {c1, rq.row0, tile0, nG, c.g * p.heads.G};
+        } else {
           __threadfence();
-          if (row == 0) p.arrive[NG * c0 + x] = 0;            // for the next call
-          if (!dead) {
-            M = -CUDART_INF_F;
+          ptx::named_bar_sync(1 + x, GT);
+          if (row == 0) s_last[x] = atomicAdd(p.arrive + NG * c0 + x, 1) == c1 - c0;
+          ptx::named_bar_sync(1 + x, GT);
+          if (s_last[x]) {
+            __threadfence();
+            if (row == 0) p.arrive[NG * c0 + x] = 0;            // for the next call
+            if (!dead) {
+              M = -CUDART_INF_F;
 #pragma unroll 4
-            for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_ml + part_of(cc) * GT + row).x);
-            float o[HD] = {};
-            L = 0.f;
-            float2 ml = __ldcg(p.part_ml + part_of(c0) * GT + row);
-            for (int cc = c0; cc <= c1; ++cc) {
-              const float2 now = ml;
-              if (cc < c1) ml = __ldcg(p.part_ml + part_of(cc + 1) * GT + row);
-              const float f = now.y != 0.f ? ex2(now.x - M) : 0.f;
-              L += f * now.y;
-              const float4* src = reinterpret_cast<const float4*>(p.part_o) + part_of(cc) * (HD / 4) * GT + row;
+              for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_ml + part_of(cc) * GT + row).x);
+              float o[HD] = {};
+              L = 0.f;
+              float2 ml = __ldcg(p.part_ml + part_of(c0) * GT + row);
+              for (int cc = c0; cc <= c1; ++cc) {
+                const float2 now = ml;
+                if (cc < c1) ml = __ldcg(p.part_ml + part_of(cc + 1) * GT + row);
+                const float f = now.y != 0.f ? ex2(now.x - M) : 0.f;
+                L += f * now.y;
+                const float4* src = reinterpret_cast<const float4*>(p.part_o) + part_of(cc) * (HD / 4) * GT + row;
 #pragma unroll
-              for (int j = 0; j < HD / 4; ++j) {
-                const float4 v = __ldcg(src + j * GT);
-                if (now.y != 0.f) {
-                  o[4 * j] += f * v.x;
-                  o[4 * j + 1] += f * v.y;
-                  o[4 * j + 2] += f * v.z;
-                  o[4 * j + 3] += f * v.w;
+                for (int j = 0; j < HD / 4; ++j) {
+                  const float4 v = __ldcg(src + j * GT);
+                  if (now.y != 0.f) {
+                    o[4 * j] += f * v.x;
+                    o[4 * j + 1] += f * v.y;
+                    o[4 * j + 2] += f * v.z;
+                    o[4 * j + 3] += f * v.w;
+                  }
                 }
               }
-            }
 #pragma unroll
-            for (int b = 0; b < HD / 32; ++b) put(b, reinterpret_cast<float(&)[32]>(o[32 * b]), 1.f / L);
-            send();
+              for (int b = 0; b < HD / 32; ++b) put(b, reinterpret_cast<float(&)[32]>(o[32 * b]), 1.f / L);
+              send();
+            }
           }
         }
       }
@@ -1112,8 +1118,93 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   }
 }
 
+// Joins the tiles that shares' borders cut, each 32 rows (a lane to a row) to a block of
+// eight warps, which share out the parts for the weights and the columns for the sums.
+// Blocks x: the CTA that holds a tile's first piece.  (32 warps to a block, a warp for
+// four columns, took longer: 128 rows over 4096 slots 32 us against 27.)
 template <int HD, int NG>
-dflash_status launch_tc(const PagedAttnParams& p, const dflash_pages& pages, cudaStream_t st) {
+__global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnParams p) {
+  constexpr int GT = Tc<HD, NG>::kGroup, kRound = 64, kFours = HD / 4, kCols = kFours / 8;
+  constexpr int kAtOnce = 16 / kCols;                        // parts whose loads are in flight
+  __shared__ float sF[kRound][32];
+  __shared__ float sW[2][8][32];
+  __shared__ __align__(16) uint2 sOut[32][kFours];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const PagedCut cut = p.cut[blockIdx.x];
+  const int rho = cut.rho0 + blockIdx.y * 32 + lane;
+  if (cut.c1 < 0 || rho - lane >= cut.nG) return;            // block-uniform
+  const int c0 = blockIdx.x, parts = cut.c1 - c0 + 1;
+  const int x = blockIdx.y * 32 / GT, row = blockIdx.y * 32 % GT + lane;
+  const bool live = rho < cut.nG;
+  auto at = [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0)) * NG + x; };
+  auto ml_of = [&](int k) { return live ? __ldcg(p.part_ml + at(k) * GT + row) : make_float2(-CUDART_INF_F, 0.f); };
+  float M = -CUDART_INF_F, L = 0.f;
+  for (int k = warp; k < parts; k += 8) M = fmaxf(M, ml_of(k).x);
+  sW[0][warp][lane] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, sW[0][w][lane]);
+  float4 acc[kCols] = {};
+  for (int r0 = 0; r0 < parts; r0 += kRound) {
+    const int n = min(parts - r0, kRound);
+    if (r0) __syncthreads();
+    for (int k = warp; k < n; k += 8) {
+      const float2 ml = ml_of(r0 + k);
+      const float f = ml.y != 0.f ? ex2(ml.x - M) : -1.f;    // (-1: a part that saw no key)
+      if (ml.y != 0.f) L += f * ml.y;
+      sF[k][lane] = f;
+    }
+    __syncthreads();
+    for (int k0 = 0; k0 < n; k0 += kAtOnce) {
+      float4 v[kAtOnce][kCols];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                            (at(r0 + min(k0 + k, n - 1)) * kFours + warp * kCols) * GT + row;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) v[k][j] = __ldcg(src + j * GT);
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float f = k0 + k < n ? sF[k0 + k][lane] : -1.f;
+        if (f >= 0.f) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            acc[j].x += f * v[k][j].x;
+            acc[j].y += f * v[k][j].y;
+            acc[j].z += f * v[k][j].z;
+            acc[j].w += f * v[k][j].w;
+          }
+        }
+      }
+    }
+  }
+  sW[1][warp][lane] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) L += sW[1][w][lane];
+  const float inv = 1.f / L;
+#pragma unroll
+  for (int j = 0; j < kCols; ++j)                            // a row that saw no key: zeros
+    sOut[lane][(warp * kCols + j) ^ (lane & 15)] =
+        L == 0.f ? make_uint2(0, 0)
+                 : make_uint2(mmas::pack_bf16(acc[j].x * inv, acc[j].y * inv),
+                              mmas::pack_bf16(acc[j].z * inv, acc[j].w * inv));
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * kFours; i += 256) {
+    const int r = i / kFours, ch = i % kFours, to = rho - lane + r;
+    if (to >= cut.nG) break;
+    const int tok = p.heads.quot(to), head = cut.head0 + to - tok * p.heads.G;
+    reinterpret_cast<uint2*>(p.out + (long long)(cut.row0 + tok) * p.out_ld + (long long)head * HD)[ch] =
+        sOut[r][ch ^ (r & 15)];
+  }
+}
+
+template <int HD, int NG>
+dflash_status launch_tc(PagedAttnParams p, const dflash_pages& pages, cudaStream_t st) {
   using S = Tc<HD, NG>;
   static bool set[64] = {};
   int dev = 0;
@@ -1129,13 +1220,22 @@ dflash_status launch_tc(const PagedAttnParams& p, const dflash_pages& pages, cud
       !encode_kmajor_map(&maps.v, pages.v, rows, HD, HD, box))
     return set_error(DFLASH_ERR_CUDA, "paged attention: cannot encode the TMA descriptors");
   TraceScope ts("paged_attn_tc", st);
-  launch_k(paged_attn_tc_kernel<HD, NG>, dim3(num_sms() * S::kPerSm), dim3(S::kThreads), S::kBytes, st, maps, p);
+  const int grid = num_sms() * S::kPerSm;
+  // A few parts to a tile are joined by the last CTA to arrive, which costs no launch
+  // and hides behind the others' work; many by a kernel of their own, since one CTA
+  // reads a part in about 2 us: 16 rows over 8192 slots (38 parts) 33 us against 95, 128
+  // over 4096 (19) 27 against 34; a prompt chunk (2) 245 against 237.
+  const long long tiles = (p.n_rows * (long long)p.heads.G + S::kRows - 1) / S::kRows * p.pv.n_kv;
+  if (tiles * 4 >= grid) p.cut = nullptr;
+  launch_k(paged_attn_tc_kernel<HD, NG>, dim3(grid), dim3(S::kThreads), S::kBytes, st, maps, p);
+  if (p.cut)
+    launch_k(paged_join_kernel<HD, NG>, dim3(grid, S::kRows / 32), dim3(256), 0, st, p);
   return DFLASH_OK;
 }
 
 // Header, arrival counters, (max, sum) pairs, partial rows.
 struct PagedWs {
-  size_t arrive, ml, o, bytes;
+  size_t arrive, cut, ml, o, bytes;
 };
 // Every kernel: two CTAs an SM at most, two counters an SM, and for each SM two
 // slots of 256 rows (or 2 x 2 of 128, or of 16).
@@ -1143,7 +1243,8 @@ PagedWs paged_ws(int sms, int head_dim) {
   PagedWs w;
   const size_t rows = (size_t)sms * 2 * 256;
   w.arrive = 256;
-  w.ml = w.arrive + align_up((size_t)sms * 2 * sizeof(int), 256);
+  w.cut = w.arrive + align_up((size_t)sms * 2 * sizeof(int), 256);
+  w.ml = w.cut + align_up((size_t)sms * 2 * sizeof(PagedCut), 256);
   w.o = w.ml + align_up(rows * sizeof(float2), 256);
   w.bytes = w.o + rows * head_dim * sizeof(float);
   return w;
@@ -1208,6 +1309,7 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
   p.arrive = reinterpret_cast<int*>(b + w.arrive);
   p.part_ml = reinterpret_cast<float2*>(b + w.ml);
   p.part_o = reinterpret_cast<float*>(b + w.o);
+  p.cut = reinterpret_cast<PagedCut*>(b + w.cut);
   p.status = reinterpret_cast<int*>(b);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // The smallest tile that takes all rows of a (request, KV head): keys and values

@@ -17,6 +17,12 @@ struct Heads {
   }
 };
 
+// A tile that shares' borders cut, noted by the CTA that holds its first piece: the
+// last CTA (-1: there is none), and which rows and heads they are.
+struct PagedCut {
+  int c1, row0, rho0, nG, head0;
+};
+
 struct PagedAttnParams {
   PagedView pv;
   int n_req, n_rows;
@@ -35,7 +41,8 @@ struct PagedAttnParams {
   // counters per CTA for the tile that begins there and goes on
   float* part_o;                   // [grid][2][rows][hd]
   float2* part_ml;                 // [grid][2][rows]
-  int* arrive;                     // [grid], or [grid][2] (halves of a tile)
+  int* arrive;                     // [grid] (few rows)
+  PagedCut* cut;                   // [grid] (many rows)
   int* status;
 };
 
