@@ -54,7 +54,7 @@ constexpr float kLazy = 8.f;   // a row's reference maximum may lag by this much
 // has no block barrier.  The four states meet when the tile ends.
 // Two CTAs share an SM: one streams while the other begins or ends a tile.
 constexpr int kRowsS = 16, kStepS = 64, kStagesS = 3, kThreadsS = 128, kPerSmS = 2;
-using GeoS = PagedGeo<kRowsS, kStepS, 4, kRowsS>;
+using GeoS = PagedGeo<kRowsS, kStepS, 4, kRowsS, 1>;
 
 template <int HD>
 struct SmallSmem {
@@ -436,7 +436,7 @@ struct Tc {
   static constexpr int kGroup = NG == 2 ? 128 : 64;         // rows, and threads, of a softmax group
   static constexpr int kRows = kGroup * NG, kWarps = kRows / 32;
   static constexpr int kThreads = NG == 2 ? 384 : 128, kPerSm = NG == 2 ? 1 : 2;
-  using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 12 : 3, 128>;
+  using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 12 : 3, 128, NG == 2 ? 1 : 3>;
   static constexpr int kAtomQ = kGroup * 128;               // 64 columns of a group's rows of Q
   static constexpr int kTileQ = (HD / 64) * kAtomQ;
   static constexpr int kKeys = NG == 2 ? 128 : 64;          // of a ring slot

@@ -48,10 +48,18 @@ struct PagedAttnParams {
 
 // Geometry of a kernel's work: TR query rows to a tile, KS keys to a step.  What a
 // tile weighs when the work is shared out: TC for its beginning and end, and for
-// each step 1, or 2 where the tile has more than HALF rows.
-template <int TR_, int KS_, int TC_, int HALF_>
+// each step 1, or 2 where the tile has more than HALF rows.  A share weighs MIN at
+// least (little work leaves CTAs without any).  Measured, us:
+//   256-row tiles, TC 4 / 8 / 12 / 16: 257 rows over 8192 slots 63 / 59 / 58 / 57, nine
+//     ragged chunks at head size 64 49 / 45 / 44 / 46;
+//   64-row tiles, TC 1 / 3 / 6 / 10: 32 requests of 16 rows 114 / 110 / 111 / 115;
+//     MIN 1 / 3 / 5: 16 rows over 8192 slots 33 / 24 / 23, over 2048 17.6 / 17.1 / 19.3,
+//     9 rows over 300 12.7 / 13.8 / 17.0;
+//   16-row tiles, TC 2 .. 12: no difference; MIN 1 / 2 / 4: one row over 2048 slots 10.4 /
+//     10.0 / 11.3, over 500 8.4 / 8.9 / 10.5.
+template <int TR_, int KS_, int TC_, int HALF_, int MIN_>
 struct PagedGeo {
-  static constexpr int TR = TR_, KS = KS_, TC = TC_, HALF = HALF_;
+  static constexpr int TR = TR_, KS = KS_, TC = TC_, HALF = HALF_, MIN = MIN_;
   // Shares are whole multiples of the largest weight: every CTA between the first
   // and the last of a tile then holds a step of it.
   static constexpr int UNIT = HALF_ < TR_ ? 2 : 1;
@@ -104,6 +112,7 @@ struct PagedCursor {
   int r, g, j;             // request, KV head, tile
   int at, length, weight;  // place in the tile, its length, a step's weight
   long long left;          // what is left of the share
+  int ctas;                // that have shares
   PagedReq rq;
 };
 
@@ -168,8 +177,9 @@ __device__ __forceinline__ void paged_plan(const PagedAttnParams& p, int lane, l
   for (int r = lane * run; r < last; ++r) mine += length_of(r, &q);
   long long upto = scan(mine);
   const long long total = __shfl_sync(0xffffffffu, upto, 31);
-  const long long begin = paged_share<Geo>(total, blockIdx.x, gridDim.x);
-  const long long end = paged_share<Geo>(total, blockIdx.x + 1, gridDim.x);
+  c->ctas = static_cast<int>(min((long long)gridDim.x, max(div_pos(total, Geo::MIN), 1ll)));
+  const long long begin = paged_share<Geo>(total, blockIdx.x, c->ctas);
+  const long long end = paged_share<Geo>(total, blockIdx.x + 1, c->ctas);
   *total_out = total;
   *end_out = end;
   c->left = end - begin;
@@ -243,8 +253,8 @@ __device__ __forceinline__ void paged_next(const PagedAttnParams& p, const Paged
 template <typename Geo>
 __device__ __forceinline__ void paged_owners(const PagedCursor& c, long long total, long long tile0, int all,
                                              int* c0, int* c1) {
-  *c0 = paged_owner<Geo>(total, tile0 + Geo::TC, gridDim.x);
-  *c1 = paged_owner<Geo>(total, tile0 + Geo::TC + (long long)(all - 1) * c.weight, gridDim.x);
+  *c0 = paged_owner<Geo>(total, tile0 + Geo::TC, c.ctas);
+  *c1 = paged_owner<Geo>(total, tile0 + Geo::TC + (long long)(all - 1) * c.weight, c.ctas);
 }
 
 }  // namespace dfl
