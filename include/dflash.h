@@ -517,14 +517,14 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
  * kernel; results do not depend on it being tight.  Sizes stay on the device,
  * so a captured call serves contexts that grow.  The work (requests x KV heads
  * x query tiles x key tiles) is split evenly over the SMs; a tile split between
- * CTAs is joined in key order by the last of them, so results do not depend on
- * timing.  A visible slot whose page is not there reads as zeros and records
+ * CTAs is joined in key order, so results do not depend on timing.  A visible slot whose page is not there reads as zeros and records
  * DFLASH_ERR_INVALID_ARG in the workspace status word.
- * Requires DFLASH_BF16 pages, n_q a multiple of n_kv, strides that are
- * multiples of 8 elements and 16-byte aligned q and out.  ws of
+ * Requires DFLASH_BF16 pages, n_q a multiple of n_kv, n_rows * n_q < 2^30,
+ * strides that are multiples of 8 elements and 16-byte aligned q and out.  ws of
  * dflash_paged_attention_workspace_bytes bytes, zeroed once
  * (dflash_workspace_init) before the first call; every call leaves its counters
- * at zero.  Calls sharing a workspace must not overlap. */
+ * at zero, unless the status word reads DFLASH_ERR_TIMEOUT: then the workspace
+ * has to be zeroed again.  Calls sharing a workspace must not overlap. */
 size_t dflash_paged_attention_workspace_bytes(int n_q, int n_kv, int head_dim);
 dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n_rows, int n_q,
                                      const int32_t* row_off, const int32_t* pos0, int max_rows,

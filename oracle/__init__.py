@@ -17,7 +17,10 @@ scores), with no tiling, fusion or reordering:
 * ``ddtree``   - Algorithm 1 (best-first heap over rank tuples), the tree
                  attention mask and the verifier walk (DDTree page, sections
                  3.4.3-3.4.5);
-* ``cycle``    - the speedup identity of Equation 1 (DFlash page, 3.4.1).
+* ``cycle``    - the speedup identity of Equation 1 (DFlash page, 3.4.1);
+* ``paged``    - the target's pass over a paged cache: norm and rotation, append,
+                 attention, filtered sampling (DDTree page, 3.4.5; DFlash page,
+                 3.4.4).
 
 Each function is pinned by tests in ``tests/test_oracle_*.py`` against facts
 the pages or mathematics fix (worked examples, closed forms, brute force,
