@@ -57,7 +57,10 @@ constexpr float kLazy = 8.f;   // a row's reference maximum may lag by this much
 // take 99 us, 6.2 TB/s of the 6.8 that a copy reaches; with one CTA to an SM 136.  One
 // request over 2048 slots takes 10 us: launch, plan, one step and the join.
 constexpr int kRowsS = 16, kStepS = 64, kStagesS = 3, kThreadsS = 128, kPerSmS = 2;
-using GeoS = PagedGeo<kRowsS, kStepS, 4, kRowsS, 1>;
+// Parts of a tile whose loads are in flight when they are joined (8 / 16 / 20: one row over
+// 2048 slots 10.0 / 9.9 / 9.6 us, four rows 15.6 / 15.5 / 14.1, one over 500 9.0 / 9.2 / 9.3).
+constexpr int kJoinS = 20;
+using GeoS = PagedGeo<kRowsS, kStepS, 4, kRowsS, 2>;
 
 template <int HD>
 struct SmallSmem {
@@ -362,16 +365,16 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
           float M = -CUDART_INF_F, L = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int k = 0; k < parts; ++k) M = fmaxf(M, sPart[k * kRowsS + row].x);
-          for (int k0 = 0; k0 < parts; k0 += 8) {        // eight loads in flight
-            float4 v[8];
+          for (int k0 = 0; k0 < parts; k0 += kJoinS) {    // their loads in flight
+            float4 v[kJoinS];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kJoinS; ++k) {
               const int cc = c0 + min(k0 + k, parts - 1);
               v[k] = __ldcg(reinterpret_cast<const float4*>(
                   p.part_o + (((size_t)cc * 2 + (cc == c0)) * kRowsS + row) * HD + col));
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kJoinS; ++k) {
               const float2 ml = sPart[min(k0 + k, parts - 1) * kRowsS + row];
               if (k0 + k >= parts || ml.y == 0.f) continue;
               const float f = ex2(ml.x - M);

@@ -56,7 +56,7 @@ struct PagedAttnParams {
 //     MIN 1 / 3 / 5: 16 rows over 8192 slots 33 / 24 / 23, over 2048 17.6 / 17.1 / 19.3,
 //     9 rows over 300 12.7 / 13.8 / 17.0;
 //   16-row tiles, TC 2 .. 12: no difference; MIN 1 / 2 / 4: one row over 2048 slots 10.4 /
-//     10.0 / 11.3, over 500 8.4 / 8.9 / 10.5.
+//     10.0 / 11.3, over 500 8.4 / 8.9 / 10.5, four rows over 2048 18.9 / 15.6 / -.
 template <int TR_, int KS_, int TC_, int HALF_, int MIN_>
 struct PagedGeo {
   static constexpr int TR = TR_, KS = KS_, TC = TC_, HALF = HALF_, MIN = MIN_;

@@ -32,8 +32,8 @@ dflash_status check_pages(const dflash_pages* p, const char* what, PagedView* ou
               "%s: page_size must be a power of two in [16, 1024]", what);
   DFL_REQUIRE(p->n_kv >= 1 && p->n_pages >= 1 && p->table_ld >= 1,
               "%s: need n_kv, n_pages and table_ld >= 1", what);
-  DFL_REQUIRE((long long)p->table_ld * p->page_size < (1ll << 31),
-              "%s: a request's slots exceed 2^31", what);
+  DFL_REQUIRE((long long)p->table_ld * p->page_size <= (1ll << 30),
+              "%s: a request's slots exceed 2^30", what);      // (and rows added do not pass 2^31)
   DFL_REQUIRE((long long)p->n_pages * p->n_kv * p->page_size < (1ll << 31),
               "%s: the pool's rows exceed 2^31", what);
   DFL_REQUIRE(p->k && p->v && p->table, "%s: null pool or table", what);

@@ -442,7 +442,8 @@ dflash_status dflash_tree_rope(int n_req, int B, int n_heads, int head_dim, floa
  *   k, v   T [n_pages][n_kv][page_size][head_dim] (device), 16-byte aligned
  *   table  int32 [n_req][table_ld] (device)
  * Requires page_size a power of two in [16, 1024], head_dim 64 or 128,
- * table_ld >= 1, n_pages >= 1; dtype DFLASH_BF16 or DFLASH_F32. */
+ * table_ld >= 1, table_ld * page_size <= 2^30, n_pages >= 1,
+ * n_pages * n_kv * page_size < 2^31; dtype DFLASH_BF16 or DFLASH_F32. */
 typedef struct dflash_pages {
   void* k;
   void* v;
@@ -550,7 +551,7 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
  * +inf they share the mass.  A row of -inf alone gives tok -1, logp -inf.
  *   logits  [rows] of dtype, ld elements apart, vocab <= ld
  * Masses are 64-bit sums of fp32 exponentials with 40 fractional bits, so
- * results depend neither on timing nor on the other rows.  rows may be 0.
+ * results depend neither on timing nor on what other rows hold.  rows may be 0.
  * Requires 1 <= vocab <= 2^22.  Needs no workspace. */
 dflash_status dflash_logits_sample_filtered(int rows, int vocab, long long ld, int dtype,
                                             const void* logits, const float* temperature,

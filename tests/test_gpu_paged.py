@@ -560,3 +560,24 @@ def test_pools_past_32_bit_offsets():
                 t = ctx[r] + i
                 assert torch.equal(d["pv"][own[r, t // page], :, t % page].reshape(-1), v[off[r] + i])
         _check(d, out)
+
+
+@pytest.mark.parametrize("rows,ctx,n_q,n_kv,hd,page,tree", [
+    ([16] * 10 + [7], [50 + 61 * i for i in range(11)], 32, 8, 128, 16, False),
+    ([16] * 10 + [7], [50 + 61 * i for i in range(11)], 32, 8, 64, 64, True),
+    ([150, 90, 33], [300, 700, 0], 32, 8, 128, 64, False),
+    ([150, 90, 33], [300, 700, 0], 32, 8, 128, 16, True),
+    ([600], [500], 16, 8, 64, 128, False),
+    ([260, 300], [90, 31], 16, 8, 64, 32, True),
+])
+def test_attention_more_tiles_than_parts(rows, ctx, n_q, n_kv, hd, page, tree):
+    """Tiles enough that each falls into few parts, which the CTAs join themselves."""
+    test_attention((rows, ctx, n_q, n_kv, hd, page, tree))
+
+
+@pytest.mark.parametrize("rows,ctx,n_q,n_kv,hd,tree", [
+    ([16], [30000], 4, 1, 128, False), ([12], [27000], 4, 1, 64, True), ([64], [10000], 4, 1, 128, False),
+    ([33], [7000], 8, 1, 64, True), ([100, 0, 1], [4000, 3, 800], 4, 1, 128, False)])
+def test_attention_few_tiles_in_many_parts(rows, ctx, n_q, n_kv, hd, tree):
+    """One long context on all SMs: tens of parts to a tile, more than are weighed at once."""
+    test_attention((rows, ctx, n_q, n_kv, hd, 16, tree))

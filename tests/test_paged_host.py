@@ -116,3 +116,9 @@ def test_binding_refuses_host_tensors():
         binding.qk_norm_rope(None, None, None, None, 0.0, 0.0, None, 64)
     with pytest.raises(ValueError):
         binding.logits_sample_filtered(z(2, 10), z(2), z(2, dtype=torch.int32), z(2))
+
+
+def test_slots_past_the_limit(lib):
+    """A request's slots, and the rows added to them, stay within 32 bits."""
+    assert _append(lib, _pages(table_ld=(1 << 26) + 1)) == 1 and _attn(lib, _pages(table_ld=(1 << 26) + 1)) == 1
+    assert _append(lib, _pages(table_ld=1 << 26), n_rows=0) == 0 and _attn(lib, _pages(table_ld=1 << 26), n_rows=0) == 0
