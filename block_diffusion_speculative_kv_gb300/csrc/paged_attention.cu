@@ -420,18 +420,22 @@ void launch_small(const PagedAttnParams& p, cudaStream_t st) {
 // two CTAs share an SM: memory bounds these tiles, and one CTA streams while the
 // other begins or ends a tile.
 // What bounds them.  NG = 1: memory; 32 requests of 16 rows over 512 .. 8192 slots take
-// 110 us, 5.5 TB/s.  NG = 2: a prompt chunk of 2048 rows over 8192 slots takes 237 us,
-// 1.30 PFLOP/s; of the 3250 clocks of a step the tensor cores work 2100, the rest is the
-// chain scores - softmax - product of each group, which the other group's only partly
-// hides.  The exponential unit is not it: with one exponential in four as a polynomial
-// on the FMA pipe the chunk took 262 us, with one in eight 241.  Small tiles, short
+// 110 us, 5.5 TB/s.  NG = 2: a prompt chunk of 2048 rows over 8192 slots takes 231 us,
+// 1.34 PFLOP/s.  A step of a group is a chain: 420 clocks to read the scores from TMEM,
+// 400 for their maximum, 1250 for the probabilities, 900 for the rest of P V and the
+// next scores; the other group's hides behind it.  The tensor cores need 2830 a step at
+// least, not the 2080 of their rate: both operands of the scores come from shared
+// memory, 8 KB to an MMA of 64 clocks, which is all that it delivers.  The exponential
+// unit is not it: with one exponential in four as a polynomial on the FMA pipe the chunk
+// took 262 us against 237, with one in eight 241; nor did it help to read half the scores
+// while the other half's maximum is found (240 against 231), or to form the first 32 keys
+// of P before the maximum is known (231).  Small tiles, short
 // contexts: beginning and ending a tile, about 6 us for the query rows on their way in
 // and O on its way out, 257 rows over 8192 slots 57 us.
 // After the softmax warps, one loads (TMA, a ring of K and V tiles that runs ahead
 // over tile borders; a box is a page, or a slot of a larger one), the next one
-// issues the MMAs.  A
-// row's O is rescaled only when its maximum has risen by more than 8 (base-2
-// units) over the reference in use.  Every wait is bounded (2 s); on expiry the CTA
+// issues the MMAs.  A row's O is rescaled only when its maximum has risen by more
+// than 8 (base-2 units) over the reference in use.  Every wait is bounded (2 s); on expiry the CTA
 // records DFLASH_ERR_TIMEOUT, lets its copies and MMAs land, frees TMEM and returns.
 constexpr int kStepT = 128;
 // Registers with NG = 2: the launch's 168 for each of three warpgroups, of which
@@ -455,6 +459,10 @@ struct Tc {
   static constexpr int kTileQ = (HD / 64) * kAtomQ;
   static constexpr int kKeys = NG == 2 ? 128 : 64;          // of a ring slot
   static constexpr int kPer = kStepT / kKeys;               // slots of a step's K, or V
+  // Keys of P that go out first: what the tensor cores do with the rest before the
+  // next scores lies on the chain (64 / 96 keys first: the chunk above 237 / 231 us).
+  // NG = 1: a slot of V.
+  static constexpr int kEarly = NG == 2 ? 96 : 64;
   static constexpr int kAtom = kKeys * 128, kSlot = (HD / 64) * kAtom;
   static constexpr int kSlots = HD == 64 ? 8 : NG == 2 ? 5 : 6;
   static constexpr int kRing = NG * kTileQ;                 // after Q
@@ -689,7 +697,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
             const uint32_t s = vs[kPer == 2 ? h : 0];
             const uint64_t v0 = dv + s * (S::kSlot >> 4);
 #pragma unroll
-            for (int j = 4 * h; j < 4 * h + 4; ++j)
+            for (int j = h * (S::kEarly / 16); j < (h ? kStepT : S::kEarly) / 16; ++j)
               ptx::mma_bf16_ta(tbase_o + 128 * x, tbase + 128 * x + j * 8,
                                v0 + (j % (S::kKeys / 16)) * (2048 >> 4), idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
             if (h == 1) ptx::mma_commit(&pv_done[x]);
@@ -875,20 +883,19 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
           const float2 sc2 = make_float2(sc, sc), nb2 = make_float2(-base, -base);
           float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
+          for (int b = 0; b < 4; ++b) {
+            float pk[16];                                      // (two bf16 each)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int b = 2 * h + (j >> 4), e = 2 * (j & 15);
+            for (int j = 0; j < 16; ++j) {
               const float2 y = __ffma2_rn(
-                  make_float2(__uint_as_float(u[b][e]), __uint_as_float(u[b][e + 1])), sc2, nb2);
+                  make_float2(__uint_as_float(u[b][2 * j]), __uint_as_float(u[b][2 * j + 1])), sc2, nb2);
               const float2 w = make_float2(ex2(y.x), ex2(y.y));
               rs[j & 1] = __fadd2_rn(rs[j & 1], w);
-              pk[j] = mmas::pack_bf16(w.x, w.y);
+              pk[j] = __uint_as_float(mmas::pack_bf16(w.x, w.y));
             }
-            ptx::tmem_st_32x32(aS + 32 * h, pk);
-            if (h == 0 && early) {
-              // the first half of P may meet V while the second is formed
+            ptx::tmem_st_32x16(aS + 16 * b, pk);
+            if (b == S::kEarly / 32 - 1 && early) {
+              // the first keys of P may meet V while the others are formed
               ptx::tmem_wait_st();
               ptx::tc_fence_before();
               __syncwarp();
