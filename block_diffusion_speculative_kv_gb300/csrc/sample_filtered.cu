@@ -14,7 +14,8 @@
 //
 // One cluster of 2, 4 or 8 CTAs per row: each CTA keeps its slice of the row in
 // shared memory (rows too long for that are read again from global memory), so HBM
-// sees the logits once.  Counts and masses are whole numbers (a mass has 40
+// sees the logits once.  (Many long rows, whose slices would leave an SM one or two
+// CTAs, are read again too.)  Counts and masses are whole numbers (a mass has 40
 // fractional bits), so their sums over lanes, warps and CTAs do not depend on
 // the order and every pass agrees with every other.
 //
@@ -43,10 +44,10 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxima = 8 * kThreads;              // parts of a row whose maxima are compared
 constexpr int kMaxSlice = 196 * 1024;              // resident slice bytes
-constexpr int kManySlice = 52 * 1024;              // of several CTAs to an SM
+constexpr int kManySlice = 52 * 1024, kFewSlice = 40 * 1024;   // of three, four CTAs to an SM
 constexpr int kListK = 512, kList = 1024;          // largest k, and tokens, of the gathered list
 constexpr int kListPer = kList / kThreads;
-constexpr int kBins = 1024;                        // of a search level
+constexpr int kBins = 1024;                        // of a search level (512: no faster, 256: 165 us, not 132)
 constexpr int kNearRow = 8192;                     // tokens kept near the border, of a row
 // A bin's weight bounds are widened by this much: exponents of up to 44 times a
 // few roundings of 2^-24 stay below 2^-15.
@@ -1288,13 +1289,18 @@ void launch_sample(const SampleParams& p, int rows, cudaStream_t st) {
   // smallest cluster whose slices let several CTAs share an SM.  With top-p 0.9, bf16,
   // clusters of 8 / 4 / 2, us: 400 rows of 8192 124 / 59 / 42, of 50000 156 / 89 / 76, of
   // 100000 176 / 137 / 234, of 151936 211 / 212 / 312; 32 rows of 50000 25 / 24 / 30;
-  // one row of 151936 27 / 36 / 56.
+  // one row of 151936 27 / 36 / 56.  Slices of which few fit an SM are worse than none: 128
+  // rows of 250000 118 resident in clusters of 8, 109 read again (from L2, mostly) in
+  // clusters of 4; fp32, 400 rows of 75000 231 / 173, of 151936 444 / 248; bf16, 480 rows
+  // of 151936 with mixed filters 132 / 136.
   auto slice = [&](int cl) { return ((long long)p.vocab * (int)sizeof(T) + cl - 1) / cl; };
   auto fits = [&](int cl) { return (long long)rows * cl * 2 > num_sms() && slice(cl) <= kManySlice; };
   if (slice(8) > kMaxSlice)
     launch_cluster<T, false, 8>(p, rows, st);
-  else if (!fits(4))
+  else if (!fits(4) && (slice(8) <= kFewSlice || (long long)rows * 4 <= num_sms()))
     launch_cluster<T, true, 8>(p, rows, st);
+  else if (!fits(4))
+    launch_cluster<T, false, 4>(p, rows, st);
   else if (!fits(2))
     launch_cluster<T, true, 4>(p, rows, st);
   else

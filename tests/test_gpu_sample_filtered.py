@@ -232,9 +232,10 @@ def test_sampled_targets_walk_the_tree():
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("n,vocab", [(90, 1000), (45, 4099), (80, 24000), (40, 45001)])
+@pytest.mark.parametrize("n,vocab", [(200, 1), (150, 3), (160, 33), (90, 1000), (45, 4099), (80, 24000), (40, 45001), (42, 100001)])
 def test_sample_many_rows(n, vocab, dtype):
-    """Rows enough that two or four CTAs share one, every row with its own filters."""
+    """Rows enough that two or four CTAs share one, every row with its own filters; the
+    last in fp32 long enough to be read again instead of kept."""
     rng = np.random.default_rng(n)
     x = _logits(rng, n, vocab, dtype, scale=math.sqrt(2.0))
     how = dict(temperature=rng.choice([0.0, 0.6, 1.0, 2.0], size=n), top_k=rng.choice([0, 0, 0, 1, 30, 300, 700], size=n),
