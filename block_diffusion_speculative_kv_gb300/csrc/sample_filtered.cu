@@ -224,6 +224,7 @@ __device__ __forceinline__ uint64_t fix(float w) {
 template <typename T>
 struct Codes {
   static constexpr int kShift = sizeof(T) == 2 ? 16 : 0;
+  static constexpr uint32_t kMinusZero = 0x7FFFFFFFu >> kShift;   // no token's: of() folds -0 onto +0
   __device__ static __forceinline__ uint32_t of(float x) { return ordered_bits(x) >> kShift; }
   __device__ static __forceinline__ float value(uint32_t c) {
     uint32_t k = c << kShift;
@@ -1035,8 +1036,10 @@ sample_filtered_kernel(const SampleParams p) {
           else nhi = mid - 1;
         }
       }
-      lo = nlo;
-      hi = nhi;
+      // Tokens are told from the bracket by value, where -0 is 0, and counted by code: a
+      // bracket that ended at the code of -0 would count the zeros in front of the bins.
+      hi = nhi == C::kMinusZero ? nhi - 1 : nhi;
+      lo = min(nlo, hi);
     }
   };
 

@@ -266,3 +266,25 @@ def test_sample_mass_in_few_tokens(far):
             x[torch.arange(n), torch.as_tensor(rng.integers(0, vocab, size=n))] = far + 0.25 * j
         for p in (0.2, 0.5, 0.9, 0.999):
             _check(x, rng.random(n), dict(top_p=[p] * n))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sample_border_just_below_zero(dtype):
+    """Borders among the smallest negative numbers, next to logits of both zeros: the
+    codes of a search's bracket skip -0, which no token has.  The best token's value
+    moves, so that brackets end at every place."""
+    n = 192
+    vocab = 3000
+    x = torch.zeros(n, vocab, device=DEV)
+    x[:, ::3] = -0.0
+    x[:, 600:] = -1e-39                                # (subnormal in both types)
+    x[:, 2000:] = -3.0
+    x[:, 7] = torch.arange(n, device=DEV) / 16 + 4
+    x = x.to(dtype)
+    u = (np.arange(n) + 0.5) / n
+    for how in (dict(top_k=1000), dict(top_k=600), dict(top_k=601), dict(top_p=0.6), dict(top_p=0.6, top_k=1500),
+                dict(temperature=0.01, top_k=900, top_p=0.999)):
+        _check(x, u, {k: [v] * n for k, v in how.items()})
+    # the first 1000 ids, of 600 tokens at 0 or above and ties below them
+    tok, lp = _run(x, [1.0] * n, dict(top_k=[1000] * n, temperature=[1e30] * n))
+    assert (tok == 999).all() and np.allclose(lp, -math.log(1000), atol=1e-6)
