@@ -154,7 +154,8 @@ struct Turns {
   }
 };
 
-// i / n for 0 <= i < 2^31 / n, with m = divide_by(n).
+// i / n for 0 <= i < 2^31 / n, with m = divide_by(n).  A CTA divides i < 8 n (its
+// rows' heads), so n may be 2^14 (kMaxHeads, below).
 struct DivideBy {
   uint32_t n, m;
   __device__ __forceinline__ int operator()(int i) const {
@@ -172,6 +173,8 @@ constexpr int kThreads = 256;
 // 7.2, of 8197 rows 58.7 and 30.0 (5.6 TB/s); the append of 8 heads 3.2 and 3.8, 4.7
 // and 4.0, 24.8 and 14.9.
 constexpr int kNormRows = 8, kAppendRows = 8;
+constexpr int kMaxHeads = 1 << 14;
+static_assert((long long)kNormRows * kMaxHeads * kMaxHeads <= 1ll << 31 && kAppendRows <= kNormRows, "DivideBy");
 
 struct NormRopeParams {
   int n_rows, n_q, n_kv;
@@ -394,6 +397,7 @@ dflash_status dflash_qk_norm_rope(int n_rows, int n_q, int n_kv, int head_dim, i
                                   long long q_out_ld, void* k_out, long long k_out_ld,
                                   void* stream) {
   DFL_REQUIRE(n_rows >= 0 && n_q >= 0 && n_kv >= 0, "qk norm rope: sizes must be >= 0");
+  DFL_REQUIRE(n_q <= kMaxHeads && n_kv <= kMaxHeads, "qk norm rope: more than %d heads", kMaxHeads);
   DFL_REQUIRE(head_dim == 64 || head_dim == 128, "qk norm rope: head_dim must be 64 or 128");
   DFL_REQUIRE(dtype == DFLASH_F32 || dtype == DFLASH_BF16, "qk norm rope: dtype must be F32 or BF16");
   DFL_REQUIRE(eps >= 0.f && eps < 1e30f, "qk norm rope: eps must be >= 0");
@@ -455,6 +459,7 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
   const dflash_status s = check_pages(pages, "paged append", &p.pv);
   if (s) return s;
   DFL_REQUIRE(n_req >= 0 && n_rows >= 0, "paged append: sizes must be >= 0");
+  DFL_REQUIRE(2 * (long long)pages->n_kv <= kMaxHeads, "paged append: more than %d KV heads", kMaxHeads / 2);
   DFL_REQUIRE(kv_ld >= (long long)pages->n_kv * pages->head_dim, "paged append: row stride too small");
   DFL_REQUIRE(theta == 0.f || (theta > 0.f && theta < 1e30f),
               "paged append: theta must be 0 (no rotation) or positive");

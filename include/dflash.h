@@ -470,8 +470,8 @@ typedef struct dflash_pages {
  *                 is not allowed
  *   q_gain/k_gain T [head_dim]
  *   pos           int32 [n_rows] (device)
- * n_q or n_kv may be 0 (its pointers are then not read).  head_dim 64 or 128;
- * T = dtype.  Any stride of at least heads * head_dim elements; rows and
+ * n_q or n_kv may be 0 (its pointers are then not read), and 16384 at most.
+ * head_dim 64 or 128; T = dtype.  Any stride of at least heads * head_dim elements; rows and
  * buffers on 16-byte boundaries take the vector path.  Needs no workspace. */
 dflash_status dflash_qk_norm_rope(int n_rows, int n_q, int n_kv, int head_dim, int dtype,
                                   const void* q_gain, const void* k_gain, float eps, float theta,
@@ -491,7 +491,8 @@ dflash_status dflash_qk_norm_rope(int n_rows, int n_q, int n_kv, int head_dim, i
  * Not stored: a row with a negative pos, and a row whose slot has no page (past
  * the table, or an entry outside [0, n_pages)).  No other slot is written.  Two
  * rows of one call must not share a slot (requests that share a page may share
- * only slots that neither writes).  n_rows may be 0.  Needs no workspace. */
+ * only slots that neither writes).  n_rows may be 0, n_kv 8192 at most.  Needs
+ * no workspace. */
 dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_rows,
                                   const int32_t* row_off, const int32_t* pos0,
                                   const int32_t* pos, const void* k, const void* v,

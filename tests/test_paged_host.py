@@ -122,3 +122,34 @@ def test_slots_past_the_limit(lib):
     """A request's slots, and the rows added to them, stay within 32 bits."""
     assert _append(lib, _pages(table_ld=(1 << 26) + 1)) == 1 and _attn(lib, _pages(table_ld=(1 << 26) + 1)) == 1
     assert _append(lib, _pages(table_ld=1 << 26), n_rows=0) == 0 and _attn(lib, _pages(table_ld=1 << 26), n_rows=0) == 0
+
+
+def test_heads_past_the_limit(lib):
+    """Head counts whose index arithmetic would leave 32 bits."""
+    def norm(n_q, n_kv, n=0):
+        big = 1 << 24
+        return lib.dflash_qk_norm_rope(n, n_q, n_kv, 128, 1, P, P, 1e-6, 1e6, P, P, big, P, big, P, big, P, big, None)
+
+    assert norm(16384, 16384) == 0
+    for n_q, n_kv in ((16385, 1), (1, 16385), (23171, 0), ((1 << 31) - 1, 0)):
+        assert norm(n_q, n_kv) == 1 and norm(n_q, n_kv, n=4) == 1
+
+    def append(n_kv, n_rows=0):
+        return _append(lib, _pages(n_kv=n_kv), n_rows=n_rows, ld=1 << 24)
+
+    assert append(8192) == 0
+    for n_kv in (8193, 11586, 100000):
+        assert append(n_kv) == 1 and append(n_kv, n_rows=4) == 1
+
+
+def test_division_within_the_limit():
+    """The quotient by a rounded-up reciprocal is exact for eight rows of 16384 heads,
+    and one too large soon after 23170."""
+    def quot(i, n):
+        return i if n == 1 else (i * ((2 ** 32 + n - 1) // n)) >> 32
+
+    for n in list(range(1, 300)) + list(range(16384 - 300, 16385)):
+        for r in range(1, 9):
+            for i in (r * n - 1, r * n - n):
+                assert quot(i, n) == i // n
+    assert any(quot(8 * n - 1, n) == 8 for n in range(23171, 33000))
