@@ -526,14 +526,21 @@ def logits_sample_filtered(logits: torch.Tensor, u: torch.Tensor, tok: torch.Ten
                            top_p: Optional[torch.Tensor] = None,
                            min_p: Optional[torch.Tensor] = None, vocab: Optional[int] = None,
                            stream=None):
-    """One token per row of logits [rows, ld] from u in [0, 1), under per-row temperature,
-    top_k, top_p and min_p (None: off); logp is its log-share of the kept mass."""
-    rows = logits.shape[0]
+    """One token per row of logits [rows, columns] from u in [0, 1), under per-row temperature,
+    top_k, top_p and min_p (None: off); logp is its log-share of the kept mass.  vocab: the
+    first columns alone."""
+    if logits.dim() != 2:
+        raise ValueError("logits: expected [rows, columns]")
+    rows, width = logits.shape
+    if vocab is None:
+        vocab = width
+    elif vocab > width:                       # (the library knows the rows' stride alone)
+        raise ValueError(f"vocab: {vocab} of {width} columns")
     dev = _together(logits, u, tok, logp, temperature, top_k, top_p, min_p)
     lp, ld = _rows(logits, "logits")
     f32 = torch.float32
     _check(lib().dflash_logits_sample_filtered(
-        rows, logits.shape[1] if vocab is None else vocab, ld, _dtype_code(logits), lp,
+        rows, vocab, ld, _dtype_code(logits), lp,
         _vec(temperature, rows, f32, "temperature"), _vec(top_k, rows, torch.int32, "top_k"),
         _vec(top_p, rows, f32, "top_p"), _vec(min_p, rows, f32, "min_p"), _vec(u, rows, f32, "u"),
         _vec(tok, rows, torch.int32, "tok"), _vec(logp, rows, f32, "logp"), _handle(stream, dev)))

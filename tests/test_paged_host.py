@@ -153,3 +153,18 @@ def test_division_within_the_limit():
             for i in (r * n - 1, r * n - n):
                 assert quot(i, n) == i // n
     assert any(quot(8 * n - 1, n) == 8 for n in range(23171, 33000))
+
+
+def test_sample_vocab_within_the_view():
+    """A view's rows may lie further apart than its columns reach: vocab is bound by the
+    columns, or the last row would be read past its storage."""
+    wide = torch.zeros(3, 40)
+    args = torch.zeros(3), torch.zeros(3, dtype=torch.int32), torch.zeros(3)
+    for view, vocab in ((wide[:, 3:], 38), (wide[:, 3:], 40), (wide[:, :10], 11), (wide[:1, :10], 40), (wide, 41)):
+        n = len(view)
+        with pytest.raises(ValueError, match="vocab"):
+            binding.logits_sample_filtered(view, *(a[:n] for a in args), vocab=vocab)
+    with pytest.raises(ValueError, match="CUDA"):              # (accepted as far as that goes)
+        binding.logits_sample_filtered(wide[:, 3:], *args, vocab=37)
+    with pytest.raises(ValueError, match="logits"):
+        binding.logits_sample_filtered(wide[0], *args)
