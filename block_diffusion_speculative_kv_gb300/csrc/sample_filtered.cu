@@ -141,7 +141,7 @@ struct Shared {
   uint64_t found_cum, before[2];
   uint64_t share[2];                     // measures of this CTA's share of the bins
   uint32_t near_n[kWarps];               // a warp's tokens near the border
-  double below;                          // T ln(min-p): what min-p keeps reaches max + this
+  double below;                          // T ln(min-p), or 0: what min-p keeps reaches max + this
   float hi, lo;                          // log2(e) / T in two parts
 };
 
@@ -647,7 +647,8 @@ sample_filtered_kernel(const SampleParams p) {
     const float hi = __fdiv_rd(1.4426950216293335f, temp);
     sh.hi = fminf(fmaxf(hi, 1e-38f), 3e38f);               // (T = inf: all alike)
     sh.lo = hi > 3e38f ? 1e-38f : fmaxf((fmaf(-hi, temp, 1.4426950216293335f) + 1.925963033500e-8f) / temp, 1e-38f);
-    if (temp > 0.f && min_p > 0.f) sh.below = static_cast<double>(temp) * log(static_cast<double>(fminf(min_p, 1.f)));
+    if (temp > 0.f && min_p > 0.f)                         // (T = inf times ln 1 is no number)
+      sh.below = min_p < 1.f ? static_cast<double>(temp) * log(static_cast<double>(min_p)) : 0.;
   }
   Reducer<CL> red{&sh};
 

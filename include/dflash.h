@@ -541,7 +541,8 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
  *   top_k        k > 0 keeps the k best tokens (logit desc, id asc)
  *   top_p        p < 1 keeps, of those in that order, a token if the mass before
  *                it is below p times theirs (the best always)
- *   min_p        m > 0 keeps tokens with l_v - max l >= T ln(min(m, 1))
+ *   min_p        m > 0 keeps tokens with l_v - max l >= T ln m, and from m = 1 on
+ *                those alone that equal the best, at any T
  *   draw         the first kept token, by id, whose cumulated mass exceeds u
  *                times the kept mass, u in [0, 1) (clamped)
  *   tok  int32 [rows], logp fp32 [rows] (device) out: the token, and the log of

@@ -288,3 +288,22 @@ def test_sample_border_just_below_zero(dtype):
     # the first 1000 ids, of 600 tokens at 0 or above and ties below them
     tok, lp = _run(x, [1.0] * n, dict(top_k=[1000] * n, temperature=[1e30] * n))
     assert (tok == 999).all() and np.allclose(lp, -math.log(1000), atol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("top_k", [0, 50, 300, 1000])
+def test_sample_infinite_temperature_with_min_p(top_k, dtype):
+    """At T = inf all tokens weigh the same; a min-p of 1 or more still leaves the best
+    alone, a smaller one everything.  (inf * ln 1 has no value of its own.)"""
+    rng = np.random.default_rng(top_k)
+    x = _logits(rng, 1, 3000, dtype).repeat(6, 1)
+    p = [0.5, 1.0, 7.0] * 2
+    how = dict(temperature=[float("inf")] * 6, min_p=p, top_k=[top_k] * 6)
+    _check(x, [0.7] * 6, how)
+    tok, lp = _run(x, [0.7] * 6, how)
+    best = int(x[0].argmax())
+    for i in (1, 2, 4, 5):
+        assert tok[i] == best and lp[i] == 0
+    assert abs(lp[0] + math.log(top_k or 3000)) < 1e-5
+    # with top-p between them
+    _check(x, [0.3] * 6, dict(how, top_p=[0.4] * 6))
