@@ -16,8 +16,9 @@
 // shared memory (rows too long for that are read again from global memory), so HBM
 // sees the logits once.  (Many long rows, whose slices would leave an SM one or two
 // CTAs, are read again too.)  Counts and masses are whole numbers (a mass has 40
-// fractional bits), so their sums over lanes, warps and CTAs do not depend on
-// the order and every pass agrees with every other.
+// fractional bits, every token's rounded for itself), so their sums over lanes, warps
+// and CTAs do not depend on the order, every pass agrees with every other, and a row's
+// result does not depend on the way it takes or on the size of its cluster.
 //
 // Two ways from there.  A small top-k (2 .. 512): the r-th best of a CTA's share of
 // 2048 maxima over parts of the row, r = ceil(k / CTAs), is a value that r of its
@@ -213,12 +214,36 @@ __device__ __forceinline__ void count_if_below(uint32_t a, float x, float limit)
       "f"(x), "f"(limit)
       : "memory");
 }
-// w 2^40, w in [0, 8], rounded: in two 32-bit conversions (64-bit ones are slow).
+// A token's mass: its weight w in [0, 1] times 2^40, rounded, in two 32-bit conversions
+// (64-bit ones are slow).
 __device__ __forceinline__ uint64_t fix(float w) {
   const uint32_t h = __float2uint_rz(w * 1048576.f);                     // 2^20 steps
   const uint32_t l = __float2uint_rn(fmaf(-__uint2float_rn(h), 9.5367431640625e-7f, w) * kOne);
   return ((uint64_t)h << 20) + l;
 }
+
+// The sum of fix(w) over a thread's weights in [0, 1], a pair at a time and without a
+// conversion: adding 12 (whose neighbours are 2^-20 apart) rounds w to 2^-20, adding
+// 1.5 2^-17 (2^-40 apart) rounds what is left to 2^-40, and either sum's bits count the
+// steps.  32 bits hold 2048 weights' steps, above or below; a thread has no more of a
+// row of 2^22 tokens in a cluster of 8.
+struct Masses {
+  static constexpr float kHigh = 12.f, kLow = 1.1444091796875e-5f;   // kLow: 1.5 2^-17
+  uint32_t high = 0, low = 0, n = 0;
+  __device__ __forceinline__ void add(float2 w) {
+    const float2 t = __fadd2_rn(w, make_float2(kHigh, kHigh));
+    const float2 h = __fadd2_rn(t, make_float2(-kHigh, -kHigh));
+    const float2 r = __fadd2_rn(__ffma2_rn(h, make_float2(-1.f, -1.f), w), make_float2(kLow, kLow));
+    high += __float_as_uint(t.x) + __float_as_uint(t.y);
+    low += __float_as_uint(r.x) + __float_as_uint(r.y);
+    n += 2;
+  }
+  __device__ __forceinline__ uint64_t sum() const {
+    const uint32_t h = high - n * __float_as_uint(kHigh);
+    const int32_t l = static_cast<int32_t>(low - n * __float_as_uint(kLow));
+    return ((uint64_t)h << 20) + static_cast<int64_t>(l);
+  }
+};
 
 // The search runs over the ordered codes of the values (16 bits for bf16).
 template <typename T>
@@ -788,13 +813,15 @@ sample_filtered_kernel(const SampleParams p) {
     bool linear = reach < 1e30f, guess = by_mass && linear;
     close = false;
     if (by_mass && !linear) {              // the whole in a pass of its own
-      uint64_t whole = 0, none = 0;
+      Masses all;
       part.each(lo0_v, [&](int, const float (&x)[8]) {
-        float s8 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s8 += x[e] > lo0_v ? w(x[e]) : 0.f;
-        whole += fix(s8);
+        for (int e = 0; e < 8; e += 2) {
+          const float2 y = w.at(w.dist(x[e], x[e + 1]));
+          all.add(make_float2(x[e] > lo0_v ? y.x : 0.f, x[e + 1] > lo0_v ? y.y : 0.f));
+        }
       });
+      uint64_t whole = all.sum(), none = 0;
       red.template both<false>(whole, none);
       target = mass_target(top_p, whole + extra);
       if (target > whole) return Found{lo, whole, target};
@@ -809,6 +836,7 @@ sample_filtered_kernel(const SampleParams p) {
       if (lane == 0) sh.near_n[warp] = close ? sh.near_n[warp] : 0;
       __syncthreads();
       uint64_t sum = 0, in_sum = 0;
+      Masses over;
       const uint32_t hist_c = mmas::smem_u32(sh.hist);
       // (no branch per token: nearly every warp has one in the bracket)
       auto bin_code = [&](float x) {
@@ -824,27 +852,29 @@ sample_filtered_kernel(const SampleParams p) {
         };
         if (by_mass && lo0 == floor_all) {
           part.all([&](int, const float (&x)[8]) {
-            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
               const float2 d = w.dist(x[e], x[e + 1]);
-              s2 = __fadd2_rn(s2, w.at(d));
+              over.add(w.at(d));
               bin(d.x, true);
               bin(d.y, true);
             }
-            sum += fix(s2.x + s2.y);
           });
         } else {
           part.each(by_mass ? lo0_v : fmaxf(lo_v, far_v), [&](int, const float (&x)[8]) {
-            float s8 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (by_mass) s8 += x[e] > lo0_v ? w(x[e]) : 0.f;
-              bin(x[e] - mx, x[e] >= lo_v);
+            for (int e = 0; e < 8; e += 2) {
+              const float2 d = w.dist(x[e], x[e + 1]);
+              if (by_mass) {
+                const float2 y = w.at(d);
+                over.add(make_float2(x[e] > lo0_v ? y.x : 0.f, x[e + 1] > lo0_v ? y.y : 0.f));
+              }
+              bin(d.x, x[e] >= lo_v);
+              bin(d.y, x[e + 1] >= lo_v);
             }
-            if (by_mass) sum += fix(s8);
           });
         }
+        if (by_mass) sum = over.sum();
       } else if (close) {
         sum = over_sum;
         for (uint32_t i = lane; i < sh.near_n[warp]; i += 32) {
@@ -855,13 +885,11 @@ sample_filtered_kernel(const SampleParams p) {
       } else {
         part.each(lo_v, [&](int i, const float (&x)[8]) {
           if (by_mass) {
-            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
               const float2 y = w.at(w.dist(x[e], x[e + 1]));
-              s2 = __fadd2_rn(s2, make_float2(x[e] > hi_v ? y.x : 0.f, x[e + 1] > hi_v ? y.y : 0.f));
+              over.add(make_float2(x[e] > hi_v ? y.x : 0.f, x[e + 1] > hi_v ? y.y : 0.f));
             }
-            sum += fix(s2.x + s2.y);
           } else {
             uint32_t n8 = 0;
 #pragma unroll
@@ -886,6 +914,7 @@ sample_filtered_kernel(const SampleParams p) {
           }
         });
         if (by_mass) {
+          sum = over.sum();
           over_sum = sum;                                  // of this thread's tokens above hi_v
           over_v = hi_v;
         }
@@ -1022,15 +1051,9 @@ sample_filtered_kernel(const SampleParams p) {
           const float v = C::value(mid);
           uint64_t ge = 0, zero = 0;
           part.each(v, [&](int, const float (&x)[8]) {
-            float s8 = 0.f;
-            uint32_t n8 = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (x[e] >= v) {
-                if (by_mass) s8 += w(x[e]);
-                else ++n8;
-              }
-            ge += by_mass ? fix(s8) : n8;
+              if (x[e] >= v) ge += by_mass ? fix(w(x[e])) : 1;
           });
           red.template both<false>(ge, zero);
           if (ge >= target) nlo = mid;
@@ -1104,12 +1127,12 @@ sample_filtered_kernel(const SampleParams p) {
   uint64_t gt = over_sum;
   uint32_t ties = 0;
   if (t == -CUDART_INF_F) {
+    Masses all;
     part.all([&](int, const float (&x)[8]) {               // nothing was filtered
-      float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) s2 = __fadd2_rn(s2, w.at(w.dist(x[e], x[e + 1])));
-      gt += fix(s2.x + s2.y);
+      for (int e = 0; e < 8; e += 2) all.add(w.at(w.dist(x[e], x[e + 1])));
     });
+    gt += all.sum();
   } else if (close) {
     for (uint32_t i = lane; i < sh.near_n[warp]; i += 32) {
       const float x = near[i];
@@ -1117,6 +1140,7 @@ sample_filtered_kernel(const SampleParams p) {
       if (x == t) ++ties;
     }
   } else {
+    Masses rest;
     part.each(t, [&](int, const float (&x)[8]) {
       uint32_t in = 0;                                     // above the border, not yet summed
 #pragma unroll
@@ -1125,15 +1149,14 @@ sample_filtered_kernel(const SampleParams p) {
         if (x[e] == t) ++ties;
       }
       if (in) {
-        float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           const float2 y = w.at(w.dist(x[e], x[e + 1]));
-          s2 = __fadd2_rn(s2, make_float2((in >> e) & 1u ? y.x : 0.f, (in >> e) & 2u ? y.y : 0.f));
+          rest.add(make_float2((in >> e) & 1u ? y.x : 0.f, (in >> e) & 2u ? y.y : 0.f));
         }
-        gt += fix(s2.x + s2.y);
       }
     });
+    gt += rest.sum();
   }
   __syncwarp();
   gt = warp_sum(gt);
@@ -1197,16 +1220,14 @@ sample_filtered_kernel(const SampleParams p) {
       tie = 0;
       if (i >= its.n) return;
       its.at(i).get(x);
-      float s[2] = {0.f, 0.f}, over[2] = {0.f, 0.f};       // (in pairs, as they were summed)
+      Masses above;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = x[e] > t ? w(x[e]) : 0.f;
-        if (x[e] > over_v) over[e & 1] += y;
-        else if (close) g += fix(y);                       // (as these were)
-        else s[e & 1] += y;
-        tie += x[e] == t ? 1 : 0;
+      for (int e = 0; e < 8; e += 2) {
+        const float2 y = w.at(w.dist(x[e], x[e + 1]));
+        above.add(make_float2(x[e] > t ? y.x : 0.f, x[e + 1] > t ? y.y : 0.f));
+        tie += (x[e] == t ? 1 : 0) + (x[e + 1] == t ? 1 : 0);
       }
-      g += fix(s[0] + s[1]) + fix(over[0] + over[1]);
+      g = above.sum();
     };
     uint64_t sg = 0;
     uint32_t st = 0, tie;
@@ -1241,18 +1262,15 @@ sample_filtered_kernel(const SampleParams p) {
           if (lane == __ffs(any) - 1) {
             const uint64_t t0 = ct + it - tie;
             uint64_t g0 = cg + ig - g;
-            float s[2] = {0.f, 0.f}, over[2] = {0.f, 0.f}, got = 0.f;
+            float got = 0.f;
             uint32_t seen = 0;
             int id = -1;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const bool above = x[e] > t, at = x[e] == t;
-              if (above && x[e] > over_v) over[e & 1] += w(x[e]);
-              else if (above && close) g0 += fix(w(x[e]));
-              else if (above) s[e & 1] += w(x[e]);
+              if (above) g0 += fix(w(x[e]));
               if (at) ++seen;
-              if (id < 0 && (above || at) &&
-                  g0 + fix(s[0] + s[1]) + fix(over[0] + over[1]) + kept_ties(t0 + seen) * one > goal) {
+              if (id < 0 && (above || at) && g0 + kept_ties(t0 + seen) * one > goal) {
                 id = its.id0 + i + e;
                 got = x[e];
               }

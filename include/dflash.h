@@ -552,8 +552,9 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
  * A NaN logit counts as -inf; tokens at -inf are never drawn; where some are
  * +inf they share the mass.  A row of -inf alone gives tok -1, logp -inf.
  *   logits  [rows] of dtype, ld elements apart, vocab <= ld
- * Masses are 64-bit sums of fp32 exponentials with 40 fractional bits, so
- * results depend neither on timing nor on what other rows hold.  rows may be 0.
+ * A token's mass is its fp32 exponential in steps of 2^-40 of the best's, and
+ * masses are added as 64-bit whole numbers, so results depend neither on timing
+ * nor on the other rows, their number included.  rows may be 0.
  * Requires 1 <= vocab <= 2^22.  Needs no workspace. */
 dflash_status dflash_logits_sample_filtered(int rows, int vocab, long long ld, int dtype,
                                             const void* logits, const float* temperature,

@@ -307,3 +307,48 @@ def test_sample_infinite_temperature_with_min_p(top_k, dtype):
     assert abs(lp[0] + math.log(top_k or 3000)) < 1e-5
     # with top-p between them
     _check(x, [0.3] * 6, dict(how, top_p=[0.4] * 6))
+
+
+def test_sample_small_masses_next_to_large_ones():
+    """A token keeps its own mass whatever its neighbours weigh: seven tokens of 2^-24.1
+    beside the best one, at u = 1 (the last mass) and in the best one's log share."""
+    w = math.exp(-16.7)
+    for dtype in (F32, BF):
+        x = torch.full((2, 8), -16.7, device=DEV)
+        x[:, 0] = 0.0
+        x = x.to(dtype)
+        w = math.exp(float(x[0, 1]))
+        tok, lp = _run(x, [1.0, 0.0], dict())
+        assert tok.tolist() == [7, 0]
+        # a mass is a multiple of 2^-40: half a step for each of seven; their sum with the
+        # best one's, 1 + 7 w, reaches the logarithm as an fp32 number: half a step of 2^-23
+        assert abs(lp[1] + math.log1p(7 * w)) <= 7 * 2.0 ** -41 + 7 * w * 2.0 ** -20 + 2.0 ** -24
+
+
+def test_sample_does_not_depend_on_the_batch():
+    """A row gives the same token and the same log share alone (a cluster of eight CTAs)
+    and among many (of two or four), whichever way its border is found."""
+    # the k best in places where clusters of two gather them and clusters of eight search
+    vocab, k = 16000, 500
+    row = torch.full((1, vocab), -30.0, device=DEV)
+    row[0, 3000:3300] = row[0, 12000:12300] = -16.7
+    row[0, 3000] = 0.0
+    how = dict(top_k=[k])
+    many = 60
+    u = [0.2, 0.99999]
+    for ui in u:
+        t1, l1 = _run(row, [ui], how)
+        t2, l2 = _run(row.repeat(many, 1), [ui] * many, {n: v * many for n, v in how.items()})
+        assert (t2 == t1[0]).all() and (l2 == l1[0]).all()
+    _check(row, u[:1], how)
+    rng = np.random.default_rng(12)
+    for dtype in (F32, BF):
+        for vocab in (5000, 24001, 70001):
+            x = _logits(rng, 4, vocab, dtype, scale=3.0)
+            x[2] = torch.round(x[2].float() * 4).to(dtype) / 4     # long ties
+            for how in GRID + [dict(top_k=500), dict(top_k=500, top_p=0.9), dict(top_k=3000, top_p=0.99, min_p=1e-4)]:
+                u = rng.random(4)
+                t2, l2 = _run(x.repeat(24, 1), np.tile(u, 24), {n: [v] * 96 for n, v in how.items()})
+                for i in range(4):
+                    t1, l1 = _run(x[i:i + 1], u[i:i + 1], {n: [v] for n, v in how.items()})
+                    assert (t2[i::4] == t1[0]).all() and (l2[i::4] == l1[0]).all(), (dtype, vocab, how, i)
