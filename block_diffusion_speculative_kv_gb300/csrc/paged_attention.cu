@@ -117,12 +117,13 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
     const int k0 = pc.first * kStepS + warp * 16;   // this warp's first key of the piece
     const int head0 = c.g * p.heads.G;
 
+    bool missing = false;                       // a page is not there (warp-uniform)
     auto load = [&](int i) {
       const int t0 = k0 + i * kStepS;
       uint8_t* dst = ring + (i % kStagesS) * 2 * S::kTile;
       if (i < n) {
         const int page = t0 < kend ? page_of(p.pv, c.r, t0) : -1;
-        if (page < 0 && t0 < kend && lane == 0) record_status(p.status, DFLASH_ERR_INVALID_ARG);
+        missing |= page < 0 && t0 < kend;
         const long long at = page < 0 ? 0 : pool_row(p.pv, page, c.g, t0) * HD;
         const uint32_t dk = mmas::smem_u32(dst), dv = dk + S::kTile;
 #pragma unroll
@@ -283,6 +284,11 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
       }
       __syncwarp();   // the slot may be loaded again
     }
+
+    if (missing)
+      for (int t0 = k0; t0 < min(k0 + n * kStepS, kend); t0 += kStepS)
+        if (page_of(p.pv, c.r, t0) < 0 && paged_seen<GeoS>(p, c, t0, min(t0 + 16, kend), lane) && lane == 0)
+          record_status(p.status, DFLASH_ERR_INVALID_ARG);
 
     // the four warps' states, of the tile's live rows
     const int live = min(kRowsS, nG - rho0);
@@ -597,11 +603,12 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
         return lane < nb && i < n && t < kend ? __ldg(table + (t >> p.pv.page_shift)) : -1;
       };
       int entry = entry_of(0);
+      bool missing = false;
       for (int i = 0; i < n && ok; ++i) {
         const int t = slot_of(i), page = entry;
         entry = entry_of(i + 1);
         const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.pv.n_pages);
-        if (!there && lane < nb && t < kend) record_status(p.status, DFLASH_ERR_INVALID_ARG);
+        missing |= !there && lane < nb && t < kend;
         const int y = there ? static_cast<int>(pool_row(p.pv, page, c.g, t)) : nowhere;
         for (int kv = 0; kv < 2 * kPer && ok; ++kv, ++it) {   // K's slots, then V's
           const int s = it % R, part = kv % kPer;
@@ -617,6 +624,11 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
                                kv >= kPer ? &maps.v : &maps.k, &full[s], 64 * h, y, pol);
         }
       }
+      // pages that are not there: an error if some row of the tile sees their slots
+      if (__any_sync(0xffffffffu, missing))
+        for (int t0 = pc.first * kStepT; t0 < min((pc.first + n) * kStepT, kend); t0 += box)
+          if (page_of(p.pv, c.r, t0) < 0 && paged_seen<Geo>(p, c, t0, min(t0 + box, kend), lane) && lane == 0)
+            record_status(p.status, DFLASH_ERR_INVALID_ARG);
     }
     if (!ok && lane == 0) fail();
     // every copy must land before the CTA exits

@@ -132,6 +132,30 @@ struct PagedPiece {
   }
 };
 
+// Whether some row of the cursor's tile sees one of the slots [t, end), where `end` is at
+// most the end of what the tile's rows may see.  Warp-collective, and rare: asked only
+// of slots that are not there.
+template <typename Geo>
+__device__ __forceinline__ bool paged_seen(const PagedAttnParams& p, const PagedCursor& c, int t, int end, int lane) {
+  const PagedReq& rq = c.rq;
+  if (t >= end) return false;
+  if (!rq.masked || t < rq.p0) return true;                  // (causal: the last row sees them)
+  const int b0 = t - rq.p0, b1 = static_cast<int>(min((long long)(end - rq.p0), 32ll * p.mask_ld));
+  const int first = p.heads.quot(c.j * Geo::TR);
+  const int last = p.heads.quot(min(c.j * Geo::TR + Geo::TR - 1, rq.n * p.heads.G - 1));
+  bool sees = false;
+  for (int i = first + lane; i <= last; i += 32) {
+    const uint32_t* m = p.mask + (size_t)(rq.row0 + i) * p.mask_ld;
+    for (int w = b0 >> 5; w * 32 < b1; ++w) {
+      uint32_t u = m[w];
+      if (w * 32 < b0) u &= 0xFFFFFFFFu << (b0 & 31);
+      if (b1 - w * 32 < 32) u &= (1u << (b1 & 31)) - 1u;
+      sees |= u != 0;
+    }
+  }
+  return __any_sync(0xffffffffu, sees);
+}
+
 // a / b for a >= 0, b > 0; almost always within 32 bits, where it is quick.
 __device__ __forceinline__ long long div_pos(long long a, long long b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);

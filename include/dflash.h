@@ -519,8 +519,10 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
  * kernel; results do not depend on it being tight.  Sizes stay on the device,
  * so a captured call serves contexts that grow.  The work (requests x KV heads
  * x query tiles x key tiles) is split evenly over the SMs; a tile split between
- * CTAs is joined in key order, so results do not depend on timing.  A visible slot whose page is not there reads as zeros and records
- * DFLASH_ERR_INVALID_ARG in the workspace status word.
+ * CTAs is joined in key order, so results do not depend on timing.  A slot that some
+ * row sees and whose page is not there reads as zeros and records
+ * DFLASH_ERR_INVALID_ARG in the workspace status word; pages that no row sees
+ * (behind a tree's last node) need not be there.
  * Requires DFLASH_BF16 pages, n_q a multiple of n_kv, n_rows * n_q < 2^30,
  * strides that are multiples of 8 elements and 16-byte aligned q and out.  ws of
  * dflash_paged_attention_workspace_bytes bytes, zeroed once

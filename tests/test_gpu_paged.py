@@ -581,3 +581,23 @@ def test_attention_more_tiles_than_parts(rows, ctx, n_q, n_kv, hd, page, tree):
 def test_attention_few_tiles_in_many_parts(rows, ctx, n_q, n_kv, hd, tree):
     """One long context on all SMs: tens of parts to a tile, more than are weighed at once."""
     test_attention((rows, ctx, n_q, n_kv, hd, 16, tree))
+
+
+@pytest.mark.parametrize("n,n_q", [(10, 2), (30, 4), (90, 8)])
+def test_attention_pages_that_no_row_sees_may_be_missing(n, n_q):
+    """A draft tree in a request of more rows (those past its last node see nothing new):
+    pages behind the last node need not be there.  With a bit for one of them they do."""
+    d = _build([n, 2], [24, 40], n_q, 2, 128, 16, True, seed=2)
+    nodes = n // 2
+    d["mask"][nodes:n] = 0
+    d["table"][0, -(-(24 + nodes) // 16):] = -1
+    out, ws = _attend(d)
+    torch.cuda.synchronize()
+    assert bd.read_status(ws) == 0
+    _check(d, out)
+    j = n - 1
+    d["mask"][1, j // 32] |= np.uint32(1 << (j % 32))
+    out, ws = _attend(d)
+    torch.cuda.synchronize()
+    assert bd.read_status(ws) == 1
+    _check(d, out)                                   # the slot reads as zeros
