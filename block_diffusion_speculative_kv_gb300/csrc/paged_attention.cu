@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
       for (int t0 = k0; t0 < min(k0 + n * kStepS, kend); t0 += kStepS)
         if (page_of(p.pv, c.r, t0) < 0 && paged_seen<GeoS>(p, c, t0, min(t0 + 16, kend), lane) && lane == 0)
           record_status(p.status, DFLASH_ERR_INVALID_ARG);
+    if (warp == 0) paged_past<GeoS>(p, c, lane);
 
     // the four warps' states, of the tile's live rows
     const int live = min(kRowsS, nG - rho0);
@@ -734,6 +735,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
       }
       it += 2 * kPer * n;
       ++unit;
+      paged_past<Geo>(p, c, lane);
     }
     if (!ok && lane == 0) fail();
     // the MMAs already issued finish before TMEM is released

@@ -522,7 +522,10 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
  * CTAs is joined in key order, so results do not depend on timing.  A slot that some
  * row sees and whose page is not there reads as zeros and records
  * DFLASH_ERR_INVALID_ARG in the workspace status word; pages that no row sees
- * (behind a tree's last node) need not be there.
+ * (behind a tree's last node) need not be there.  A slot that some row sees past
+ * the table (pos0[r] + j >= table_ld * page_size) records the same error and is
+ * left out of the softmax; so does a request with rows whose pos0 is negative
+ * (taken as 0) or past the table (taken as its end).
  * Requires DFLASH_BF16 pages, n_q a multiple of n_kv, n_rows * n_q < 2^30,
  * strides that are multiples of 8 elements and 16-byte aligned q and out.  ws of
  * dflash_paged_attention_workspace_bytes bytes, zeroed once

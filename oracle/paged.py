@@ -80,8 +80,8 @@ def visible(n, p0, kv, mask=None):
 
 def attention(q, pool_k, pool_v, table, row_off, pos0, n_q, mask=None):
     """q [rows, n_q, head_dim] -> (out, spread): the softmax average over the
-    slots each row sees, and the same average of |v| (the scale that rounding
-    errors of the weights act on)."""
+    slots each row sees (those past the table left out), and the same average of
+    |v| (the scale that rounding errors of the weights act on)."""
     n_kv, hd = pool_k.shape[1], pool_k.shape[3]
     page = pool_k.shape[2]
     out, spread = np.zeros(q.shape), np.zeros(q.shape)

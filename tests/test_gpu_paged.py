@@ -601,3 +601,36 @@ def test_attention_pages_that_no_row_sees_may_be_missing(n, n_q):
     torch.cuda.synchronize()
     assert bd.read_status(ws) == 1
     _check(d, out)                                   # the slot reads as zeros
+
+
+@pytest.mark.parametrize("n,n_q", [(3, 2), (30, 4), (90, 8)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attention_slots_past_the_table_are_reported(n, n_q, tree):
+    """Slots that a row sees past its page table: an error in the status word, and the
+    softmax runs over the slots that the table has."""
+    def status(d):
+        out, ws = _attend(d)
+        torch.cuda.synchronize()
+        got = bd.read_status(ws)
+        _check(dict(d, ctx=[min(c, cap) for c in d["ctx"]]), out)   # (past the table: all of it is seen)
+        return got
+
+    cap = 160
+    base = _build([n, 2], [cap - n, 40], n_q, 2, 128, 16, tree, seed=6)
+    assert base["table"].shape[1] * 16 == cap
+    assert status(base) == 0                         # up to the table's last slot
+    for p0 in (cap - n + 1, cap - 1, cap, cap + 1, 1 << 30, 2 ** 31 - 1):
+        assert status(dict(base, ctx=[p0, 40])) == 1, p0
+        # a request without rows sees nothing
+        none = dict(base, off=np.array([0, 0, 2], dtype=np.int32), ctx=[p0, 40], rows=[0, 2])
+        assert status(none) == 0, p0
+    out, ws = _attend(dict(base, ctx=[-1, 40]))
+    torch.cuda.synchronize()
+    assert bd.read_status(ws) == 1                   # there is no slot before the first
+    if tree:
+        # the rows past a tree's last node may lie past the table: no row sees them
+        m = base["mask"].copy()
+        m[n // 2:n] = 0
+        assert status(dict(base, mask=m, ctx=[cap - n // 2, 40])) == 0
+        m[0, (n - 1) // 32] |= np.uint32(1 << ((n - 1) % 32))
+        assert status(dict(base, mask=m, ctx=[cap - n // 2, 40])) == 1
