@@ -442,15 +442,16 @@ void launch_small(const PagedAttnParams& p, cudaStream_t st) {
 // After the softmax warps, one loads (TMA, a ring of K and V tiles that runs ahead
 // over tile borders; a box is a page, or a slot of a larger one), the next one
 // issues the MMAs.  A row's O is rescaled only when its maximum has risen by more
-// than 8 (base-2 units) over the reference in use.  Every wait is bounded (2 s); on expiry the CTA
-// records DFLASH_ERR_TIMEOUT, lets its copies and MMAs land, frees TMEM and returns.
+// than 8 (base-2 units) over the reference in use.  Every wait is bounded (2 s, or the limit in
+// the workspace header); on expiry the CTA records DFLASH_ERR_TIMEOUT, lets its copies and
+// MMAs land (2 s at most), frees TMEM and returns.
 constexpr int kStepT = 128;
 // Registers with NG = 2: the launch's 168 for each of three warpgroups, of which
 // the softmax groups take 216 (a row of scores in registers) and the other one
 // keeps 72: 2 * 216 + 72 = 3 * 168.
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "register split");
-constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kTimeoutNs = 2000000000ull, kMaxLimitNs = 60000000000ull;
 
 struct PagedTcMaps {
   CUtensorMap k, v;    // pools as [n_pages * n_kv * page_size][HD], box 64 x min(page_size, slot)
@@ -523,7 +524,8 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   uint64_t* p_ready = q_full + 3;                            // [NG][half]
   uint64_t* pv_done = q_full + 7;                            // [NG]
   uint64_t* drain = q_full + 9;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(q_full + 10);
+  uint64_t* wait_ns = q_full + 10 + (threadIdx.x >> 5);      // limit of a wait, a word to a warp
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(q_full + 22);
   volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(tslot + 2);    // [2]
   // keys with a value that is not finite: [group][step % 4][word].  Group 1 may
@@ -564,7 +566,11 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   pdl_trigger();
   long long total, end;
   PagedCursor c;
+  // the workspace header's limit (dflash_workspace_set_wait_limit), read beside the plan
+  const uint64_t limit = *reinterpret_cast<const volatile uint64_t*>(p.status + 2);
   paged_plan<Geo>(p, lane, &total, &end, &c);
+  if (lane == 0) *wait_ns = limit == 0 || limit > kMaxLimitNs ? kTimeoutNs : limit;
+  __syncwarp();
 
   auto fail = [&]() {
     if (!*abort) record_status(p.status, DFLASH_ERR_TIMEOUT);
@@ -573,7 +579,11 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   // bounded waits; the loader and the issuer back off between polls, since they
   // share schedulers with the softmax
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    return ptx::mbar_wait_bounded(b, parity, kTimeoutNs, abort);
+    if (ptx::mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!ptx::mbar_try_wait(b, parity))
+      if (*abort || global_ns() - t0 > *wait_ns) return false;
+    return true;
   };
 
   if (warp >= kLoad) {

@@ -201,7 +201,9 @@ dflash_status dflash_read_status(void* ws, int* device_status, void* stream);
 
 /* Set the time limit of every bounded device-side wait of the tensor-core GEMM
  * launches that use this workspace (ring slots, the phase counters of a GEMM
- * chain, split-tile partial sums, the fused top-K's arrivals).  The pages have
+ * chain, split-tile partial sums, the fused top-K's arrivals) and of the paged
+ * attention's tensor-core launches (its kernel for at most 16 query rows of a
+ * request and KV head waits for nothing but its own copies).  The pages have
  * no counterpart: this is the failure-detection hook.  limit_ns = 0 restores
  * the default of 2 s; values above 60 s also mean the default.  A wait that
  * runs out records DFLASH_ERR_TIMEOUT in the status word; the CTA then waits

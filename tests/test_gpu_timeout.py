@@ -116,3 +116,58 @@ def test_set_wait_limit_rejects_small_workspace():
     with pytest.raises(bd.DflashError) as ei:
         bd.workspace_set_wait_limit(ws, LIMIT_NS)
     assert ei.value.status == 1
+
+
+@pytest.mark.parametrize("rows,ctx,n_q,page", [
+    ([64] * 20, 2000, 4, 64),        # 64-row tiles, joined by the last of their CTAs
+    ([64] * 12, 8000, 4, 16),        # 64-row tiles, joined by a kernel
+    ([1500], 3000, 16, 128),         # 256-row tiles, joined by the last of their CTAs
+    ([64] * 8, 8000, 16, 64),        # 256-row tiles, joined by a kernel
+])
+def test_paged_attention_wait_runs_out_then_recovers(rows, ctx, n_q, page):
+    """The tensor-core kernels of the paged attention.  Their waits are shorter than a
+    GEMM's, 1 to 2 us within a tile, less than a poll may sleep.  So the new tokens' values
+    are infinite, which the softmax adds to its rows one by one (some 100 us to a tile),
+    while the CTA's other warps wait for it, those that go on to a second tile too."""
+    n_kv, hd = 4, 128
+    ctx = [ctx + 50 * i for i in range(len(rows))]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    need = [-(-(n + c) // page) for n, c in zip(rows, ctx)]
+    table = torch.full((len(rows), max(need)), -1, dtype=torch.int32, device="cuda")
+    order = torch.randperm(sum(need), generator=g, device="cuda").to(torch.int32)
+    at = 0
+    for r, m in enumerate(need):
+        table[r, :m] = order[at:at + m]
+        at += m
+    pk, pv = (torch.randn(sum(need), n_kv, page, hd, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    pages = bd.Pages(pk, pv, table)
+    finite = bd.Pages(pk, pv.clone(), table)
+    for r, (n, c) in enumerate(zip(rows, ctx)):
+        for t in range(c // page, (c + n - 1) // page + 1):
+            a, b = max(c - t * page, 0), min(c + n - t * page, page)
+            pv[table[r, t], :, a:b] = float("inf")
+    q = torch.randn(sum(rows), n_q * hd, generator=g, device="cuda").to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    off = torch.tensor(np.concatenate([[0], np.cumsum(rows)]), **i32)
+    pos0 = torch.tensor(ctx, **i32)
+    ws = torch.zeros(bd.paged_attention_workspace_bytes(n_q, n_kv, hd), dtype=torch.uint8, device="cuda")
+
+    def run(pages):
+        out = torch.full_like(q, float("nan"))
+        bd.paged_attention(pages, q, off, pos0, max(rows), out, ws)
+        torch.cuda.synchronize()
+        return out
+
+    usual, want = run(finite), run(pages)
+    assert bd.read_status(ws) == 0 and torch.isfinite(usual).all() and (want == float("inf")).all()   # (every row sees its own)
+
+    bd.workspace_set_wait_limit(ws, LIMIT_NS)
+    run(pages)
+    assert bd.read_status(ws) == TIMEOUT
+
+    # the context is intact, and after workspace_init the call is what it was
+    assert float((torch.ones(8, device="cuda") * 2).sum()) == 16.0
+    bd.workspace_init(ws)
+    for _ in range(2):
+        assert torch.equal(run(finite), usual) and torch.equal(run(pages), want)
+        assert bd.read_status(ws) == 0
