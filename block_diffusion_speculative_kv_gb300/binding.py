@@ -382,14 +382,15 @@ def _together(*tensors) -> int:
 
 
 def _rows(t: torch.Tensor, name: str):
-    """Pointer and row stride of a [rows, columns] view whose columns are adjacent."""
+    """Pointer and row stride of a [rows, columns] view whose columns are adjacent (the
+    stride of a single row says nothing: its width)."""
     by = t.stride()
     if len(by) != 2:
         raise ValueError(f"{name}: expected [rows, columns]")
     n, width = t.shape
     if by[1] != 1 and width > 1:
         raise ValueError(f"{name}: expected adjacent columns")
-    return t.data_ptr(), by[0] if n > 1 else max(by[0], width)
+    return t.data_ptr(), by[0] if n > 1 else width
 
 
 def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str):

@@ -634,3 +634,32 @@ def test_attention_slots_past_the_table_are_reported(n, n_q, tree):
         assert status(dict(base, mask=m, ctx=[cap - n // 2, 40])) == 0
         m[0, (n - 1) // 32] |= np.uint32(1 << ((n - 1) % 32))
         assert status(dict(base, mask=m, ctx=[cap - n // 2, 40])) == 1
+
+
+def test_one_row_out_of_a_wider_tensor():
+    """The row stride of a single row says nothing: keys out of a projection's row beside
+    values of their own, and rows whose stride is no multiple of eight."""
+    rng = np.random.default_rng(17)
+    pk, pv, table, off = _paged(rng, [1], [20], 2, 64, 16)
+    kv = _t(rng.normal(size=(3, 300)))
+    k, v = kv[1:2, 8:136], kv[1:2, 136:264].clone()
+    a, b = pk.clone(), pv.clone()
+    bd.paged_append(bd.Pages(a, b, _i(table)), k, v, _i(off), _i([20]), theta=THETA)
+    c, e = pk.clone(), pv.clone()
+    bd.paged_append(bd.Pages(c, e, _i(table)), k.clone(), v, _i(off), _i([20]), theta=THETA)
+    wide = _t(rng.normal(size=(2, 261)))
+    q, out = wide[:1, :256], torch.full((1, 259), 7.0, dtype=BF, device=DEV)[:, :256]
+    want, ws = torch.empty(1, 256, dtype=BF, device=DEV), _ws(4, 2, 64)
+    pages = bd.Pages(a, b, _i(table))
+    bd.paged_attention(pages, q.clone(), _i(off), _i([20]), 1, want, ws)
+    bd.paged_attention(pages, q, _i(off), _i([20]), 1, out, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, c) and torch.equal(b, e) and torch.equal(out, want)
+    # in place and out of place, of two strides
+    g = _t(rng.normal(size=64))
+    pos = _i([5])
+    y = torch.empty(1, 256, dtype=BF, device=DEV)
+    bd.qk_norm_rope(q, None, g, None, 1e-6, THETA, pos, 64, y)
+    bd.qk_norm_rope(q, None, g, None, 1e-6, THETA, pos, 64)
+    torch.cuda.synchronize()
+    assert torch.equal(q, y)
