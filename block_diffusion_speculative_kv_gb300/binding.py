@@ -505,8 +505,8 @@ def paged_attention(pages: Pages, q: torch.Tensor, row_off: torch.Tensor, pos0: 
         raise ValueError("q and out: expected bf16 [rows, n_q * head_dim]")
     if q.dim() != 2 or q.shape[1] % hd:
         raise ValueError(f"q: expected [rows, heads * {hd}]")
-    if mask is not None and (mask.dim() != 2 or mask.shape[0] != n):
-        raise ValueError("mask: expected [rows, words]")
+    if mask is not None and (mask.dim() != 2 or mask.shape[0] != n or mask.shape[1] == 0):
+        raise ValueError("mask: expected [rows, words]")       # (no words: a null pointer, causal)
     dev = _together(pages.pool_k, q, row_off, pos0, out, ws, mask)
     if not ws.is_contiguous():
         raise ValueError("ws: expected a contiguous tensor")

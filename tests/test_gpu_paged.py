@@ -663,3 +663,11 @@ def test_one_row_out_of_a_wider_tensor():
     bd.qk_norm_rope(q, None, g, None, 1e-6, THETA, pos, 64)
     torch.cuda.synchronize()
     assert torch.equal(q, y)
+
+
+def test_attention_refuses_a_mask_of_no_words():
+    """(Its pointer is null, which the library takes as causal.)"""
+    d = _build([1, 2], [100, 40], 4, 2, 128, 16, False)
+    d["mask"] = np.zeros((3, 0), dtype=np.uint32)
+    with pytest.raises(ValueError, match="mask"):
+        _attend(d)
