@@ -50,6 +50,7 @@ __device__ __forceinline__ int request_of(const int32_t* row_off, int n_req, int
   return lo;
 }
 
-dflash_status check_pages(const dflash_pages* p, const char* what, PagedView* out);
+// (n_req 0: a table of no rows, whose pointer may be null)
+dflash_status check_pages(const dflash_pages* p, int n_req, const char* what, PagedView* out);
 
 }  // namespace dfl

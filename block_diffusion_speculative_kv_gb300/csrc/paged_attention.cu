@@ -1313,7 +1313,7 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
                                      int mask_ld, void* out, long long out_ld, void* ws,
                                      size_t ws_bytes, void* stream) {
   PagedAttnParams p{};
-  const dflash_status s = check_pages(pages, "paged attention", &p.pv);
+  const dflash_status s = check_pages(pages, n_req, "paged attention", &p.pv);
   if (s) return s;
   const int hd = pages->head_dim;
   if (pages->dtype != DFLASH_BF16)

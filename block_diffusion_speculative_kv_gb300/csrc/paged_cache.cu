@@ -22,7 +22,7 @@
 
 namespace dfl {
 
-dflash_status check_pages(const dflash_pages* p, const char* what, PagedView* out) {
+dflash_status check_pages(const dflash_pages* p, int n_req, const char* what, PagedView* out) {
   DFL_REQUIRE(p, "%s: null pages", what);
   DFL_REQUIRE(p->dtype == DFLASH_F32 || p->dtype == DFLASH_BF16, "%s: dtype must be F32 or BF16",
               what);
@@ -36,7 +36,7 @@ dflash_status check_pages(const dflash_pages* p, const char* what, PagedView* ou
               "%s: a request's slots exceed 2^30", what);      // (and rows added do not pass 2^31)
   DFL_REQUIRE((long long)p->n_pages * p->n_kv * p->page_size < (1ll << 31),
               "%s: the pool's rows exceed 2^31", what);
-  DFL_REQUIRE(p->k && p->v && p->table, "%s: null pool or table", what);
+  DFL_REQUIRE(p->k && p->v && (p->table || n_req == 0), "%s: null pool or table", what);
   DFL_REQUIRE(((reinterpret_cast<uintptr_t>(p->k) | reinterpret_cast<uintptr_t>(p->v)) & 15) == 0,
               "%s: pools must be 16-byte aligned", what);
   *out = PagedView{p->k, p->v, p->table, p->table_ld, p->n_pages, log2_int(p->page_size), p->n_kv};
@@ -456,7 +456,7 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
                                   const int32_t* pos, const void* k, const void* v,
                                   long long kv_ld, float theta, void* stream) {
   AppendParams p{};
-  const dflash_status s = check_pages(pages, "paged append", &p.pv);
+  const dflash_status s = check_pages(pages, n_req, "paged append", &p.pv);
   if (s) return s;
   DFL_REQUIRE(n_req >= 0 && n_rows >= 0, "paged append: sizes must be >= 0");
   DFL_REQUIRE(2 * (long long)pages->n_kv <= kMaxHeads, "paged append: more than %d KV heads", kMaxHeads / 2);

@@ -168,3 +168,10 @@ def test_sample_vocab_within_the_view():
         binding.logits_sample_filtered(wide[:, 3:], *args, vocab=37)
     with pytest.raises(ValueError, match="logits"):
         binding.logits_sample_filtered(wide[0], *args)
+
+
+def test_no_requests_need_no_table(lib):
+    """An empty batch: a table of no rows has a null pointer."""
+    none = _pages(table=0)
+    assert _append(lib, none, n_req=0) == 0 and _attn(lib, none, n_req=0) == 0
+    assert _append(lib, none, n_req=1, n_rows=0) == 1 and _attn(lib, none, n_req=1, n_rows=0) == 1
