@@ -1264,7 +1264,6 @@ dflash_status launch_tc(PagedAttnParams p, const dflash_pages& pages, cudaStream
   if (!encode_kmajor_map(&maps.k, pages.k, rows, HD, HD, box) ||
       !encode_kmajor_map(&maps.v, pages.v, rows, HD, HD, box))
     return set_error(DFLASH_ERR_CUDA, "paged attention: cannot encode the TMA descriptors");
-  TraceScope ts("paged_attn_tc", st);
   const int grid = num_sms() * S::kPerSm;
   // A few parts to a tile are joined by the last CTA to arrive, which costs no launch
   // and hides behind the others' work; many by a kernel of their own, since one CTA
@@ -1272,9 +1271,14 @@ dflash_status launch_tc(PagedAttnParams p, const dflash_pages& pages, cudaStream
   // over 4096 (19) 27 against 34; a prompt chunk (2) 245 against 237.
   const long long tiles = (p.n_rows * (long long)p.heads.G + S::kRows - 1) / S::kRows * p.pv.n_kv;
   if (tiles * 4 >= grid) p.cut = nullptr;
-  launch_k(paged_attn_tc_kernel<HD, NG>, dim3(grid), dim3(S::kThreads), S::kBytes, st, maps, p);
-  if (p.cut)
+  {
+    TraceScope ts("paged_attn_tc", st);
+    launch_k(paged_attn_tc_kernel<HD, NG>, dim3(grid), dim3(S::kThreads), S::kBytes, st, maps, p);
+  }
+  if (p.cut) {
+    TraceScope ts("paged_join", st);
     launch_k(paged_join_kernel<HD, NG>, dim3(grid, S::kRows / 32), dim3(256), 0, st, p);
+  }
   return DFLASH_OK;
 }
 

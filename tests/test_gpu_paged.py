@@ -671,3 +671,19 @@ def test_attention_refuses_a_mask_of_no_words():
     d["mask"] = np.zeros((3, 0), dtype=np.uint32)
     with pytest.raises(ValueError, match="mask"):
         _attend(d)
+
+
+def test_trace_hook_sees_every_launch():
+    """One pair of callbacks to a kernel, the join of tiles in many parts among them."""
+    seen = []
+    bd.set_trace_hook(lambda kernel, phase, stream: seen.append((kernel, phase)))
+    try:
+        for rows, names in (([1], ["paged_attn_small"]), ([40], ["paged_attn_tc", "paged_join"]),
+                            ([4000], ["paged_attn_tc"])):
+            d = _build(rows, [600], 8, 8, 64, 64, False)
+            seen.clear()
+            _attend(d)
+            torch.cuda.synchronize()
+            assert seen == [(n, p) for n in names for p in (0, 1)]
+    finally:
+        bd.set_trace_hook(None)
