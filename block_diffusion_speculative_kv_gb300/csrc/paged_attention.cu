@@ -427,8 +427,8 @@ void launch_small(const PagedAttnParams& p, cudaStream_t st) {
 // two CTAs share an SM: memory bounds these tiles, and one CTA streams while the
 // other begins or ends a tile.
 // What bounds them.  NG = 1: memory; 32 requests of 16 rows over 512 .. 8192 slots take
-// 110 us, 5.5 TB/s.  NG = 2: a prompt chunk of 2048 rows over 8192 slots takes 231 us,
-// 1.34 PFLOP/s.  A step of a group is a chain: 420 clocks to read the scores from TMEM,
+// 110 us, 5.5 TB/s.  NG = 2: a prompt chunk of 2048 rows over 8192 slots takes 230 us,
+// 1.35 PFLOP/s.  A step of a group is a chain: 420 clocks to read the scores from TMEM,
 // 400 for their maximum, 1250 for the probabilities, 900 for the rest of P V and the
 // next scores; the other group's hides behind it.  The tensor cores need 2830 a step at
 // least, not the 2080 of their rate: both operands of the scores come from shared
@@ -438,7 +438,7 @@ void launch_small(const PagedAttnParams& p, cudaStream_t st) {
 // while the other half's maximum is found (240 against 231), or to form the first 32 keys
 // of P before the maximum is known (231).  Small tiles, short
 // contexts: beginning and ending a tile, about 6 us for the query rows on their way in
-// and O on its way out, 257 rows over 8192 slots 57 us.
+// and O on its way out, 257 rows over 8192 slots 56 us.
 // After the softmax warps, one loads (TMA, a ring of K and V tiles that runs ahead
 // over tile borders; a box is a page, or a slot of a larger one), the next one
 // issues the MMAs.  A row's O is rescaled only when its maximum has risen by more
@@ -1267,8 +1267,13 @@ dflash_status launch_tc(PagedAttnParams p, const dflash_pages& pages, cudaStream
   const int grid = num_sms() * S::kPerSm;
   // A few parts to a tile are joined by the last CTA to arrive, which costs no launch
   // and hides behind the others' work; many by a kernel of their own, since one CTA
-  // reads a part in about 2 us: 16 rows over 8192 slots (38 parts) 33 us against 95, 128
-  // over 4096 (19) 27 against 34; a prompt chunk (2) 245 against 237.
+  // reads a part in about 2 us.  Measured, by a kernel / by the last CTA, us: 16 rows over
+  // 8192 slots (38 parts) 27 / 45, 128 over 4096 (19) 30 / 37; trees of 129, 257, 385 and
+  // 513 rows over 8192 (6.3, 3.8, 2.7, 2.1) 40 / 45, 55.5 / 56.1, 70 / 69, 84 / 82; 6, 9,
+  // 10, 12 and 16 chains of 16 over 4096 (6.3, 4.2, 3.8, 3.2, 2.4) 34 / 37, 42.1 / 42.4,
+  // 44.4 / 46.4, 49 / 51, 59.5 / 59.9; a prompt chunk (1.6) 243 / 235.  (They meet
+  // between two and three parts in 64-row tiles, at three in 256-row ones; the rule's
+  // four costs 2 us at most.)
   const long long tiles = (p.n_rows * (long long)p.heads.G + S::kRows - 1) / S::kRows * p.pv.n_kv;
   if (tiles * 4 >= grid) p.cut = nullptr;
   {

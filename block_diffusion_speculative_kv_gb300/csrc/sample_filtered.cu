@@ -30,9 +30,10 @@
 //
 // Neither bandwidth nor any unit bounds it, but the chain of block and cluster
 // barriers between the steps of a row, of which an SM holds four CTAs: 480 rows of
-// 151936 bf16 logits take 48 us greedy (6.3 waves of clusters; their bytes alone
-// 21.5), 80 without filters, 92 with top-k 50, 250 with top-p 0.9 and 131 with
-// filters of every kind mixed; one fp32 row with top-k 50 takes 13.7, greedy 5.5.
+// 151936 bf16 logits take 49 us greedy (6.3 waves of clusters; their bytes alone
+// 21.5), 87 without filters, 92 with top-k 50, 251 with top-p 0.9 and 133 with
+// filters of every kind mixed; one fp32 row takes 5 greedy, 12 with top-k 50, 13 with
+// top-p and min-p on top of it and 33 with top-p 0.95 alone.
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -492,8 +493,9 @@ __device__ __noinline__ void draw_sorted(const SampleParams& p, int row, Shared*
 // The same for a longer list in s->list; block-collective.  The border (t, m) as for a
 // whole row, found by halving the range of codes; a thread holds kListPer tokens.
 // (Counting costs n per token, halving some 50 block sums whatever n: 480 rows with
-// top-k 50, about 70 tokens, 97 us counted and 114 halved; with top-k 400, about 450,
-// 165 and 129.  The border between them is what half a block's threads hold.)
+// top-k 50, about 70 tokens, 92 us counted and 113 halved, one fp32 row 12 and 18; 480 with
+// top-k 400, about 450, 165 and 130.  The border between them is what half a block's
+// threads hold.)
 template <int SHIFT>
 __device__ __noinline__ void draw_halving(const SampleParams& p, int row, Shared* s, int n, int k, float top_p,
                                          float min_p, float uf, float temp, float from, const Weight& w) {
@@ -1309,12 +1311,13 @@ void launch_sample(const SampleParams& p, int rows, cudaStream_t st) {
   // Small clusters repeat less of a row's fixed work and leave room for more rows at
   // once, large ones are sooner done with a row: once there is a CTA to every SM, the
   // smallest cluster whose slices let several CTAs share an SM.  With top-p 0.9, bf16,
-  // clusters of 8 / 4 / 2, us: 400 rows of 8192 124 / 59 / 42, of 50000 156 / 89 / 76, of
-  // 100000 176 / 137 / 234, of 151936 211 / 212 / 312; 32 rows of 50000 25 / 24 / 30;
-  // one row of 151936 27 / 36 / 56.  Slices of which few fit an SM are worse than none: 128
-  // rows of 250000 118 resident in clusters of 8, 109 read again (from L2, mostly) in
-  // clusters of 4; fp32, 400 rows of 75000 231 / 173, of 151936 444 / 248; bf16, 480 rows
-  // of 151936 with mixed filters 132 / 136.
+  // clusters of 8 / 4 / 2, us: 400 rows of 8192 122 / 57 / 38, of 50000 157 / 89 / 74, of
+  // 100000 177 / 133 / 210, of 151936 213 / 202 / 282; 32 rows of 50000 23 / 22 / 27;
+  // one row of 151936 25 / 31 / 48.  Slices of which few fit an SM are worse than none: 128
+  // rows of 250000 118 resident in clusters of 8, 105 read again (from L2, mostly) in
+  // clusters of 4; fp32, 400 rows of 151936 447 / 244.  At kFewSlice it depends on the
+  // filters: bf16, 480 rows of 151936 (37 KB) with mixed filters 134 / 136, 400 with top-p
+  // 0.9 213 / 188; fp32, 400 of 75000 with top-p 0.9 234 / 170.
   auto slice = [&](int cl) { return ((long long)p.vocab * (int)sizeof(T) + cl - 1) / cl; };
   auto fits = [&](int cl) { return (long long)rows * cl * 2 > num_sms() && slice(cl) <= kManySlice; };
   if (slice(8) > kMaxSlice)

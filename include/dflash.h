@@ -518,16 +518,17 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
  *   out   bf16 [n_rows] rows out_ld apart; rows at or past row_off[n_req] are
  *         left as they are
  * max_rows is a host bound on the rows of one request, used to choose the
- * kernel; results do not depend on it being tight.  Sizes stay on the device,
- * so a captured call serves contexts that grow.  The work (requests x KV heads
- * x query tiles x key tiles) is split evenly over the SMs; a tile split between
- * CTAs is joined in key order, so results do not depend on timing.  A slot that some
- * row sees and whose page is not there reads as zeros and records
- * DFLASH_ERR_INVALID_ARG in the workspace status word; pages that no row sees
- * (behind a tree's last node) need not be there.  A slot that some row sees past
- * the table (pos0[r] + j >= table_ld * page_size) records the same error and is
- * left out of the softmax; so does a request with rows whose pos0 is negative
- * (taken as 0) or past the table (taken as its end).
+ * kernel; it need not be tight, nor hold (results differ by the order of fp32
+ * sums).  Sizes stay on the device, so a captured call serves contexts that
+ * grow.  The work (requests x KV heads x query tiles x key tiles) is split
+ * evenly over the SMs; a tile split between CTAs is joined in key order, so
+ * results do not depend on timing.
+ * DFLASH_ERR_INVALID_ARG in the workspace status word: some row sees a slot
+ * whose page is not there (it reads as zeros), or a slot past the table,
+ * pos0[r] + j >= table_ld * page_size (it is left out of the softmax), or a
+ * request with rows has a pos0 that is negative (taken as 0) or past the table
+ * (taken as its end).  Slots that no row sees, as behind a tree's last node,
+ * need neither a page nor a place in the table.
  * Requires DFLASH_BF16 pages, n_q a multiple of n_kv, n_rows * n_q < 2^30,
  * strides that are multiples of 8 elements and 16-byte aligned q and out.  ws of
  * dflash_paged_attention_workspace_bytes bytes, zeroed once
