@@ -23,7 +23,8 @@
 //
 // Rows whose mask hides a key must not meet that key's value: 0 * NaN is not 0.
 // In steps where some row may not see some key, values that are not finite are
-// looked for, and such a step takes its second product row by row.
+// looked for: they count as zeros in the second product, and rows that see one take
+// the value itself.  So what no row sees changes no bit of a result.
 #include <cmath>
 
 #include <math_constants.h>
@@ -242,44 +243,41 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
             odd |= not_finite8(*reinterpret_cast<const uint4*>(tile + S::kTile + (lane + 32 * u) * 16));
           odd = __any_sync(0xffffffffu, odd);
         }
-        if (!odd) {
-          const uint32_t pf[4] = {mmas::pack_bf16(s[0][0], s[0][1]), mmas::pack_bf16(s[0][2], s[0][3]),
-                                  mmas::pack_bf16(s[1][0], s[1][1]), mmas::pack_bf16(s[1][2], s[1][3])};
-#pragma unroll
-          for (int nt = 0; nt < kNt; nt += 2) {
-            uint32_t b0, b1, b2, b3;
-            mmas::ldsm_x4_t(sV + mmas::swz<HD>((((lane >> 3) & 1) << 3) + (lane & 7), nt + (lane >> 4)),
-                            b0, b1, b2, b3);
-            mmas::mma16816(o[nt], pf, b0, b1);
-            mmas::mma16816(o[nt + 1], pf, b2, b3);
-          }
-        } else {
-          // a value that is not finite: each row adds the keys it sees, one by one
+        if (odd) {
+          // A value that is not finite: rows that see it take the value itself (times any
+          // weight it is the same inf or NaN), and it counts as zero in the product.
           for (int key = 0; key < 16; ++key) {
             const int nt = key >> 3, from = (lane & ~3) | ((key & 7) >> 1);
-            float pr[2];
-            bool see[2];
             const unsigned sb = __shfl_sync(0xffffffffu, seen, from);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float x = nt ? ((key & 1) ? s[1][2 * h + 1] : s[1][2 * h])
-                                 : ((key & 1) ? s[0][2 * h + 1] : s[0][2 * h]);
-              pr[h] = __bfloat162float(__float2bfloat16_rn(__shfl_sync(0xffffffffu, x, from)));
-              see[h] = (sb >> (4 * nt + 2 * h + (key & 1))) & 1u;
-            }
 #pragma unroll
             for (int t = 0; t < kNt; ++t) {
               const uint32_t w = *reinterpret_cast<const uint32_t*>(
                   tile + S::kTile + mmas::swz<HD>(key, t) + cq * 2);
-              const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xFFFF0000u);
+              const float v[2] = {__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)};
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                if (see[h]) {
-                  o[t][2 * h] += pr[h] * v0;
-                  o[t][2 * h + 1] += pr[h] * v1;
-                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (((sb >> (4 * nt + 2 * h + (key & 1))) & 1u) && !(fabsf(v[e]) <= CUDART_MAX_NORMAL_F))
+                    o[t][2 * h + e] += v[e];
             }
           }
+          __syncwarp();
+          for (int u = 0; u < kCh / 2; ++u) {
+            uint4* w = reinterpret_cast<uint4*>(ring + (i % kStagesS) * 2 * S::kTile + S::kTile) + lane + 32 * u;
+            *w = make_uint4(zero_not_finite(w->x), zero_not_finite(w->y), zero_not_finite(w->z), zero_not_finite(w->w));
+          }
+          __syncwarp();
+        }
+        const uint32_t pf[4] = {mmas::pack_bf16(s[0][0], s[0][1]), mmas::pack_bf16(s[0][2], s[0][3]),
+                                mmas::pack_bf16(s[1][0], s[1][1]), mmas::pack_bf16(s[1][2], s[1][3])};
+#pragma unroll
+        for (int nt = 0; nt < kNt; nt += 2) {
+          uint32_t b0, b1, b2, b3;
+          mmas::ldsm_x4_t(sV + mmas::swz<HD>((((lane >> 3) & 1) << 3) + (lane & 7), nt + (lane >> 4)),
+                          b0, b1, b2, b3);
+          mmas::mma16816(o[nt], pf, b0, b1);
+          mmas::mma16816(o[nt + 1], pf, b2, b3);
         }
       }
       __syncwarp();   // the slot may be loaded again

@@ -687,3 +687,29 @@ def test_trace_hook_sees_every_launch():
             assert seen == [(n, p) for n in names for p in (0, 1)]
     finally:
         bd.set_trace_hook(None)
+
+
+@pytest.mark.parametrize("rows,n_q", [([1] * 60, 14), ([2, 3, 0, 4] * 10, 8), ([7, 20] * 4, 6), ([40, 100], 8)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attention_what_no_row_sees_changes_no_bit(rows, n_q, bad):
+    """Slots between others that no row's mask has a bit for, of NaN keys and of values
+    that are not finite; some rows see nothing new, some nothing at all."""
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        ctx = [int(c) * (i % 5 > 0) for i, c in enumerate(rng.integers(1, 60, size=len(rows)))]
+        d = _build(rows, ctx, n_q, 2, 128, 64, True, seed=seed)
+        m = (rng.integers(0, 1 << 32, size=d["mask"].shape) & rng.integers(0, 1 << 32, size=d["mask"].shape)).astype(np.uint32)
+        m[rng.random(len(m)) < 0.4] = 0
+        d["mask"] = m
+        clean, ws = _attend(d)
+        dirty = dict(d, pk=torch.full_like(d["pk"], float("nan")), pv=torch.full_like(d["pv"], bad))
+        for r, (n, c) in enumerate(zip(rows, ctx)):
+            a = d["off"][r]
+            for t in np.flatnonzero(op.visible(n, c, n + c, m[a:a + n]).any(0)):
+                pg = d["table"][r, t // 64]
+                dirty["pk"][pg, :, t % 64] = d["pk"][pg, :, t % 64]
+                dirty["pv"][pg, :, t % 64] = d["pv"][pg, :, t % 64]
+        got, _ = _attend(dirty, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(got, clean)
+        _check(d, got)
