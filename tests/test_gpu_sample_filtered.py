@@ -352,3 +352,19 @@ def test_sample_does_not_depend_on_the_batch():
                 for i in range(4):
                     t1, l1 = _run(x[i:i + 1], u[i:i + 1], {n: [v] for n, v in how.items()})
                     assert (t2[i::4] == t1[0]).all() and (l2[i::4] == l1[0]).all(), (dtype, vocab, how, i)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sample_largest_vocabulary(dtype):
+    """2^22 equal logits: the most tokens to a thread, each of the largest mass, whose sum
+    is 2^62; then random ones."""
+    vocab = 1 << 22
+    x = torch.zeros(3, vocab, dtype=dtype, device=DEV)
+    for how, kept in ((dict(), vocab), (dict(top_p=0.5), vocab // 2), (dict(top_k=1000000), 1000000),
+                      (dict(top_k=3000000, top_p=0.25), 750000), (dict(top_k=500), 500)):
+        tok, lp = _run(x, [0.5, 0.0, 1.0], {k: [v] * 3 for k, v in how.items()})
+        assert tok.tolist() == [kept // 2, 0, kept - 1]
+        assert np.all(np.abs(lp + math.log(kept)) <= 2.0 ** -23 * math.log(kept) + 2.0 ** -23)
+    rng = np.random.default_rng(13)
+    x = _logits(rng, 2, vocab, dtype)
+    _check(x, rng.random(2), dict(top_p=[1.0, 0.9], top_k=[0, 2000000]))
