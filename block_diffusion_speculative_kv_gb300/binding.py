@@ -65,6 +65,13 @@ class PagesStruct(C.Structure):
                 ("n_kv", C.c_int), ("head_dim", C.c_int), ("dtype", C.c_int)]
 
 
+class PagesE4M3Struct(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("table", C.c_void_p), ("table_ld", C.c_int),
+                ("n_pages", C.c_int), ("page_size", C.c_int), ("n_kv", C.c_int),
+                ("head_dim", C.c_int)]
+
+
 def sampling_arg(sampling):
     """None, or (temperature, seed[, row_offset]) -> a Sampling pointer argument."""
     if sampling is None:
@@ -113,6 +120,14 @@ _SIGS = {
     "dflash_paged_attention_workspace_bytes": (_sz, [_i, _i, _i]),
     "dflash_paged_attention": (_i, [C.POINTER(PagesStruct), _i, _i, _i, _vp, _vp, _i, _vp,
                                     C.c_longlong, _vp, _i, _vp, C.c_longlong, _vp, _sz, _vp]),
+    "dflash_paged_append_e4m3": (_i, [C.POINTER(PagesE4M3Struct), _i, _i, _vp, _vp, _vp, _i, _vp,
+                                      _vp, C.c_longlong, C.c_float, _vp]),
+    "dflash_paged_attention_e4m3_workspace_bytes": (_sz, [_i, _i, _i]),
+    "dflash_paged_attention_e4m3": (_i, [C.POINTER(PagesE4M3Struct), _i, _i, _i, _vp, _vp, _i, _vp,
+                                         C.c_longlong, _vp, _i, _vp, C.c_longlong, _vp, _sz, _vp]),
+    "dflash_logits_adjust": (_i, [_i, _i, _i, _i, _vp, C.c_longlong, _vp, C.c_longlong, _vp, _vp,
+                                  _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _vp,
+                                  C.c_longlong, _vp]),
     "dflash_logits_sample_filtered": (_i, [_i, _i, C.c_longlong, _i, _vp, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _vp]),
     "dflash_linear_workspace_bytes": (_sz, [_i, _i, _i]),
@@ -494,12 +509,8 @@ def paged_attention_workspace_bytes(n_q: int, n_kv: int, head_dim: int) -> int:
     return int(lib().dflash_paged_attention_workspace_bytes(n_q, n_kv, head_dim))
 
 
-def paged_attention(pages: Pages, q: torch.Tensor, row_off: torch.Tensor, pos0: torch.Tensor,
-                    max_rows: int, out: torch.Tensor, ws: torch.Tensor,
-                    mask: Optional[torch.Tensor] = None, stream=None):
-    """q, out [rows, n_q*head_dim] (bf16): request r's rows row_off[r] .. are its tokens
-    at slots pos0[r] .., causal, or by mask [rows, words] (int32 view of the bits over
-    the request's rows)."""
+def _attend(call, pages, q: torch.Tensor, row_off: torch.Tensor, pos0: torch.Tensor, max_rows: int,
+            out: torch.Tensor, ws: torch.Tensor, mask: Optional[torch.Tensor], stream):
     n, hd = q.shape[0], pages.head_dim
     if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape != q.shape:
         raise ValueError("q and out: expected bf16 [rows, n_q * head_dim]")
@@ -512,12 +523,147 @@ def paged_attention(pages: Pages, q: torch.Tensor, row_off: torch.Tensor, pos0: 
         raise ValueError("ws: expected a contiguous tensor")
     qp, ql = _rows(q, "q")
     op, ol = _rows(out, "out")
-    _check(lib().dflash_paged_attention(
+    _check(call(
         pages.ref, pages.n_req, n, q.shape[1] // hd,
         _vec(row_off, pages.n_req + 1, torch.int32, "row_off"),
         _vec(pos0, pages.n_req, torch.int32, "pos0"), max_rows, qp, ql,
         None if mask is None else _vec(mask, mask.numel(), torch.int32, "mask"),
         0 if mask is None else mask.shape[1], op, ol, ws.data_ptr(), ws.nbytes,
+        _handle(stream, dev)))
+
+
+def paged_attention(pages: Pages, q: torch.Tensor, row_off: torch.Tensor, pos0: torch.Tensor,
+                    max_rows: int, out: torch.Tensor, ws: torch.Tensor,
+                    mask: Optional[torch.Tensor] = None, stream=None):
+    """q, out [rows, n_q*head_dim] (bf16): request r's rows row_off[r] .. are its tokens
+    at slots pos0[r] .., causal, or by mask [rows, words] (int32 view of the bits over
+    the request's rows)."""
+    _attend(lib().dflash_paged_attention, pages, q, row_off, pos0, max_rows, out, ws, mask, stream)
+
+
+class PagesE4M3:
+    """A paged KV cache of one layer in 8 bits: pools [n_pages, n_kv, page_size, head_dim]
+    of float8_e4m3fn (or its bytes, uint8), scales [n_pages, n_kv, page_size / 16] of
+    float8_e8m0fnu (or uint8: 2^(b - 127)), one to a block of 16 slots, and the page
+    table.  Keeps the tensors alive; their entries may change between calls, their
+    storage not."""
+
+    def __init__(self, pool_k: torch.Tensor, pool_v: torch.Tensor, scale_k: torch.Tensor,
+                 scale_v: torch.Tensor, table: torch.Tensor):
+        codes, scales = (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
+        if pool_k.dim() != 4 or pool_k.shape != pool_v.shape or pool_k.dtype not in codes or \
+                pool_v.dtype not in codes:
+            raise ValueError("pools: expected two [n_pages, n_kv, page_size, head_dim] in 8 bits")
+        n_pages, n_kv, page, head_dim = pool_k.shape
+        for t in (scale_k, scale_v):
+            if t.dtype not in scales or t.shape != (n_pages, n_kv, page // 16):
+                raise ValueError("scales: expected two [n_pages, n_kv, page_size / 16] in 8 bits")
+        if table.dim() != 2 or table.dtype != torch.int32:
+            raise ValueError("table: expected int32 [n_req, pages]")
+        held = (pool_k, pool_v, scale_k, scale_v, table)
+        if not all(t.is_contiguous() for t in held):
+            raise ValueError("pools, scales and table must be contiguous")
+        if any(t.device != pool_k.device for t in held):
+            raise ValueError("pools, scales and table must be on one device")
+        if not pool_k.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        self.pool_k, self.pool_v, self.scale_k, self.scale_v, self.table = held
+        self.n_kv, self.head_dim, self.n_req = n_kv, head_dim, table.shape[0]
+        self.struct = PagesE4M3Struct(pool_k.data_ptr(), pool_v.data_ptr(), scale_k.data_ptr(),
+                                      scale_v.data_ptr(), table.data_ptr(), table.shape[1], n_pages,
+                                      page, n_kv, head_dim)
+        self.ref = C.byref(self.struct)
+
+
+def paged_append_e4m3(pages: PagesE4M3, k: torch.Tensor, v: torch.Tensor, row_off: torch.Tensor,
+                      pos0: torch.Tensor, theta: float = 0.0, pos: Optional[torch.Tensor] = None,
+                      stream=None):
+    """paged_append into a cache in 8 bits: k and v bf16 or fp32 [rows, n_kv*head_dim]."""
+    n, width = k.shape[0], pages.n_kv * pages.head_dim
+    if k.dtype is not v.dtype or k.shape != v.shape or k.dim() != 2 or k.shape[1] != width:
+        raise ValueError(f"k and v: expected [rows, {width}] of one type")
+    dev = _together(pages.pool_k, k, v, row_off, pos0, pos)
+    kp, kl = _rows(k, "k")
+    vp, vl = _rows(v, "v")
+    if kl != vl:
+        raise ValueError("k and v must have one row stride")
+    _check(lib().dflash_paged_append_e4m3(
+        pages.ref, pages.n_req, n, _vec(row_off, pages.n_req + 1, torch.int32, "row_off"),
+        _vec(pos0, pages.n_req, torch.int32, "pos0"), _vec(pos, n, torch.int32, "pos"),
+        _dtype_code(k), kp, vp, kl, theta, _handle(stream, dev)))
+
+
+def paged_attention_e4m3_workspace_bytes(n_q: int, n_kv: int, head_dim: int) -> int:
+    return int(lib().dflash_paged_attention_e4m3_workspace_bytes(n_q, n_kv, head_dim))
+
+
+def paged_attention_e4m3(pages: PagesE4M3, q: torch.Tensor, row_off: torch.Tensor,
+                         pos0: torch.Tensor, max_rows: int, out: torch.Tensor, ws: torch.Tensor,
+                         mask: Optional[torch.Tensor] = None, stream=None):
+    """paged_attention over a cache in 8 bits."""
+    _attend(lib().dflash_paged_attention_e4m3, pages, q, row_off, pos0, max_rows, out, ws, mask, stream)
+
+
+def _table(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str):
+    """Pointer and width of a contiguous [n, width] table of dtype (None: none)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} [{n}, entries]")
+    return (t.data_ptr(), t.shape[1]) if t.shape[1] else (None, 0)
+
+
+def logits_adjust(logits: torch.Tensor, out: torch.Tensor, row_off: torch.Tensor,
+                  history: Optional[torch.Tensor] = None,
+                  history_len: Optional[torch.Tensor] = None,
+                  prompt_len: Optional[torch.Tensor] = None,
+                  repetition: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None,
+                  frequency: Optional[torch.Tensor] = None, tok: Optional[torch.Tensor] = None,
+                  mask: Optional[torch.Tensor] = None, bias_tok: Optional[torch.Tensor] = None,
+                  bias_val: Optional[torch.Tensor] = None, allowed: Optional[torch.Tensor] = None,
+                  vocab: Optional[int] = None, stream=None):
+    """Bias, penalties for repeated tokens and a grammar's allowed tokens on the logits
+    [rows, columns] of ragged requests, into out (or in place).  A row's past is its
+    request's history [n_req, entries] up to history_len, the first prompt_len of it the
+    prompt, and tok [rows] of the rows it sees: by mask [rows, words] (int32 view of the
+    bits), or those up to itself.  bias_tok, bias_val [n_req, entries], allowed
+    [rows, words] (int32 view of the bits).  vocab: the first columns alone."""
+    if logits.dim() != 2 or out.shape != logits.shape or out.dtype is not logits.dtype:
+        raise ValueError("logits and out: expected [rows, columns] of one type")
+    if row_off.numel() == 0:
+        raise ValueError("row_off: expected n_req + 1 entries")
+    rows, width = logits.shape
+    n_req = row_off.numel() - 1
+    if vocab is None:
+        vocab = width
+    elif vocab > width:                       # (the library knows the rows' stride alone)
+        raise ValueError(f"vocab: {vocab} of {width} columns")
+    dev = _together(logits, out, row_off, history, history_len, prompt_len, repetition, presence,
+                    frequency, tok, mask, bias_tok, bias_val, allowed)
+    lp, ld = _rows(logits, "logits")
+    op, old = _rows(out, "out")
+    f32, i32 = torch.float32, torch.int32
+    hp, hl = _table(history, n_req, i32, "history")
+    if hp is not None and history_len is None:
+        raise ValueError("history without history_len")
+    if mask is not None and mask.shape[-1] == 0:              # (no words: a null pointer, a chain)
+        raise ValueError("mask: expected [rows, words]")
+    mp, ml = _table(mask, rows, i32, "mask")
+    if (bias_tok is None) != (bias_val is None) or \
+            (bias_tok is not None and bias_tok.shape != bias_val.shape):
+        raise ValueError("bias_tok and bias_val: expected one shape")
+    bt, nb = _table(bias_tok, n_req, i32, "bias_tok")
+    bv, _ = _table(bias_val, n_req, f32, "bias_val")
+    ap, al = (None, 0) if allowed is None else _rows(allowed, "allowed")
+    if allowed is not None and (allowed.dtype is not i32 or allowed.shape[0] != rows or
+                                32 * allowed.shape[1] < vocab):
+        raise ValueError("allowed: expected int32 [rows, a bit for each token]")
+    _check(lib().dflash_logits_adjust(
+        n_req, rows, vocab, _dtype_code(logits), lp, ld, op, old, _vec(row_off, n_req + 1, i32, "row_off"),
+        hp, hl, _vec(history_len, n_req, i32, "history_len"), _vec(prompt_len, n_req, i32, "prompt_len"),
+        _vec(repetition, n_req, f32, "repetition"), _vec(presence, n_req, f32, "presence"),
+        _vec(frequency, n_req, f32, "frequency"), _vec(tok, rows, i32, "tok"), mp, ml, bt, bv, nb, ap, al,
         _handle(stream, dev)))
 
 

@@ -63,6 +63,22 @@ __host__ __device__ __forceinline__ size_t align_up(size_t a, size_t b) {
   return (a + b - 1) / b * b;
 }
 
+// The last i in [0, n) that begins at or before a place, where begins(i) is true for a
+// prefix of them, 0 among it.  All lanes of a warp call it; each round narrows the range
+// 32-fold.
+template <typename F>
+__device__ __forceinline__ int last_begun(int n, int lane, F begins) {
+  int lo = 0, hi = n - 1;   // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const long long i = lo + (long long)step * (lane + 1);
+    const int past = __popc(__ballot_sync(0xffffffffu, i <= hi && begins(static_cast<int>(i))));
+    lo += past * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
 // Number of SMs of the current device (cached per device on the host).
 int num_sms();
 

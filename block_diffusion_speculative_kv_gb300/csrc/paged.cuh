@@ -20,6 +20,9 @@ inline int log2_int(int v) {
   return s;
 }
 
+// Slots of a page that share a scale (8-bit pools).
+constexpr int kScaleBlock = 16;
+
 // Page of a slot of request r, or -1 where there is none.
 __device__ __forceinline__ int page_of(const PagedView& pv, int r, int slot) {
   const int i = slot >> pv.page_shift;
@@ -52,5 +55,6 @@ __device__ __forceinline__ int request_of(const int32_t* row_off, int n_req, int
 
 // (n_req 0: a table of no rows, whose pointer may be null)
 dflash_status check_pages(const dflash_pages* p, int n_req, const char* what, PagedView* out);
+dflash_status check_pages(const dflash_pages_e4m3* p, int n_req, const char* what, PagedView* out);
 
 }  // namespace dfl

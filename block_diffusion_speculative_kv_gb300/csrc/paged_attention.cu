@@ -39,14 +39,6 @@ namespace dfl {
 
 namespace {
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-constexpr float kLazy = 8.f;   // a row's reference maximum may lag by this much (base-2 units)
-
 // ---------------------------------------------------------------------------
 // Few query rows (decoding): tiles of 16 rows on warp-level MMAs.
 // ---------------------------------------------------------------------------
@@ -58,9 +50,6 @@ constexpr float kLazy = 8.f;   // a row's reference maximum may lag by this much
 // take 99 us, 6.2 TB/s of the 6.8 that a copy reaches; with one CTA to an SM 136.  One
 // request over 2048 slots takes 10 us: launch, plan, one step and the join.
 constexpr int kRowsS = 16, kStepS = 64, kStagesS = 3, kThreadsS = 128, kPerSmS = 2;
-// Parts of a tile whose loads are in flight when they are joined (8 / 16 / 20: one row over
-// 2048 slots 10.0 / 9.9 / 9.6 us, four rows 15.6 / 15.5 / 14.1, one over 500 9.0 / 9.2 / 9.3).
-constexpr int kJoinS = 20;
 using GeoS = PagedGeo<kRowsS, kStepS, 4, kRowsS, 2>;
 
 template <int HD>
@@ -305,92 +294,7 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
       if ((lane & 3) == 0) sMl[warp * 16 + ra + 8 * h] = make_float2(m[h], l[h]);
     }
     __syncthreads();
-    // a thread takes four columns of a row: HD / 4 neighbours make a row
-    const int items = live * (HD / 4);
-    auto write = [&](int row, int col, const float4& v, float L) {
-      const int rho = rho0 + row, to = p.heads.quot(rho);
-      const float inv = 1.f / L;                         // a row that saw no key: zeros
-      *reinterpret_cast<uint2*>(p.out + (long long)(rq.row0 + to) * p.out_ld +
-                                (long long)(head0 + rho - to * p.heads.G) * HD + col) =
-          L == 0.f ? make_uint2(0, 0)
-                   : make_uint2(mmas::pack_bf16(v.x * inv, v.y * inv), mmas::pack_bf16(v.z * inv, v.w * inv));
-    };
-    auto add = [](float4& a, float f, const float4& v) {
-      a.x += f * v.x;
-      a.y += f * v.y;
-      a.z += f * v.z;
-      a.w += f * v.w;
-    };
-    const bool whole = n == pc.all;
-    int c0 = 0, c1 = 0;
-    if (!whole) paged_owners<GeoS>(c, total, end - c.left - c.at, pc.all, &c0, &c1);
-    const int bid = blockIdx.x;
-    const size_t slot = (size_t)bid * 2 + (bid == c0 ? 1 : 0);
-    for (int i = tid; i < items; i += kThreadsS) {
-      const int row = i / (HD / 4), col = i % (HD / 4) * 4;
-      float M = -CUDART_INF_F, L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, sMl[w * 16 + row].x);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 ml = sMl[w * 16 + row];
-        if (ml.y == 0.f) continue;                       // this warp saw nothing for the row
-        const float f = ex2(ml.x - M);
-        L += f * ml.y;
-        add(acc, f, *reinterpret_cast<const float4*>(sO + (w * 16 + row) * S::kLd + col));
-      }
-      if (whole) {
-        write(row, col, acc, L);
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + (slot * kRowsS + row) * HD + col) = acc;
-        if (col == 0) p.part_ml[slot * kRowsS + row] = make_float2(M, L);
-      }
-    }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) *sLast = atomicAdd(p.arrive + c0, 1) == c1 - c0;
-      __syncthreads();
-      if (*sLast) {
-        __threadfence();
-        if (tid == 0) p.arrive[c0] = 0;                  // for the next call
-        // the pieces' (max, sum) first, all at once, into the idle ring
-        float2* sPart = reinterpret_cast<float2*>(smem);
-        const int parts = c1 - c0 + 1;
-        for (int i = tid; i < parts * kRowsS; i += kThreadsS) {
-          const int cc = c0 + i / kRowsS;
-          sPart[i] = i % kRowsS < live
-                         ? __ldcg(p.part_ml + ((size_t)cc * 2 + (cc == c0)) * kRowsS + i % kRowsS)
-                         : make_float2(-CUDART_INF_F, 0.f);
-        }
-        __syncthreads();
-        for (int i = tid; i < items; i += kThreadsS) {
-          const int row = i / (HD / 4), col = i % (HD / 4) * 4;
-          float M = -CUDART_INF_F, L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k = 0; k < parts; ++k) M = fmaxf(M, sPart[k * kRowsS + row].x);
-          for (int k0 = 0; k0 < parts; k0 += kJoinS) {    // their loads in flight
-            float4 v[kJoinS];
-#pragma unroll
-            for (int k = 0; k < kJoinS; ++k) {
-              const int cc = c0 + min(k0 + k, parts - 1);
-              v[k] = __ldcg(reinterpret_cast<const float4*>(
-                  p.part_o + (((size_t)cc * 2 + (cc == c0)) * kRowsS + row) * HD + col));
-            }
-#pragma unroll
-            for (int k = 0; k < kJoinS; ++k) {
-              const float2 ml = sPart[min(k0 + k, parts - 1) * kRowsS + row];
-              if (k0 + k >= parts || ml.y == 0.f) continue;
-              const float f = ex2(ml.x - M);
-              L += f * ml.y;
-              add(acc, f, v[k]);
-            }
-          }
-          write(row, col, acc, L);
-        }
-      }
-    }
+    paged_finish_small<HD, kRowsS, S::kLd, kThreadsS, GeoS>(p, c, pc, total, end, rho0, live, sO, sMl, smem, sLast);
     __syncthreads();                                     // the ring is free again
   }
 }
@@ -477,19 +381,6 @@ struct Tc {
   static constexpr int kTmem = 256 * NG;                    // S_x at 128 x (P_x over it), then O_x
   static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
-
-// Bits of keys [b, b + 32) relative to the first new token: 1 = seen.
-__device__ __forceinline__ uint32_t seen_word(const uint32_t* mrow, int mask_ld, int b) {
-  if (b <= -32) return 0xFFFFFFFFu;                          // context
-  const int w = b >> 5, sh = b & 31;                         // floor: w = -1 for b in (-32, 0)
-  const uint32_t lo = w < 0 ? 0xFFFFFFFFu : (w < mask_ld ? __ldg(mrow + w) : 0u);
-  const uint32_t hi = w + 1 < mask_ld ? __ldg(mrow + w + 1) : 0u;
-  return __funnelshift_r(lo, hi, sh);
-}
-// The low n bits (n clamped to [0, 32]).
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
-}
 
 // Whether a value among eight is infinite or NaN: x * 0 is NaN for those, and
 // sticks in the sum.
@@ -1283,23 +1174,6 @@ dflash_status launch_tc(PagedAttnParams p, const dflash_pages& pages, cudaStream
     launch_k(paged_join_kernel<HD, NG>, dim3(grid, S::kRows / 32), dim3(256), 0, st, p);
   }
   return DFLASH_OK;
-}
-
-// Header, arrival counters, (max, sum) pairs, partial rows.
-struct PagedWs {
-  size_t arrive, cut, ml, o, bytes;
-};
-// Every kernel: two CTAs an SM at most, two counters an SM, and for each SM two
-// slots of 256 rows (or 2 x 2 of 128, or of 16).
-PagedWs paged_ws(int sms, int head_dim) {
-  PagedWs w;
-  const size_t rows = (size_t)sms * 2 * 256;
-  w.arrive = 256;
-  w.cut = w.arrive + align_up((size_t)sms * 2 * sizeof(int), 256);
-  w.ml = w.cut + align_up((size_t)sms * 2 * sizeof(PagedCut), 256);
-  w.o = w.ml + align_up(rows * sizeof(float2), 256);
-  w.bytes = w.o + rows * head_dim * sizeof(float);
-  return w;
 }
 
 }  // namespace

@@ -2,9 +2,20 @@
 // kernels (paged_attention.cu).
 #pragma once
 
+#include <math_constants.h>
+
+#include "mma_sync.cuh"
 #include "paged.cuh"
 
 namespace dfl {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLazy = 8.f;   // a row's reference maximum may lag by this much (base-2 units)
 
 // Query heads per KV head, and division by them: the quotient by 2^32 / G rounded
 // down is exact or one too small.
@@ -292,6 +303,140 @@ __device__ __forceinline__ void paged_owners(const PagedCursor& c, long long tot
                                              int* c0, int* c1) {
   *c0 = paged_owner<Geo>(total, tile0 + Geo::TC, c.ctas);
   *c1 = paged_owner<Geo>(total, tile0 + Geo::TC + (long long)(all - 1) * c.weight, c.ctas);
+}
+
+// Bits of keys [b, b + 32) relative to the first new token: 1 = seen.
+__device__ __forceinline__ uint32_t seen_word(const uint32_t* mrow, int mask_ld, int b) {
+  if (b <= -32) return 0xFFFFFFFFu;                          // context
+  const int w = b >> 5, sh = b & 31;                         // floor: w = -1 for b in (-32, 0)
+  const uint32_t lo = w < 0 ? 0xFFFFFFFFu : (w < mask_ld ? __ldg(mrow + w) : 0u);
+  const uint32_t hi = w + 1 < mask_ld ? __ldg(mrow + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+// The low n bits (n clamped to [0, 32]).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// Parts of a tile whose loads are in flight when they are joined (8 / 16 / 20: one row over
+// 2048 slots 10.0 / 9.9 / 9.6 us, four rows 15.6 / 15.5 / 14.1, one over 500 9.0 / 9.2 / 9.3).
+constexpr int kJoin = 20;
+
+// The end of a piece of a tile of few rows: the states of its four warps, sO [4][ROWS][LD]
+// unnormalised and sMl [4][ROWS] (max, sum), of which `live` rows count, become rows of
+// out; or, where shares' borders cut the tile, a part of it, and the last of its CTAs to
+// arrive joins the parts, in key order.  scratch: at least ROWS x 8 bytes x grid, free
+// once sO has been read.  Block-collective; sLast: one int.
+template <int HD, int ROWS, int LD, int THREADS, typename Geo>
+__device__ __forceinline__ void paged_finish_small(const PagedAttnParams& p, const PagedCursor& c,
+                                                   const PagedPiece& pc, long long total, long long end, int rho0,
+                                                   int live, const float* sO, const float2* sMl, void* scratch,
+                                                   int* sLast) {
+  const PagedReq& rq = c.rq;
+  const int tid = threadIdx.x, head0 = c.g * p.heads.G;
+  // a thread takes four columns of a row: HD / 4 neighbours make a row
+  const int items = live * (HD / 4);
+  auto write = [&](int row, int col, const float4& v, float L) {
+    const int rho = rho0 + row, to = p.heads.quot(rho);
+    const float inv = 1.f / L;                         // a row that saw no key: zeros
+    *reinterpret_cast<uint2*>(p.out + (long long)(rq.row0 + to) * p.out_ld +
+                              (long long)(head0 + rho - to * p.heads.G) * HD + col) =
+        L == 0.f ? make_uint2(0, 0)
+                 : make_uint2(mmas::pack_bf16(v.x * inv, v.y * inv), mmas::pack_bf16(v.z * inv, v.w * inv));
+  };
+  auto add = [](float4& a, float f, const float4& v) {
+    a.x += f * v.x;
+    a.y += f * v.y;
+    a.z += f * v.z;
+    a.w += f * v.w;
+  };
+  const bool whole = pc.n == pc.all;
+  int c0 = 0, c1 = 0;
+  if (!whole) paged_owners<Geo>(c, total, end - c.left - c.at, pc.all, &c0, &c1);
+  const int bid = blockIdx.x;
+  const size_t slot = (size_t)bid * 2 + (bid == c0 ? 1 : 0);
+  for (int i = tid; i < items; i += THREADS) {
+    const int row = i / (HD / 4), col = i % (HD / 4) * 4;
+    float M = -CUDART_INF_F, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, sMl[w * ROWS + row].x);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 ml = sMl[w * ROWS + row];
+      if (ml.y == 0.f) continue;                       // this warp saw nothing for the row
+      const float f = ex2(ml.x - M);
+      L += f * ml.y;
+      add(acc, f, *reinterpret_cast<const float4*>(sO + (w * ROWS + row) * LD + col));
+    }
+    if (whole) {
+      write(row, col, acc, L);
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (slot * ROWS + row) * HD + col) = acc;
+      if (col == 0) p.part_ml[slot * ROWS + row] = make_float2(M, L);
+    }
+  }
+  if (!whole) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) *sLast = atomicAdd(p.arrive + c0, 1) == c1 - c0;
+    __syncthreads();
+    if (*sLast) {
+      __threadfence();
+      if (tid == 0) p.arrive[c0] = 0;                  // for the next call
+      // the pieces' (max, sum) first, all at once, into the idle ring
+      float2* sPart = reinterpret_cast<float2*>(scratch);
+      const int parts = c1 - c0 + 1;
+      for (int i = tid; i < parts * ROWS; i += THREADS) {
+        const int cc = c0 + i / ROWS;
+        sPart[i] = i % ROWS < live
+                       ? __ldcg(p.part_ml + ((size_t)cc * 2 + (cc == c0)) * ROWS + i % ROWS)
+                       : make_float2(-CUDART_INF_F, 0.f);
+      }
+      __syncthreads();
+      for (int i = tid; i < items; i += THREADS) {
+        const int row = i / (HD / 4), col = i % (HD / 4) * 4;
+        float M = -CUDART_INF_F, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < parts; ++k) M = fmaxf(M, sPart[k * ROWS + row].x);
+        for (int k0 = 0; k0 < parts; k0 += kJoin) {    // their loads in flight
+          float4 v[kJoin];
+#pragma unroll
+          for (int k = 0; k < kJoin; ++k) {
+            const int cc = c0 + min(k0 + k, parts - 1);
+            v[k] = __ldcg(reinterpret_cast<const float4*>(
+                p.part_o + (((size_t)cc * 2 + (cc == c0)) * ROWS + row) * HD + col));
+          }
+#pragma unroll
+          for (int k = 0; k < kJoin; ++k) {
+            const float2 ml = sPart[min(k0 + k, parts - 1) * ROWS + row];
+            if (k0 + k >= parts || ml.y == 0.f) continue;
+            const float f = ex2(ml.x - M);
+            L += f * ml.y;
+            add(acc, f, v[k]);
+          }
+        }
+        write(row, col, acc, L);
+      }
+    }
+  }
+}
+
+// Header, arrival counters, (max, sum) pairs, partial rows.
+struct PagedWs {
+  size_t arrive, cut, ml, o, bytes;
+};
+// Every kernel: per_sm CTAs an SM at most, one counter to a CTA (two where it has an SM
+// alone), and for each SM two slots of 256 rows (or fewer rows to more CTAs).
+inline PagedWs paged_ws(int sms, int head_dim, int per_sm = 2) {
+  PagedWs w;
+  const size_t rows = (size_t)sms * 2 * 256;
+  w.arrive = 256;
+  w.cut = w.arrive + align_up((size_t)sms * per_sm * sizeof(int), 256);
+  w.ml = w.cut + align_up((size_t)sms * per_sm * sizeof(PagedCut), 256);
+  w.o = w.ml + align_up(rows * sizeof(float2), 256);
+  w.bytes = w.o + rows * head_dim * sizeof(float);
+  return w;
 }
 
 }  // namespace dfl

@@ -17,6 +17,9 @@
 // p 2^-64 turns and the frequency's 53 bits).
 #include <cmath>
 
+#include <cuda_fp8.h>
+#include <math_constants.h>
+
 #include "kernels.h"
 #include "paged.cuh"
 
@@ -40,6 +43,16 @@ dflash_status check_pages(const dflash_pages* p, int n_req, const char* what, Pa
   DFL_REQUIRE(((reinterpret_cast<uintptr_t>(p->k) | reinterpret_cast<uintptr_t>(p->v)) & 15) == 0,
               "%s: pools must be 16-byte aligned", what);
   *out = PagedView{p->k, p->v, p->table, p->table_ld, p->n_pages, log2_int(p->page_size), p->n_kv};
+  return DFLASH_OK;
+}
+
+dflash_status check_pages(const dflash_pages_e4m3* p, int n_req, const char* what, PagedView* out) {
+  DFL_REQUIRE(p, "%s: null pages", what);
+  const dflash_pages same = {p->k,         p->v,    p->table,    p->table_ld, p->n_pages,
+                             p->page_size, p->n_kv, p->head_dim, DFLASH_BF16};
+  const dflash_status s = check_pages(&same, n_req, what, out);
+  if (s) return s;
+  DFL_REQUIRE(p->k_scale && p->v_scale, "%s: null scales", what);
   return DFLASH_OK;
 }
 
@@ -359,6 +372,152 @@ __global__ void __launch_bounds__(kThreads, 3) paged_append_kernel(const AppendP
   }
 }
 
+// ---------------------------------------------------------------------------
+// The append into a cache held in 8 bits
+// ---------------------------------------------------------------------------
+// A scale belongs to a block of 16 slots, so a block is a CTA's, and a block of one KV
+// head's keys or values a warp's: the warp holds all its rows in registers (16 rows of
+// 128 elements are 64 to a lane), rotates them, finds the largest element and the
+// scale, and writes the codes.  Memory bounds it: rows in once, codes and scales out.
+struct AppendE4M3Params {
+  PagedView pv;
+  uint8_t *k_scale, *v_scale;
+  int n_req, n_rows;
+  const int32_t *row_off, *pos0, *pos;
+  const void *k, *v;
+  long long kv_ld;
+  int rotate;
+  RopeTurns fr;
+};
+
+// Biased exponent of the smallest power of two >= 2^-127 at which `top` (finite, >= 0)
+// is at most 448 = 1.75 * 2^8.
+__device__ __forceinline__ int scale_for(float top) {
+  const uint32_t b = __float_as_uint(top);
+  return max(static_cast<int>(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0), 0);
+}
+// 2^(127 - b) for a biased exponent 0 <= b <= 253.
+__device__ __forceinline__ float unscale(int b) { return __uint_as_float(static_cast<uint32_t>(254 - b) << 23); }
+
+__device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) |
+         static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
+}
+__device__ __forceinline__ float2 values2(uint32_t codes) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3)));
+}
+// Four codes times f (a power of two below 1), rounded again.
+__device__ __forceinline__ uint32_t recode4(uint32_t c, float f) {
+  const float2 a = values2(c & 0xFFFFu), b = values2(c >> 16), f2 = make_float2(f, f);
+  return codes4(__fmul2_rn(a, f2), __fmul2_rn(b, f2));
+}
+
+// Blocks of requests lie on a line without a prefix sum: those of request r, at most
+// (n + 30) / 16 for its n rows, begin at row_off[r] / 16 + 2 r.
+__device__ __forceinline__ int first_block(const AppendE4M3Params& p, int r) {
+  return (min(max(__ldg(p.row_off + r), 0), p.n_rows) >> 4) + 2 * r;
+}
+
+template <typename T, int HD, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) paged_append_e4m3_kernel(const AppendE4M3Params p) {
+  constexpr int kLanes = HD / 16, kHalf = HD / 2, kPass = 32 / kLanes, kPasses = kScaleBlock / kPass;
+  __shared__ Turns<HD> cs[kScaleBlock];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % kLanes;
+  pdl_wait();
+  pdl_trigger();
+  const int req = last_begun(p.n_req, lane, [&](int r) { return first_block(p, r) <= static_cast<int>(blockIdx.x); });
+  const int row0 = min(max(p.row_off[req], 0), p.n_rows);
+  const int n = min(max(p.row_off[req + 1], row0), p.n_rows) - row0, p0 = p.pos0[req];
+  const long long s0 = ((long long)(p0 >> 4) + (static_cast<int>(blockIdx.x) - first_block(p, req))) * kScaleBlock;
+  if (n == 0 || s0 >= (long long)p0 + n || s0 < 0 || s0 >= (1ll << 30)) return;    // block-uniform
+  const int slot0 = static_cast<int>(s0), page = page_of(p.pv, req, slot0);
+  if (page < 0) return;
+  const int lead = row0 - p0 + slot0;                      // row of the block's first slot, were it new
+  const int old = min(max(p0 - slot0, 0), kScaleBlock);    // slots that hold earlier tokens
+  const int end = static_cast<int>(min((long long)p0 + n - slot0, (long long)kScaleBlock));
+
+  // the slots whose rows are stored
+  auto stored = [&](int s) { return s >= old && s < end && (!p.pos || __ldg(p.pos + lead + s) >= 0); };
+  const uint32_t live = __ballot_sync(0xffffffffu, lane < kScaleBlock && stored(lane));
+  if (live == 0) return;
+
+  const int items = 2 * p.pv.n_kv, warps = gridDim.y * (kThreads / 32);
+  Eight<T> a[kPasses], b[kPasses];
+  auto load = [&](int h) {
+    const bool is_k = h < p.pv.n_kv;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int s = i * kPass + lane / kLanes;
+      if (!((live >> s) & 1u)) continue;
+      const T* src = static_cast<const T*>(is_k ? p.k : p.v) + (lead + s) * p.kv_ld +
+                     (long long)(is_k ? h : h - p.pv.n_kv) * HD + 8 * sub;
+      a[i].template load<VEC>(src);
+      b[i].template load<VEC>(src + kHalf);
+    }
+  };
+  int h = blockIdx.y * (kThreads / 32) + warp;
+  if (h < items) load(h);
+  if (p.rotate) {
+    for (int i = tid; i < kScaleBlock * kHalf; i += kThreads) {
+      const int s = i / kHalf;
+      if ((live >> s) & 1u)
+        cs[s].put(i % kHalf, turn_cs(p.pos ? __ldg(p.pos + lead + s) : slot0 + s, p.fr.f[i % kHalf]));
+    }
+    __syncthreads();
+  }
+  for (; h < items; h += warps) {
+    const bool is_k = h < p.pv.n_kv;
+    const int g = is_k ? h : h - p.pv.n_kv;
+    const long long row = pool_row(p.pv, page, g, slot0);
+    uint8_t* scale = (is_k ? p.k_scale : p.v_scale) + row / kScaleBlock;
+    const int was = old > 0 ? min(static_cast<int>(*scale), 253) : 0;
+    float2 x[kPasses][4], y[kPasses][4];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int s = i * kPass + lane / kLanes;
+      if (!((live >> s) & 1u)) continue;
+      a[i].get(x[i]);
+      b[i].get(y[i]);
+      if (is_k && p.rotate) cs[s].rotate(x[i], y[i], sub);
+      auto see = [&](float& v) {                           // (NaN is no maximum)
+        if (!(fabsf(v) <= CUDART_MAX_NORMAL_F)) v = CUDART_NAN_F;
+        top = fmaxf(top, fabsf(v));
+      };
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        see(x[i][j].x);
+        see(x[i][j].y);
+        see(y[i][j].x);
+        see(y[i][j].y);
+      }
+    }
+    if (h + warps < items) load(h + warps);
+    const int fits = scale_for(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+    const int now = max(fits, was);
+    const float f = unscale(now);
+    const float2 f2 = make_float2(f, f);
+    uint8_t* dst = static_cast<uint8_t*>(is_k ? p.pv.k : p.pv.v) + row * HD;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int s = i * kPass + lane / kLanes;
+      uint2* lo = reinterpret_cast<uint2*>(dst + s * HD + 8 * sub);
+      uint2* hi = reinterpret_cast<uint2*>(dst + s * HD + kHalf + 8 * sub);
+      if ((live >> s) & 1u) {
+        *lo = make_uint2(codes4(__fmul2_rn(x[i][0], f2), __fmul2_rn(x[i][1], f2)),
+                         codes4(__fmul2_rn(x[i][2], f2), __fmul2_rn(x[i][3], f2)));
+        *hi = make_uint2(codes4(__fmul2_rn(y[i][0], f2), __fmul2_rn(y[i][1], f2)),
+                         codes4(__fmul2_rn(y[i][2], f2), __fmul2_rn(y[i][3], f2)));
+      } else if (s < old && now > was) {
+        const float shift = __uint_as_float(static_cast<uint32_t>(127 - min(now - was, 64)) << 23);   // 2^(was - now)
+        *lo = make_uint2(recode4(lo->x, shift), recode4(lo->y, shift));
+        *hi = make_uint2(recode4(hi->x, shift), recode4(hi->y, shift));
+      }
+    }
+    if (lane == 0) *scale = static_cast<uint8_t>(now);
+  }
+}
+
 bool many(int rows) { return rows >= 6 * num_sms(); }
 
 template <typename T, int HD, bool VEC>
@@ -377,6 +536,15 @@ void launch_append(const AppendParams& p, cudaStream_t st) {
              dim3(kThreads), 0, st, p);
   else
     launch_k(paged_append_kernel<T, HD, VEC, 1>, dim3(p.n_rows), dim3(kThreads), 0, st, p);
+}
+
+// One item to a warp where there are few blocks (latency), all of a block's to one CTA
+// where there are many, which then forms the rotations once.
+template <typename T, int HD, bool VEC>
+void launch_append_e4m3(const AppendE4M3Params& p, cudaStream_t st) {
+  const int blocks = (p.n_rows >> 4) + 2 * p.n_req, per = kThreads / 32;
+  const int split = blocks >= 4 * num_sms() ? 1 : (2 * p.pv.n_kv + per - 1) / per;
+  launch_k(paged_append_e4m3_kernel<T, HD, VEC>, dim3(blocks, split), dim3(kThreads), 0, st, p);
 }
 
 bool aligned16(const void* p, long long ld_bytes) {
@@ -491,6 +659,51 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
     pages->dtype == DFLASH_BF16 ? go(__nv_bfloat16()) : go(float());
   }
   return check_launch("paged append");
+}
+
+dflash_status dflash_paged_append_e4m3(const dflash_pages_e4m3* pages, int n_req, int n_rows,
+                                       const int32_t* row_off, const int32_t* pos0,
+                                       const int32_t* pos, int dtype, const void* k,
+                                       const void* v, long long kv_ld, float theta, void* stream) {
+  AppendE4M3Params p{};
+  const dflash_status s = check_pages(pages, n_req, "paged append e4m3", &p.pv);
+  if (s) return s;
+  DFL_REQUIRE(n_req >= 0 && n_rows >= 0, "paged append e4m3: sizes must be >= 0");
+  DFL_REQUIRE((n_rows >> 4) + 2 * (long long)n_req < (1ll << 30), "paged append e4m3: too many rows and requests");
+  DFL_REQUIRE(dtype == DFLASH_F32 || dtype == DFLASH_BF16, "paged append e4m3: dtype must be F32 or BF16");
+  DFL_REQUIRE(2 * (long long)pages->n_kv <= kMaxHeads, "paged append e4m3: more than %d KV heads", kMaxHeads / 2);
+  DFL_REQUIRE(kv_ld >= (long long)pages->n_kv * pages->head_dim, "paged append e4m3: row stride too small");
+  DFL_REQUIRE(theta == 0.f || (theta > 0.f && theta < 1e30f),
+              "paged append e4m3: theta must be 0 (no rotation) or positive");
+  if (n_req == 0 || n_rows == 0) return DFLASH_OK;
+  DFL_REQUIRE(row_off && pos0 && k && v, "paged append e4m3: null pointer argument");
+  p.k_scale = pages->k_scale;
+  p.v_scale = pages->v_scale;
+  p.n_req = n_req;
+  p.n_rows = n_rows;
+  p.row_off = row_off;
+  p.pos0 = pos0;
+  p.pos = pos;
+  p.k = k;
+  p.v = v;
+  p.kv_ld = kv_ld;
+  p.rotate = theta > 0.f;
+  if (p.rotate) p.fr = rope_turns(theta, pages->head_dim);
+  const long long es = dtype == DFLASH_F32 ? 4 : 2;
+  const bool vec = aligned16(k, kv_ld * es) && aligned16(v, kv_ld * es);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    TraceScope ts("paged_append_e4m3", st);
+    auto go = [&](auto t) {
+      using T = decltype(t);
+      if (pages->head_dim == 128)
+        vec ? launch_append_e4m3<T, 128, true>(p, st) : launch_append_e4m3<T, 128, false>(p, st);
+      else
+        vec ? launch_append_e4m3<T, 64, true>(p, st) : launch_append_e4m3<T, 64, false>(p, st);
+    };
+    dtype == DFLASH_BF16 ? go(__nv_bfloat16()) : go(float());
+  }
+  return check_launch("paged append e4m3");
 }
 
 }  // extern "C"

@@ -30,7 +30,9 @@
  * layout.  dflash_logits_topk / dflash_logits_sample run step a6 alone.
  * The target's own side of a cycle over a paged cache is dflash_qk_norm_rope,
  * dflash_paged_append, dflash_paged_attention and, after its LM head,
- * dflash_logits_sample_filtered (the walk's target_tok).
+ * dflash_logits_adjust and dflash_logits_sample_filtered (the walk's
+ * target_tok).  dflash_paged_append_e4m3 and dflash_paged_attention_e4m3 serve a
+ * cache held in 8 bits.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -541,6 +543,110 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
                                      const void* q, long long q_ld, const uint32_t* mask,
                                      int mask_ld, void* out, long long out_ld, void* ws,
                                      size_t ws_bytes, void* stream);
+
+/* A paged KV cache held in 8 bits: slots, pages and table as in dflash_pages,
+ * elements as e4m3 codes (one sign, four exponent, three fraction bits; largest
+ * 448, 0x7F and 0xFF NaN, no infinities), and one scale for every 16 slots (a
+ * block) of a KV head, keys and values apart.  A scale is a power of two kept as
+ * its biased exponent: byte b stands for 2^(b - 127), and an element for its
+ * code's value times its block's scale.
+ *   k, v              uint8 [n_pages][n_kv][page_size][head_dim] (device),
+ *                     16-byte aligned
+ *   k_scale, v_scale  uint8 [n_pages][n_kv][page_size / 16] (device)
+ *   table             int32 [n_req][table_ld] (device)
+ * Limits as for dflash_pages. */
+typedef struct dflash_pages_e4m3 {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  const int32_t* table;
+  int table_ld;
+  int n_pages;
+  int page_size;
+  int n_kv;
+  int head_dim;
+} dflash_pages_e4m3;
+
+/* dflash_paged_append into a cache held in 8 bits; k and v are rows of T = dtype.
+ * For every block that takes rows of a request, and each KV head of keys (rotated,
+ * in fp32) and of values:
+ *   e     the smallest exponent >= -127 with max |y| <= 448 * 2^e over the
+ *         elements y that are stored; if slots of the block lie before pos0[r]
+ *         (earlier tokens of the request), at least the block's present exponent,
+ *         and where it grew their codes c become round(c * 2^(old - e))
+ *   code  round(y * 2^-e), to the nearest, ties to even; NaN for a y that is
+ *         infinite or NaN, which counts for no maximum
+ * So a block that begins at or after pos0[r] forgets what it held, and slots at or
+ * past pos0[r] (of a drafted token that was refused, say) are void.  A code keeps
+ * its value exactly at a larger scale unless that value falls below 2^-6 of the
+ * scale (the codes' subnormals): token by token or at once makes a difference
+ * there alone.
+ * Rows, row_off, pos0, pos, theta and rows that are not stored: as there.
+ * Requests that share a page may share only blocks that neither writes.  Needs no
+ * workspace. */
+dflash_status dflash_paged_append_e4m3(const dflash_pages_e4m3* pages, int n_req, int n_rows,
+                                       const int32_t* row_off, const int32_t* pos0,
+                                       const int32_t* pos, int dtype, const void* k,
+                                       const void* v, long long kv_ld, float theta, void* stream);
+
+/* dflash_paged_attention over a cache held in 8 bits: the same rows, masks, bounds,
+ * workspace rules (of dflash_paged_attention_e4m3_workspace_bytes bytes) and
+ * errors; q and out bf16.  Codes enter the products as they are, exactly; scales
+ * are applied to fp32 scores and weights.  A NaN code reaches the rows that see
+ * its slot; what no row sees, scales included, may hold anything. */
+size_t dflash_paged_attention_e4m3_workspace_bytes(int n_q, int n_kv, int head_dim);
+dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_req, int n_rows,
+                                          int n_q, const int32_t* row_off, const int32_t* pos0,
+                                          int max_rows, const void* q, long long q_ld,
+                                          const uint32_t* mask, int mask_ld, void* out,
+                                          long long out_ld, void* ws, size_t ws_bytes,
+                                          void* stream);
+
+/* Logits before sampling: bias, penalties for repeated tokens, and the tokens a
+ * grammar allows, for the rows of every request, rows row_off[r] ..
+ * row_off[r+1] - 1 (one decoded token, a drafted chain, the nodes of a tree).  In
+ * this order, in fp32, rounded once:
+ *   bias        y = l + bias_val[r][j] for v = bias_tok[r][j] (listed twice: the
+ *               later entry counts)
+ *   repetition  y = y > 0 ? y / repetition[r] : y * repetition[r] for a token that
+ *               the row's past holds
+ *   frequency,  y = y - frequency[r] * c - presence[r] for a token that it holds
+ *   presence    c > 0 times outside the prompt
+ *   allowed     y = -inf where bit v % 32 of word v / 32 of the row is not set
+ * A row's past: history[r][0 .. history_len[r]), of which the first prompt_len[r]
+ * are the prompt's (the request's tokens before its rows), then the tokens
+ * tok[row_off[r] + j] of the rows j of its request that it sees, by bit j of its
+ * mask row (a tree: its ancestors and itself; the mask ddtree_build writes), or
+ * j <= its own place where mask is NULL.  So drafted rows are penalised as they
+ * would be if their path had been generated.  Tokens outside [0, vocab) count for
+ * nothing (-1 fills a list).
+ *   logits   T [rows] rows ld elements apart, T = dtype; out T likewise, out_ld
+ *            apart.  out may be logits (with one row stride); other overlap is
+ *            not allowed.  Columns from vocab on, and rows at or past
+ *            row_off[n_req], are left as they are
+ *   history  int32 [n_req][history_ld]; history_len, prompt_len int32 [n_req]
+ *            (lengths below 0 count as 0, past history_ld as history_ld;
+ *            prompt_len NULL: 0).  history may be NULL: none
+ *   repetition, presence, frequency  fp32 [n_req], NULL: off
+ *   tok      int32 [rows], NULL: rows' own tokens count for nothing
+ *   mask     uint32 [rows][mask_ld], NULL: a chain.  Bits past mask_ld words are
+ *            not set
+ *   bias_tok int32, bias_val fp32 [n_req][n_bias], n_bias 0: none
+ *   allowed  uint32 [rows] rows allowed_ld words apart, NULL: all
+ * All device pointers; lengths and offsets stay on the device, so a captured call
+ * serves histories that grow.  Results do not depend on timing.  rows may be 0.
+ * Requires 1 <= vocab <= 2^22, allowed_ld * 32 >= vocab, n_bias <= 2^20,
+ * rows + n_req < 2^30.  Needs no workspace. */
+dflash_status dflash_logits_adjust(int n_req, int rows, int vocab, int dtype, const void* logits,
+                                   long long ld, void* out, long long out_ld,
+                                   const int32_t* row_off, const int32_t* history, int history_ld,
+                                   const int32_t* history_len, const int32_t* prompt_len,
+                                   const float* repetition, const float* presence,
+                                   const float* frequency, const int32_t* tok,
+                                   const uint32_t* mask, int mask_ld, const int32_t* bias_tok,
+                                   const float* bias_val, int n_bias, const uint32_t* allowed,
+                                   long long allowed_ld, void* stream);
 
 /* The target's token of every row, from given random numbers (DFlash page,
  * 3.4.4: verification at temperature 1; DDTree page, 3.4.5: the walk's target
