@@ -31,7 +31,7 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-rdc=true", "-Xcompiler"
 
 # Compiled as whole programs: setmaxnreg (a register split between warpgroups)
 # is ignored under separate compilation.
-WHOLE_PROGRAM = {"paged_attention.cu"}
+WHOLE_PROGRAM = {"paged_attention.cu", "paged_attention_e4m3.cu"}
 
 
 def _nvcc() -> str:

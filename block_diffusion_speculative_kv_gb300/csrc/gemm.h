@@ -28,6 +28,10 @@ TcPlan tc_plan(int M_rows, int N_feat, int K, int grid, int tk_kpad = 0);
 bool encode_kmajor_map(CUtensorMap* map, const void* base, int rows, int K,
                        long long row_stride_elems, int box_rows);
 
+// The same of rows of 64 or 128 bytes without gaps, box = box_rows rows, swizzled within
+// the row's length.
+bool encode_bytes_map(CUtensorMap* map, const void* base, int rows, int row_bytes, int box_rows);
+
 // One phase of a GEMM chain: acc = X . W^T, then the epilogue.
 struct GemmPhase {
   const CUtensorMap* tmW;  // weight map [N][K], box 64 x 128 (encode_kmajor_map)

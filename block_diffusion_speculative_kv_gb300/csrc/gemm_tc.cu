@@ -1563,6 +1563,18 @@ bool encode_kmajor_map(CUtensorMap* map, const void* base, int rows, int K,
   return r == CUDA_SUCCESS;
 }
 
+bool encode_bytes_map(CUtensorMap* map, const void* base, int rows, int row_bytes, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || (row_bytes != 64 && row_bytes != 128)) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int tc_row_tile(int M_rows) {
   int n = 16;
   while (n < M_rows && n < 256) n <<= 1;

@@ -1052,91 +1052,6 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
   }
 }
 
-// Joins the tiles that shares' borders cut, each 32 rows (a lane to a row) to a block of
-// eight warps, which share out the parts for the weights and the columns for the sums.
-// Blocks x: the CTA that holds a tile's first piece.  (32 warps to a block, a warp for
-// four columns, took longer: 128 rows over 4096 slots 32 us against 27.)
-template <int HD, int NG>
-__global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnParams p) {
-  constexpr int GT = Tc<HD, NG>::kGroup, kRound = 64, kFours = HD / 4, kCols = kFours / 8;
-  constexpr int kAtOnce = 16 / kCols;                        // parts whose loads are in flight
-  __shared__ float sF[kRound][32];
-  __shared__ float sW[2][8][32];
-  __shared__ __align__(16) uint2 sOut[32][kFours];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_trigger();
-  const PagedCut cut = p.cut[blockIdx.x];
-  const int rho = cut.rho0 + blockIdx.y * 32 + lane;
-  if (cut.c1 < 0 || rho - lane >= cut.nG) return;            // block-uniform
-  const int c0 = blockIdx.x, parts = cut.c1 - c0 + 1;
-  const int x = blockIdx.y * 32 / GT, row = blockIdx.y * 32 % GT + lane;
-  const bool live = rho < cut.nG;
-  auto at = [&](int k) { return ((size_t)(c0 + k) * 2 + (k == 0)) * NG + x; };
-  auto ml_of = [&](int k) { return live ? __ldcg(p.part_ml + at(k) * GT + row) : make_float2(-CUDART_INF_F, 0.f); };
-  float M = -CUDART_INF_F, L = 0.f;
-  for (int k = warp; k < parts; k += 8) M = fmaxf(M, ml_of(k).x);
-  sW[0][warp][lane] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, sW[0][w][lane]);
-  float4 acc[kCols] = {};
-  for (int r0 = 0; r0 < parts; r0 += kRound) {
-    const int n = min(parts - r0, kRound);
-    if (r0) __syncthreads();
-    for (int k = warp; k < n; k += 8) {
-      const float2 ml = ml_of(r0 + k);
-      const float f = ml.y != 0.f ? ex2(ml.x - M) : -1.f;    // (-1: a part that saw no key)
-      if (ml.y != 0.f) L += f * ml.y;
-      sF[k][lane] = f;
-    }
-    __syncthreads();
-    for (int k0 = 0; k0 < n; k0 += kAtOnce) {
-      float4 v[kAtOnce][kCols];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const float4* src = reinterpret_cast<const float4*>(p.part_o) +
-                            (at(r0 + min(k0 + k, n - 1)) * kFours + warp * kCols) * GT + row;
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) v[k][j] = __ldcg(src + j * GT);
-      }
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const float f = k0 + k < n ? sF[k0 + k][lane] : -1.f;
-        if (f >= 0.f) {
-#pragma unroll
-          for (int j = 0; j < kCols; ++j) {
-            acc[j].x += f * v[k][j].x;
-            acc[j].y += f * v[k][j].y;
-            acc[j].z += f * v[k][j].z;
-            acc[j].w += f * v[k][j].w;
-          }
-        }
-      }
-    }
-  }
-  sW[1][warp][lane] = L;
-  __syncthreads();
-  L = 0.f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) L += sW[1][w][lane];
-  const float inv = 1.f / L;
-#pragma unroll
-  for (int j = 0; j < kCols; ++j)                            // a row that saw no key: zeros
-    sOut[lane][(warp * kCols + j) ^ (lane & 15)] =
-        L == 0.f ? make_uint2(0, 0)
-                 : make_uint2(mmas::pack_bf16(acc[j].x * inv, acc[j].y * inv),
-                              mmas::pack_bf16(acc[j].z * inv, acc[j].w * inv));
-  __syncthreads();
-  for (int i = threadIdx.x; i < 32 * kFours; i += 256) {
-    const int r = i / kFours, ch = i % kFours, to = rho - lane + r;
-    if (to >= cut.nG) break;
-    const int tok = p.heads.quot(to), head = cut.head0 + to - tok * p.heads.G;
-    reinterpret_cast<uint2*>(p.out + (long long)(cut.row0 + tok) * p.out_ld + (long long)head * HD)[ch] =
-        sOut[r][ch ^ (r & 15)];
-  }
-}
-
 template <int HD, int NG>
 dflash_status launch_tc(PagedAttnParams p, const dflash_pages& pages, cudaStream_t st) {
   using S = Tc<HD, NG>;
@@ -1171,7 +1086,7 @@ dflash_status launch_tc(PagedAttnParams p, const dflash_pages& pages, cudaStream
   }
   if (p.cut) {
     TraceScope ts("paged_join", st);
-    launch_k(paged_join_kernel<HD, NG>, dim3(grid, S::kRows / 32), dim3(256), 0, st, p);
+    launch_k(paged_join_kernel<HD, NG, S::kGroup>, dim3(grid, S::kRows / 32), dim3(256), 0, st, p);
   }
   return DFLASH_OK;
 }

@@ -18,6 +18,7 @@
 // The work is shared out as in paged_attention.h.
 #include <cmath>
 
+#include <cuda_fp8.h>
 #include <math_constants.h>
 
 #include "gemm.h"
@@ -54,6 +55,12 @@ __device__ __forceinline__ uint32_t half2_hi(uint32_t codes) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t h;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  return h;
+}
+// The same, at most the largest finite number.
+__device__ __forceinline__ uint32_t pack_f16_finite(float lo, float hi) {
+  uint32_t h;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
   return h;
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -471,6 +478,890 @@ dflash_status launch_small(const PagedE4M3Params& p, const dflash_pages_e4m3& pa
   return DFLASH_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Many query rows (chains, trees, prompt chunks): tensor-core tiles.
+// ---------------------------------------------------------------------------
+// The tiles, the turns of the softmax groups and the joins are those of the 16-bit
+// cache's kernel (paged_attention.cu): NG MMA tiles of 128 query rows (NG = 1: 64 rows, two
+// CTAs to an SM) against steps of 128 keys, S_x and O_x in TMEM, P_x over S_x as the A
+// operand of P V.  What differs:
+//   Q K^T  takes the key codes as TMA brings them, on the e4m3 cores: a row of q is the
+//     sum of two codes, hi + lo, at a power of two at which its largest element lies in
+//     [128, 256).  bf16's 8 bits are two codes' 4 + 4, so that is exact for elements down
+//     to 2^-10 of the row's largest, and off by 2^-17 of the largest below.  Twice the
+//     products at twice the rate: the time of the 16-bit form, and no conversion of K.
+//   P V    runs in fp16, since e4m3's 4 bits of P would not do: warps of their own turn
+//     the value codes into an fp16 tile in shared memory, laid out as TMA would, while
+//     the softmax of the step runs.  The last steps of a tile, where some row may not see
+//     some key, are also looked through for NaN: such a code counts as zero, its key is
+//     noted, and rows that see it become NaN in its column.
+//   scales come with the loads, 8 + 8 to a step, and are applied as in the small tiles:
+//     a key block's to its 16 scores, a value block's in the exponent of its 16 weights,
+//     2^((s - m) + b - r), and the sum l takes each 16's sum back at 2^(r - b).
+constexpr int kStepT = 128;
+// Registers: NG = 2, the launch's 168 for each of three warpgroups, of which the softmax
+// groups take 216 and the other one keeps 72; NG = 1, 128 for each of two: 208 for the one
+// with the softmax warps, 48 for the converting one.
+template <int NG>
+struct Regs {
+  static constexpr int kMost = NG == 2 ? 216 : 208, kLeast = NG == 2 ? 72 : 48;
+  static_assert(NG == 2 ? 2 * kMost + kLeast <= 3 * 168 : kMost + kLeast <= 2 * 128, "register split");
+};
+
+template <int HD, int NG>
+struct Tc {
+  static constexpr int kGroup = NG == 2 ? 128 : 64;         // rows, and threads, of a softmax group
+  static constexpr int kRows = kGroup * NG, kWarps = kRows / 32;
+  static constexpr int kThreads = NG == 2 ? 384 : 256, kPerSm = NG == 2 ? 1 : 2;
+  static constexpr int kConv = NG == 2 ? 2 : 4;             // converting warps
+  using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 12 : 3, 128, NG == 2 ? 1 : 3>;
+  static constexpr int kAtomQ = kGroup * 128;               // 128 bytes of a group's rows of Q
+  static constexpr int kTileQ = (HD / 64) * kAtomQ;         // hi and lo
+  static constexpr int kKeys = NG == 2 ? 128 : 64;          // of a ring slot
+  static constexpr int kPer = kStepT / kKeys;               // slots of a step's K, or V
+  static constexpr int kEarly = NG == 2 ? 96 : 64;          // keys of P that go out first
+  static constexpr int kSlot = kKeys * HD;                  // of codes
+  static constexpr int kAtom = kKeys * 128, kTileV = (HD / 64) * kAtom;     // of values in fp16
+  static constexpr int kK = NG == 2 ? 3 : 4, kV = NG == 2 ? 2 : 4, kC = 2;  // ring slots
+  static constexpr int kRingK = NG * kTileQ, kRingV = kRingK + kK * kSlot, kRingC = kRingV + kV * kSlot;
+  static constexpr int kBar = kRingC + kC * kTileV;
+  static constexpr int kBars = 2 * (kK + kV + kC) + 10;
+  static constexpr int kWait = kBar + kBars * 8, kWord = kWait + kThreads / 32 * 8;
+  static constexpr int kNote = kWord + 16, kScale = (kNote + 64 + 15) / 16 * 16, kMl = kScale + 8 * 64;
+  static constexpr int kBytes = kMl + (NG == 2 ? 1024 : 0);
+  static constexpr int kTmem = 256 * NG;                    // S_x at 128 x (P_x over it), then O_x
+  static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+struct TcMaps {
+  CUtensorMap k, v;    // pools as rows of head_dim bytes, box min(page_size, slot) rows
+};
+
+template <int HD, int NG>
+__global__ void __launch_bounds__(Tc<HD, NG>::kThreads, Tc<HD, NG>::kPerSm)
+paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Params p) {
+  using S = Tc<HD, NG>;
+  using Geo = typename S::Geo;
+  constexpr int kPer = S::kPer, GT = S::kGroup;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (ptx::smem_addr(smem) & 1023) {                         // (the swizzle counts on it)
+    record_status(p.status, DFLASH_ERR_UNSUPPORTED);
+    return;
+  }
+  uint8_t* sQ = smem;                                        // [NG][HD / 64][GT][128]
+  uint8_t* sK = smem + S::kRingK;                            // slots of [kKeys][HD] codes
+  uint8_t* sV = smem + S::kRingV;
+  uint8_t* sC = smem + S::kRingC;                            // slots of [HD / 64][kKeys][64] fp16
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::kBar);
+  uint64_t *k_full = bar, *k_empty = k_full + S::kK, *v_full = k_empty + S::kK, *v_empty = v_full + S::kV;
+  uint64_t *c_full = v_empty + S::kV, *c_empty = c_full + S::kC;
+  uint64_t* q_full = c_empty + S::kC;
+  uint64_t* s_ready = q_full + 1;                            // [2]
+  uint64_t* p_ready = q_full + 3;                            // [2][half]
+  uint64_t* pv_done = q_full + 7;                            // [2]
+  uint64_t* drain = q_full + 9;
+  uint64_t* wait_ns = reinterpret_cast<uint64_t*>(smem + S::kWait) + (threadIdx.x >> 5);   // limit of a wait
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + S::kWord);
+  volatile int* abort = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile int* s_last = reinterpret_cast<volatile int*>(tslot + 2);    // [2]
+  // keys with a NaN: [step % 4][16 keys], steps counted over all pieces.  A group reads a step's when it has its next
+  // scores, before it hands out P for them; the converting warps are two steps past that
+  // at most.
+  volatile uint16_t* notes = reinterpret_cast<volatile uint16_t*>(smem + S::kNote);
+  // (2^a, b) of a step's blocks: [step % 8][8].  The loads are at most the K ring's three
+  // steps past the scores, those two past the softmax.
+  float2* sScale = reinterpret_cast<float2*>(smem + S::kScale);
+  float2* sMl = reinterpret_cast<float2*>(smem + S::kMl);    // [128] (NG = 2)
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kLoad = S::kWarps, kIssue = S::kWarps + 1, kConvert = S::kWarps + 2;    // warps
+  if (tid == 0) {
+    for (int s = 0; s < S::kK; ++s) {
+      ptx::mbar_init(&k_full[s], 1);
+      ptx::mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < S::kV; ++s) {
+      ptx::mbar_init(&v_full[s], 1);
+      ptx::mbar_init(&v_empty[s], S::kConv);
+    }
+    for (int s = 0; s < S::kC; ++s) {
+      ptx::mbar_init(&c_full[s], S::kConv);
+      ptx::mbar_init(&c_empty[s], 1);
+    }
+    ptx::mbar_init(q_full, S::kWarps);
+    for (int x = 0; x < 2; ++x) {
+      ptx::mbar_init(&s_ready[x], 1);
+      ptx::mbar_init(&p_ready[2 * x], GT / 32);
+      ptx::mbar_init(&p_ready[2 * x + 1], GT / 32);
+      ptx::mbar_init(&pv_done[x], 1);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kIssue) {
+    ptx::tmem_alloc(tslot, S::kTmem);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tbase = *tslot;
+  const uint32_t tbase_o = tbase + 128 * NG;                 // O_x at 128 x from here
+
+  pdl_wait();
+  pdl_trigger();
+  long long total, end;
+  PagedCursor c;
+  // the workspace header's limit (dflash_workspace_set_wait_limit), read beside the plan
+  const uint64_t limit = *reinterpret_cast<const volatile uint64_t*>(p.status + 2);
+  paged_plan<Geo>(p, lane, &total, &end, &c);
+  if (lane == 0) *wait_ns = limit == 0 || limit > kMaxLimitNs ? kTimeoutNs : limit;
+  __syncwarp();
+
+  auto fail = [&]() {
+    if (!*abort) record_status(p.status, DFLASH_ERR_TIMEOUT);
+    *abort = 1;
+  };
+  auto wait = [&](uint64_t* b, uint32_t parity) {            // bounded
+    if (ptx::mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!ptx::mbar_try_wait(b, parity))
+      if (*abort || global_ns() - t0 > *wait_ns) return false;
+    return true;
+  };
+  auto all = [&](bool landed) { return __all_sync(0xffffffffu, landed); };
+
+  // ---------------- values into fp16 ----------------
+  auto convert = [&]() {
+    constexpr int kPieces = HD / 16, kRound = 32 / kPieces, kMine = S::kKeys / S::kConv;
+    const int w = warp - kConvert;
+    const int ch = lane % kPieces, flip = HD == 128 ? ch >> 2 : 0;
+    uint32_t iv = 0;                                         // slots converted
+    bool ok = true;
+    for (PagedPiece pc; c.left > 0 && ok; paged_next<Geo>(p, pc, &c)) {
+      pc = PagedPiece::of<Geo>(c);
+      if (pc.n <= 0) continue;
+      const int kend = c.rq.key_end<Geo>(c.j, p.heads);
+      const int plain = min(c.rq.masked ? c.rq.p0 : c.rq.p0 + p.heads.quot(c.j * S::kRows) + 1, kend);
+      for (int i = 0; i < pc.n && ok; ++i) {
+        const int key0 = (pc.first + i) * kStepT;
+        const bool check = key0 + kStepT > plain;
+        for (int part = 0; part < kPer && ok; ++part, ++iv) {
+          const uint32_t s = iv % S::kV, t = iv % S::kC;
+          ok = all(wait(&v_full[s], iv / S::kV & 1u) && wait(&c_empty[t], (iv / S::kC & 1u) ^ 1u));
+          if (!ok) break;
+          const uint8_t* from = sV + s * S::kSlot;
+          uint8_t* to = sC + t * S::kTileV;
+          uint32_t bad[kMine / 16] = {};
+#pragma unroll (NG == 2 ? 4 : 2)
+          for (int k0 = 0; k0 < kMine; k0 += kRound) {
+            const int key = w * kMine + k0 + lane / kPieces;
+            uint4 u = *reinterpret_cast<const uint4*>(
+                from + key * HD + ((HD == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
+            if (check) {
+              if (key0 + part * S::kKeys + key >= kend) u = make_uint4(0, 0, 0, 0);
+              const uint4 x = make_uint4(nan_bytes(u.x), nan_bytes(u.y), nan_bytes(u.z), nan_bytes(u.w));
+              const uint32_t hit = __ballot_sync(0xffffffffu, (x.x | x.y | x.z | x.w) != 0);
+              if (hit) {                                     // (rare)
+                u = make_uint4(u.x & ~x.x, u.y & ~x.y, u.z & ~x.z, u.w & ~x.w);
+#pragma unroll
+                for (int k = 0; k < kRound; ++k)
+                  if ((hit >> (k * kPieces)) & ((1u << kPieces) - 1u)) {
+                    const int at = k0 + k;
+#pragma unroll
+                    for (int g = 0; g < kMine / 16; ++g)
+                      if (at / 16 == g) bad[g] |= 1u << (at % 16);
+                  }
+              }
+            }
+            const uint4 a = make_uint4(half2_lo(u.x), half2_hi(u.x), half2_lo(u.y), half2_hi(u.y));
+            const uint4 b = make_uint4(half2_lo(u.z), half2_hi(u.z), half2_lo(u.w), half2_hi(u.w));
+            // 32 bytes of the row's 64-column atom; the upper half's lanes store the other
+            // piece first (no bank conflicts)
+            uint8_t* row = to + (ch >> 2) * S::kAtom + key * 128;
+            const int c16 = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(row + (((c16 + flip) ^ (key & 7)) << 4)) = flip ? b : a;
+            *reinterpret_cast<uint4*>(row + (((c16 + 1 - flip) ^ (key & 7)) << 4)) = flip ? a : b;
+          }
+          if (check && lane == 0) {
+#pragma unroll
+            for (int g = 0; g < kMine / 16; ++g)
+              notes[(iv / kPer & 3) * 8 + (part * S::kKeys + w * kMine) / 16 + g] = static_cast<uint16_t>(bad[g]);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(&c_full[t]);
+            ptx::mbar_arrive(&v_empty[s]);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) fail();
+  };
+  // ---------------- loads ----------------
+  auto load = [&]() {
+    const int box = min(1 << p.pv.page_shift, S::kKeys);
+    const int nb = kStepT / box;                             // boxes of a step's K, or V
+    const int per_slot = S::kKeys / box;
+    const uint64_t pol = ptx::policy_evict_last();
+    if (lane == 0) {
+      ptx::prefetch_tmap(&maps.k);
+      ptx::prefetch_tmap(&maps.v);
+    }
+    const int nowhere = (p.pv.n_pages * p.pv.n_kv) << p.pv.page_shift;   // past the pool: zeros
+    uint32_t ik = 0, iv = 0;                                 // slots loaded
+    bool ok = true;
+    for (PagedPiece pc; c.left > 0 && ok; paged_next<Geo>(p, pc, &c)) {
+      pc = PagedPiece::of<Geo>(c);
+      if (pc.n <= 0) continue;
+      const int n = pc.n, kend = c.rq.key_end<Geo>(c.j, p.heads);
+      const int32_t* table = p.pv.table + (size_t)c.r * p.pv.table_ld;
+      // this lane's 16 slots of step i (lanes 0 .. 7): their page's table entry, asked for
+      // two steps ahead, and their place in the pool and scales, one step ahead
+      auto entry_of = [&](int i) {
+        const int t = (pc.first + i) * kStepT + lane * kScaleBlock;
+        return lane < 8 && i < n && t < kend ? __ldg(table + (t >> p.pv.page_shift)) : -1;
+      };
+      bool missing = false;
+      struct Place {
+        int row;
+        uint32_t a, b;
+      };
+      auto place_of = [&](int i, int page) {
+        const int t = (pc.first + i) * kStepT + lane * kScaleBlock;
+        Place at = {nowhere, 127u, 127u};
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.pv.n_pages)) {
+          const long long row = pool_row(p.pv, page, c.g, t);
+          at.row = static_cast<int>(row);
+          at.a = __ldg(p.k_scale + row / kScaleBlock);
+          at.b = __ldg(p.v_scale + row / kScaleBlock);
+        } else {
+          missing |= lane < 8 && i < n && t < kend;
+        }
+        return at;
+      };
+      int entry = entry_of(0);
+      Place next = place_of(0, entry);
+      entry = entry_of(1);
+      for (int i = 0; i < n && ok; ++i) {
+        const Place now = next;
+        if (i + 1 < n) next = place_of(i + 1, entry);
+        entry = entry_of(i + 2);
+        // lane b's box: the first of its 16-slot blocks
+        const int y = __shfl_sync(0xffffffffu, now.row, min(lane * box / kScaleBlock, 7));
+        auto fill = [&](uint64_t* full, uint64_t* empty, uint32_t it, int slots, uint8_t* ring, const CUtensorMap* map,
+                        int part) {
+          const uint32_t s = it % slots;
+          if (!all(wait(&empty[s], (it / slots & 1u) ^ 1u))) return false;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], S::kSlot);
+          __syncwarp();
+          const int b = lane - part * per_slot;              // this lane's box in the slot
+          if (b >= 0 && b < per_slot && lane < nb) ptx::tma_load_2d(ring + s * S::kSlot + b * box * HD, map, &full[s], 0, y, pol);
+          return true;
+        };
+        for (int part = 0; part < kPer && ok; ++part, ++ik) {
+          if (part == 0) {                                   // (the scales before the keys' arrival)
+            const uint32_t s = ik % S::kK;
+            ok = all(wait(&k_empty[s], (ik / S::kK & 1u) ^ 1u));
+            if (!ok) break;
+            if (lane < 8)
+              sScale[(ik / kPer & 7) * 8 + lane] =
+                  make_float2(scale_of(now.a), static_cast<float>(static_cast<int>(now.b)) - 127.f);
+            __syncwarp();
+          }
+          ok = fill(k_full, k_empty, ik, S::kK, sK, &maps.k, part);
+        }
+        for (int part = 0; part < kPer && ok; ++part, ++iv)
+          ok = fill(v_full, v_empty, iv, S::kV, sV, &maps.v, part);
+      }
+      // pages that are not there: an error if some row of the tile sees their slots
+      if (__any_sync(0xffffffffu, missing))
+        for (int t0 = pc.first * kStepT; t0 < min((pc.first + n) * kStepT, kend); t0 += box)
+          if (page_of(p.pv, c.r, t0) < 0 && paged_seen<Geo>(p, c, t0, min(t0 + box, kend), lane) && lane == 0)
+            record_status(p.status, DFLASH_ERR_INVALID_ARG);
+    }
+    if (!ok && lane == 0) fail();
+    // every copy must land before the CTA exits
+    auto landed = [&](uint64_t* full, uint32_t it, uint32_t slots) {
+      for (uint32_t s = 0; s < slots && s < it; ++s)
+        ptx::mbar_wait_bounded(&full[s], (it - 1 - s) / slots & 1u, kTimeoutNs, nullptr);
+    };
+    landed(k_full, ik, S::kK);
+    landed(v_full, iv, S::kV);
+  };
+  // ---------------- MMA issue ----------------
+  auto issue = [&]() {
+    // The whole warp runs the loop, so that addresses and descriptors stay in
+    // uniform registers; one elected lane issues.
+    const bool elected = ptx::elect_one();
+    const uint64_t dq = ptx::sw128_kmajor_desc(ptx::smem_addr(sQ));
+    const uint64_t dk = HD == 128 ? ptx::sw128_kmajor_desc(ptx::smem_addr(sK)) : ptx::sw64_kmajor_desc(ptx::smem_addr(sK));
+    const uint64_t dv = ptx::sw128_mnmajor_desc(ptx::smem_addr(sC), S::kAtom, 1024);
+    constexpr uint32_t idesc_s = ptx::idesc_f32(128, S::kKeys);
+    constexpr uint32_t idesc_pv = ptx::idesc_f32(128, HD) | (1u << 16);   // B transposed
+    uint32_t it = 0, unit = 0, np[2] = {0, 0};               // ring base, units, PV products of x
+    uint32_t ks[kPer] = {}, vs[kPer] = {};                   // ring slots in use
+    bool ok = true;
+    for (PagedPiece pc; c.left > 0 && ok; paged_next<Geo>(p, pc, &c)) {
+      pc = PagedPiece::of<Geo>(c);
+      if (pc.n <= 0) continue;
+      const int n = pc.n, nt = NG == 2 && min(c.rq.n * p.heads.G - c.j * S::kRows, S::kRows) > 128 ? 2 : 1;
+      ok = all(wait(q_full, unit & 1u));
+      const int jobs0 = NG == 1 || nt == 2 ? n : (n + 1) / 2, jobs1 = NG == 1 ? 0 : (nt == 2 ? n : n / 2);
+      // group x's i-th job is this step; ring slots of a step are numbered on from `it`
+      auto step_of = [&](int x, int i) { return NG == 1 || nt == 2 ? i : 2 * i + x; };
+      auto slot_at = [&](uint32_t at, int slots) { return __shfl_sync(0xffffffffu, at % slots, 0); };
+      // Waits that the loads decide come before the one that the softmax decides, and
+      // between that one and the next scores there is nothing but MMAs.
+      auto scores = [&](int x) {                             // one lane: S_x of the K in ks
+        const uint64_t q0 = dq + (nt == 2 ? x * (S::kTileQ >> 4) : 0);
+#pragma unroll
+        for (int part = 0; part < kPer; ++part) {
+          const uint32_t s = ks[part];
+          const uint64_t k0 = dk + s * (S::kSlot >> 4);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {             // hi, then lo
+            const int lo = kk / (HD / 32), at = kk % (HD / 32) * 32;
+            ptx::mma_e4m3(tbase + 128 * x + part * S::kKeys,
+                          q0 + ((lo * (HD == 128 ? S::kAtomQ : 64) + at) >> 4), k0 + (at >> 4), idesc_s,
+                          kk > 0 ? 1u : 0u);
+          }
+          if (part == kPer - 1) ptx::mma_commit(&s_ready[x]);
+          if (nt == 1 || x == 1) ptx::mma_commit(&k_empty[s]);
+        }
+      };
+      auto wait_k = [&](int x, int i) {
+        const uint32_t at = it + kPer * step_of(x, i);
+        bool got = true;
+#pragma unroll
+        for (int part = 0; part < kPer; ++part) {
+          ks[part] = slot_at(at + part, S::kK);
+          got = got && all(wait(&k_full[(at + part) % S::kK], (at + part) / S::kK & 1u));
+        }
+        return got;
+      };
+      // job i of group x: P V, then the scores of job i + 1
+      auto turn = [&](int x, int i, bool more) {
+        const bool shared = nt == 2 && x == 1;               // group 0 has waited for these
+        const uint32_t at = it + kPer * step_of(x, i);
+        if (!shared) {
+#pragma unroll
+          for (int part = 0; part < kPer; ++part) {
+            vs[part] = slot_at(at + part, S::kC);
+            if (!all(wait(&c_full[(at + part) % S::kC], (at + part) / S::kC & 1u))) return false;
+          }
+          if (more && !wait_k(x, i + 1)) return false;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {                        // P arrives in two halves
+          if (!all(wait(&p_ready[2 * x + h], np[x] & 1u))) return false;
+          ptx::tc_fence_after();
+          if (elected) {
+            const uint32_t s = vs[kPer == 2 ? h : 0];
+            const uint64_t v0 = dv + s * (S::kTileV >> 4);
+#pragma unroll
+            for (int j = h * (S::kEarly / 16); j < (h ? kStepT : S::kEarly) / 16; ++j)
+              ptx::mma_bf16_ta(tbase_o + 128 * x, tbase + 128 * x + j * 8,
+                               v0 + (j % (S::kKeys / 16)) * (2048 >> 4), idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
+            if (h == 1) ptx::mma_commit(&pv_done[x]);
+            if ((kPer == 2 || h == 1) && (nt == 1 || x == 1)) ptx::mma_commit(&c_empty[s]);
+            if (h == 1 && more) scores(x);
+          }
+          __syncwarp();
+        }
+        ++np[x];
+        return true;
+      };
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (x == 1 && jobs1 == 0) break;
+        if (nt == 1 || x == 0) ok = wait_k(x, 0);
+        ptx::tc_fence_after();
+        if (ok && elected) scores(x);
+        __syncwarp();
+      }
+      for (int i = 0; i < jobs0 && ok; ++i) {
+        ok = turn(0, i, i + 1 < jobs0);
+        if (ok && i < jobs1) ok = turn(1, i, i + 1 < jobs1);
+      }
+      it += kPer * n;
+      ++unit;
+      paged_past<Geo>(p, c, lane);
+    }
+    if (!ok && lane == 0) fail();
+    // the MMAs already issued finish before TMEM is released
+    if (unit > 0 || !ok) {
+      if (elected) ptx::mma_commit(drain);
+      __syncwarp();
+      ptx::mbar_wait_bounded(drain, 0u, kTimeoutNs, nullptr);
+    }
+    __syncwarp();
+  };
+  // ---------------- softmax: group x = warp / 4, a row to a thread ----------------
+  auto softmax = [&]() {
+    const int x = warp / (GT / 32), wg = warp % (GT / 32), row = wg * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
+    const uint32_t aS = tbase + 128 * x + lane_off, aO = tbase_o + 128 * x + lane_off;
+    uint32_t it = 0, nj = 0;                                 // steps, jobs of this group
+    bool ok = true;
+    if (p.cut && tid == 0) p.cut[blockIdx.x].c1 = -1;
+    for (PagedPiece pc; c.left > 0; paged_next<Geo>(p, pc, &c)) {
+      pc = PagedPiece::of<Geo>(c);
+      if (pc.n <= 0) continue;
+      const PagedReq rq = c.rq;
+      const int n = pc.n, nG = rq.n * p.heads.G, tile0 = c.j * S::kRows;
+      const int nt = NG == 2 && min(nG - tile0, S::kRows) > 128 ? 2 : 1;
+      const int kend = rq.key_end<Geo>(c.j, p.heads);
+      const int rho0 = tile0 + (nt == 2 ? x * GT : 0);       // first row of this group's MMA tile
+      const int rho = rho0 + row;
+      const bool live = rho < nG;
+      const int tok = live ? p.heads.quot(rho) : 0, head = c.g * p.heads.G + (live ? rho - tok * p.heads.G : 0);
+      const int jobs = NG == 1 || nt == 2 ? n : (n + 1 - x) / 2;
+      // Q as two codes into shared memory (rows of 128 bytes, 128-byte swizzle): HD / 8
+      // lanes read a row, whose address its own lane knows; that lane keeps what a score
+      // of the codes counts
+      float count = 0.f;
+      {
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(
+            p.q + (long long)(rq.row0 + tok) * p.q_ld + (long long)head * HD);
+        const unsigned on = __ballot_sync(0xffffffffu, live);
+        constexpr int kLanes = HD / 8, kLines = 32 / kLanes;     // lanes of a row, rows of a round
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kLines) {
+          const int rr = r0 + lane / kLanes, ch = lane % kLanes;
+          const uint4* src = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, mine, rr)) + ch;
+          const uint4 u = (on >> rr) & 1u ? __ldg(src) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = max(static_cast<int>(top >> 7), 16);                               // biased exponent
+          const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);          // 2^(134 - e)
+          const float down = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(e - 7) << 23),
+                                         (lane - r0) * kLanes & 31);
+          if (static_cast<unsigned>(lane - r0) < static_cast<unsigned>(kLines)) count = down * p.scale_log2;
+          uint32_t hi[2] = {}, lo[2] = {};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float2 v = make_float2(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+            v.x = fmaf(v.x, 0.f, v.x);                       // (an infinity becomes NaN)
+            v.y = fmaf(v.y, 0.f, v.y);
+            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+            const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+            const __nv_fp8x2_storage_t l =
+                __nv_cvt_float2_to_fp8x2(make_float2(v.x - f.x, v.y - f.y), __NV_SATFINITE, __NV_E4M3);
+            hi[k >> 1] |= static_cast<uint32_t>(h) << (16 * (k & 1));
+            lo[k >> 1] |= static_cast<uint32_t>(l) << (16 * (k & 1));
+          }
+          if (nt == 2 || x == 0) {
+            uint8_t* tile = sQ + (nt == 2 ? x : 0) * S::kTileQ;
+            const int line = wg * 32 + rr;
+            auto put = [&](int byte, const uint32_t (&codes)[2]) {      // byte of the row: atom, 16-byte piece
+              *reinterpret_cast<uint2*>(tile + (byte >> 7) * S::kAtomQ + line * 128 +
+                                        ((((byte & 127) >> 4) ^ (line & 7)) << 4) + (byte & 15)) =
+                  make_uint2(codes[0], codes[1]);
+            };
+            put(8 * ch, hi);
+            put(HD + 8 * ch, lo);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_full);
+
+      // first slot past what the row sees (causal), the mask row, and the keys
+      // that every row of the warp, and of the whole tile, sees
+      const int lim = live ? (rq.masked ? kend : min(rq.p0 + tok + 1, kend)) : 0;
+      const uint32_t* mrow = rq.masked ? p.mask + (size_t)(rq.row0 + tok) * p.mask_ld : nullptr;
+      const int first = p.heads.quot(min(rho0 + wg * 32, nG - 1));
+      const int plain_w = rho0 + wg * 32 >= nG ? 0 : min(rq.masked ? rq.p0 : rq.p0 + first + 1, kend);
+      const int plain_t = min(rq.masked ? rq.p0 : rq.p0 + p.heads.quot(tile0) + 1, kend);
+      const bool dead = rho0 + wg * 32 >= nG;        // no live row in this warp
+      float m = -CUDART_INF_F, r = -CUDART_INF_F, l = 0.f;
+      // A step's P V ran with zeros for NaN codes.  Once it is done (the next scores are, or
+      // pv_done), a row that sees such a key becomes NaN in the code's column.
+      int late = -1;                                         // first key of the step to be looked through, or none
+      uint32_t late_note = 0, late_seen[4];
+      auto repair = [&]() {
+        if (late < 0 || dead) return;
+#pragma unroll 1
+        for (int g = 0; g < 8; ++g) {
+          uint32_t keys = notes[late_note * 8 + g];
+          const uint32_t s4 = g < 2 ? late_seen[0] : g < 4 ? late_seen[1] : g < 6 ? late_seen[2] : late_seen[3];
+          const uint32_t sees = g & 1 ? s4 >> 16 : s4;
+          while (keys) {                                     // warp-uniform
+            const int j = __ffs(keys) - 1;
+            keys &= keys - 1;
+            const int key = late + 16 * g + j, page = page_of(p.pv, c.r, key);
+            if (page < 0) continue;
+            const uint8_t* v = static_cast<const uint8_t*>(p.pv.v) + pool_row(p.pv, page, c.g, key) * HD;
+            const bool see = (sees >> j) & 1u;
+#pragma unroll 1
+            for (int cb = 0; cb < HD / 16; ++cb) {
+              float o[16];
+              ptx::tmem_ld_32x16(aO + 16 * cb, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (see && (v[16 * cb + e] & 127) == 127) o[e] = CUDART_NAN_F;
+              ptx::tmem_st_32x16(aO + 16 * cb, o);
+              ptx::tmem_wait_st();
+            }
+          }
+        }
+      };
+      // (after a wait has run out the loop only runs on to the group's barrier)
+      for (int i = 0; i < jobs; ++i, ++nj) {
+        const int t = NG == 1 || nt == 2 ? i : 2 * i + x, key0 = (pc.first + t) * kStepT;
+        if (ok) ok = all(wait(&s_ready[x], nj & 1u));
+        if (!ok) continue;
+        uint32_t seen[4];
+        if (!dead) {
+          ptx::tc_fence_after();
+          if (late >= 0) repair();
+          const float2* scale = sScale + (it + t & 7) * 8;
+          const bool cut = key0 + kStepT > plain_w;          // some key is hidden from some row
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            seen[b] = 0xFFFFFFFFu;
+            if (cut) {
+              const int k = key0 + 32 * b;
+              seen[b] = low_bits(lim - k);
+              if (rq.masked && seen[b]) seen[b] &= seen_word(mrow, p.mask_ld, k - rq.p0);
+            }
+          }
+          uint32_t u[4][32];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) ptx::tmem_ld_32x32(aS + 32 * b, u[b]);
+          // a block's factor and exponent (no infinity times zero, nor zero times infinity)
+          auto factor = [&](float a) { return fminf(fmaxf(count * a, 0x1p-126f), 0x1p90f); };
+          ptx::tmem_wait_ld();
+          if (cut) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((seen[b] >> j) & 1u)) u[b][j] = 0xff800000u;
+          }
+          float top[8], mx = -CUDART_INF_F, mr = -CUDART_INF_F;     // of a block; of all; with b
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const uint32_t* w = &u[g >> 1][16 * (g & 1)];
+            float a0 = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), __uint_as_float(w[2]));
+            float a1 = fmaxf(fmaxf(__uint_as_float(w[3]), __uint_as_float(w[4])), __uint_as_float(w[5]));
+#pragma unroll
+            for (int j = 6; j < 14; j += 4) {
+              a0 = fmaxf(fmaxf(a0, __uint_as_float(w[j])), __uint_as_float(w[j + 1]));
+              a1 = fmaxf(fmaxf(a1, __uint_as_float(w[j + 2])), __uint_as_float(w[j + 3]));
+            }
+            a0 = fmaxf(fmaxf(a0, __uint_as_float(w[14])), __uint_as_float(w[15]));
+            top[g] = fmaxf(a0, a1) * factor(scale[g].x);
+            mx = fmaxf(mx, top[g]);
+          }
+          const float base = fmaxf(m, mx);
+#pragma unroll
+          for (int g = 0; g < 8; ++g) mr = fmaxf(mr, (top[g] - base) + scale[g].y);      // (NaN where nothing is seen)
+          const bool raise = mx > m + kLazy || mr > r + (m - base) + kLazy;
+          if (__any_sync(0xffffffffu, raise)) {
+            float f = 1.f;
+            if (raise) {
+              const float was = m - base + r, r2 = fmaxf(was, mr);
+              f = ex2(was - r2);
+              l *= ex2(m - base);
+              m = base;
+              r = r2;
+            }
+            if (i > 0) {
+              // the products so far must be in O before it is scaled
+              ok = all(wait(&pv_done[x], (nj - 1) & 1u));
+              if (ok) {
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int b = 0; b < HD / 16; ++b) {
+                  float o[16];
+                  ptx::tmem_ld_32x16(aO + 16 * b, o);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) o[j] *= f;
+                  ptx::tmem_st_32x16(aO + 16 * b, o);
+                }
+              }
+            }
+          }
+          const bool none = m == -CUDART_INF_F;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            float pk[16];                                      // (two fp16 each)
+#pragma unroll
+            for (int g = 2 * b; g < 2 * b + 2; ++g) {
+              const float2 sc = scale[g];
+              // 2^-60 of the largest weight is as good as none: l keeps its share
+              const float d = none ? 0.f : fmaxf(sc.y - r, -60.f), add = none ? 0.f : d - m;
+              const float2 f2 = make_float2(factor(sc.x), factor(sc.x)), a2 = make_float2(add, add);
+              float2 rs = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float2 y = __ffma2_rn(make_float2(__uint_as_float(u[b][16 * (g & 1) + 2 * j]),
+                                                        __uint_as_float(u[b][16 * (g & 1) + 2 * j + 1])), f2, a2);
+                const float2 w = make_float2(ex2(y.x), ex2(y.y));
+                rs = __fadd2_rn(rs, w);
+                pk[8 * (g & 1) + j] = __uint_as_float(pack_f16_finite(w.x, w.y));
+              }
+              l = fmaf(rs.x + rs.y, ex2(-d), l);
+            }
+            ptx::tmem_st_32x16(aS + 16 * b, pk);
+            if (b == S::kEarly / 32 - 1) {
+              // the first keys of P may meet V while the others are formed
+              ptx::tmem_wait_st();
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0 && ok) ptx::mbar_arrive(&p_ready[2 * x]);
+            }
+          }
+          ptx::tmem_wait_st();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) {
+          if (dead) ptx::mbar_arrive(&p_ready[2 * x]);
+          ptx::mbar_arrive(&p_ready[2 * x + 1]);
+        }
+        late = key0 + kStepT > plain_t ? key0 : -1;
+        if (late >= 0) {
+          late_note = it + t & 3;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) late_seen[b] = seen[b];
+        }
+      }
+      if (ok && jobs > 0) {
+        ok = all(wait(&pv_done[x], (nj - 1) & 1u));
+        if (ok) ptx::tc_fence_after();
+        if (ok) repair();
+      }
+      if (ptx::named_bar_or(5, GT * NG, !ok)) {
+        ok = false;
+        break;
+      }
+      // ---- the tile's rows ----  (O with m as its reference: times 2^r)
+      const float own = m == -CUDART_INF_F ? 0.f : ex2(r);
+      float M = m, L = l, fa = own, fb = 0.f;                // weights of the two halves
+      float* sB = reinterpret_cast<float*>(sQ);              // [128][HD], chunks of 4 swizzled
+      if (NG == 2 && nt == 1) {
+        if (x == 1) {
+          sMl[row] = make_float2(m, l);
+          if (jobs > 0) {
+#pragma unroll
+            for (int b = 0; b < HD / 32; ++b) {
+              uint32_t o[32];
+              ptx::tmem_ld_32x32(aO + 32 * b, o);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4*>(sB + row * HD + 4 * ((8 * b + j) ^ (row & 7))) =
+                    make_float4(__uint_as_float(o[4 * j]) * own, __uint_as_float(o[4 * j + 1]) * own,
+                                __uint_as_float(o[4 * j + 2]) * own, __uint_as_float(o[4 * j + 3]) * own);
+            }
+          }
+        }
+        ptx::named_bar_sync(5, GT * NG);
+        if (x == 0) {
+          const float2 ml = sMl[row];
+          if (ml.y != 0.f) {
+            M = fmaxf(m, ml.x);
+            const float f = l != 0.f ? ex2(m - M) : 0.f;
+            fa = f * own;
+            fb = ex2(ml.x - M);
+            L = f * l + fb * ml.y;
+          }
+        }
+      }
+      const bool mine = nt == 2 || x == 0;                   // this group writes its rows
+      const bool whole = n == pc.all;
+      int c0 = 0, c1 = 0;
+      if (!whole) paged_owners<Geo>(c, total, end - c.left - c.at, pc.all, &c0, &c1);
+      // partials: [slot][NG][HD / 4][GT rows] of four columns, so that a warp's lanes
+      // are neighbours in memory
+      auto part_of = [&](int cc) { return ((size_t)cc * 2 + (cc == c0)) * NG + x; };
+      const size_t slot = part_of(blockIdx.x);
+      // The warp's 32 bf16 rows go out through shared memory, so that HD / 8
+      // lanes write a row together: in the group's part of Q, or, a lane each, in
+      // its row of the joined half, over columns that it has read.
+      const int stage_ld = NG == 2 && nt == 1 ? HD * 4 : HD * 2;
+      uint8_t* stage = sQ + warp * 32 * stage_ld;
+      auto put = [&](int b, const float (&o)[32], float inv) {    // 32 columns of the row
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w4[e] = L == 0.f ? 0u : mmas::pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
+          *reinterpret_cast<uint4*>(stage + lane * stage_ld + (((4 * b + j) ^ (lane & 7)) << 4)) =
+              make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+      };
+      auto send = [&]() {
+        __syncwarp();
+        const unsigned long long mine_to = reinterpret_cast<unsigned long long>(
+            p.out + (long long)(rq.row0 + tok) * p.out_ld + (long long)head * HD);
+        const unsigned on = __ballot_sync(0xffffffffu, live);
+        constexpr int kLines = 256 / HD;
+#pragma unroll 8
+        for (int r0 = 0; r0 < 32; r0 += kLines) {
+          const int rr = r0 + lane / (HD / 8), ch = lane % (HD / 8);
+          uint4* to = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, mine_to, rr)) + ch;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * stage_ld + ((ch ^ (rr & 7)) << 4));
+          if ((on >> rr) & 1u) *to = w;
+        }
+      };
+      if (mine && !dead) {
+        const float inv = 1.f / L;
+#pragma unroll 2
+        for (int b = 0; b < HD / 32; ++b) {
+          uint32_t u[32];
+          ptx::tmem_ld_32x32(aO + 32 * b, u);
+          ptx::tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = fa == 0.f ? 0.f : __uint_as_float(u[j]) * fa;
+          if (fb != 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 v = *reinterpret_cast<const float4*>(sB + row * HD + 4 * ((8 * b + j) ^ (row & 7)));
+              o[4 * j] += fb * v.x;
+              o[4 * j + 1] += fb * v.y;
+              o[4 * j + 2] += fb * v.z;
+              o[4 * j + 3] += fb * v.w;
+            }
+          }
+          if (whole) {
+            put(b, o, inv);
+          } else if (live) {
+            float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + 8 * b) * GT + row;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              __stcg(po + j * GT, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+          }
+        }
+        if (whole) send();
+      }
+      ptx::tc_fence_before();
+      if (!whole && mine) {
+        if (live) __stcg(p.part_ml + slot * GT + row, make_float2(M, L));
+        if (p.cut) {
+          if (tid == 0 && c0 == static_cast<int>(blockIdx.x))   // its first piece
+            p.cut[c0] = {c1, rq.row0, tile0, nG, c.g * p.heads.G};
+        } else {
+          __threadfence();
+          ptx::named_bar_sync(1 + x, GT);
+          if (row == 0) s_last[x] = atomicAdd(p.arrive + NG * c0 + x, 1) == c1 - c0;
+          ptx::named_bar_sync(1 + x, GT);
+          if (s_last[x]) {
+            __threadfence();
+            if (row == 0) p.arrive[NG * c0 + x] = 0;            // for the next call
+            if (!dead) {
+              M = -CUDART_INF_F;
+#pragma unroll 4
+              for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_ml + part_of(cc) * GT + row).x);
+              float o[HD] = {};
+              L = 0.f;
+              float2 ml = __ldcg(p.part_ml + part_of(c0) * GT + row);
+              for (int cc = c0; cc <= c1; ++cc) {
+                const float2 now = ml;
+                if (cc < c1) ml = __ldcg(p.part_ml + part_of(cc + 1) * GT + row);
+                const float f = now.y != 0.f ? ex2(now.x - M) : 0.f;
+                L += f * now.y;
+                const float4* src = reinterpret_cast<const float4*>(p.part_o) + part_of(cc) * (HD / 4) * GT + row;
+#pragma unroll
+                for (int j = 0; j < HD / 4; ++j) {
+                  const float4 v = __ldcg(src + j * GT);
+                  if (now.y != 0.f) {
+                    o[4 * j] += f * v.x;
+                    o[4 * j + 1] += f * v.y;
+                    o[4 * j + 2] += f * v.z;
+                    o[4 * j + 3] += f * v.w;
+                  }
+                }
+              }
+#pragma unroll
+              for (int b = 0; b < HD / 32; ++b) put(b, reinterpret_cast<float(&)[32]>(o[32 * b]), 1.f / L);
+              send();
+            }
+          }
+        }
+      }
+      it += n;
+      // the rows on their way out lie where the next tile's queries go
+      ptx::named_bar_sync(5, GT * NG);
+    }
+    if (!ok) fail();
+  };
+
+  // (a warpgroup changes its registers in one instruction)
+  if constexpr (NG == 2) {
+    if (warp >= kLoad) {
+      ptx::regs_dec<Regs<NG>::kLeast>();
+      if (warp == kLoad) load();
+      else if (warp == kIssue) issue();
+      else convert();
+    } else {
+      ptx::regs_inc<Regs<NG>::kMost>();
+      softmax();
+    }
+  } else {
+    if (warp >= kConvert) {
+      ptx::regs_dec<Regs<NG>::kLeast>();
+      convert();
+    } else {
+      ptx::regs_inc<Regs<NG>::kMost>();
+      if (warp == kLoad) load();
+      else if (warp == kIssue) issue();
+      else softmax();
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kIssue) {
+    __syncwarp();
+    ptx::tmem_dealloc(tbase, S::kTmem);
+  }
+}
+
+template <int HD, int NG>
+dflash_status launch_tc(PagedE4M3Params p, const dflash_pages_e4m3& pages, cudaStream_t st) {
+  using S = Tc<HD, NG>;
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    cudaFuncSetAttribute(paged_attn_tc_e4m3_kernel<HD, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  TcMaps maps;
+  const int rows = pages.n_pages * pages.n_kv * pages.page_size;
+  const int box = pages.page_size < S::kKeys ? pages.page_size : S::kKeys;
+  if (!encode_bytes_map(&maps.k, pages.k, rows, HD, box) || !encode_bytes_map(&maps.v, pages.v, rows, HD, box))
+    return set_error(DFLASH_ERR_CUDA, "paged attention e4m3: cannot encode the TMA descriptors");
+  const int grid = num_sms() * S::kPerSm;
+  // A few parts to a tile are joined by the last CTA to arrive, many by a kernel of their
+  // own: the rule of the 16-bit cache (paged_attention.cu).
+  const long long tiles = (p.n_rows * (long long)p.heads.G + S::kRows - 1) / S::kRows * p.pv.n_kv;
+  if (tiles * 4 >= grid) p.cut = nullptr;
+  {
+    TraceScope ts("paged_attn_tc_e4m3", st);
+    launch_k(paged_attn_tc_e4m3_kernel<HD, NG>, dim3(grid), dim3(S::kThreads), S::kBytes, st, maps, p);
+  }
+  if (p.cut) {
+    TraceScope ts("paged_join", st);
+    launch_k(paged_join_kernel<HD, NG, S::kGroup>, dim3(grid, S::kRows / 32), dim3(256), 0, st,
+             static_cast<const PagedAttnParams&>(p));
+  }
+  return DFLASH_OK;
+}
+
 }  // namespace
 }  // namespace dfl
 
@@ -538,8 +1429,12 @@ dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_
   dflash_status e;
   if (rows <= 8)
     e = hd == 128 ? launch_small<128, 1>(p, *pages, st) : launch_small<64, 1>(p, *pages, st);
-  else
+  else if (rows <= 16)
     e = hd == 128 ? launch_small<128, 2>(p, *pages, st) : launch_small<64, 2>(p, *pages, st);
+  else if (rows <= Tc<128, 1>::kRows)
+    e = hd == 128 ? launch_tc<128, 1>(p, *pages, st) : launch_tc<64, 1>(p, *pages, st);
+  else
+    e = hd == 128 ? launch_tc<128, 2>(p, *pages, st) : launch_tc<64, 2>(p, *pages, st);
   if (e) return e;
   return check_launch("paged attention e4m3");
 }

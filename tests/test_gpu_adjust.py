@@ -78,7 +78,7 @@ def _check(d, out, ref=None, size=None):
     on = np.isfinite(ref)
     half = torch.finfo(d["logits"].dtype).eps / 2
     tol = 4 * 2.0 ** -24 * size + half * np.abs(np.where(on, ref, 0.0)) * (1 + 2.0 ** -7)
-    assert np.all(np.abs(got - ref)[on] <= tol[on])
+    assert np.all(np.abs(got[on] - ref[on]) <= tol[on])
     same = on & (ref == was)
     assert np.array_equal(got[same], was[same])
     assert torch.all(out[n:] == 7.0) or out.data_ptr() == d["logits"].data_ptr()

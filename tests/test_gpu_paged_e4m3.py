@@ -11,9 +11,10 @@ Tolerances, element by element:
   spread), and below fp16's normal range by 2^-25 of the largest weight: with
   W = max over keys of p 2^b (b the value block's exponent), W 2^-25 sum |d| over the
   keys' value codes d; the output to bf16, 2^-8 |ref|; fp32 sums over kv keys add
-  kv 2^-24 of the spread, twice; a score's fp32 sum of head_dim products, q's 2^-39 of its
-  row's largest element (in fp16) times the norm of a key, and an exponential's 2^-22 move
-  the exponents by delta = (head_dim + 8) 2^-24 S + 2^-20, S a bound of
+  kv 2^-24 of the spread, twice; a score's fp32 sum of head_dim products, the rounding of q's
+  elements (fp16: 2^-39 of the row's largest; two codes: 2^-17 of it, so that at most
+  2^-17 max|q| sum |k| / sqrt(hd) <= 2^-17 max|q| |k|) and an exponential's 2^-22 move the
+  exponents by delta = (head_dim + 8) 2^-24 S + 2^-17 max|q| |k| + 2^-20, S a bound of
   sum |q k| / sqrt(hd).  A probability p = e^s / sum e^s then lies between p e^(-2 delta) and
   p e^(2 delta), so that sum |p' - p| |v| <= (e^(2 delta) - 1) sum p |v| (2 delta of the
   spread where delta is small; nothing is claimed where scores pass fp32's resolution)."""
@@ -237,8 +238,8 @@ def _check(d, out):
     key = np.linalg.norm(np.nan_to_num(pk[used]), axis=-1).max() if len(used) else 0.0
     kv = max(a + b for a, b in zip(d["rows"], d["ctx"]))
     s = np.linalg.norm(q, axis=-1, keepdims=True) * key / math.sqrt(hd)
-    top = np.abs(q).max(-1, keepdims=True) * math.sqrt(hd)
-    delta = (hd + 8) * 2.0 ** -24 * s + 2.0 ** -39 * top * key + 2.0 ** -20 + kv * 2.0 ** -24
+    top = np.abs(q).max(-1, keepdims=True)
+    delta = (hd + 8) * 2.0 ** -24 * s + 2.0 ** -17 * top * key + 2.0 ** -20 + kv * 2.0 ** -24
     tol = (2.0 ** -11 + np.expm1(np.minimum(2 * delta, 300.0))) * spread * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(ref) + \
         2.0 ** -25 * _small_weights(d, q) * (1 + 2.0 ** -7) + 1e-30
     live = int(d["off"][-1])
