@@ -1091,6 +1091,17 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
             }
           }
           const bool none = m == -CUDART_INF_F;
+          // Scores so large that d - m below would lose bits: s - m first, on its own (rare).
+          const bool far = __any_sync(0xffffffffu, !none && fabsf(base) > 0x1p20f);
+          if (far) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const float f = factor(scale[g].x);
+#pragma unroll
+              for (int j = 16 * (g & 1); j < 16 * (g & 1) + 16; ++j)
+                u[g >> 1][j] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(u[g >> 1][j]), f), none ? 0.f : m));
+            }
+          }
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             float pk[16];                                      // (two fp16 each)
@@ -1098,8 +1109,9 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
             for (int g = 2 * b; g < 2 * b + 2; ++g) {
               const float2 sc = scale[g];
               // 2^-60 of the largest weight is as good as none: l keeps its share
-              const float d = none ? 0.f : fmaxf(sc.y - r, -60.f), add = none ? 0.f : d - m;
-              const float2 f2 = make_float2(factor(sc.x), factor(sc.x)), a2 = make_float2(add, add);
+              const float d = none ? 0.f : fmaxf(sc.y - r, -60.f), add = none || far ? d : d - m;
+              const float f1 = far ? 1.f : factor(sc.x);
+              const float2 f2 = make_float2(f1, f1), a2 = make_float2(add, add);
               float2 rs = make_float2(0.f, 0.f);
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
