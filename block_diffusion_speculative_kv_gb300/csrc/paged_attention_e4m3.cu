@@ -499,36 +499,33 @@ dflash_status launch_small(const PagedE4M3Params& p, const dflash_pages_e4m3& pa
 //     a key block's to its 16 scores, a value block's in the exponent of its 16 weights,
 //     2^((s - m) + b - r), and the sum l takes each 16's sum back at 2^(r - b).
 constexpr int kStepT = 128;
-// Registers: NG = 2, the launch's 168 for each of three warpgroups, of which the softmax
-// groups take 216 and the other one keeps 72; NG = 1, 128 for each of two: 208 for the one
-// with the softmax warps, 48 for the converting one.
-template <int NG>
-struct Regs {
-  static constexpr int kMost = NG == 2 ? 216 : 208, kLeast = NG == 2 ? 72 : 48;
-  static_assert(NG == 2 ? 2 * kMost + kLeast <= 3 * 168 : kMost + kLeast <= 2 * 128, "register split");
-};
+// Registers with NG = 2: the launch's 96 for each of five warpgroups, of which the four of
+// the softmax take 104 and the other one keeps 64.
+constexpr int kRegsSoftmax = 104, kRegsOther = 64;
+static_assert(4 * kRegsSoftmax + kRegsOther <= 5 * 96, "register split");
 
 template <int HD, int NG>
 struct Tc {
-  static constexpr int kGroup = NG == 2 ? 128 : 64;         // rows, and threads, of a softmax group
-  static constexpr int kRows = kGroup * NG, kWarps = kRows / 32;
-  static constexpr int kThreads = NG == 2 ? 384 : 256, kPerSm = NG == 2 ? 1 : 2;
-  static constexpr int kConv = NG == 2 ? 2 : 4;             // converting warps
+  static constexpr int kGroup = NG == 2 ? 128 : 64;         // rows of a softmax group, two threads to a row
+  static constexpr int kRows = kGroup * NG, kWarps = kRows / 16;
+  static constexpr int kThreads = NG == 2 ? 640 : 256, kPerSm = NG == 2 ? 1 : 2;
+  // Warps.  A warp reaches the TMEM lanes (rows) of its number modulo 4 alone.
+  static constexpr int kLoad = NG == 2 ? 16 : 2, kIssue = kLoad + 1, kConvert = NG == 2 ? 18 : 6, kConv = 2;
   using Geo = PagedGeo<kRows, kStepT, NG == 2 ? 12 : 3, 128, NG == 2 ? 1 : 3>;
   static constexpr int kAtomQ = kGroup * 128;               // 128 bytes of a group's rows of Q
   static constexpr int kTileQ = (HD / 64) * kAtomQ;         // hi and lo
   static constexpr int kKeys = NG == 2 ? 128 : 64;          // of a ring slot
   static constexpr int kPer = kStepT / kKeys;               // slots of a step's K, or V
-  static constexpr int kEarly = NG == 2 ? 96 : 64;          // keys of P that go out first
   static constexpr int kSlot = kKeys * HD;                  // of codes
   static constexpr int kAtom = kKeys * 128, kTileV = (HD / 64) * kAtom;     // of values in fp16
-  static constexpr int kK = NG == 2 ? 3 : 4, kV = NG == 2 ? 2 : 4, kC = 2;  // ring slots
+  static constexpr int kK = NG == 2 ? 3 : 4, kV = NG == 2 ? 2 : 3, kC = 2;  // ring slots
   static constexpr int kRingK = NG * kTileQ, kRingV = kRingK + kK * kSlot, kRingC = kRingV + kV * kSlot;
   static constexpr int kBar = kRingC + kC * kTileV;
   static constexpr int kBars = 2 * (kK + kV + kC) + 10;
   static constexpr int kWait = kBar + kBars * 8, kWord = kWait + kThreads / 32 * 8;
   static constexpr int kNote = kWord + 16, kScale = (kNote + 64 + 15) / 16 * 16, kMl = kScale + 8 * 64;
-  static constexpr int kBytes = kMl + (NG == 2 ? 1024 : 0);
+  static constexpr int kSwap = kMl + (NG == 2 ? 1024 : 0);
+  static constexpr int kBytes = kSwap + NG * 2 * kGroup * 4;
   static constexpr int kTmem = 256 * NG;                    // S_x at 128 x (P_x over it), then O_x
   static_assert(kPerSm * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
@@ -572,9 +569,11 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
   // steps past the scores, those two past the softmax.
   float2* sScale = reinterpret_cast<float2*>(smem + S::kScale);
   float2* sMl = reinterpret_cast<float2*>(smem + S::kMl);    // [128] (NG = 2)
+  // what a row's two threads tell each other: [half][NG][GT]
+  volatile float* sSwap = reinterpret_cast<volatile float*>(smem + S::kSwap);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kLoad = S::kWarps, kIssue = S::kWarps + 1, kConvert = S::kWarps + 2;    // warps
+  constexpr int kLoad = S::kLoad, kIssue = S::kIssue, kConvert = S::kConvert;
   if (tid == 0) {
     for (int s = 0; s < S::kK; ++s) {
       ptx::mbar_init(&k_full[s], 1);
@@ -653,28 +652,13 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
           if (!ok) break;
           const uint8_t* from = sV + s * S::kSlot;
           uint8_t* to = sC + t * S::kTileV;
-          uint32_t bad[kMine / 16] = {};
-#pragma unroll (NG == 2 ? 4 : 2)
-          for (int k0 = 0; k0 < kMine; k0 += kRound) {
+          auto take = [&](int k0) {
             const int key = w * kMine + k0 + lane / kPieces;
-            uint4 u = *reinterpret_cast<const uint4*>(
+            return *reinterpret_cast<const uint4*>(
                 from + key * HD + ((HD == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
-            if (check) {
-              if (key0 + part * S::kKeys + key >= kend) u = make_uint4(0, 0, 0, 0);
-              const uint4 x = make_uint4(nan_bytes(u.x), nan_bytes(u.y), nan_bytes(u.z), nan_bytes(u.w));
-              const uint32_t hit = __ballot_sync(0xffffffffu, (x.x | x.y | x.z | x.w) != 0);
-              if (hit) {                                     // (rare)
-                u = make_uint4(u.x & ~x.x, u.y & ~x.y, u.z & ~x.z, u.w & ~x.w);
-#pragma unroll
-                for (int k = 0; k < kRound; ++k)
-                  if ((hit >> (k * kPieces)) & ((1u << kPieces) - 1u)) {
-                    const int at = k0 + k;
-#pragma unroll
-                    for (int g = 0; g < kMine / 16; ++g)
-                      if (at / 16 == g) bad[g] |= 1u << (at % 16);
-                  }
-              }
-            }
+          };
+          auto put = [&](int k0, const uint4& u) {
+            const int key = w * kMine + k0 + lane / kPieces;
             const uint4 a = make_uint4(half2_lo(u.x), half2_hi(u.x), half2_lo(u.y), half2_hi(u.y));
             const uint4 b = make_uint4(half2_lo(u.z), half2_hi(u.z), half2_lo(u.w), half2_hi(u.w));
             // 32 bytes of the row's 64-column atom; the upper half's lanes store the other
@@ -683,11 +667,33 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
             const int c16 = (ch & 3) * 2;
             *reinterpret_cast<uint4*>(row + (((c16 + flip) ^ (key & 7)) << 4)) = flip ? b : a;
             *reinterpret_cast<uint4*>(row + (((c16 + 1 - flip) ^ (key & 7)) << 4)) = flip ? a : b;
-          }
-          if (check && lane == 0) {
+          };
+          if (!check) {
+#pragma unroll 1
+            for (int k0 = 0; k0 < kMine; k0 += 4 * kRound) {
+              uint4 u[4];
 #pragma unroll
-            for (int g = 0; g < kMine / 16; ++g)
-              notes[(iv / kPer & 3) * 8 + (part * S::kKeys + w * kMine) / 16 + g] = static_cast<uint16_t>(bad[g]);
+              for (int k = 0; k < 4; ++k) u[k] = take(k0 + k * kRound);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) put(k0 + k * kRound, u[k]);
+            }
+          } else {
+            uint32_t bad = 0;                                // of 16 keys
+#pragma unroll 1
+            for (int k0 = 0; k0 < kMine; k0 += kRound) {
+              uint4 u = take(k0);
+              if (key0 + part * S::kKeys + w * kMine + k0 + lane / kPieces >= kend) u = make_uint4(0, 0, 0, 0);
+              const uint4 x = make_uint4(nan_bytes(u.x), nan_bytes(u.y), nan_bytes(u.z), nan_bytes(u.w));
+              const uint32_t hit = __ballot_sync(0xffffffffu, (x.x | x.y | x.z | x.w) != 0);
+              for (int k = 0; k < kRound; ++k)
+                if ((hit >> (k * kPieces)) & ((1u << kPieces) - 1u)) bad |= 1u << ((k0 + k) & 15);
+              put(k0, make_uint4(u.x & ~x.x, u.y & ~x.y, u.z & ~x.z, u.w & ~x.w));
+              if (((k0 + kRound) & 15) == 0) {
+                if (lane == 0)
+                  notes[(iv / kPer & 3) * 8 + (part * S::kKeys + w * kMine + k0) / 16] = static_cast<uint16_t>(bad);
+                bad = 0;
+              }
+            }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -862,7 +868,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
             const uint32_t s = vs[kPer == 2 ? h : 0];
             const uint64_t v0 = dv + s * (S::kTileV >> 4);
 #pragma unroll
-            for (int j = h * (S::kEarly / 16); j < (h ? kStepT : S::kEarly) / 16; ++j)
+            for (int j = 4 * h; j < 4 * h + 4; ++j)
               ptx::mma_bf16_ta(tbase_o + 128 * x, tbase + 128 * x + j * 8,
                                v0 + (j % (S::kKeys / 16)) * (2048 >> 4), idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
             if (h == 1) ptx::mma_commit(&pv_done[x]);
@@ -898,11 +904,24 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
     }
     __syncwarp();
   };
-  // ---------------- softmax: group x = warp / 4, a row to a thread ----------------
+  // ---------------- softmax ----------------
+  // Group x's rows, two threads to a row: half h takes 64 of a step's keys, and half of
+  // O's columns.  Both know m and r; each has a sum of its own.
   auto softmax = [&]() {
-    const int x = warp / (GT / 32), wg = warp % (GT / 32), row = wg * 32 + lane;
+    constexpr int kCols = HD / 2;
+    const int x = NG == 2 ? (warp >> 2) & 1 : 0, h = NG == 2 ? warp >> 3 : warp >> 2;
+    const int wg = NG == 2 ? warp & 3 : warp & 1, row = wg * 32 + lane;
+    const int pair = 1 + x * 4 + wg, group = 9 + x, everyone = 11;       // barriers
     const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
-    const uint32_t aS = tbase + 128 * x + lane_off, aO = tbase_o + 128 * x + lane_off;
+    const uint32_t aS = tbase + 128 * x + lane_off, aO = tbase_o + 128 * x + kCols * h + lane_off;
+    volatile float *said = sSwap + (h * NG + x) * GT + row, *heard = sSwap + ((h ^ 1) * NG + x) * GT + row;
+    auto swap = [&](float v) {                               // the other thread's value
+      *said = v;
+      ptx::named_bar_sync(pair, 64);
+      const float o = *heard;
+      ptx::named_bar_sync(pair, 64);
+      return o;
+    };
     uint32_t it = 0, nj = 0;                                 // steps, jobs of this group
     bool ok = true;
     if (p.cut && tid == 0) p.cut[blockIdx.x].c1 = -1;
@@ -918,57 +937,55 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
       const bool live = rho < nG;
       const int tok = live ? p.heads.quot(rho) : 0, head = c.g * p.heads.G + (live ? rho - tok * p.heads.G : 0);
       const int jobs = NG == 1 || nt == 2 ? n : (n + 1 - x) / 2;
-      // Q as two codes into shared memory (rows of 128 bytes, 128-byte swizzle): HD / 8
-      // lanes read a row, whose address its own lane knows; that lane keeps what a score
-      // of the codes counts
+      const bool dead = rho0 + wg * 32 >= nG;        // no live row in this warp
+      // Q as two codes into shared memory (rows of 128 bytes, 128-byte swizzle), half a row
+      // to a thread.  count: what a score of the codes counts
       float count = 0.f;
-      {
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(
-            p.q + (long long)(rq.row0 + tok) * p.q_ld + (long long)head * HD);
-        const unsigned on = __ballot_sync(0xffffffffu, live);
-        constexpr int kLanes = HD / 8, kLines = 32 / kLanes;     // lanes of a row, rows of a round
+      if (!dead) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(rq.row0 + tok) * p.q_ld +
+                                                          (long long)head * HD + kCols * h);
+        uint4 u[kCols / 8];
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += kLines) {
-          const int rr = r0 + lane / kLanes, ch = lane % kLanes;
-          const uint4* src = reinterpret_cast<const uint4*>(__shfl_sync(0xffffffffu, mine, rr)) + ch;
-          const uint4 u = (on >> rr) & 1u ? __ldg(src) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          uint32_t top = 0;
+        for (int i = 0; i < kCols / 8; ++i) u[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        uint32_t top = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+        for (int i = 0; i < kCols / 8; ++i) {
+          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int e = max(static_cast<int>(top >> 7), 16);                               // biased exponent
-          const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);          // 2^(134 - e)
-          const float down = __shfl_sync(0xffffffffu, __uint_as_float(static_cast<uint32_t>(e - 7) << 23),
-                                         (lane - r0) * kLanes & 31);
-          if (static_cast<unsigned>(lane - r0) < static_cast<unsigned>(kLines)) count = down * p.scale_log2;
-          uint32_t hi[2] = {}, lo[2] = {};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float2 v = make_float2(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
-            v.x = fmaf(v.x, 0.f, v.x);                       // (an infinity becomes NaN)
-            v.y = fmaf(v.y, 0.f, v.y);
-            const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-            const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-            const __nv_fp8x2_storage_t l =
-                __nv_cvt_float2_to_fp8x2(make_float2(v.x - f.x, v.y - f.y), __NV_SATFINITE, __NV_E4M3);
-            hi[k >> 1] |= static_cast<uint32_t>(h) << (16 * (k & 1));
-            lo[k >> 1] |= static_cast<uint32_t>(l) << (16 * (k & 1));
-          }
-          if (nt == 2 || x == 0) {
-            uint8_t* tile = sQ + (nt == 2 ? x : 0) * S::kTileQ;
-            const int line = wg * 32 + rr;
-            auto put = [&](int byte, const uint32_t (&codes)[2]) {      // byte of the row: atom, 16-byte piece
-              *reinterpret_cast<uint2*>(tile + (byte >> 7) * S::kAtomQ + line * 128 +
-                                        ((((byte & 127) >> 4) ^ (line & 7)) << 4) + (byte & 15)) =
-                  make_uint2(codes[0], codes[1]);
-            };
-            put(8 * ch, hi);
-            put(HD + 8 * ch, lo);
-          }
+          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        top = max(top, __float_as_uint(swap(__uint_as_float(top))));
+        const int e = max(static_cast<int>(top >> 7), 16);                               // biased exponent
+        const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);          // 2^(134 - e)
+        count = __uint_as_float(static_cast<uint32_t>(e - 7) << 23) * p.scale_log2;
+        if (nt == 2 || x == 0) {
+          uint8_t* tile = sQ + (nt == 2 ? x : 0) * S::kTileQ + row * 128;
+#pragma unroll
+          for (int i = 0; i < kCols / 8; i += 2) {           // 16 elements: a piece of hi, one of lo
+            uint32_t hi[4] = {}, lo[4] = {};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint4& q = u[i + (k >> 2)];
+              const uint32_t w = (k & 3) == 0 ? q.x : (k & 3) == 1 ? q.y : (k & 3) == 2 ? q.z : q.w;
+              float2 v = make_float2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+              v.x = fmaf(v.x, 0.f, v.x);                     // (an infinity becomes NaN)
+              v.y = fmaf(v.y, 0.f, v.y);
+              const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+              const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3)));
+              const __nv_fp8x2_storage_t b =
+                  __nv_cvt_float2_to_fp8x2(make_float2(v.x - f.x, v.y - f.y), __NV_SATFINITE, __NV_E4M3);
+              hi[k >> 1] |= static_cast<uint32_t>(a) << (16 * (k & 1));
+              lo[k >> 1] |= static_cast<uint32_t>(b) << (16 * (k & 1));
+            }
+            auto put = [&](int byte, const uint32_t (&w)[4]) {           // byte of the row: atom, piece
+              *reinterpret_cast<uint4*>(tile + (byte >> 7) * S::kAtomQ + ((((byte & 127) >> 4) ^ (row & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            };
+            put(kCols * h + 8 * i, hi);
+            put(HD + kCols * h + 8 * i, lo);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(q_full);
@@ -978,30 +995,34 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
       const int lim = live ? (rq.masked ? kend : min(rq.p0 + tok + 1, kend)) : 0;
       const uint32_t* mrow = rq.masked ? p.mask + (size_t)(rq.row0 + tok) * p.mask_ld : nullptr;
       const int first = p.heads.quot(min(rho0 + wg * 32, nG - 1));
-      const int plain_w = rho0 + wg * 32 >= nG ? 0 : min(rq.masked ? rq.p0 : rq.p0 + first + 1, kend);
+      const int plain_w = dead ? 0 : min(rq.masked ? rq.p0 : rq.p0 + first + 1, kend);
       const int plain_t = min(rq.masked ? rq.p0 : rq.p0 + p.heads.quot(tile0) + 1, kend);
-      const bool dead = rho0 + wg * 32 >= nG;        // no live row in this warp
+      auto sees = [&](int k) {                               // keys [k, k + 32), a bit to a key
+        uint32_t bits = low_bits(lim - k);
+        if (rq.masked && bits) bits &= seen_word(mrow, p.mask_ld, k - rq.p0);
+        return bits;
+      };
       float m = -CUDART_INF_F, r = -CUDART_INF_F, l = 0.f;
       // A step's P V ran with zeros for NaN codes.  Once it is done (the next scores are, or
       // pv_done), a row that sees such a key becomes NaN in the code's column.
       int late = -1;                                         // first key of the step to be looked through, or none
-      uint32_t late_note = 0, late_seen[4];
+      uint32_t late_note = 0;
       auto repair = [&]() {
         if (late < 0 || dead) return;
 #pragma unroll 1
         for (int g = 0; g < 8; ++g) {
           uint32_t keys = notes[late_note * 8 + g];
-          const uint32_t s4 = g < 2 ? late_seen[0] : g < 4 ? late_seen[1] : g < 6 ? late_seen[2] : late_seen[3];
-          const uint32_t sees = g & 1 ? s4 >> 16 : s4;
-          while (keys) {                                     // warp-uniform
+          if (keys == 0) continue;                           // (warp-uniform)
+          const uint32_t mine = sees(late + 16 * g);
+          while (keys) {
             const int j = __ffs(keys) - 1;
             keys &= keys - 1;
             const int key = late + 16 * g + j, page = page_of(p.pv, c.r, key);
             if (page < 0) continue;
-            const uint8_t* v = static_cast<const uint8_t*>(p.pv.v) + pool_row(p.pv, page, c.g, key) * HD;
-            const bool see = (sees >> j) & 1u;
+            const uint8_t* v = static_cast<const uint8_t*>(p.pv.v) + pool_row(p.pv, page, c.g, key) * HD + kCols * h;
+            const bool see = (mine >> j) & 1u;
 #pragma unroll 1
-            for (int cb = 0; cb < HD / 16; ++cb) {
+            for (int cb = 0; cb < kCols / 16; ++cb) {
               float o[16];
               ptx::tmem_ld_32x16(aO + 16 * cb, o);
 #pragma unroll
@@ -1013,172 +1034,171 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
           }
         }
       };
-      // (after a wait has run out the loop only runs on to the group's barrier)
+      // (after a wait has run out the loop only runs on to everyone's barrier)
       for (int i = 0; i < jobs; ++i, ++nj) {
-        const int t = NG == 1 || nt == 2 ? i : 2 * i + x, key0 = (pc.first + t) * kStepT;
-        if (ok) ok = all(wait(&s_ready[x], nj & 1u));
         if (!ok) continue;
-        uint32_t seen[4];
-        if (!dead) {
-          ptx::tc_fence_after();
-          if (late >= 0) repair();
-          const float2* scale = sScale + (it + t & 7) * 8;
-          const bool cut = key0 + kStepT > plain_w;          // some key is hidden from some row
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            seen[b] = 0xFFFFFFFFu;
-            if (cut) {
-              const int k = key0 + 32 * b;
-              seen[b] = low_bits(lim - k);
-              if (rq.masked && seen[b]) seen[b] &= seen_word(mrow, p.mask_ld, k - rq.p0);
-            }
-          }
-          uint32_t u[4][32];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) ptx::tmem_ld_32x32(aS + 32 * b, u[b]);
-          // a block's factor and exponent (no infinity times zero, nor zero times infinity)
-          auto factor = [&](float a) { return fminf(fmaxf(count * a, 0x1p-126f), 0x1p90f); };
-          ptx::tmem_wait_ld();
-          if (cut) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((seen[b] >> j) & 1u)) u[b][j] = 0xff800000u;
-          }
-          float top[8], mx = -CUDART_INF_F, mr = -CUDART_INF_F;     // of a block; of all; with b
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const uint32_t* w = &u[g >> 1][16 * (g & 1)];
-            float a0 = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), __uint_as_float(w[2]));
-            float a1 = fmaxf(fmaxf(__uint_as_float(w[3]), __uint_as_float(w[4])), __uint_as_float(w[5]));
-#pragma unroll
-            for (int j = 6; j < 14; j += 4) {
-              a0 = fmaxf(fmaxf(a0, __uint_as_float(w[j])), __uint_as_float(w[j + 1]));
-              a1 = fmaxf(fmaxf(a1, __uint_as_float(w[j + 2])), __uint_as_float(w[j + 3]));
-            }
-            a0 = fmaxf(fmaxf(a0, __uint_as_float(w[14])), __uint_as_float(w[15]));
-            top[g] = fmaxf(a0, a1) * factor(scale[g].x);
-            mx = fmaxf(mx, top[g]);
-          }
-          const float base = fmaxf(m, mx);
-#pragma unroll
-          for (int g = 0; g < 8; ++g) mr = fmaxf(mr, (top[g] - base) + scale[g].y);      // (NaN where nothing is seen)
-          const bool raise = mx > m + kLazy || mr > r + (m - base) + kLazy;
-          if (__any_sync(0xffffffffu, raise)) {
-            float f = 1.f;
-            if (raise) {
-              const float was = m - base + r, r2 = fmaxf(was, mr);
-              f = ex2(was - r2);
-              l *= ex2(m - base);
-              m = base;
-              r = r2;
-            }
-            if (i > 0) {
-              // the products so far must be in O before it is scaled
-              ok = all(wait(&pv_done[x], (nj - 1) & 1u));
-              if (ok) {
-                ptx::tc_fence_after();
-#pragma unroll 1
-                for (int b = 0; b < HD / 16; ++b) {
-                  float o[16];
-                  ptx::tmem_ld_32x16(aO + 16 * b, o);
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) o[j] *= f;
-                  ptx::tmem_st_32x16(aO + 16 * b, o);
-                }
-              }
-            }
-          }
-          const bool none = m == -CUDART_INF_F;
-          // Scores so large that d - m below would lose bits: s - m first, on its own (rare).
-          const bool far = __any_sync(0xffffffffu, !none && fabsf(base) > 0x1p20f);
-          if (far) {
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const float f = factor(scale[g].x);
-#pragma unroll
-              for (int j = 16 * (g & 1); j < 16 * (g & 1) + 16; ++j)
-                u[g >> 1][j] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(u[g >> 1][j]), f), none ? 0.f : m));
-            }
-          }
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            float pk[16];                                      // (two fp16 each)
-#pragma unroll
-            for (int g = 2 * b; g < 2 * b + 2; ++g) {
-              const float2 sc = scale[g];
-              // 2^-60 of the largest weight is as good as none: l keeps its share
-              const float d = none ? 0.f : fmaxf(sc.y - r, -60.f), add = none || far ? d : d - m;
-              const float f1 = far ? 1.f : factor(sc.x);
-              const float2 f2 = make_float2(f1, f1), a2 = make_float2(add, add);
-              float2 rs = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float2 y = __ffma2_rn(make_float2(__uint_as_float(u[b][16 * (g & 1) + 2 * j]),
-                                                        __uint_as_float(u[b][16 * (g & 1) + 2 * j + 1])), f2, a2);
-                const float2 w = make_float2(ex2(y.x), ex2(y.y));
-                rs = __fadd2_rn(rs, w);
-                pk[8 * (g & 1) + j] = __uint_as_float(pack_f16_finite(w.x, w.y));
-              }
-              l = fmaf(rs.x + rs.y, ex2(-d), l);
-            }
-            ptx::tmem_st_32x16(aS + 16 * b, pk);
-            if (b == S::kEarly / 32 - 1) {
-              // the first keys of P may meet V while the others are formed
-              ptx::tmem_wait_st();
-              ptx::tc_fence_before();
-              __syncwarp();
-              if (lane == 0 && ok) ptx::mbar_arrive(&p_ready[2 * x]);
-            }
-          }
-          ptx::tmem_wait_st();
+        const int t = NG == 1 || nt == 2 ? i : 2 * i + x, key0 = (pc.first + t) * kStepT;
+        ok = all(wait(&s_ready[x], nj & 1u));
+        if (dead) {
+          if (ok && lane == 0) ptx::mbar_arrive(&p_ready[2 * x + h]);
+          continue;
         }
+        ptx::tc_fence_after();
+        if (ok && late >= 0) repair();
+        late = key0 + kStepT > plain_t ? key0 : -1;
+        late_note = it + t & 3;
+        const float2* scale = sScale + (it + t & 7) * 8 + 4 * h;
+        // a block's factor (no infinity times zero, nor zero times infinity)
+        auto factor = [&](float a) { return fminf(fmaxf(count * a, 0x1p-126f), 0x1p90f); };
+        uint32_t u[2][32];
+        ptx::tmem_ld_32x32(aS + 64 * h, u[0]);
+        ptx::tmem_ld_32x32(aS + 64 * h + 32, u[1]);
+        const int k0 = key0 + 64 * h;
+        uint32_t seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        const bool hide = k0 + 64 > plain_w;                 // some key is hidden from some row
+        if (hide) {
+          seen[0] = sees(k0);
+          seen[1] = sees(k0 + 32);
+        }
+        ptx::tmem_wait_ld();
+        if (hide) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((seen[b] >> j) & 1u)) u[b][j] = 0xff800000u;
+        }
+        float top[4], mx = -CUDART_INF_F, mr = -CUDART_INF_F;       // of a block; of all; with its exponent
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t* w = &u[g >> 1][16 * (g & 1)];
+          float a0 = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), __uint_as_float(w[2]));
+          float a1 = fmaxf(fmaxf(__uint_as_float(w[3]), __uint_as_float(w[4])), __uint_as_float(w[5]));
+#pragma unroll
+          for (int j = 6; j < 14; j += 4) {
+            a0 = fmaxf(fmaxf(a0, __uint_as_float(w[j])), __uint_as_float(w[j + 1]));
+            a1 = fmaxf(fmaxf(a1, __uint_as_float(w[j + 2])), __uint_as_float(w[j + 3]));
+          }
+          a0 = fmaxf(fmaxf(a0, __uint_as_float(w[14])), __uint_as_float(w[15]));
+          const float2 sc = scale[g];
+          top[g] = fmaxf(a0, a1) * factor(sc.x);
+          mx = fmaxf(mx, top[g]);
+          mr = fmaxf(mr, (top[g] - m) + sc.y);               // (NaN where nothing has been seen)
+        }
+        const bool raise = mx > m + kLazy || mr > r + kLazy;
+        // Both have read their scores when they have met: P may go over them.
+        ptx::tc_fence_before();
+        if (ptx::named_bar_or(pair, 64, raise || !ok)) {     // (rare)
+          const float other = swap(ok ? mx : CUDART_NAN_F);
+          ok = all(ok && !(other != other));
+          if (!ok) continue;
+          const float base = fmaxf(m, fmaxf(mx, other));
+          mr = -CUDART_INF_F;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) mr = fmaxf(mr, (top[g] - base) + scale[g].y);
+          mr = fmaxf(mr, swap(mr));
+          float f = 1.f;
+          if (base > m + kLazy || mr > r + (m - base) + kLazy) {
+            const float was = m - base + r, r2 = fmaxf(was, mr);
+            f = ex2(was - r2);
+            l *= ex2(m - base);
+            m = base;
+            r = r2;
+          }
+          if (i > 0) {
+            // the products so far must be in O before it is scaled
+            ok = all(wait(&pv_done[x], (nj - 1) & 1u));
+            if (ok) {
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int b = 0; b < kCols / 16; ++b) {
+                float o[16];
+                ptx::tmem_ld_32x16(aO + 16 * b, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] *= f;
+                ptx::tmem_st_32x16(aO + 16 * b, o);
+              }
+              ptx::tmem_wait_st();
+            }
+            ptx::tc_fence_before();
+            if (ptx::named_bar_or(pair, 64, !ok)) ok = false;       // (P of either half meets all of O)
+            if (!ok) continue;
+          }
+        }
+        ptx::tc_fence_after();
+        const bool none = m == -CUDART_INF_F;
+        // Scores so large that d - m below would lose bits: s - m first, on its own (rare).
+        const bool far = __any_sync(0xffffffffu, !none && fabsf(m) > 0x1p20f);
+        if (far) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float f = factor(scale[g].x);
+#pragma unroll
+            for (int j = 16 * (g & 1); j < 16 * (g & 1) + 16; ++j)
+              u[g >> 1][j] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(u[g >> 1][j]), f), none ? 0.f : m));
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float pk[16];                                      // (two fp16 each)
+#pragma unroll
+          for (int g = 2 * b; g < 2 * b + 2; ++g) {
+            const float2 sc = scale[g];
+            // 2^-60 of the largest weight is as good as none: l keeps its share
+            const float d = none ? 0.f : fmaxf(sc.y - r, -60.f), add = none || far ? d : d - m;
+            const float f1 = far ? 1.f : factor(sc.x);
+            const float2 f2 = make_float2(f1, f1), a2 = make_float2(add, add);
+            float2 rs = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(u[b][16 * (g & 1) + 2 * j]),
+                                                      __uint_as_float(u[b][16 * (g & 1) + 2 * j + 1])), f2, a2);
+              const float2 w = make_float2(ex2(y.x), ex2(y.y));
+              rs = __fadd2_rn(rs, w);
+              pk[8 * (g & 1) + j] = __uint_as_float(pack_f16_finite(w.x, w.y));
+            }
+            l = fmaf(rs.x + rs.y, ex2(-d), l);
+          }
+          ptx::tmem_st_32x16(aS + 32 * h + 16 * b, pk);
+        }
+        ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) {
-          if (dead) ptx::mbar_arrive(&p_ready[2 * x]);
-          ptx::mbar_arrive(&p_ready[2 * x + 1]);
-        }
-        late = key0 + kStepT > plain_t ? key0 : -1;
-        if (late >= 0) {
-          late_note = it + t & 3;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) late_seen[b] = seen[b];
-        }
+        if (lane == 0) ptx::mbar_arrive(&p_ready[2 * x + h]);
       }
       if (ok && jobs > 0) {
         ok = all(wait(&pv_done[x], (nj - 1) & 1u));
         if (ok) ptx::tc_fence_after();
         if (ok) repair();
       }
-      if (ptx::named_bar_or(5, GT * NG, !ok)) {
+      if (ptx::named_bar_or(everyone, 2 * GT * NG, !ok)) {
         ok = false;
         break;
       }
       // ---- the tile's rows ----  (O with m as its reference: times 2^r)
+      if (!dead) l += swap(l);
       const float own = m == -CUDART_INF_F ? 0.f : ex2(r);
-      float M = m, L = l, fa = own, fb = 0.f;                // weights of the two halves
+      float M = m, L = l, fa = own, fb = 0.f;                // weights of the two groups' halves
       float* sB = reinterpret_cast<float*>(sQ);              // [128][HD], chunks of 4 swizzled
       if (NG == 2 && nt == 1) {
-        if (x == 1) {
-          sMl[row] = make_float2(m, l);
+        if (x == 1 && !dead) {
+          if (h == 0) sMl[row] = make_float2(m, l);
           if (jobs > 0) {
 #pragma unroll
-            for (int b = 0; b < HD / 32; ++b) {
+            for (int b = 0; b < kCols / 32; ++b) {
               uint32_t o[32];
               ptx::tmem_ld_32x32(aO + 32 * b, o);
               ptx::tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<float4*>(sB + row * HD + 4 * ((8 * b + j) ^ (row & 7))) =
+                *reinterpret_cast<float4*>(sB + row * HD + 4 * ((kCols / 4 * h + 8 * b + j) ^ (row & 7))) =
                     make_float4(__uint_as_float(o[4 * j]) * own, __uint_as_float(o[4 * j + 1]) * own,
                                 __uint_as_float(o[4 * j + 2]) * own, __uint_as_float(o[4 * j + 3]) * own);
             }
           }
         }
-        ptx::named_bar_sync(5, GT * NG);
-        if (x == 0) {
+        ptx::named_bar_sync(everyone, 2 * GT * NG);
+        if (x == 0 && !dead) {
           const float2 ml = sMl[row];
           if (ml.y != 0.f) {
             M = fmaxf(m, ml.x);
@@ -1197,40 +1217,41 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
       // are neighbours in memory
       auto part_of = [&](int cc) { return ((size_t)cc * 2 + (cc == c0)) * NG + x; };
       const size_t slot = part_of(blockIdx.x);
-      // The warp's 32 bf16 rows go out through shared memory, so that HD / 8
-      // lanes write a row together: in the group's part of Q, or, a lane each, in
-      // its row of the joined half, over columns that it has read.
-      const int stage_ld = NG == 2 && nt == 1 ? HD * 4 : HD * 2;
-      uint8_t* stage = sQ + warp * 32 * stage_ld;
-      auto put = [&](int b, const float (&o)[32], float inv) {    // 32 columns of the row
+      // The warp's 32 half rows in bf16 go out through shared memory, so that neighbouring
+      // lanes write a row together: in a part of Q of its own, or, a lane each, in its
+      // half of its row of the joined group, over columns that it has read.
+      constexpr int kOut = HD / 16;                          // 16-byte pieces of a half row
+      const bool joined = NG == 2 && nt == 1;
+      const int stage_ld = joined ? HD * 4 : kCols * 2;
+      uint8_t* stage = joined ? sQ + wg * 32 * stage_ld + h * kCols * 4 : sQ + ((h * NG + x) * (GT / 32) + wg) * 32 * stage_ld;
+      auto put = [&](int b, const float (&o)[32], float inv) {    // 32 columns of the half row
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t w4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w4[e] = L == 0.f ? 0u : mmas::pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
-          *reinterpret_cast<uint4*>(stage + lane * stage_ld + (((4 * b + j) ^ (lane & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(stage + lane * stage_ld + (((4 * b + j) ^ (lane & (kOut - 1))) << 4)) =
               make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
       };
       auto send = [&]() {
         __syncwarp();
         const unsigned long long mine_to = reinterpret_cast<unsigned long long>(
-            p.out + (long long)(rq.row0 + tok) * p.out_ld + (long long)head * HD);
+            p.out + (long long)(rq.row0 + tok) * p.out_ld + (long long)head * HD + kCols * h);
         const unsigned on = __ballot_sync(0xffffffffu, live);
-        constexpr int kLines = 256 / HD;
-#pragma unroll 8
-        for (int r0 = 0; r0 < 32; r0 += kLines) {
-          const int rr = r0 + lane / (HD / 8), ch = lane % (HD / 8);
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 32 / kOut) {
+          const int rr = r0 + lane / kOut, ch = lane % kOut;
           uint4* to = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, mine_to, rr)) + ch;
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * stage_ld + ((ch ^ (rr & 7)) << 4));
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * stage_ld + ((ch ^ (rr & (kOut - 1))) << 4));
           if ((on >> rr) & 1u) *to = w;
         }
       };
       if (mine && !dead) {
         const float inv = 1.f / L;
-#pragma unroll 2
-        for (int b = 0; b < HD / 32; ++b) {
+#pragma unroll
+        for (int b = 0; b < kCols / 32; ++b) {
           uint32_t u[32];
           ptx::tmem_ld_32x32(aO + 32 * b, u);
           ptx::tmem_wait_ld();
@@ -1240,7 +1261,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
           if (fb != 0.f) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float4 v = *reinterpret_cast<const float4*>(sB + row * HD + 4 * ((8 * b + j) ^ (row & 7)));
+              const float4 v = *reinterpret_cast<const float4*>(sB + row * HD + 4 * ((kCols / 4 * h + 8 * b + j) ^ (row & 7)));
               o[4 * j] += fb * v.x;
               o[4 * j + 1] += fb * v.y;
               o[4 * j + 2] += fb * v.z;
@@ -1250,7 +1271,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
           if (whole) {
             put(b, o, inv);
           } else if (live) {
-            float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + 8 * b) * GT + row;
+            float4* po = reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + kCols / 4 * h + 8 * b) * GT + row;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               __stcg(po + j * GT, make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
@@ -1260,44 +1281,47 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
       }
       ptx::tc_fence_before();
       if (!whole && mine) {
-        if (live) __stcg(p.part_ml + slot * GT + row, make_float2(M, L));
+        if (live && h == 0) __stcg(p.part_ml + slot * GT + row, make_float2(M, L));
         if (p.cut) {
           if (tid == 0 && c0 == static_cast<int>(blockIdx.x))   // its first piece
             p.cut[c0] = {c1, rq.row0, tile0, nG, c.g * p.heads.G};
         } else {
           __threadfence();
-          ptx::named_bar_sync(1 + x, GT);
-          if (row == 0) s_last[x] = atomicAdd(p.arrive + NG * c0 + x, 1) == c1 - c0;
-          ptx::named_bar_sync(1 + x, GT);
+          ptx::named_bar_sync(group, 2 * GT);
+          if (row == 0 && h == 0) s_last[x] = atomicAdd(p.arrive + NG * c0 + x, 1) == c1 - c0;
+          ptx::named_bar_sync(group, 2 * GT);
           if (s_last[x]) {
             __threadfence();
-            if (row == 0) p.arrive[NG * c0 + x] = 0;            // for the next call
+            if (row == 0 && h == 0) p.arrive[NG * c0 + x] = 0;  // for the next call
             if (!dead) {
               M = -CUDART_INF_F;
 #pragma unroll 4
               for (int cc = c0; cc <= c1; ++cc) M = fmaxf(M, __ldcg(p.part_ml + part_of(cc) * GT + row).x);
-              float o[HD] = {};
-              L = 0.f;
-              float2 ml = __ldcg(p.part_ml + part_of(c0) * GT + row);
-              for (int cc = c0; cc <= c1; ++cc) {
-                const float2 now = ml;
-                if (cc < c1) ml = __ldcg(p.part_ml + part_of(cc + 1) * GT + row);
-                const float f = now.y != 0.f ? ex2(now.x - M) : 0.f;
-                L += f * now.y;
-                const float4* src = reinterpret_cast<const float4*>(p.part_o) + part_of(cc) * (HD / 4) * GT + row;
+#pragma unroll 1
+              for (int b = 0; b < kCols / 32; ++b) {
+                float o[32] = {};
+                L = 0.f;
+                float2 ml = __ldcg(p.part_ml + part_of(c0) * GT + row);
+                for (int cc = c0; cc <= c1; ++cc) {
+                  const float2 now = ml;
+                  if (cc < c1) ml = __ldcg(p.part_ml + part_of(cc + 1) * GT + row);
+                  const float f = now.y != 0.f ? ex2(now.x - M) : 0.f;
+                  L += f * now.y;
+                  const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                                      (part_of(cc) * (HD / 4) + kCols / 4 * h + 8 * b) * GT + row;
 #pragma unroll
-                for (int j = 0; j < HD / 4; ++j) {
-                  const float4 v = __ldcg(src + j * GT);
-                  if (now.y != 0.f) {
-                    o[4 * j] += f * v.x;
-                    o[4 * j + 1] += f * v.y;
-                    o[4 * j + 2] += f * v.z;
-                    o[4 * j + 3] += f * v.w;
+                  for (int j = 0; j < 8; ++j) {
+                    const float4 v = __ldcg(src + j * GT);
+                    if (now.y != 0.f) {
+                      o[4 * j] += f * v.x;
+                      o[4 * j + 1] += f * v.y;
+                      o[4 * j + 2] += f * v.z;
+                      o[4 * j + 3] += f * v.w;
+                    }
                   }
                 }
+                put(b, o, 1.f / L);
               }
-#pragma unroll
-              for (int b = 0; b < HD / 32; ++b) put(b, reinterpret_cast<float(&)[32]>(o[32 * b]), 1.f / L);
               send();
             }
           }
@@ -1305,7 +1329,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
       }
       it += n;
       // the rows on their way out lie where the next tile's queries go
-      ptx::named_bar_sync(5, GT * NG);
+      ptx::named_bar_sync(everyone, 2 * GT * NG);
     }
     if (!ok) fail();
   };
@@ -1313,24 +1337,19 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
   // (a warpgroup changes its registers in one instruction)
   if constexpr (NG == 2) {
     if (warp >= kLoad) {
-      ptx::regs_dec<Regs<NG>::kLeast>();
+      ptx::regs_dec<kRegsOther>();
       if (warp == kLoad) load();
       else if (warp == kIssue) issue();
       else convert();
     } else {
-      ptx::regs_inc<Regs<NG>::kMost>();
+      ptx::regs_inc<kRegsSoftmax>();
       softmax();
     }
   } else {
-    if (warp >= kConvert) {
-      ptx::regs_dec<Regs<NG>::kLeast>();
-      convert();
-    } else {
-      ptx::regs_inc<Regs<NG>::kMost>();
-      if (warp == kLoad) load();
-      else if (warp == kIssue) issue();
-      else softmax();
-    }
+    if (warp == kLoad) load();
+    else if (warp == kIssue) issue();
+    else if (warp >= kConvert) convert();
+    else softmax();
   }
 
   ptx::tc_fence_before();
