@@ -10,10 +10,14 @@
 //
 // HBM bounds it: logits in once, out once (a bit more for each token with a grammar).
 // A CTA takes one stretch of the vocabulary for several rows of one request: it counts
-// the request's history in that stretch once, in shared memory, and from row to row
-// adds and takes away the tokens by which their paths differ.  A bit for each token
-// says whether it occurred or has a bias at all; most 16-byte pieces have none and are
-// only copied.
+// the request's history in that stretch once, in shared memory, makes a sorted list of
+// the tokens that occurred or have a bias, and lists the rows' own tokens that lie there.
+// Then every warp works for itself, without another barrier: it brings 2 KB of a row,
+// picks from the list what the row's path holds, changes the listed tokens, a lane to a
+// token, in a buffer of its own, and writes the 2 KB.  A history of 8192 tokens touches one
+// token in 35, one of almost every 128 neighbours: changed where they are, in the
+// registers of the lanes that have them, they made the warps' instructions the limit (480
+// bf16 rows of 151936: 159 us).
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -45,38 +49,9 @@ struct AdjustParams {
   long long allowed_ld;
 };
 
-// 16 bytes of a row as fp32.
 template <typename T>
-struct Piece {
+struct Piece {                    // 16 bytes of a row
   static constexpr int V = 16 / sizeof(T);
-  float v[V];
-  __device__ __forceinline__ void get(const uint4& u) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
-    }
-  }
-  __device__ __forceinline__ uint4 set() const {
-    uint32_t w[4];
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
 };
 
 // Groups of ROWS rows lie on a line without a prefix sum: those of request r begin at
@@ -86,14 +61,37 @@ __device__ __forceinline__ int first_group(const AdjustParams& p, int r) {
   return min(max(__ldg(p.row_off + r), 0), p.rows) / ROWS + r;
 }
 
+constexpr int kWarps = kThreads / 32;
+constexpr int kDeep = 4;          // 16-byte pieces of a row to a lane at a time
+constexpr int kRowTokens = 512;   // of a request's rows in a stretch; more are looked up one by one
+constexpr int kPath = 64;         // a row's own tokens in a warp's part of a stretch, likewise
+
+template <typename T, int C>
+struct Stretch {
+  static constexpr int V = Piece<T>::V, kPart = 32 * kDeep * V, kParts = C / kPart, kWords = C / 32 + 2;
+  static_assert(C % kPart == 0 && C / 32 <= kThreads - 2);
+  uint4 buffer[kWarps][32 * kDeep];                        // a part of a row, a warp's
+  uint32_t count[C + V];                                   // times generated; the top bit: in the prompt
+  uint32_t bias[C + V];                                    // 1 + place in the list of biases
+  uint32_t some[kWords];                                   // tokens that occurred or have a bias
+  uint32_t path[kWarps][kPart / 32];                       // tokens that the warp's row has in its path
+  int row[kRowTokens];                                     // rows' own tokens in the stretch: row, token
+  int rows, sum[kWarps];
+  uint16_t token[kRowTokens];
+  uint16_t before[kWords];                                 // set bits before a word
+  uint16_t list[C + V];                                    // the set bits, ascending
+  uint16_t entry[kWarps][kPath];
+};
+
 template <typename T, int C, int ROWS>
-__global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const AdjustParams p) {
-  constexpr int V = Piece<T>::V, kN = C / V / kThreads;    // pieces of a row to a thread, and one more
-  static_assert(C % (V * kThreads) == 0);
-  __shared__ uint32_t sCount[C];                           // times generated; the top bit: in the prompt
-  __shared__ uint32_t sBias[C];                            // 1 + place in the list of biases
-  __shared__ uint32_t sSome[C / 32 + 1];                   // tokens that may have changed
-  const int tid = threadIdx.x, lane = tid & 31, c0 = blockIdx.y * C, c1 = min(c0 + C, p.vocab);
+__global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const AdjustParams p) {
+  // Pieces lie on 16-byte boundaries, so a row's first one may begin up to V - 1 tokens
+  // before it; stretch y is pieces y C / V .. of every row, tokens y C - V + 1 .. at most.
+  using S = Stretch<T, C>;
+  constexpr int V = S::V, kPart = S::kPart, kParts = S::kParts;
+  extern __shared__ __align__(16) uint8_t smem[];
+  S& s = *reinterpret_cast<S*>(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, base = blockIdx.y * C - V;
   pdl_wait();
   pdl_trigger();
   const int group = blockIdx.x;
@@ -108,134 +106,249 @@ __global__ void __launch_bounds__(kThreads) logits_adjust_kernel(const AdjustPar
   const bool track = rho != 1.f || phi != 0.f || pi != 0.f;
   const bool change = track || p.n_bias > 0;
 
-  auto note = [&](int t) { atomicOr(&sSome[t >> 5], 1u << (t & 31)); };
-  auto path = [&](int j, int by) {                         // the request's row j joins the past, or leaves it
-    const int t = __ldg(p.tok + row0 + j) - c0;
-    if (static_cast<unsigned>(t) >= static_cast<unsigned>(c1 - c0)) return;
-    atomicAdd(&sCount[t], static_cast<uint32_t>(by));
-    if (by > 0) note(t);
+  // a token's place in the stretch, if it has one
+  auto place = [&](int t) {
+    const unsigned a = static_cast<unsigned>(t) < static_cast<unsigned>(p.vocab) ? t - base : C + V;
+    return a < C + V ? static_cast<int>(a) : -1;
   };
+  auto note = [&](int a) { atomicOr(&s.some[a >> 5], 1u << (a & 31)); };
   const int words = p.mask ? min(p.mask_ld, (n + 31) / 32) : 0;
-  auto sees = [&](int i, int j) {
+  auto sees = [&](int i, int j) {                          // whether row i's path holds row j (of the request)
+    if (!p.mask) return j <= i;
     return (j >> 5) < words && ((__ldg(p.mask + (size_t)(row0 + i) * p.mask_ld + (j >> 5)) >> (j & 31)) & 1u);
   };
 
   if (change) {
-    for (int t = tid; t < C; t += kThreads) {
-      sCount[t] = 0;
-      sBias[t] = 0;
+    for (int a = tid; a < (C + V) / 4; a += kThreads) {
+      reinterpret_cast<uint4*>(s.count)[a] = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(s.bias)[a] = make_uint4(0, 0, 0, 0);
     }
-    if (tid <= C / 32) sSome[tid] = 0;
+    if (tid < S::kWords) s.some[tid] = 0;
+    for (int a = tid; a < kWarps * (kPart / 32); a += kThreads) (&s.path[0][0])[a] = 0;
+    if (tid == 0) s.rows = 0;
     __syncthreads();
     if (track) {
       const int len = p.history ? min(max(__ldg(p.history_len + req), 0), p.history_ld) : 0;
       const int prompt = p.prompt_len ? __ldg(p.prompt_len + req) : 0;
+      auto count = [&](int i, int t) {
+        const int a = place(t);
+        if (a < 0) return;
+        i < prompt ? atomicOr(&s.count[a], 0x80000000u) : atomicAdd(&s.count[a], 1u);
+        note(a);
+      };
+      // (four at a time, from the 16-byte boundary before the first)
       const int32_t* h = p.history + (size_t)req * p.history_ld;
-#pragma unroll 8
-      for (int i = tid; i < len; i += kThreads) {
-        const int t = __ldg(h + i) - c0;
-        if (static_cast<unsigned>(t) >= static_cast<unsigned>(c1 - c0)) continue;
-        i < prompt ? atomicOr(&sCount[t], 0x80000000u) : atomicAdd(&sCount[t], 1u);
-        note(t);
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(h) >> 2) & 3;
+      constexpr int kAtOnce = 8;
+      for (int i = tid * 4 - off; i < len; i += kAtOnce * kThreads * 4) {
+        int4 t[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int at = i + k * kThreads * 4;
+          if (at >= 0 && at + 4 <= len) {
+            t[k] = __ldg(reinterpret_cast<const int4*>(h + at));
+          } else {
+            auto one = [&](int e) { return at + e >= 0 && at + e < len ? __ldg(h + at + e) : -1; };
+            t[k] = make_int4(one(0), one(1), one(2), one(3));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int at = i + k * kThreads * 4;
+          count(at, t[k].x);
+          count(at + 1, t[k].y);
+          count(at + 2, t[k].z);
+          count(at + 3, t[k].w);
+        }
       }
-      if (p.tok && !p.mask)                                // the rows before this group
-        for (int j = tid; j < i0; j += kThreads) path(j, 1);
+      // The rows' own tokens: of a chain the ones before this group are everyone's past,
+      // and the ones after it nobody's.
+      if (p.tok)
+        for (int j = tid; j < (p.mask ? n : i1); j += kThreads) {
+          const int a = place(__ldg(p.tok + row0 + j));
+          if (a < 0) continue;
+          if (!p.mask && j < i0) {
+            atomicAdd(&s.count[a], 1u);
+            note(a);
+          } else {
+            const int e = atomicAdd(&s.rows, 1);
+            if (e < kRowTokens) {
+              s.row[e] = j;
+              s.token[e] = static_cast<uint16_t>(a);
+            }
+          }
+        }
     }
     for (int j = tid; j < p.n_bias; j += kThreads) {
-      const int t = __ldg(p.bias_tok + (size_t)req * p.n_bias + j) - c0;
-      if (static_cast<unsigned>(t) >= static_cast<unsigned>(c1 - c0)) continue;
-      atomicMax(&sBias[t], static_cast<uint32_t>(j + 1));
-      note(t);
+      const int a = place(__ldg(p.bias_tok + (size_t)req * p.n_bias + j));
+      if (a < 0) continue;
+      atomicMax(&s.bias[a], static_cast<uint32_t>(j + 1));
+      note(a);
     }
+    __syncthreads();
+    // the list: a thread to a word of bits, behind those of the words before
+    uint32_t bits = tid < S::kWords ? s.some[tid] : 0u;
+    int upto = __popc(bits);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) s.sum[warp] = upto;
+    __syncthreads();
+    int at = upto - __popc(bits);
+    for (int w = 0; w < warp; ++w) at += s.sum[w];
+    if (tid < S::kWords) s.before[tid] = static_cast<uint16_t>(at);
+    for (; bits; bits &= bits - 1) s.list[at++] = static_cast<uint16_t>(tid * 32 + __ffs(bits) - 1);
+    __syncthreads();
   }
+  const int listed = change && track ? s.rows : 0;
+  auto rank = [&](int a) { return s.before[a >> 5] + __popc(s.some[a >> 5] & ((1u << (a & 31)) - 1u)); };
 
-  auto fix = [&](float y, int t) {
-    const uint32_t count = sCount[t], b = sBias[t];
-    if (b) y += __ldg(p.bias_val + (size_t)req * p.n_bias + b - 1);
-    if (count) y = y > 0.f ? y / rho : y * rho;
-    const uint32_t c = count & 0x7FFFFFFFu;
-    if (c) y = y - phi * static_cast<float>(c) - pi;
-    return y;
-  };
-
-  for (int i = i0; i < i1; ++i) {
+  uint4* buffer = s.buffer[warp];
+  T* value = reinterpret_cast<T*>(buffer);
+  for (int item = warp; item < (i1 - i0) * kParts; item += kWarps) {
+    const int i = i0 + item / kParts, part = item % kParts;
     const long long row = row0 + i;
     const T* in = static_cast<const T*>(p.logits) + row * p.ld;
     T* out = static_cast<T*>(p.out) + row * p.out_ld;
-    // pieces lie on 16-byte boundaries of the row; the first may begin before the stretch
-    const int off_in = static_cast<int>(reinterpret_cast<uintptr_t>(in) / sizeof(T)) & (V - 1);
-    const bool same = (static_cast<int>(reinterpret_cast<uintptr_t>(out) / sizeof(T)) & (V - 1)) == off_in;
-    const int t0 = (c0 + off_in) / V * V - off_in;
-    uint4 u[kN + 1];
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(in) / sizeof(T)) & (V - 1);
+    const bool same = (static_cast<int>(reinterpret_cast<uintptr_t>(out) / sizeof(T)) & (V - 1)) == off;
+    const int t0 = blockIdx.y * C + part * kPart - off;    // the part's first token
+    uint4 u[kDeep];
 #pragma unroll
-    for (int k = 0; k <= kN; ++k) {
-      const int t = t0 + (tid + k * kThreads) * V;
-      if (t >= c1) continue;
-      if (t >= c0 && t + V <= c1) {
+    for (int k = 0; k < kDeep; ++k) {
+      const int t = t0 + (k * 32 + lane) * V;
+      if (t >= p.vocab) continue;
+      if (t >= 0 && t + V <= p.vocab) {
         u[k] = *reinterpret_cast<const uint4*>(in + t);
       } else {
         __align__(16) T e[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) e[j] = t + j >= c0 && t + j < c1 ? in[t + j] : T(0.f);
+        for (int j = 0; j < V; ++j) e[j] = t + j >= 0 && t + j < p.vocab ? in[t + j] : T(0.f);
         u[k] = *reinterpret_cast<const uint4*>(e);
       }
     }
-    if (track && p.tok) {
-      if (p.mask) {
-        for (int j = tid; j < n; j += kThreads) {
-          const bool now = sees(i, j), was = i > i0 && sees(i - 1, j);
-          if (now != was) path(j, now ? 1 : -1);
-        }
-      } else if (tid == 0) {
-        path(i, 1);
-      }
-    }
-    if (change) __syncthreads();
+    uint32_t may[kDeep];                                   // a bit to an element
     const uint32_t* allowed = p.allowed ? p.allowed + row * p.allowed_ld : nullptr;
 #pragma unroll
-    for (int k = 0; k <= kN; ++k) {
-      const int t = t0 + (tid + k * kThreads) * V;
-      if (t >= c1) continue;
-      const bool full = t >= c0 && t + V <= c1;
-      uint32_t may = 0xFFFFFFFFu, some = 0;                // a bit to an element
-      if (allowed) {
-        const int w = t >> 5, last = (p.vocab - 1) >> 5;
-        const uint32_t lo = w >= 0 ? __ldg(allowed + w) : 0u;
-        const uint32_t hi = (t & 31) + V > 32 && w < last ? __ldg(allowed + w + 1) : 0u;
-        may = __funnelshift_r(lo, hi, t & 31);
-      }
-      if (change) {
-        const int a = t - c0, w = a >> 5;                  // (a > -V: the word before the first has no bit)
-        some = __funnelshift_r(w >= 0 ? sSome[w] : 0u, sSome[w + 1], a & 31);
-      }
-      Piece<T> x;
-      x.get(u[k]);
-      if (some & ((1u << V) - 1u)) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if ((some >> j) & 1u) x.v[j] = fix(x.v[j], t - c0 + j);
-      }
-      if ((may & ((1u << V) - 1u)) != (1u << V) - 1u) {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (!((may >> j) & 1u)) x.v[j] = -CUDART_INF_F;
-      }
-      if (full && same) {
-        *reinterpret_cast<uint4*>(out + t) = x.set();
+    for (int k = 0; k < kDeep; ++k) {
+      const int t = t0 + (k * 32 + lane) * V;
+      may[k] = 0xFFFFFFFFu;
+      if (!allowed || t >= p.vocab) continue;
+      const int w = t >> 5, last = (p.vocab - 1) >> 5;
+      const uint32_t lo = w >= 0 ? __ldg(allowed + w) : 0u;
+      const uint32_t hi = (t & 31) + V > 32 && w < last ? __ldg(allowed + w + 1) : 0u;
+      may[k] = __funnelshift_r(lo, hi, t & 31);
+    }
+    if (change) {
+      // places count from the part's first token from here on
+      const int a0 = t0 - base, r0 = rank(a0), r1 = rank(a0 + kPart);
+      // what the row's path has in this part
+      int own = 0;
+      if (listed > kRowTokens) {
+        own = kPath + 1;
       } else {
+        for (int e0 = 0; e0 < listed; e0 += 32) {
+          const int e = e0 + lane, a = e < listed ? s.token[e] - a0 : -1;
+          const bool on = a >= 0 && a < kPart && sees(i, s.row[e]);
+          const uint32_t who = __ballot_sync(0xffffffffu, on);
+          const int at = own + __popc(who & ((1u << lane) - 1u));
+          if (on) {
+            atomicOr(&s.path[warp][a >> 5], 1u << (a & 31));
+            if (at < kPath) s.entry[warp][at] = static_cast<uint16_t>(a);
+          }
+          own += __popc(who);
+        }
+      }
+      if (own > 0 || r1 > r0) {                            // (warp-uniform)
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (t + j >= c0 && t + j < c1) out[t + j] = from_f32<T>(x.v[j]);
+        for (int k = 0; k < kDeep; ++k) buffer[k * 32 + lane] = u[k];
+        __syncwarp();
+        auto fix = [&](int a, uint32_t more) {             // `more` times in the path
+          const uint32_t b = s.bias[a0 + a], count = s.count[a0 + a] + more;
+          float y = to_f32(value[a]);
+          if (b) y += __ldg(p.bias_val + (size_t)req * p.n_bias + b - 1);
+          if (count) y = y > 0.f ? y / rho : y * rho;
+          const uint32_t c = count & 0x7FFFFFFFu;
+          if (c) y = y - phi * static_cast<float>(c) - pi;
+          value[a] = from_f32<T>(y);
+        };
+        if (own <= kPath) {
+          for (int e = r0 + lane; e < r1; e += 32) {
+            const int a = s.list[e] - a0;
+            if (!((s.path[warp][a >> 5] >> (a & 31)) & 1u)) fix(a, 0);
+          }
+          for (int e = lane; e < own; e += 32) {
+            const int a = s.entry[warp][e];
+            uint32_t more = 0;
+            bool first = true;
+            for (int f = 0; f < own; ++f)
+              if (s.entry[warp][f] == a) {
+                first &= f >= e;
+                ++more;
+              }
+            if (first) fix(a, more);
+          }
+        } else {                                           // too many to list
+          for (int a = lane; a < kPart; a += 32) {
+            uint32_t more = 0;
+            for (int j = p.mask ? 0 : i0; j < (p.mask ? n : i + 1); ++j)
+              if (__ldg(p.tok + row0 + j) == t0 + a && sees(i, j)) ++more;
+            if (t0 + a >= 0 && t0 + a < p.vocab) fix(a, more);
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) u[k] = buffer[k * 32 + lane];
+        if (own) {                                         // no path for the next row yet
+          for (int w = lane; w < kPart / 32; w += 32) s.path[warp][w] = 0;
+        }
+        __syncwarp();
       }
     }
-    if (change && i + 1 < i1) __syncthreads();             // the counts change for the next row
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const int t = t0 + (k * 32 + lane) * V;
+      if (t >= p.vocab) continue;
+      if ((may[k] & ((1u << V) - 1u)) != (1u << V) - 1u) {
+        constexpr uint32_t kNone = sizeof(T) == 2 ? 0xFF80u : 0xFF800000u;     // -infinity
+        uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (!((may[k] >> j) & 1u)) {
+            if constexpr (sizeof(T) == 2)
+              w[j / 2] = j & 1 ? (w[j / 2] & 0xFFFFu) | kNone << 16 : (w[j / 2] & 0xFFFF0000u) | kNone;
+            else
+              w[j] = kNone;
+          }
+        u[k] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (t >= 0 && t + V <= p.vocab && same) {
+        *reinterpret_cast<uint4*>(out + t) = u[k];
+      } else {
+        const T* e = reinterpret_cast<const T*>(&u[k]);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (t + j >= 0 && t + j < p.vocab) out[t + j] = e[j];
+      }
+    }
   }
 }
 
 template <typename T, int C, int ROWS>
 void launch(const AdjustParams& p, cudaStream_t st) {
+  using S = Stretch<T, C>;
+  static bool set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    cudaFuncSetAttribute(logits_adjust_kernel<T, C, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(S));
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
   const int groups = p.rows / ROWS + p.n_req;
-  launch_k(logits_adjust_kernel<T, C, ROWS>, dim3(groups, (p.vocab + C - 1) / C), dim3(kThreads), 0, st, p);
+  launch_k(logits_adjust_kernel<T, C, ROWS>, dim3(groups, (p.vocab + S::V - 1 + C - 1) / C), dim3(kThreads), sizeof(S),
+           st, p);
 }
 
 }  // namespace
@@ -273,9 +386,9 @@ extern "C" dflash_status dflash_logits_adjust(
     TraceScope ts("logits_adjust", st);
     const bool few = (rows / 16 + n_req) * (long long)((vocab + 4095) / 4096) < 2 * num_sms();
     if (dtype == DFLASH_BF16)
-      few ? launch<__nv_bfloat16, 2048, 4>(p, st) : launch<__nv_bfloat16, 4096, 16>(p, st);
+      few ? launch<__nv_bfloat16, 1024, 4>(p, st) : launch<__nv_bfloat16, 2048, 16>(p, st);
     else
-      few ? launch<float, 1024, 4>(p, st) : launch<float, 4096, 16>(p, st);
+      few ? launch<float, 1024, 4>(p, st) : launch<float, 2048, 16>(p, st);
   }
   return check_launch("logits adjust");
 }

@@ -255,3 +255,19 @@ def test_a_tree_node_is_penalised_as_its_path_would_be():
             assert torch.equal(one_out[0], out[row])
             bd.logits_sample_filtered(one_out, u[row:row + 1], one_tok, one_lp, temperature=temp[:1], top_k=top_k[:1])
             assert int(one_tok) == int(choice[row])
+
+
+def test_adjust_more_row_tokens_than_are_listed():
+    """A mask over a thousand rows whose tokens all lie close together, paths of hundreds."""
+    rng = np.random.default_rng(4)
+    n, vocab = 1000, 700
+    d = _case([n], vocab, F32, [300], False, 5, False, low=0.1)
+    mask = rng.integers(0, 1 << 32, size=(n + 1, 32), dtype=np.uint64).astype(np.uint32)
+    mask[::2] &= rng.integers(0, 1 << 32, size=mask[::2].shape, dtype=np.uint64).astype(np.uint32) & 0x11111111
+    mask[5:60] = 0
+    mask[20] = 1 << 31
+    for tokens in (rng.integers(0, 60, size=n + 1), rng.integers(-1, vocab, size=n + 1)):
+        e = dict(d, mask=mask, tok=tokens.astype(np.int32))
+        out = _run(e)
+        torch.cuda.synchronize()
+        _check(e, out)
