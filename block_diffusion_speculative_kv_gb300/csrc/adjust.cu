@@ -62,11 +62,11 @@ __device__ __forceinline__ int first_group(const AdjustParams& p, int r) {
 }
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kDeep = 4;          // 16-byte pieces of a row to a lane at a time
 constexpr int kRowTokens = 512;   // of a request's rows in a stretch; more are looked up one by one
 constexpr int kPath = 64;         // a row's own tokens in a warp's part of a stretch, likewise
 
-template <typename T, int C>
+// kDeep: 16-byte pieces of a row that a lane has at a time.
+template <typename T, int C, int kDeep>
 struct Stretch {
   static constexpr int V = Piece<T>::V, kPart = 32 * kDeep * V, kParts = C / kPart, kWords = C / 32 + 2;
   static_assert(C % kPart == 0 && C / 32 <= kThreads - 2);
@@ -83,11 +83,11 @@ struct Stretch {
   uint16_t entry[kWarps][kPath];
 };
 
-template <typename T, int C, int ROWS>
-__global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const AdjustParams p) {
+template <typename T, int C, int kDeep, int ROWS>
+__global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_kernel(const AdjustParams p) {
   // Pieces lie on 16-byte boundaries, so a row's first one may begin up to V - 1 tokens
   // before it; stretch y is pieces y C / V .. of every row, tokens y C - V + 1 .. at most.
-  using S = Stretch<T, C>;
+  using S = Stretch<T, C, kDeep>;
   constexpr int V = S::V, kPart = S::kPart, kParts = S::kParts;
   extern __shared__ __align__(16) uint8_t smem[];
   S& s = *reinterpret_cast<S*>(smem);
@@ -107,8 +107,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const Adjust
   const bool change = track || p.n_bias > 0;
 
   // a token's place in the stretch, if it has one
+  // (a token that is none may have one too, before the row's first or behind its last: it
+  // changes what is not written)
   auto place = [&](int t) {
-    const unsigned a = static_cast<unsigned>(t) < static_cast<unsigned>(p.vocab) ? t - base : C + V;
+    const unsigned a = static_cast<unsigned>(t) - static_cast<unsigned>(base);
     return a < C + V ? static_cast<int>(a) : -1;
   };
   auto note = [&](int a) { atomicOr(&s.some[a >> 5], 1u << (a & 31)); };
@@ -236,10 +238,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const Adjust
       const int t = t0 + (k * 32 + lane) * V;
       may[k] = 0xFFFFFFFFu;
       if (!allowed || t >= p.vocab) continue;
-      const int w = t >> 5, last = (p.vocab - 1) >> 5;
-      const uint32_t lo = w >= 0 ? __ldg(allowed + w) : 0u;
-      const uint32_t hi = (t & 31) + V > 32 && w < last ? __ldg(allowed + w + 1) : 0u;
-      may[k] = __funnelshift_r(lo, hi, t & 31);
+      const int w = t >> 5, sh = t & 31;
+      uint32_t x = w >= 0 ? __ldg(allowed + w) >> sh : 0u;
+      if (sh + V > 32 && w < (p.vocab - 1) >> 5) x |= __ldg(allowed + w + 1) << (32 - sh);      // (sh > 0)
+      may[k] = x;
     }
     if (change) {
       // places count from the part's first token from here on
@@ -312,16 +314,19 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const Adjust
       const int t = t0 + (k * 32 + lane) * V;
       if (t >= p.vocab) continue;
       if ((may[k] & ((1u << V) - 1u)) != (1u << V) - 1u) {
-        constexpr uint32_t kNone = sizeof(T) == 2 ? 0xFF80u : 0xFF800000u;     // -infinity
+        constexpr uint32_t kNone = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;     // -infinity
         uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (!((may[k] >> j) & 1u)) {
-            if constexpr (sizeof(T) == 2)
-              w[j / 2] = j & 1 ? (w[j / 2] & 0xFFFFu) | kNone << 16 : (w[j / 2] & 0xFFFF0000u) | kNone;
-            else
-              w[j] = kNone;
+        for (int j = 0; j < 4; ++j) {
+          uint32_t keep;
+          if constexpr (sizeof(T) == 2) {                  // two bits, each to a half of the word
+            const uint32_t two = may[k] >> (2 * j);
+            keep = (two & 1u) * 0xFFFFu + (two & 2u) * 0x7FFF8000u;
+          } else {
+            keep = 0u - ((may[k] >> j) & 1u);
           }
+          w[j] = (w[j] & keep) | (kNone & ~keep);
+        }
         u[k] = make_uint4(w[0], w[1], w[2], w[3]);
       }
       if (t >= 0 && t + V <= p.vocab && same) {
@@ -336,18 +341,22 @@ __global__ void __launch_bounds__(kThreads, 4) logits_adjust_kernel(const Adjust
   }
 }
 
-template <typename T, int C, int ROWS>
+// Measured, us, 32 x 15 bf16 rows and a tree of 257 fp32 ones, of 151936: stretches of 4 KB, 2 KB
+// of them to a warp at a time 78 and 62, 4 KB 89 and 62; of 8 KB 84 and 70 (histories are
+// counted half as often, but the stretch of the commonest tokens is a longer one); groups of 32
+// rows 77 and (4 KB to a warp) 57, of 8 rows 94 and 66.
+template <typename T, int C, int kDeep, int ROWS>
 void launch(const AdjustParams& p, cudaStream_t st) {
-  using S = Stretch<T, C>;
+  using S = Stretch<T, C, kDeep>;
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    cudaFuncSetAttribute(logits_adjust_kernel<T, C, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(S));
+    cudaFuncSetAttribute(logits_adjust_kernel<T, C, kDeep, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(S));
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   const int groups = p.rows / ROWS + p.n_req;
-  launch_k(logits_adjust_kernel<T, C, ROWS>, dim3(groups, (p.vocab + S::V - 1 + C - 1) / C), dim3(kThreads), sizeof(S),
+  launch_k(logits_adjust_kernel<T, C, kDeep, ROWS>, dim3(groups, (p.vocab + S::V - 1 + C - 1) / C), dim3(kThreads), sizeof(S),
            st, p);
 }
 
@@ -386,9 +395,9 @@ extern "C" dflash_status dflash_logits_adjust(
     TraceScope ts("logits_adjust", st);
     const bool few = (rows / 16 + n_req) * (long long)((vocab + 4095) / 4096) < 2 * num_sms();
     if (dtype == DFLASH_BF16)
-      few ? launch<__nv_bfloat16, 1024, 4>(p, st) : launch<__nv_bfloat16, 2048, 16>(p, st);
+      few ? launch<__nv_bfloat16, 1024, 4, 4>(p, st) : launch<__nv_bfloat16, 2048, 4, 16>(p, st);
     else
-      few ? launch<float, 1024, 4>(p, st) : launch<float, 2048, 16>(p, st);
+      few ? launch<float, 1024, 4, 4>(p, st) : launch<float, 1024, 8, 32>(p, st);
   }
   return check_launch("logits adjust");
 }

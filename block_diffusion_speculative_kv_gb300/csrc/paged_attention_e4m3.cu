@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // KV head.  Which key, column or element a lane holds is free as long as both operands
 // agree: a lane reads its codes as 16-byte pieces of a slot, and turns them into fragments
 // by conversion alone (and, for V, a byte permutation that pairs two slots).
-constexpr int kStepS = 64, kStagesS = 6, kThreadsS = 128, kPerSmS = 2;
+constexpr int kStepS = 64, kStagesS = 3, kThreadsS = 128, kPerSmS = 3;
 
 template <int NT>
 using GeoS = PagedGeo<8 * NT, kStepS, 4, 8 * NT, 2>;
@@ -1402,7 +1402,7 @@ extern "C" {
 
 size_t dflash_paged_attention_e4m3_workspace_bytes(int n_q, int n_kv, int head_dim) {
   if (n_kv < 1 || n_q < n_kv || n_q % n_kv || (head_dim != 64 && head_dim != 128)) return 0;
-  return paged_ws(num_sms(), head_dim).bytes;
+  return paged_ws(num_sms(), head_dim, kPerSmS).bytes;
 }
 
 dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_req, int n_rows,
@@ -1428,7 +1428,7 @@ dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_
   DFL_REQUIRE(row_off && pos0 && q && out, "paged attention e4m3: null pointer argument");
   DFL_REQUIRE(((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0,
               "paged attention e4m3: q and out must be 16-byte aligned");
-  const PagedWs w = paged_ws(num_sms(), hd);
+  const PagedWs w = paged_ws(num_sms(), hd, kPerSmS);
   if (!ws || ws_bytes < w.bytes)
     return set_error(DFLASH_ERR_WORKSPACE, "paged attention e4m3 workspace needs %zu bytes, got %zu",
                      w.bytes, ws_bytes);

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 3) paged_append_kernel(const AppendP
 // A scale belongs to a block of 16 slots, so a block is a CTA's, and a block of one KV
 // head's keys or values a warp's: the warp holds all its rows in registers (16 rows of
 // 128 elements are 64 to a lane), rotates them, finds the largest element and the
-// scale, and writes the codes.  Memory bounds it: rows in once, codes and scales out.
+// scale, rotates them again and writes the codes.  Memory bounds it: rows in once, codes and scales out.
 struct AppendE4M3Params {
   PagedView pv;
   uint8_t *k_scale, *v_scale;
@@ -419,7 +419,7 @@ __device__ __forceinline__ int first_block(const AppendE4M3Params& p, int r) {
 }
 
 template <typename T, int HD, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) paged_append_e4m3_kernel(const AppendE4M3Params p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) paged_append_e4m3_kernel(const AppendE4M3Params p) {
   constexpr int kLanes = HD / 16, kHalf = HD / 2, kPass = 32 / kLanes, kPasses = kScaleBlock / kPass;
   __shared__ Turns<HD> cs[kScaleBlock];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % kLanes;
@@ -430,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_e4m3_kernel(const Ap
   const int n = min(max(p.row_off[req + 1], row0), p.n_rows) - row0, p0 = p.pos0[req];
   const long long s0 = ((long long)(p0 >> 4) + (static_cast<int>(blockIdx.x) - first_block(p, req))) * kScaleBlock;
   if (n == 0 || s0 >= (long long)p0 + n || s0 < 0 || s0 >= (1ll << 30)) return;    // block-uniform
-  const int slot0 = static_cast<int>(s0), page = page_of(p.pv, req, slot0);
-  if (page < 0) return;
+  const int slot0 = static_cast<int>(s0);
   const int lead = row0 - p0 + slot0;                      // row of the block's first slot, were it new
   const int old = min(max(p0 - slot0, 0), kScaleBlock);    // slots that hold earlier tokens
   const int end = static_cast<int>(min((long long)p0 + n - slot0, (long long)kScaleBlock));
@@ -457,6 +456,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_e4m3_kernel(const Ap
   };
   int h = blockIdx.y * (kThreads / 32) + warp;
   if (h < items) load(h);
+  const int page = page_of(p.pv, req, slot0);              // (asked for beside the rows)
+  if (page < 0) return;                                    // block-uniform
   if (p.rotate) {
     for (int i = tid; i < kScaleBlock * kHalf; i += kThreads) {
       const int s = i / kHalf;
@@ -471,32 +472,34 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_e4m3_kernel(const Ap
     const long long row = pool_row(p.pv, page, g, slot0);
     uint8_t* scale = (is_k ? p.k_scale : p.v_scale) + row / kScaleBlock;
     const int was = old > 0 ? min(static_cast<int>(*scale), 253) : 0;
-    float2 x[kPasses][4], y[kPasses][4];
+    // (turned once for the maximum and once more for the codes: 64 values in fp32 would
+    // leave an SM 16 warps)
+    auto turned = [&](int i, float2 (&x)[4], float2 (&y)[4]) {
+      a[i].get(x);
+      b[i].get(y);
+      if (is_k && p.rotate) cs[i * kPass + lane / kLanes].rotate(x, y, sub);
+    };
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int s = i * kPass + lane / kLanes;
-      if (!((live >> s) & 1u)) continue;
-      a[i].get(x[i]);
-      b[i].get(y[i]);
-      if (is_k && p.rotate) cs[s].rotate(x[i], y[i], sub);
-      auto see = [&](float& v) {                           // (NaN is no maximum)
-        if (!(fabsf(v) <= CUDART_MAX_NORMAL_F)) v = CUDART_NAN_F;
-        top = fmaxf(top, fabsf(v));
+      if (!((live >> (i * kPass + lane / kLanes)) & 1u)) continue;
+      float2 x[4], y[4];
+      turned(i, x, y);
+      auto see = [&](float v) {                            // (what is not finite is no maximum)
+        v = fabsf(v);
+        if (v <= CUDART_MAX_NORMAL_F) top = fmaxf(top, v);
       };
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        see(x[i][j].x);
-        see(x[i][j].y);
-        see(y[i][j].x);
-        see(y[i][j].y);
+        see(x[j].x);
+        see(x[j].y);
+        see(y[j].x);
+        see(y[j].y);
       }
     }
-    if (h + warps < items) load(h + warps);
     const int fits = scale_for(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
     const int now = max(fits, was);
     const float f = unscale(now);
-    const float2 f2 = make_float2(f, f);
     uint8_t* dst = static_cast<uint8_t*>(is_k ? p.pv.k : p.pv.v) + row * HD;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -504,16 +507,26 @@ __global__ void __launch_bounds__(kThreads, 2) paged_append_e4m3_kernel(const Ap
       uint2* lo = reinterpret_cast<uint2*>(dst + s * HD + 8 * sub);
       uint2* hi = reinterpret_cast<uint2*>(dst + s * HD + kHalf + 8 * sub);
       if ((live >> s) & 1u) {
-        *lo = make_uint2(codes4(__fmul2_rn(x[i][0], f2), __fmul2_rn(x[i][1], f2)),
-                         codes4(__fmul2_rn(x[i][2], f2), __fmul2_rn(x[i][3], f2)));
-        *hi = make_uint2(codes4(__fmul2_rn(y[i][0], f2), __fmul2_rn(y[i][1], f2)),
-                         codes4(__fmul2_rn(y[i][2], f2), __fmul2_rn(y[i][3], f2)));
+        float2 x[4], y[4];
+        turned(i, x, y);
+        auto scaled = [&](float2& v) {                     // (an infinity becomes NaN)
+          v = __fmul2_rn(v, make_float2(f, f));
+          v = __ffma2_rn(v, make_float2(0.f, 0.f), v);
+        };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          scaled(x[j]);
+          scaled(y[j]);
+        }
+        *lo = make_uint2(codes4(x[0], x[1]), codes4(x[2], x[3]));
+        *hi = make_uint2(codes4(y[0], y[1]), codes4(y[2], y[3]));
       } else if (s < old && now > was) {
         const float shift = __uint_as_float(static_cast<uint32_t>(127 - min(now - was, 64)) << 23);   // 2^(was - now)
         *lo = make_uint2(recode4(lo->x, shift), recode4(lo->y, shift));
         *hi = make_uint2(recode4(hi->x, shift), recode4(hi->y, shift));
       }
     }
+    if (h + warps < items) load(h + warps);
     if (lane == 0) *scale = static_cast<uint8_t>(now);
   }
 }
