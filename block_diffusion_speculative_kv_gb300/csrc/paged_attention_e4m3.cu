@@ -32,6 +32,10 @@ namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull, kMaxLimitNs = 60000000000ull;
 
+// How far the references of a row's weights may lag behind their maxima (base-2 units):
+// weights up to 2^14 fit fp16, and a reference that lags loses nothing below.
+constexpr float kLag = 14.f;
+
 struct PagedE4M3Params : PagedAttnParams {
   const uint8_t *k_scale, *v_scale;
 };
@@ -55,12 +59,6 @@ __device__ __forceinline__ uint32_t half2_hi(uint32_t codes) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t h;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
-  return h;
-}
-// The same, at most the largest finite number.
-__device__ __forceinline__ uint32_t pack_f16_finite(float lo, float hi) {
-  uint32_t h;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
   return h;
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -320,7 +318,7 @@ paged_attn_small_e4m3_kernel(const __grid_constant__ PagedE4M3Maps maps, const P
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           mx[nt][h] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          raise |= mx[nt][h] > m[nt][h] + kLazy || mx[nt][h] - m[nt][h] + b > r[nt][h] + kLazy;
+          raise |= mx[nt][h] > m[nt][h] + kLag || mx[nt][h] - m[nt][h] + b > r[nt][h] + kLag;
         }
       }
       if (__any_sync(0xffffffffu, raise)) {
@@ -869,7 +867,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
             const uint64_t v0 = dv + s * (S::kTileV >> 4);
 #pragma unroll
             for (int j = 4 * h; j < 4 * h + 4; ++j)
-              ptx::mma_bf16_ta(tbase_o + 128 * x, tbase + 128 * x + j * 8,
+              ptx::mma_bf16_ta(tbase_o + 128 * x, tbase + 128 * x + 64 * h + 8 * (j & 3),
                                v0 + (j % (S::kKeys / 16)) * (2048 >> 4), idesc_pv, (i > 0 || j > 0) ? 1u : 0u);
             if (h == 1) ptx::mma_commit(&pv_done[x]);
             if ((kPer == 2 || h == 1) && (nt == 1 || x == 1)) ptx::mma_commit(&c_empty[s]);
@@ -1085,9 +1083,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
           mx = fmaxf(mx, top[g]);
           mr = fmaxf(mr, (top[g] - m) + sc.y);               // (NaN where nothing has been seen)
         }
-        const bool raise = mx > m + kLazy || mr > r + kLazy;
-        // Both have read their scores when they have met: P may go over them.
-        ptx::tc_fence_before();
+        const bool raise = mx > m + kLag || mr > r + kLag;
         if (ptx::named_bar_or(pair, 64, raise || !ok)) {     // (rare)
           const float other = swap(ok ? mx : CUDART_NAN_F);
           ok = all(ok && !(other != other));
@@ -1098,7 +1094,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
           for (int g = 0; g < 4; ++g) mr = fmaxf(mr, (top[g] - base) + scale[g].y);
           mr = fmaxf(mr, swap(mr));
           float f = 1.f;
-          if (base > m + kLazy || mr > r + (m - base) + kLazy) {
+          if (base > m + kLag || mr > r + (m - base) + kLag) {
             const float was = m - base + r, r2 = fmaxf(was, mr);
             f = ex2(was - r2);
             l *= ex2(m - base);
@@ -1139,27 +1135,24 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
           }
         }
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float pk[16];                                      // (two fp16 each)
+        for (int g = 0; g < 4; ++g) {                        // P over the half's own scores
+          const float2 sc = scale[g];
+          // 2^-60 of the largest weight is as good as none: l keeps its share
+          const float d = none ? 0.f : fmaxf(sc.y - r, -60.f), add = none || far ? d : d - m;
+          const float f1 = far ? 1.f : factor(sc.x);
+          const float2 f2 = make_float2(f1, f1), a2 = make_float2(add, add);
+          float2 rs = make_float2(0.f, 0.f);
+          uint32_t pk[8];
 #pragma unroll
-          for (int g = 2 * b; g < 2 * b + 2; ++g) {
-            const float2 sc = scale[g];
-            // 2^-60 of the largest weight is as good as none: l keeps its share
-            const float d = none ? 0.f : fmaxf(sc.y - r, -60.f), add = none || far ? d : d - m;
-            const float f1 = far ? 1.f : factor(sc.x);
-            const float2 f2 = make_float2(f1, f1), a2 = make_float2(add, add);
-            float2 rs = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 y = __ffma2_rn(make_float2(__uint_as_float(u[b][16 * (g & 1) + 2 * j]),
-                                                      __uint_as_float(u[b][16 * (g & 1) + 2 * j + 1])), f2, a2);
-              const float2 w = make_float2(ex2(y.x), ex2(y.y));
-              rs = __fadd2_rn(rs, w);
-              pk[8 * (g & 1) + j] = __uint_as_float(pack_f16_finite(w.x, w.y));
-            }
-            l = fmaf(rs.x + rs.y, ex2(-d), l);
+          for (int j = 0; j < 8; ++j) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(u[g >> 1][16 * (g & 1) + 2 * j]),
+                                                    __uint_as_float(u[g >> 1][16 * (g & 1) + 2 * j + 1])), f2, a2);
+            const float2 w = make_float2(ex2(y.x), ex2(y.y));
+            rs = __fadd2_rn(rs, w);
+            pk[j] = pack_f16(w.x, w.y);
           }
-          ptx::tmem_st_32x16(aS + 32 * h + 16 * b, pk);
+          l = fmaf(rs.x + rs.y, ex2(-d), l);
+          ptx::tmem_st_32x8(aS + 64 * h + 8 * g, pk);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
