@@ -1449,9 +1449,22 @@ dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_
   p.k_scale = pages->k_scale;
   p.v_scale = pages->v_scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // The tile by the query rows of the largest request and KV head (8 KV heads of 128; tiles of
+  // 8 / 16 / 64 / 256 rows, us):
+  //   32 requests over 4096 slots:  8 rows 56 / 68 / 85 / 102, 16 rows 93 / 72 / 86 / 102,
+  //     24 rows 133 / 123 / 88 / 103, 64 rows 323 / 228 / 87 / 104, 80 rows - / - / 152 / 120;
+  //   1 request over 8192:  8 rows 21 / 24 / 29 / 29, 16 rows 21 / 28 / 29 / 29,
+  //     32 rows 23 / 29 / 30 / 30, 64 rows 33 / 31 / 32 / 31, 128 rows - / - / 33 / 33.
+  // Many slots take the smallest tile that holds the rows: theirs are read once.  Few are
+  // joined from many parts, quickest where the rows are spread over several small tiles:
+  //   16 rows: 1 x 2048 15 / 19 / 23 / -, 4 x 2048 19 / 22 / 25 / -, 2 x 16384 34 / 36 / 38 / -,
+  //     4 x 16384 50 / 45 / 53 / -;
+  //   32 rows: 4 x 2048 25 / 25 / 26 / -, 2 x 16384 50 / 44 / 38 / -.
+  // The lengths are on the device; the page table's width bounds them.
   const long long rows = (long long)max_rows * p.heads.G;
+  const bool few = (((long long)n_req * pages->n_kv * pages->table_ld) << p.pv.page_shift) <= 1 << 17;
   dflash_status e;
-  if (rows <= 8)
+  if (rows <= (few ? 32 : 8))
     e = hd == 128 ? launch_small<128, 1>(p, *pages, st) : launch_small<64, 1>(p, *pages, st);
   else if (rows <= 16)
     e = hd == 128 ? launch_small<128, 2>(p, *pages, st) : launch_small<64, 2>(p, *pages, st);

@@ -30,6 +30,7 @@ from oracle import quant as oq
 from test_gpu_paged import BF, CASES, DEV, F32, THETA, _f64, _i, _paged, _t, _tree_mask
 
 pytestmark = pytest.mark.gpu
+WIDE = 1 << 17         # slots of a page table that may hold long requests
 
 
 def _u8(a):
@@ -197,7 +198,10 @@ def _attend(d, ws=None, out=None, max_rows=None, stream=None):
     out = torch.full_like(d["q"], 7.0) if out is None else out
     ws = _ws(d["n_q"], d["n_kv"], d["hd"]) if ws is None else ws
     mask = None if d["mask"] is None else torch.as_tensor(d["mask"].view(np.int32), device=DEV)
-    pages = bd.PagesE4M3(*(_u8(d[x]) for x in ("ck", "cv", "sk", "sv")), _i(d["table"]))
+    table = _i(d["table"])
+    if d.get("wide"):                                # as a serving loop keeps it: for lengths to come
+        table = torch.nn.functional.pad(table, (0, WIDE // d["ck"].shape[2]), value=-1)
+    pages = bd.PagesE4M3(*(_u8(d[x]) for x in ("ck", "cv", "sk", "sv")), table)
     bd.paged_attention_e4m3(pages, d["q"], _i(d["off"]), _i(d["ctx"]), max(d["rows"]) if max_rows is None else max_rows,
                             out, ws, mask=mask, stream=stream)
     return out, ws
@@ -276,13 +280,28 @@ def test_attention_tiles_in_few_and_many_parts(rows, ctx, n_q, n_kv, hd, page, t
     test_attention((rows, ctx, n_q, n_kv, hd, page, tree))
 
 
+@pytest.mark.parametrize("case", [c for c in CASES if 8 < max(c[0]) * c[2] // c[3] <= 64] + [
+    ([4], [700], 32, 8, 128, 16, False), ([7, 0, 5], [300, 9, 0], 4, 2, 64, 64, True), ([3], [20000], 5, 1, 128, 32, False),
+    ([8, 2], [100, 3000], 8, 2, 128, 16, True)], ids=str)
+def test_attention_wide_table(case):
+    """Tables for many slots take other tiles than those that hold few."""
+    d = dict(_build(*case), wide=True)
+    out, ws = _attend(d)
+    again, _ = _attend(d, ws)
+    torch.cuda.synchronize()
+    assert bd.read_status(ws) == 0
+    _check(d, out)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("rows,tree", [([1, 2], False), ([4], False), ([16], False), ([70, 3], False), ([90], True),
                                        ([300], False)])
 @pytest.mark.parametrize("spread,q_size", [(8.0, 2.0 ** -14), (3.0, 1.0), (0.0, 3e4), (1.0, 1e-30), (20.0, 1e-6)])
-def test_attention_scales_far_apart(rows, tree, spread, q_size):
+def test_attention_scales_far_apart(rows, tree, spread, q_size, wide):
     """Blocks whose scales differ by many octaves, queries of any size: maxima that climb
     by little, by much and by more than a step may lag."""
-    d = _build(rows, [900, 400][:len(rows)], 8, 2, 128, 16, tree, seed=4, spread=spread)
+    d = dict(_build(rows, [900, 400][:len(rows)], 8, 2, 128, 16, tree, seed=4, spread=spread), wide=wide)
     d["q"] = (d["q"].float() * q_size).to(BF)
     if q_size > 1:
         d["sk"] = (d["sk"] - 14).astype(np.uint8)
@@ -292,12 +311,13 @@ def test_attention_scales_far_apart(rows, tree, spread, q_size):
     _check(d, out)
 
 
-@pytest.mark.parametrize("rows,tree", [([1, 1], False), ([3, 1], False), ([20, 3], False), ([20, 3], True),
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("rows,tree", [([1, 1], False), ([3, 1], False), ([6, 1], True), ([20, 3], False), ([20, 3], True),
                                        ([300, 40], False), ([140, 40], True)])
-def test_attention_ignores_what_no_row_may_see(rows, tree):
+def test_attention_ignores_what_no_row_may_see(rows, tree, wide):
     """NaN codes in slots past the requests' ends and in pages of nobody, any scales in
     blocks that hold no token."""
-    d = _build(rows, [70, 9], 8, 2, 128, 16, tree)
+    d = dict(_build(rows, [70, 9], 8, 2, 128, 16, tree), wide=wide)
     clean, _ = _attend(d)
     for byte in (0, 255):
         dirty = dict(d, ck=np.full_like(d["ck"], 127), cv=np.full_like(d["cv"], 255), sk=np.full_like(d["sk"], byte),
@@ -317,13 +337,14 @@ def test_attention_ignores_what_no_row_may_see(rows, tree):
 
 @pytest.mark.parametrize("rows,n_q", [([1] * 60, 14), ([2, 3, 0, 4] * 10, 8), ([7, 20] * 4, 6), ([40, 100], 8)])
 @pytest.mark.parametrize("bad", [127, 255])
-def test_attention_what_no_row_sees_changes_no_bit(rows, n_q, bad):
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_what_no_row_sees_changes_no_bit(rows, n_q, bad, wide):
     """NaN keys and values between others that no row's mask has a bit for; some rows see
     nothing new, some nothing at all."""
     for seed in range(3):
         rng = np.random.default_rng(seed)
         ctx = [int(c) * (i % 5 > 0) for i, c in enumerate(rng.integers(1, 60, size=len(rows)))]
-        d = _build(rows, ctx, n_q, 2, 128, 64, True, seed=seed)
+        d = dict(_build(rows, ctx, n_q, 2, 128, 64, True, seed=seed), wide=wide)
         m = (rng.integers(0, 1 << 32, size=d["mask"].shape) & rng.integers(0, 1 << 32, size=d["mask"].shape)).astype(np.uint32)
         m[rng.random(len(m)) < 0.4] = 0
         d["mask"] = m
@@ -341,11 +362,12 @@ def test_attention_what_no_row_sees_changes_no_bit(rows, n_q, bad):
         _check(d, got)
 
 
-@pytest.mark.parametrize("n,ctx,tree", [(3, 40, False), (20, 40, False), (20, 0, True), (200, 130, False),
-                                        (140, 100, True)])
-def test_attention_bad_value_reaches_only_the_rows_that_see_it(n, ctx, tree):
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("n,ctx,tree", [(3, 40, False), (7, 40, False), (14, 3, True), (20, 40, False), (20, 0, True),
+                                        (200, 130, False), (140, 100, True)])
+def test_attention_bad_value_reaches_only_the_rows_that_see_it(n, ctx, tree, wide):
     for hd in (64, 128):
-        d = _build([n], [ctx], 4, 2, hd, 16, tree, seed=3)
+        d = dict(_build([n], [ctx], 4, 2, hd, 16, tree, seed=3), wide=wide)
         clean, _ = _attend(d)
         j = n // 2                                   # the new token whose value is bad
         pg = int(d["table"][0, (ctx + j) // 16])
@@ -365,9 +387,10 @@ def test_attention_bad_value_reaches_only_the_rows_that_see_it(n, ctx, tree):
         assert torch.equal(o[~hit], clean.view(n, 4, hd)[~hit])
 
 
-@pytest.mark.parametrize("n,ctx", [(3, 40), (20, 40), (90, 40)])
-def test_attention_bad_key_reaches_the_rows_that_see_it(n, ctx):
-    d = _build([n], [ctx], 4, 2, 128, 16, False, seed=3)
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("n,ctx", [(3, 40), (7, 40), (20, 40), (90, 40)])
+def test_attention_bad_key_reaches_the_rows_that_see_it(n, ctx, wide):
+    d = dict(_build([n], [ctx], 4, 2, 128, 16, False, seed=3), wide=wide)
     clean, _ = _attend(d)
     j = n // 2
     ck = d["ck"].copy()
@@ -634,3 +657,93 @@ def test_verification_layer(kind):
     # share of its spread (1 for N(0, 1)): a quarter of a row's norm bounds both amply
     x, y = _f64(a)[live], _f64(b)[live]
     assert np.all(np.linalg.norm(x - y, axis=1) <= 0.25 * np.linalg.norm(x, axis=1))
+
+
+def test_captured_graphs_share_a_workspace():
+    """Decoding, a chain and a tree captured apart with one workspace, replayed in turn: each
+    call leaves the counters as it found them."""
+    cases = [_build([1, 1], [4000, 77], 32, 8, 128, 16, False), _build([16], [900], 32, 8, 128, 32, False),
+             _build([100], [2500], 32, 8, 128, 64, True), _build([5, 2], [600, 30], 8, 8, 128, 16, False)]
+    want = [_attend(d)[0] for d in cases]
+    ws = _ws(32, 8, 128)
+    args = []
+    for d in cases:
+        mask = None if d["mask"] is None else torch.as_tensor(d["mask"].view(np.int32), device=DEV)
+        pages = bd.PagesE4M3(*(_u8(d[x]) for x in ("ck", "cv", "sk", "sv")), _i(d["table"]))
+        args.append((pages, d["q"], _i(d["off"]), _i(d["ctx"]), max(d["rows"]), torch.empty_like(d["q"]), ws, mask))
+    torch.cuda.synchronize()
+    graphs = []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            bd.paged_attention_e4m3(*a)
+        graphs.append(g)
+    for _ in range(3):
+        for a in args:
+            a[5].fill_(7.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[5], w) for a, w in zip(args, want))
+    assert bd.read_status(ws) == 0
+
+
+def test_trace_hook_sees_every_launch():
+    d = _build([1, 2], [100, 40], 4, 2, 128, 16, False)
+    few, many = _build([40], [100], 4, 2, 128, 16, False), _build([70] * 40, [5] * 40, 8, 2, 64, 16, False)
+    seen = []
+    bd.set_trace_hook(lambda kernel, phase, stream: seen.append((kernel, phase)))
+    try:
+        for x in (d, few, many):
+            _attend(x)
+        pages = bd.PagesE4M3(*(_u8(d[x]) for x in ("ck", "cv", "sk", "sv")), _i(d["table"]))
+        k = _t(np.ones((3, 256)))
+        bd.paged_append_e4m3(pages, k, k, _i(d["off"]), _i(d["ctx"]))
+        x = torch.zeros(3, 100, device=DEV)
+        bd.logits_adjust(x, x, _i([0, 3]))
+        torch.cuda.synchronize()
+    finally:
+        bd.set_trace_hook(None)
+    names = [n for n, phase in seen if phase == 0]
+    assert names == ["paged_attn_small_e4m3", "paged_attn_tc_e4m3", "paged_join", "paged_attn_tc_e4m3",
+                     "paged_append_e4m3", "logits_adjust"]
+    assert [p for _, p in seen] == [0, 1] * len(names)
+
+
+@pytest.mark.parametrize("rows,ctx,n_q,page", [
+    ([64] * 20, 2000, 4, 64),        # 64-row tiles, joined by the last of their CTAs
+    ([64] * 12, 8000, 4, 16),        # 64-row tiles, joined by a kernel
+    ([1500], 2900, 16, 128),         # 256-row tiles, joined by the last of their CTAs
+    ([64] * 8, 8000, 16, 64),        # 256-row tiles, joined by a kernel
+])
+def test_wait_runs_out_then_recovers(rows, ctx, n_q, page):
+    """The waits between the tensor-core kernel's warps, made to run out by a limit of 1 us.
+    The new tokens' values are NaN, which the softmax looks up for its rows one by one, while
+    the CTA's other warps wait for it."""
+    d = _build(rows, [ctx + 50 * i for i in range(len(rows))], n_q, 4, 128, page, False, seed=5)
+    bad = d["cv"].copy()
+    for r, (n, c) in enumerate(zip(rows, d["ctx"])):
+        for t in range(c, c + n):
+            bad[d["table"][r, t // page], :, t % page] = 127
+    held = [_u8(d[x]) for x in ("ck", "cv", "sk", "sv")]
+    table = _i(d["table"])
+    finite, pages = bd.PagesE4M3(*held, table), bd.PagesE4M3(held[0], _u8(bad), *held[2:], table)
+    off, pos0, ws = _i(d["off"]), _i(d["ctx"]), _ws(n_q, 4, 128)
+
+    def run(pages):
+        out = torch.full_like(d["q"], float("inf"))
+        bd.paged_attention_e4m3(pages, d["q"], off, pos0, max(rows), out, ws)
+        torch.cuda.synchronize()
+        return out
+
+    usual, want = run(finite), run(pages)
+    assert bd.read_status(ws) == 0 and torch.isfinite(usual).all() and torch.isnan(want).all()   # (every row sees its own)
+    bd.workspace_set_wait_limit(ws, 1000)
+    run(pages)
+    assert bd.read_status(ws) == 5
+    # the context is intact, and after workspace_init the call is what it was
+    assert float((torch.ones(8, device=DEV) * 2).sum()) == 16.0
+    bd.workspace_init(ws)
+    for _ in range(2):
+        assert torch.equal(run(finite), usual) and torch.isnan(run(pages)).all()
+        assert bd.read_status(ws) == 0
