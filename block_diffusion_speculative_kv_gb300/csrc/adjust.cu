@@ -17,7 +17,9 @@
 // token, in a buffer of its own, and writes the 2 KB.  A history of 8192 tokens touches one
 // token in 35, one of almost every 128 neighbours: changed where they are, in the
 // registers of the lanes that have them, they made the warps' instructions the limit (480
-// bf16 rows of 151936: 159 us).
+// bf16 rows of 151936: 159 us).  Now those take 76 us (4.0 TB/s; a copy 46), 257 fp32 nodes of a
+// tree 56 (5.6 TB/s), where waiting for rows bounds them; 256 bf16 requests of one row
+// after 2048 tokens each 83, half of that the histories' instructions.
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -103,16 +105,16 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
   const float rho = p.repetition ? __ldg(p.repetition + req) : 1.f;
   const float phi = p.frequency ? __ldg(p.frequency + req) : 0.f;
   const float pi = p.presence ? __ldg(p.presence + req) : 0.f;
+  const int len = p.history ? min(max(__ldg(p.history_len + req), 0), p.history_ld) : 0;
+  const int prompt = p.prompt_len ? __ldg(p.prompt_len + req) : 0;
   const bool track = rho != 1.f || phi != 0.f || pi != 0.f;
   const bool change = track || p.n_bias > 0;
 
   // a token's place in the stretch, if it has one
   // (a token that is none may have one too, before the row's first or behind its last: it
   // changes what is not written)
-  auto place = [&](int t) {
-    const unsigned a = static_cast<unsigned>(t) - static_cast<unsigned>(base);
-    return a < C + V ? static_cast<int>(a) : -1;
-  };
+  auto from = [&](int t) { return static_cast<unsigned>(t) - static_cast<unsigned>(base); };
+  auto place = [&](int t) { return from(t) < C + V ? static_cast<int>(from(t)) : -1; };
   auto note = [&](int a) { atomicOr(&s.some[a >> 5], 1u << (a & 31)); };
   const int words = p.mask ? min(p.mask_ld, (n + 31) / 32) : 0;
   auto sees = [&](int i, int j) {                          // whether row i's path holds row j (of the request)
@@ -123,15 +125,13 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
   if (change) {
     for (int a = tid; a < (C + V) / 4; a += kThreads) {
       reinterpret_cast<uint4*>(s.count)[a] = make_uint4(0, 0, 0, 0);
-      reinterpret_cast<uint4*>(s.bias)[a] = make_uint4(0, 0, 0, 0);
+      if (p.n_bias > 0) reinterpret_cast<uint4*>(s.bias)[a] = make_uint4(0, 0, 0, 0);
     }
     if (tid < S::kWords) s.some[tid] = 0;
     for (int a = tid; a < kWarps * (kPart / 32); a += kThreads) (&s.path[0][0])[a] = 0;
     if (tid == 0) s.rows = 0;
     __syncthreads();
     if (track) {
-      const int len = p.history ? min(max(__ldg(p.history_len + req), 0), p.history_ld) : 0;
-      const int prompt = p.prompt_len ? __ldg(p.prompt_len + req) : 0;
       auto count = [&](int i, int t) {
         const int a = place(t);
         if (a < 0) return;
@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
           const int at = i + k * kThreads * 4;
+          if (at >= len) continue;
           if (at >= 0 && at + 4 <= len) {
             t[k] = __ldg(reinterpret_cast<const int4*>(h + at));
           } else {
@@ -157,6 +158,9 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
           const int at = i + k * kThreads * 4;
+          if (at >= len) break;
+          // (most have none in the stretch)
+          if (min(min(from(t[k].x), from(t[k].y)), min(from(t[k].z), from(t[k].w))) >= C + V) continue;
           count(at, t[k].x);
           count(at + 1, t[k].y);
           count(at + 2, t[k].z);
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
         for (int k = 0; k < kDeep; ++k) buffer[k * 32 + lane] = u[k];
         __syncwarp();
         auto fix = [&](int a, uint32_t more) {             // `more` times in the path
-          const uint32_t b = s.bias[a0 + a], count = s.count[a0 + a] + more;
+          const uint32_t b = p.n_bias > 0 ? s.bias[a0 + a] : 0u, count = s.count[a0 + a] + more;
           float y = to_f32(value[a]);
           if (b) y += __ldg(p.bias_val + (size_t)req * p.n_bias + b - 1);
           if (count) y = y > 0.f ? y / rho : y * rho;
@@ -341,9 +345,9 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
   }
 }
 
-// Measured, us, 32 x 15 bf16 rows and a tree of 257 fp32 ones, of 151936: stretches of 4 KB, 2 KB
-// of them to a warp at a time 78 and 62, 4 KB 89 and 62; of 8 KB 84 and 70 (histories are
-// counted half as often, but the stretch of the commonest tokens is a longer one); groups of 32
+// Measured, us, 32 x 15 bf16 rows and a tree of 257 fp32 ones, of 151936 (at a time when they
+// took 78 and 57): stretches of 4 KB, 2 KB of them to a warp at a time 78 and 62, 4 KB 89 and
+// 62; of 8 KB 84 and 70 (the stretch of the commonest tokens is a longer one); groups of 32
 // rows 77 and (4 KB to a warp) 57, of 8 rows 94 and 66.
 template <typename T, int C, int kDeep, int ROWS>
 void launch(const AdjustParams& p, cudaStream_t st) {
@@ -393,11 +397,22 @@ extern "C" dflash_status dflash_logits_adjust(
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     TraceScope ts("logits_adjust", st);
+    // A request's history is gone through for every stretch of each of its groups: requests of
+    // one row, as in decoding, and many of a few rows take long stretches.  Otherwise few
+    // CTAs' worth of rows take short ones.  Measured, us, rows of 151936 after 2048 tokens,
+    // long / few / many, bf16 and fp32:
+    //   256 x 1 83 / 261 / 140, 106 / 258 / 350;  16 x 1 7.3 / 17 / 10, 10 / 17 / 23;
+    //   1 x 1 6.3 / 6.9 / 7.0, 6.4 / 6.3 / 7.4;   64 x 2 29 / 70 / 38, 42 / 74 / 93;
+    //   32 x 4 23 / 38 / 22, 36 / 43 / 52;        1 x 4 12 / 7.3 / 7.3, 13 / 6.9 / 7.8;
+    //   1 x 16 13 / 7.7 / 16, 14 / 7.4 / 11;      8 x 5 14 / 17 / 12, 15 / 19 / 15;
+    //   32 x 8 46 / 73 / 36, 66 / 79 / 62;        1 x 257 45 / 67 / 33, 66 / 74 / 54.
     const bool few = (rows / 16 + n_req) * (long long)((vocab + 4095) / 4096) < 2 * num_sms();
+    const bool apart = rows <= n_req || (!few && rows <= (dtype == DFLASH_BF16 ? 2ll : 4ll) * n_req);
     if (dtype == DFLASH_BF16)
-      few ? launch<__nv_bfloat16, 1024, 4, 4>(p, st) : launch<__nv_bfloat16, 2048, 4, 16>(p, st);
+      apart ? launch<__nv_bfloat16, 4096, 2, 4>(p, st)
+            : few ? launch<__nv_bfloat16, 1024, 4, 4>(p, st) : launch<__nv_bfloat16, 2048, 4, 16>(p, st);
     else
-      few ? launch<float, 1024, 4, 4>(p, st) : launch<float, 1024, 8, 32>(p, st);
+      apart ? launch<float, 4096, 4, 4>(p, st) : few ? launch<float, 1024, 4, 4>(p, st) : launch<float, 1024, 8, 32>(p, st);
   }
   return check_launch("logits adjust");
 }
