@@ -271,3 +271,37 @@ def test_adjust_more_row_tokens_than_are_listed():
         out = _run(e)
         torch.cuda.synchronize()
         _check(e, out)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype,hist,tree,bias,grammar,pad", [
+    ([1] * 40, 20001, F32, [25 * i for i in range(40)], False, 3, True, 0),
+    ([1] * 40, 12296, BF, [5000 - 7 * i for i in range(40)], False, 30, True, 3),
+    ([2, 0, 3, 1] * 60, 9001, F32, [9] * 240, True, 2, False, 1),
+    ([0, 2, 1, 2] * 90, 8193, BF, [30] * 360, True, 0, True, 5),
+    ([900] + [0] * 1000, 3000, F32, [40] * 1001, True, 1, False, 0),        # more row tokens than are listed
+    ([0] * 1000 + [700], 4500, BF, [40] * 1001, False, 0, False, 1),
+])
+def test_adjust_requests_of_few_rows(rows, vocab, dtype, hist, tree, bias, grammar, pad):
+    test_adjust(rows, vocab, dtype, hist, tree, bias, grammar, pad)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_adjust_alone_and_in_a_batch_agree(dtype):
+    """However rows are shared out, bit for bit: a batch, a request, a row at a time."""
+    rows = [16] * 20 + [1] * 4
+    d = _case(rows, 20000, dtype, [300 + i for i in range(24)], False, 6, True, low=0.05)
+    out = _run(d)
+    torch.cuda.synchronize()
+    for r in (0, 7, 19, 23):
+        a, b = int(d["off"][r]), int(d["off"][r + 1])
+        one = dict(d, logits=d["logits"][a:b], off=np.array([0, b - a]), tok=d["tok"][a:b], allowed=d["allowed"][a:b],
+                   **{k: d[k][r:r + 1] for k in ("history", "hist", "prompt", "rep", "pres", "freq", "bias_tok", "bias_val")})
+        got = _run(one)
+        torch.cuda.synchronize()
+        assert torch.equal(got, out[a:b])
+        last = dict(one, logits=one["logits"][-1:], off=np.array([0, 1]), allowed=one["allowed"][-1:], tok=one["tok"][-1:],
+                    history=np.concatenate([one["history"][:, :one["hist"][0]], one["tok"][None, :-1]], 1),
+                    hist=one["hist"] + b - a - 1)
+        got = _run(last)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], out[b - 1])
