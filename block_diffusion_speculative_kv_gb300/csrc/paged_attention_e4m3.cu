@@ -97,6 +97,10 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // KV head.  Which key, column or element a lane holds is free as long as both operands
 // agree: a lane reads its codes as 16-byte pieces of a slot, and turns them into fragments
 // by conversion alone (and, for V, a byte permutation that pairs two slots).
+// HBM bounds it: 32 single tokens over 512 .. 8192 slots take 57 us, 5.5 TB/s of 6.8 (of the
+// 16-bit cache 100), the tail of shares and the chain of conversions, MMAs and exponentials
+// in each warp the rest.  CTAs an SM and stages, us: 2 and 6 64, 3 and 4 58, 4 and 3 60, 3 and
+// 3 57.  One request over 2048 slots takes 11 (launch, plan, two steps, join).
 constexpr int kStepS = 64, kStagesS = 3, kThreadsS = 128, kPerSmS = 3;
 
 template <int NT>
@@ -496,6 +500,17 @@ dflash_status launch_small(const PagedE4M3Params& p, const dflash_pages_e4m3& pa
 //   scales come with the loads, 8 + 8 to a step, and are applied as in the small tiles:
 //     a key block's to its 16 scores, a value block's in the exponent of its 16 weights,
 //     2^((s - m) + b - r), and the sum l takes each 16's sum back at 2^(r - b).
+// A row has two threads, each with half of a step's keys and of O's columns: their registers
+// hold 64 scores where one thread's would hold 128 (a prompt chunk of 2048 rows over 8192 slots
+// 289 against 386 us, and 314 with 216 registers to a thread), and the halves' P V start apart.
+// References lag: m and r move only when a weight would pass 2^kLag.  What bounds it is
+// the chain scores - softmax - P V of each group, as in the 16-bit cache's kernel, with
+// conversion beside it: the chunk takes 289 us (1.07 PFLOP/s; tensor pipe 46% busy, issue slots
+// 51%).  When it took 308, it took 288 without the conversion of V, 289 without exponentials,
+// 297 with one code of q, 302 with half of P V: no one of them is the limit.  32 chains of 16
+// rows take 95, 257 nodes over 8192 slots 65: beginnings and ends of tiles.  Slower were a thread to
+// a row with two jobs of 64 keys in flight and four converting warps (381 for the chunk, 98 for the
+// chains), and the same with K turned into fp16 too, so that all MMAs are of a kind (381, 103).
 constexpr int kStepT = 128;
 // Registers with NG = 2: the launch's 96 for each of five warpgroups, of which the four of
 // the softmax take 104 and the other one keeps 64.
