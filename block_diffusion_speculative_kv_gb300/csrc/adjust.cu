@@ -64,8 +64,8 @@ __device__ __forceinline__ int first_group(const AdjustParams& p, int r) {
 }
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowTokens = 512;   // of a request's rows in a stretch; more are looked up one by one
-constexpr int kPath = 64;         // a row's own tokens in a warp's part of a stretch, likewise
+constexpr int kRowTokens = 512;   // of a request's rows in a stretch; more are looked up again for each row
+constexpr int kPath = 64;         // a row's own tokens in a warp's part of a stretch; more for each element
 
 // kDeep: 16-byte pieces of a row that a lane has at a time.
 template <typename T, int C, int kDeep>
@@ -251,21 +251,20 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
       // places count from the part's first token from here on
       const int a0 = t0 - base, r0 = rank(a0), r1 = rank(a0 + kPart);
       // what the row's path has in this part
+      // (from the list, or, if there are more, from all rows' tokens: only a tree has so many)
       int own = 0;
-      if (listed > kRowTokens) {
-        own = kPath + 1;
-      } else {
-        for (int e0 = 0; e0 < listed; e0 += 32) {
-          const int e = e0 + lane, a = e < listed ? s.token[e] - a0 : -1;
-          const bool on = a >= 0 && a < kPart && sees(i, s.row[e]);
-          const uint32_t who = __ballot_sync(0xffffffffu, on);
-          const int at = own + __popc(who & ((1u << lane) - 1u));
-          if (on) {
-            atomicOr(&s.path[warp][a >> 5], 1u << (a & 31));
-            if (at < kPath) s.entry[warp][at] = static_cast<uint16_t>(a);
-          }
-          own += __popc(who);
+      const bool all = listed > kRowTokens;
+      for (int e0 = 0, of = all ? n : listed; e0 < of; e0 += 32) {
+        const int e = e0 + lane, j = all || e >= of ? e : s.row[e];
+        const int a = e >= of ? -1 : (all ? static_cast<int>(from(__ldg(p.tok + row0 + e))) : s.token[e]) - a0;
+        const bool on = a >= 0 && a < kPart && sees(i, j);
+        const uint32_t who = __ballot_sync(0xffffffffu, on);
+        const int at = own + __popc(who & ((1u << lane) - 1u));
+        if (on) {
+          atomicOr(&s.path[warp][a >> 5], 1u << (a & 31));
+          if (at < kPath) s.entry[warp][at] = static_cast<uint16_t>(a);
         }
+        own += __popc(who);
       }
       if (own > 0 || r1 > r0) {                            // (warp-uniform)
 #pragma unroll
