@@ -608,9 +608,10 @@ def _table(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str):
     """Pointer and width of a contiguous [n, width] table of dtype (None: none)."""
     if t is None:
         return None, 0
-    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != n or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 2 or shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} [{n}, entries]")
-    return (t.data_ptr(), t.shape[1]) if t.shape[1] else (None, 0)
+    return (t.data_ptr(), shape[1]) if shape[1] else (None, 0)
 
 
 def logits_adjust(logits: torch.Tensor, out: torch.Tensor, row_off: torch.Tensor,
@@ -629,12 +630,13 @@ def logits_adjust(logits: torch.Tensor, out: torch.Tensor, row_off: torch.Tensor
     prompt, and tok [rows] of the rows it sees: by mask [rows, words] (int32 view of the
     bits), or those up to itself.  bias_tok, bias_val [n_req, entries], allowed
     [rows, words] (int32 view of the bits).  vocab: the first columns alone."""
-    if logits.dim() != 2 or out.shape != logits.shape or out.dtype is not logits.dtype:
+    shape = logits.shape
+    if len(shape) != 2 or out.shape != shape or out.dtype is not logits.dtype:
         raise ValueError("logits and out: expected [rows, columns] of one type")
-    if row_off.numel() == 0:
-        raise ValueError("row_off: expected n_req + 1 entries")
-    rows, width = logits.shape
+    rows, width = shape
     n_req = row_off.numel() - 1
+    if n_req < 0:
+        raise ValueError("row_off: expected n_req + 1 entries")
     if vocab is None:
         vocab = width
     elif vocab > width:                       # (the library knows the rows' stride alone)
