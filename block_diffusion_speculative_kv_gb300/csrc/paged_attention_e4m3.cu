@@ -7,13 +7,13 @@
 //
 //   s_t = q . c_t 2^a / sqrt(hd),   out = sum_t 2^(s_t - m) 2^b d_t / sum_t 2^(s_t - m)
 //
-// (s in base-2 units).  Codes are exact in fp16, so both products run on fp16 tensor
-// cores with the codes as they are: the key's scale multiplies the fp32 score, the
-// value's goes into the exponent of the weight, 2^((s_t - m) + b - r).  m is the running
-// maximum of s_t and r that of (s_t - m) + b: the largest term of either sum is near 1
-// whatever the blocks' scales are, so weights keep fp16's 11 bits (and lose only what
-// is below 2^-24 of the largest).  A row of q is taken to fp16 at a power of two at which
-// its largest element is near 2^15: bf16's 8 bits are kept exactly down to 2^-32 of it.
+// (s in base-2 units).  Codes enter both products as they are, as fp16 (exact) or as e4m3:
+// the key's scale multiplies the fp32 score, the value's goes into the exponent of the
+// weight, 2^((s_t - m) + b - r).  m is the running maximum of s_t and r that of
+// (s_t - m) + b: the largest term of either sum is near 1 whatever the blocks' scales are,
+// so fp16 weights keep their 11 bits (and lose only what is below 2^-24 of the largest).
+// A row of q is scaled by a power of two of its own: to fp16, its largest element near
+// 2^15, which keeps bf16's 8 bits exactly down to 2^-32 of it; or to two e4m3 codes.
 //
 // The work is shared out as in paged_attention.h.
 #include <cmath>
