@@ -510,7 +510,9 @@ dflash_status launch_small(const PagedE4M3Params& p, const dflash_pages_e4m3& pa
 // 297 with one code of q, 302 with half of P V: no one of them is the limit.  32 chains of 16
 // rows take 95, 257 nodes over 8192 slots 65: beginnings and ends of tiles.  Slower were a thread to
 // a row with two jobs of 64 keys in flight and four converting warps (381 for the chunk, 98 for the
-// chains), and the same with K turned into fp16 too, so that all MMAs are of a kind (381, 103).
+// chains), the same with K turned into fp16 too, so that all MMAs are of a kind (381, 103), and
+// halves that take turns with scores of 64 keys of their own, m and r handed on without a
+// barrier (351, 108: MMAs 64 keys wide read q twice as often).
 constexpr int kStepT = 128;
 // Registers with NG = 2: the launch's 96 for each of five warpgroups, of which the four of
 // the softmax take 104 and the other one keeps 64.
