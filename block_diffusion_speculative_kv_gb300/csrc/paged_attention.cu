@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
       if ((lane & 3) == 0) sMl[warp * 16 + ra + 8 * h] = make_float2(m[h], l[h]);
     }
     __syncthreads();
-    paged_finish_small<HD, kRowsS, S::kLd, kThreadsS, GeoS>(p, c, pc, total, end, rho0, live, sO, sMl, smem, sLast);
+    paged_finish_small<HD, kRowsS, S::kLd, kThreadsS, S::kRing, GeoS>(p, c, pc, total, end, rho0, live, sO, sMl,
+                                                                      smem, sLast);
     __syncthreads();                                     // the ring is free again
   }
 }

@@ -454,7 +454,8 @@ paged_attn_small_e4m3_kernel(const __grid_constant__ PagedE4M3Maps maps, const P
         if (ra == 0) sMl[warp * S::kRows + row] = make_float2(m[nt][h], l[nt][h]);
       }
     __syncthreads();
-    paged_finish_small<HD, S::kRows, S::kLd, kThreadsS, Geo>(p, c, pc, total, end, rho0, live, sO, sMl, smem, sLast);
+    paged_finish_small<HD, S::kRows, S::kLd, kThreadsS, S::kRing, Geo>(p, c, pc, total, end, rho0, live, sO, sMl,
+                                                                       smem, sLast);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();                                     // the ring is free again
   }
