@@ -80,6 +80,12 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
   return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(min(b, 254u) << 23);
 }
 
+// 2^x of a row's r, -127 at least: ex2 alone would make zero of what is below 2^-126.
+__device__ __forceinline__ float ex2_low(float x) {
+  const bool low = x < -64.f;
+  return ex2(low ? x + 64.f : x) * (low ? 0x1p-64f : 1.f);
+}
+
 // A word's codes that are NaN, as 0xFF bytes.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   const uint32_t top = (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
@@ -445,7 +451,7 @@ paged_attn_small_e4m3_kernel(const __grid_constant__ PagedE4M3Maps maps, const P
         for (int x = 4; x < 32; x <<= 1) l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], x);
         const int row = 8 * nt + 2 * cq + h;
         if (row >= live) continue;
-        const float g = m[nt][h] == -CUDART_INF_F ? 1.f : ex2(r[nt][h]);
+        const float g = m[nt][h] == -CUDART_INF_F ? 1.f : ex2_low(r[nt][h]);
         float* dst = sO + (warp * S::kRows + row) * S::kLd + HD / 8 * ra;
 #pragma unroll
         for (int j = 0; j < kT; j += 2)
@@ -1188,7 +1194,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
       }
       // ---- the tile's rows ----  (O with m as its reference: times 2^r)
       if (!dead) l += swap(l);
-      const float own = m == -CUDART_INF_F ? 0.f : ex2(r);
+      const float own = m == -CUDART_INF_F ? 0.f : ex2_low(r);
       float M = m, L = l, fa = own, fb = 0.f;                // weights of the two groups' halves
       float* sB = reinterpret_cast<float*>(sQ);              // [128][HD], chunks of 4 swizzled
       if (NG == 2 && nt == 1) {

@@ -1,5 +1,6 @@
 """GPU parity of the 8-bit paged cache at the ends of its ranges: requests so long that a
-tile falls into a part for every CTA.  Tolerances as in test_gpu_paged_e4m3.py."""
+tile falls into a part for every CTA, and values of the smallest scale.  Tolerances as in
+test_gpu_paged_e4m3.py."""
 import numpy as np
 import pytest
 import torch
@@ -44,3 +45,37 @@ def test_attention_of_long_requests(rows, ctx, n_q, n_kv, hd, page, tree, wide):
     assert bd.read_status(ws) == 0
     _check(d, out)
     assert torch.equal(out, again)
+
+
+KERNELS = [([1], False, False), ([3, 1], False, True), ([16], False, True), ([20], True, False), ([64, 3], False, False),
+           ([100], True, False), ([128], False, False), ([300, 40], False, False)]
+
+
+@pytest.mark.parametrize("rows,tree,wide", KERNELS)
+@pytest.mark.parametrize("ctx", [70, 3000])
+def test_attention_where_every_value_is_nan(rows, tree, wide, ctx):
+    """As an append leaves values that are NaN or infinite throughout: their blocks have the
+    smallest scale.  Another KV head's outputs keep their bits."""
+    for hd in (64, 128):
+        d = dict(_build(rows, [ctx, 9][:len(rows)], 2, 2, hd, 16, tree), wide=wide)
+        clean, _ = _attend(d)
+        cv, sv = d["cv"].copy(), d["sv"].copy()
+        cv[:, 0], sv[:, 0] = 127, 0
+        got, ws = _attend(dict(d, cv=cv, sv=sv))
+        torch.cuda.synchronize()
+        assert bd.read_status(ws) == 0
+        assert torch.isnan(got[:, :hd]).all() and torch.equal(got[:, hd:], clean[:, hd:])
+
+
+@pytest.mark.parametrize("rows,tree,wide", KERNELS)
+@pytest.mark.parametrize("ctx", [70, 3000])
+def test_attention_of_the_smallest_values(rows, tree, wide, ctx):
+    """All blocks at the smallest scale, 2^-127: outputs are normal numbers of bf16."""
+    for hd in (64, 128):
+        d = dict(_build(rows, [ctx, 9][:len(rows)], 4, 2, hd, 16, tree), wide=wide)
+        d["cv"] = np.maximum(d["cv"] & 127, 64)              # 2 .. 448: no sum below 2 (2^-126)
+        d["sv"] = np.zeros_like(d["sv"])
+        out, ws = _attend(d)
+        torch.cuda.synchronize()
+        assert bd.read_status(ws) == 0
+        _check(dict(d, sv=np.full_like(d["sv"], 127)), out.double() * 2.0 ** 127)
