@@ -1194,8 +1194,12 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
       }
       // ---- the tile's rows ----  (O with m as its reference: times 2^r)
       if (!dead) l += swap(l);
-      const float own = m == -CUDART_INF_F ? 0.f : ex2_low(r);
+      // A weight may vanish beside another; NaN times it stays NaN.  Only what saw no key
+      // counts for nothing.
+      const bool some = m != -CUDART_INF_F;
+      const float own = some ? ex2_low(r) : 0.f;
       float M = m, L = l, fa = own, fb = 0.f;                // weights of the two groups' halves
+      bool both = false;                                     // the other group's half counts
       float* sB = reinterpret_cast<float*>(sQ);              // [128][HD], chunks of 4 swizzled
       if (NG == 2 && nt == 1) {
         if (x == 1 && !dead) {
@@ -1217,7 +1221,8 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
         ptx::named_bar_sync(everyone, 2 * GT * NG);
         if (x == 0 && !dead) {
           const float2 ml = sMl[row];
-          if (ml.y != 0.f) {
+          both = ml.y != 0.f;
+          if (both) {
             M = fmaxf(m, ml.x);
             const float f = l != 0.f ? ex2(m - M) : 0.f;
             fa = f * own;
@@ -1274,8 +1279,8 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
           ptx::tmem_wait_ld();
           float o[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = fa == 0.f ? 0.f : __uint_as_float(u[j]) * fa;
-          if (fb != 0.f) {
+          for (int j = 0; j < 32; ++j) o[j] = some ? __uint_as_float(u[j]) * fa : 0.f;
+          if (both) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float4 v = *reinterpret_cast<const float4*>(sB + row * HD + 4 * ((kCols / 4 * h + 8 * b + j) ^ (row & 7)));

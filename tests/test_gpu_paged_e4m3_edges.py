@@ -1,11 +1,12 @@
 """GPU parity of the 8-bit paged cache at the ends of its ranges: requests so long that a
-tile falls into a part for every CTA, and values of the smallest scale.  Tolerances as in
-test_gpu_paged_e4m3.py."""
+tile falls into a part for every CTA, values of the smallest scale, and NaN whose weights
+vanish.  Tolerances as in test_gpu_paged_e4m3.py."""
 import numpy as np
 import pytest
 import torch
 
 from block_diffusion_speculative_kv_gb300 import binding as bd
+from oracle import quant as oq
 from test_gpu_paged_e4m3 import _attend, _build, _check
 
 pytestmark = pytest.mark.gpu
@@ -65,6 +66,37 @@ def test_attention_where_every_value_is_nan(rows, tree, wide, ctx):
         torch.cuda.synchronize()
         assert bd.read_status(ws) == 0
         assert torch.isnan(got[:, :hd]).all() and torch.equal(got[:, hd:], clean[:, hd:])
+
+
+@pytest.mark.parametrize("rows,tree,wide", KERNELS)
+@pytest.mark.parametrize("ctx", [300, 3000])
+def test_attention_nan_under_the_smallest_weight(rows, tree, wide, ctx):
+    """A NaN value whose weight vanishes beside another key's (2^-456 of it) reaches the rows
+    that see it, whichever part of the work it falls into."""
+    hd = 128
+    d = dict(_build(rows, [ctx] * len(rows), 2, 1, hd, 16, tree, spread=0.0), wide=wide)
+    d["ck"] = np.zeros_like(d["ck"])
+    d["sk"] = np.full_like(d["sk"], 127)
+    q = torch.zeros_like(d["q"])
+    q.view(-1, 2, hd)[:, :, 0] = 8.0
+    for top in (ctx - 1, ctx - 130, 3):
+        e = dict(d, q=q, ck=d["ck"].copy(), cv=d["cv"].copy())
+        at = [(r, e["table"][r, top // 16], top % 16) for r in range(len(rows))]
+        for r, pg, slot in at:
+            e["ck"][pg, 0, slot, 0] = 126                    # 448
+        for col, t in ((7, 5), (40, ctx - 140), (99, ctx - 20)):
+            for r in range(len(rows)):
+                e["cv"][e["table"][r, t // 16], 0, t % 16, col] = 127
+        out, ws = _attend(e)
+        torch.cuda.synchronize()
+        assert bd.read_status(ws) == 0
+        o = out.view(-1, 2, hd).double().cpu().numpy()
+        bad = np.zeros(hd, dtype=bool)
+        bad[[7, 40, 99]] = True
+        assert np.isnan(o[:, :, bad]).all()
+        for r, pg, slot in at:                               # elsewhere that key's value, exact in bf16
+            want = oq.held(e["cv"], e["sv"])[pg, 0, slot][~bad]
+            assert (o[e["off"][r]:e["off"][r + 1]][:, :, ~bad] == want).all()
 
 
 @pytest.mark.parametrize("rows,tree,wide", KERNELS)
