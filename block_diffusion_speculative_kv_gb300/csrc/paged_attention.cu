@@ -1056,6 +1056,7 @@ paged_attn_tc_kernel(const __grid_constant__ PagedTcMaps maps, const PagedAttnPa
 template <int HD, int NG>
 dflash_status launch_tc(PagedAttnParams p, const dflash_pages& pages, cudaStream_t st) {
   using S = Tc<HD, NG>;
+  static_assert(S::kPerSm * NG <= kMostCtas && S::kPerSm * S::kRows <= 256, "the workspace's counters and slots");
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);

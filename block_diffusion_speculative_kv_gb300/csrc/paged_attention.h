@@ -535,14 +535,17 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttnParams p
 struct PagedWs {
   size_t arrive, cut, ml, o, bytes;
 };
-// Every kernel: per_sm CTAs an SM at most, one counter to a CTA (two where it has an SM
-// alone), and for each SM two slots of 256 rows (or fewer rows to more CTAs).
-inline PagedWs paged_ws(int sms, int head_dim, int per_sm = 2) {
+// Every kernel: kMostCtas CTAs an SM at most, one counter to a CTA (two where it has an SM
+// alone), and for each SM two slots of 256 rows (or fewer rows to more CTAs).  One layout
+// for all kernels and head sizes, so that calls which share a workspace find the counters
+// where the others left zeros.
+constexpr int kMostCtas = 3;
+inline PagedWs paged_ws(int sms, int head_dim) {
   PagedWs w;
   const size_t rows = (size_t)sms * 2 * 256;
   w.arrive = 256;
-  w.cut = w.arrive + align_up((size_t)sms * per_sm * sizeof(int), 256);
-  w.ml = w.cut + align_up((size_t)sms * per_sm * sizeof(PagedCut), 256);
+  w.cut = w.arrive + align_up((size_t)sms * kMostCtas * sizeof(int), 256);
+  w.ml = w.cut + align_up((size_t)sms * kMostCtas * sizeof(PagedCut), 256);
   w.o = w.ml + align_up(rows * sizeof(float2), 256);
   w.bytes = w.o + rows * head_dim * sizeof(float);
   return w;

@@ -470,6 +470,7 @@ paged_attn_small_e4m3_kernel(const __grid_constant__ PagedE4M3Maps maps, const P
 template <int HD, int NT>
 dflash_status launch_small(const PagedE4M3Params& p, const dflash_pages_e4m3& pages, cudaStream_t st) {
   using S = Small<HD, NT>;
+  static_assert(kPerSmS <= kMostCtas && kPerSmS * S::kRows <= 256, "the workspace's counters and slots");
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1386,6 +1387,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
 template <int HD, int NG>
 dflash_status launch_tc(PagedE4M3Params p, const dflash_pages_e4m3& pages, cudaStream_t st) {
   using S = Tc<HD, NG>;
+  static_assert(S::kPerSm * NG <= kMostCtas && S::kPerSm * S::kRows <= 256, "the workspace's counters and slots");
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1424,7 +1426,7 @@ extern "C" {
 
 size_t dflash_paged_attention_e4m3_workspace_bytes(int n_q, int n_kv, int head_dim) {
   if (n_kv < 1 || n_q < n_kv || n_q % n_kv || (head_dim != 64 && head_dim != 128)) return 0;
-  return paged_ws(num_sms(), head_dim, kPerSmS).bytes;
+  return paged_ws(num_sms(), head_dim).bytes;
 }
 
 dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_req, int n_rows,
@@ -1450,7 +1452,7 @@ dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_
   DFL_REQUIRE(row_off && pos0 && q && out, "paged attention e4m3: null pointer argument");
   DFL_REQUIRE(((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0,
               "paged attention e4m3: q and out must be 16-byte aligned");
-  const PagedWs w = paged_ws(num_sms(), hd, kPerSmS);
+  const PagedWs w = paged_ws(num_sms(), hd);
   if (!ws || ws_bytes < w.bytes)
     return set_error(DFLASH_ERR_WORKSPACE, "paged attention e4m3 workspace needs %zu bytes, got %zu",
                      w.bytes, ws_bytes);

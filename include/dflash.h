@@ -536,7 +536,9 @@ dflash_status dflash_paged_append(const dflash_pages* pages, int n_req, int n_ro
  * dflash_paged_attention_workspace_bytes bytes, zeroed once
  * (dflash_workspace_init) before the first call; every call leaves its counters
  * at zero, unless the status word reads DFLASH_ERR_TIMEOUT: then the workspace
- * has to be zeroed again.  Calls sharing a workspace must not overlap. */
+ * has to be zeroed again.  Calls sharing a workspace must not overlap; it may
+ * serve calls of any heads, of dflash_paged_attention_e4m3 too, if it has the
+ * bytes that each asks for. */
 size_t dflash_paged_attention_workspace_bytes(int n_q, int n_kv, int head_dim);
 dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n_rows, int n_q,
                                      const int32_t* row_off, const int32_t* pos0, int max_rows,

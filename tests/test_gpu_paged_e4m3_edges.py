@@ -1,12 +1,13 @@
 """GPU parity of the 8-bit paged cache at the ends of its ranges: requests so long that a
-tile falls into a part for every CTA, values of the smallest scale, and NaN whose weights
-vanish.  Tolerances as in test_gpu_paged_e4m3.py."""
+tile falls into a part for every CTA, values of the smallest scale, NaN whose weights
+vanish; and a workspace that calls of both caches share.  Tolerances as in test_gpu_paged_e4m3.py."""
 import numpy as np
 import pytest
 import torch
 
 from block_diffusion_speculative_kv_gb300 import binding as bd
 from oracle import quant as oq
+from test_gpu_paged import BF, DEV, _i
 from test_gpu_paged_e4m3 import _attend, _build, _check
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +112,36 @@ def test_attention_of_the_smallest_values(rows, tree, wide, ctx):
         torch.cuda.synchronize()
         assert bd.read_status(ws) == 0
         _check(dict(d, sv=np.full_like(d["sv"], 127)), out.double() * 2.0 ** 127)
+
+
+def test_one_workspace_serves_both_caches():
+    """Calls over the 16-bit and the 8-bit cache, of every kernel, in turn on one workspace:
+    each leaves it as the others need it."""
+    n_q, n_kv, hd, page = 8, 2, 128, 16
+    shapes = [([100], [2500], True), ([1] * 40, [4000 + 61 * i for i in range(40)], False), ([16], [6000], False),
+              ([3], [20000], False), ([300, 40], [900, 5000], False), ([8, 4], [9000, 30], False)]
+    eight = [_build(rows, ctx, n_q, n_kv, hd, page, tree) for rows, ctx, tree in shapes]
+    size = max(bd.paged_attention_workspace_bytes(n_q, n_kv, hd), bd.paged_attention_e4m3_workspace_bytes(n_q, n_kv, hd))
+    assert size > 0
+
+    def sixteen(d, ws):
+        n_pages = d["ck"].shape[0]
+        gen = torch.Generator(device=DEV).manual_seed(n_pages)
+        k, v = (torch.randn(n_pages, n_kv, page, hd, generator=gen, device=DEV).to(BF) for _ in range(2))
+        mask = None if d["mask"] is None else torch.as_tensor(d["mask"].view(np.int32), device=DEV)
+        out = torch.full_like(d["q"], 7.0)
+        bd.paged_attention(bd.Pages(k, v, _i(d["table"])), d["q"], _i(d["off"]), _i(d["ctx"]), max(d["rows"]), out, ws,
+                           mask=mask)
+        return out
+
+    def fresh():
+        return torch.zeros(size, dtype=torch.uint8, device=DEV)
+
+    want = [(sixteen(d, fresh()), _attend(d, fresh())[0]) for d in eight]
+    ws = fresh()
+    for i, a in enumerate(eight):
+        for j, b in enumerate(eight):
+            x, y = sixteen(a, ws), _attend(b, ws)[0]
+            torch.cuda.synchronize()
+            assert torch.equal(x, want[i][0]) and torch.equal(y, want[j][1]), (i, j)
+    assert bd.read_status(ws) == 0
