@@ -20,8 +20,10 @@ inline int log2_int(int v) {
   return s;
 }
 
-// Slots of a page that share a scale (8-bit pools).
+// Slots of a page that share a scale (8-bit pools), and the largest scale's byte (255, which
+// stands for no number, is read as it).
 constexpr int kScaleBlock = 16;
+constexpr int kTopScale = 254;
 
 // Page of a slot of request r, or -1 where there is none.
 __device__ __forceinline__ int page_of(const PagedView& pv, int r, int slot) {

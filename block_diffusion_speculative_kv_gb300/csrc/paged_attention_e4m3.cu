@@ -75,9 +75,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t h) {
   return t;
 }
 
-// 2^(b - 127) of a scale's byte (255, which no append writes, as 254).
+// 2^(b - 127) of a scale's byte, and b - 127.
 __device__ __forceinline__ float scale_of(uint32_t b) {
-  return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(min(b, 254u) << 23);
+  return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(min(b, static_cast<uint32_t>(kTopScale)) << 23);
+}
+__device__ __forceinline__ float exponent_of(uint32_t b) {
+  return static_cast<float>(min(static_cast<int>(b), kTopScale) - 127);
 }
 
 // 2^x of a row's r, -127 at least: ex2 alone would make zero of what is below 2^-126.
@@ -300,7 +303,7 @@ paged_attn_small_e4m3_kernel(const __grid_constant__ PagedE4M3Maps maps, const P
       }
       const bool all = t0 + 16 <= plain;                 // warp-uniform
       const float ks = scale_of(scales & 0xFFu);
-      const float b = static_cast<float>(static_cast<int>(scales >> 8)) - 127.f;
+      const float b = exponent_of(scales >> 8);
       uint32_t seen = 0;                                 // bit 4 nt + e of st[nt][e] (where not all are)
       float mx[NT][2];
       bool raise = false;
@@ -796,8 +799,7 @@ paged_attn_tc_e4m3_kernel(const __grid_constant__ TcMaps maps, const PagedE4M3Pa
             ok = all(wait(&k_empty[s], (ik / S::kK & 1u) ^ 1u));
             if (!ok) break;
             if (lane < 8)
-              sScale[(ik / kPer & 7) * 8 + lane] =
-                  make_float2(scale_of(now.a), static_cast<float>(static_cast<int>(now.b)) - 127.f);
+              sScale[(ik / kPer & 7) * 8 + lane] = make_float2(scale_of(now.a), exponent_of(now.b));
             __syncwarp();
           }
           ok = fill(k_full, k_empty, ik, S::kK, sK, &maps.k, part);

@@ -401,8 +401,10 @@ __device__ __forceinline__ int scale_for(float top) {
   const uint32_t b = __float_as_uint(top);
   return max(static_cast<int>(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0), 0);
 }
-// 2^(127 - b) for a biased exponent 0 <= b <= 253.
-__device__ __forceinline__ float unscale(int b) { return __uint_as_float(static_cast<uint32_t>(254 - b) << 23); }
+// 2^(127 - b) for a biased exponent 0 <= b <= 254 (2^-127 is subnormal).
+__device__ __forceinline__ float unscale(int b) {
+  return __uint_as_float(b < kTopScale ? static_cast<uint32_t>(254 - b) << 23 : 0x00400000u);
+}
 
 __device__ __forceinline__ uint32_t codes4(float2 a, float2 b) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) |
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(kThreadsE4M3, 3) paged_append_e4m3_kernel(cons
     const int g = is_k ? h : h - p.pv.n_kv;
     const long long row = pool_row(p.pv, page, g, slot0);
     uint8_t* scale = (is_k ? p.k_scale : p.v_scale) + row / kScaleBlock;
-    const int was = old > 0 ? min(static_cast<int>(*scale), 253) : 0;
+    const int was = old > 0 ? min(static_cast<int>(*scale), kTopScale) : 0;
     float2 x[kPasses][4], y[kPasses][4];
     float top = 0.f;                                       // (a maximum passes over NaN)
 #pragma unroll

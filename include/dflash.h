@@ -550,8 +550,9 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
  * elements as e4m3 codes (one sign, four exponent, three fraction bits; largest
  * 448, 0x7F and 0xFF NaN, no infinities), and one scale for every 16 slots (a
  * block) of a KV head, keys and values apart.  A scale is a power of two kept as
- * its biased exponent: byte b stands for 2^(b - 127), and an element for its
- * code's value times its block's scale.
+ * its biased exponent: byte b stands for 2^(b - 127) (255, which no append
+ * writes, is read as 254), and an element for its code's value times its block's
+ * scale.
  *   k, v              uint8 [n_pages][n_kv][page_size][head_dim] (device),
  *                     16-byte aligned
  *   k_scale, v_scale  uint8 [n_pages][n_kv][page_size / 16] (device)

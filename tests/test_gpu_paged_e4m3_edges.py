@@ -1,14 +1,14 @@
 """GPU parity of the 8-bit paged cache at the ends of its ranges: requests so long that a
 tile falls into a part for every CTA, values of the smallest scale, NaN whose weights
-vanish; and a workspace that calls of both caches share.  Tolerances as in test_gpu_paged_e4m3.py."""
+vanish, the largest scales; and a workspace that calls of both caches share.  Tolerances as in test_gpu_paged_e4m3.py."""
 import numpy as np
 import pytest
 import torch
 
 from block_diffusion_speculative_kv_gb300 import binding as bd
 from oracle import quant as oq
-from test_gpu_paged import BF, DEV, _i
-from test_gpu_paged_e4m3 import _attend, _build, _check
+from test_gpu_paged import BF, DEV, F32, _f64, _i, _t
+from test_gpu_paged_e4m3 import _attend, _build, _check, _pool, _u8
 
 pytestmark = pytest.mark.gpu
 
@@ -145,3 +145,41 @@ def test_one_workspace_serves_both_caches():
             torch.cuda.synchronize()
             assert torch.equal(x, want[i][0]) and torch.equal(y, want[j][1]), (i, j)
     assert bd.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("byte", [253, 254, 255])
+def test_append_beside_the_largest_scales(byte):
+    """Earlier tokens at the largest scales keep their codes and their scale; 255 is read as
+    254."""
+    rng = np.random.default_rng(6)
+    n_kv, hd = 2, 64
+    table = np.array([[1, 0]], dtype=np.int32)
+    x = _t(rng.normal(size=(20, n_kv * hd)) * 5e37, F32)
+    for rows, p0 in ((2, 5), (20, 3), (1, 15)):
+        ck, _ = _pool(rng, 2, n_kv, 16, hd)
+        sk = np.full((2, n_kv, 1), byte, dtype=np.uint8)
+        got = [_u8(a) for a in (ck, ck, sk, sk)]
+        bd.paged_append_e4m3(bd.PagesE4M3(*got, _i(table)), x[:rows], x[:rows], _i([0, rows]), _i([p0]))
+        torch.cuda.synchronize()
+        x64 = _f64(x[:rows]).reshape(rows, n_kv, hd)
+        ref = oq.append(ck, ck, np.minimum(sk, 254), np.minimum(sk, 254), table, [0, rows], [p0], x64, x64, 0.0)
+        for g, r in zip(got, ref):
+            g = g.cpu().numpy()
+            assert np.array_equal(g if g.ndim == 4 else np.minimum(g, 254), r)
+
+
+@pytest.mark.parametrize("rows,tree,wide", KERNELS)
+def test_attention_reads_scale_255_as_254(rows, tree, wide):
+    for hd in (64, 128):
+        d = dict(_build(rows, [300, 9][:len(rows)], 4, 2, hd, 16, tree), wide=wide)
+        d["cv"] = d["cv"] & 129                              # 2^-9 at most: values of 2^118
+        for x in ("sv", "sk"):
+            out = []
+            for byte in (254, 255):
+                o, ws = _attend(dict(d, **{x: np.full_like(d[x], byte)}))
+                torch.cuda.synchronize()
+                assert bd.read_status(ws) == 0
+                out.append(o)
+            # sums of weights up to 2^14 times 309 such values may pass 2^128, in both alike
+            assert torch.isfinite(out[0]).any() and torch.equal(*(o.nan_to_num(0.0) for o in out))
+            assert torch.equal(*(torch.isnan(o) for o in out))
