@@ -1,6 +1,7 @@
 """GPU parity of the 8-bit paged cache at the ends of its ranges: requests so long that a
 tile falls into a part for every CTA, values of the smallest scale, NaN whose weights
-vanish, the largest scales; and a workspace that calls of both caches share.  Tolerances as in test_gpu_paged_e4m3.py."""
+vanish, the largest scales, scores far past fp32's steps; and a workspace that calls of both
+caches share.  Tolerances as in test_gpu_paged_e4m3.py."""
 import numpy as np
 import pytest
 import torch
@@ -183,3 +184,37 @@ def test_attention_reads_scale_255_as_254(rows, tree, wide):
             # sums of weights up to 2^14 times 309 such values may pass 2^128, in both alike
             assert torch.isfinite(out[0]).any() and torch.equal(*(o.nan_to_num(0.0) for o in out))
             assert torch.equal(*(torch.isnan(o) for o in out))
+
+
+@pytest.mark.parametrize("rows,tree,wide", KERNELS)
+@pytest.mark.parametrize("ctx", [300, 3000])
+@pytest.mark.parametrize("size", [4.0, 2.0 ** 10, 2.0 ** 30])
+def test_attention_of_scores_far_past_fp32_steps(rows, tree, wide, ctx, size):
+    """Scores of 2^17 to 2^46, the best key ahead of every other by a seventh: its value alone
+    comes out, exact in bf16.  Two that are equal: the mean of their values, whose blocks'
+    scales differ."""
+    hd = 128
+    d = dict(_build(rows, [ctx] * len(rows), 2, 1, hd, 16, tree, spread=0.0), wide=wide)
+    rng = np.random.default_rng(len(rows) + ctx)
+    keys = np.minimum(d["ck"] & 127, 124)                    # 384 at most
+    keys[..., 1:] = 0
+    d["ck"], d["sk"] = keys, np.full_like(d["sk"], 137)      # 2^10
+    d["sv"] = rng.integers(117, 123, size=d["sv"].shape).astype(np.uint8)
+    d["q"] = torch.zeros_like(d["q"])
+    d["q"].view(-1, 2, hd)[:, :, 0] = size
+    held = oq.held(d["cv"], d["sv"])
+    for tops in ((ctx - 1,), (2,), (ctx - 150,), (1, ctx - 3), (ctx - 40, ctx - 160), (7, 40)):
+        e = dict(d, ck=d["ck"].copy())
+        for r in range(len(rows)):
+            for t in tops:
+                e["ck"][e["table"][r, t // 16], 0, t % 16, 0] = 126     # 448
+        out, ws = _attend(e)
+        torch.cuda.synchronize()
+        assert bd.read_status(ws) == 0
+        o = _f64(out).reshape(-1, 2, hd)
+        for r in range(len(rows)):
+            v = np.stack([held[e["table"][r, t // 16], 0, t % 16] for t in tops])
+            want = v.mean(0)
+            # equal scores have equal weights, powers of two: bf16 rounds the mean
+            tol = 0.0 if len(tops) == 1 else 2.0 ** -8 * np.abs(want)
+            assert (np.abs(o[e["off"][r]:e["off"][r + 1]] - want) <= tol).all(), (r, tops)
