@@ -382,10 +382,10 @@ extern "C" dflash_status dflash_logits_adjust(
   DFL_REQUIRE(history == nullptr || (history_ld >= 1 && history_len), "logits adjust: history needs lengths");
   DFL_REQUIRE(mask == nullptr || (mask_ld >= 1 && tok), "logits adjust: a mask needs words and tokens");
   DFL_REQUIRE(n_bias >= 0 && n_bias <= (1 << 20), "logits adjust: n_bias must be in [0, 2^20]");
-  DFL_REQUIRE(n_bias == 0 || (bias_tok && bias_val), "logits adjust: null bias list");
   DFL_REQUIRE(allowed == nullptr || allowed_ld * 32 >= vocab, "logits adjust: allowed rows shorter than vocab");
   if (n_req == 0 || rows == 0) return DFLASH_OK;
   DFL_REQUIRE(logits && out && row_off, "logits adjust: null pointer argument");
+  DFL_REQUIRE(n_bias == 0 || (bias_tok && bias_val), "logits adjust: null bias list");
   DFL_REQUIRE(logits != out || ld == out_ld, "logits adjust: in place needs the same row stride");
   const size_t es = dtype == DFLASH_F32 ? 4 : 2;
   DFL_REQUIRE(((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(out)) & (es - 1)) == 0,

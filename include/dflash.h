@@ -597,7 +597,11 @@ dflash_status dflash_paged_append_e4m3(const dflash_pages_e4m3* pages, int n_req
  * workspace rules (of dflash_paged_attention_e4m3_workspace_bytes bytes) and
  * errors; q and out bf16.  Codes enter the products as they are, exactly; scales
  * are applied to fp32 scores and weights.  A NaN code reaches the rows that see
- * its slot; what no row sees, scales included, may hold anything. */
+ * its slot; what no row sees, scales included, may hold anything.  Sums are held
+ * in fp32 and divided at the end: outputs are finite while the largest value times
+ * the slots that a row sees stays below 2^113.  Queries enter as fp16 (rounded by
+ * 2^-39 of a row's largest element at most) or, in requests of many rows, as two
+ * e4m3 codes (2^-17), so max_rows moves results by that besides the order of sums. */
 size_t dflash_paged_attention_e4m3_workspace_bytes(int n_q, int n_kv, int head_dim);
 dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_req, int n_rows,
                                           int n_q, const int32_t* row_off, const int32_t* pos0,

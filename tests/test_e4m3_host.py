@@ -111,3 +111,17 @@ def test_binding_refuses_wrong_tensors():
         binding.logits_adjust(x, x, off, vocab=11)
     with pytest.raises(ValueError):
         binding.logits_adjust(x, x, z(0, dtype=torch.int32))
+
+
+def test_adjust_of_an_empty_batch_needs_no_lists(lib):
+    """Tensors without entries have null pointers, whatever their widths."""
+    def call(n_req, rows, **kw):
+        a = dict(hist=None, hist_ld=0, hist_len=None, tok=None, mask=None, mask_ld=0, bt=None, bv=None, nb=0)
+        a.update(kw)
+        return lib.dflash_logits_adjust(n_req, rows, 100, 1, None, 100, None, 100, None, a["hist"], a["hist_ld"],
+                                        a["hist_len"], None, None, None, None, a["tok"], a["mask"], a["mask_ld"],
+                                        a["bt"], a["bv"], a["nb"], None, 4, None)
+    for n_req, rows in ((0, 0), (0, 5), (3, 0)):
+        assert call(n_req, rows) == 0
+        assert call(n_req, rows, hist_ld=8, mask_ld=2, nb=7) == 0
+    assert call(0, 0, nb=-1) == 1 and call(0, 0, nb=(1 << 20) + 1) == 1
