@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxVocab = 1 << 22;
+constexpr int kMaxHistory = 1 << 30;   // (steps past a history's end do not pass 2^31)
 
 struct AdjustParams {
   int n_req, rows, vocab;
@@ -380,6 +381,8 @@ extern "C" dflash_status dflash_logits_adjust(
   DFL_REQUIRE(dtype == DFLASH_F32 || dtype == DFLASH_BF16, "logits adjust: dtype must be F32 or BF16");
   DFL_REQUIRE(ld >= vocab && out_ld >= vocab, "logits adjust: row strides smaller than vocab");
   DFL_REQUIRE(history == nullptr || (history_ld >= 1 && history_len), "logits adjust: history needs lengths");
+  DFL_REQUIRE(history == nullptr || history_ld <= kMaxHistory, "logits adjust: history rows longer than %d",
+              kMaxHistory);
   DFL_REQUIRE(mask == nullptr || (mask_ld >= 1 && tok), "logits adjust: a mask needs words and tokens");
   DFL_REQUIRE(n_bias >= 0 && n_bias <= (1 << 20), "logits adjust: n_bias must be in [0, 2^20]");
   DFL_REQUIRE(allowed == nullptr || allowed_ld * 32 >= vocab, "logits adjust: allowed rows shorter than vocab");

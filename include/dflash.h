@@ -643,8 +643,8 @@ dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_
  *   allowed  uint32 [rows] rows allowed_ld words apart, NULL: all
  * All device pointers; lengths and offsets stay on the device, so a captured call
  * serves histories that grow.  Results do not depend on timing.  rows may be 0.
- * Requires 1 <= vocab <= 2^22, allowed_ld * 32 >= vocab, n_bias <= 2^20,
- * rows + n_req < 2^30.  Needs no workspace. */
+ * Requires 1 <= vocab <= 2^22, history_ld <= 2^30, allowed_ld * 32 >= vocab,
+ * n_bias <= 2^20, rows + n_req < 2^30.  Needs no workspace. */
 dflash_status dflash_logits_adjust(int n_req, int rows, int vocab, int dtype, const void* logits,
                                    long long ld, void* out, long long out_ld,
                                    const int32_t* row_off, const int32_t* history, int history_ld,

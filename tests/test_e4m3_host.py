@@ -125,3 +125,12 @@ def test_adjust_of_an_empty_batch_needs_no_lists(lib):
         assert call(n_req, rows) == 0
         assert call(n_req, rows, hist_ld=8, mask_ld=2, nb=7) == 0
     assert call(0, 0, nb=-1) == 1 and call(0, 0, nb=(1 << 20) + 1) == 1
+
+
+def test_adjust_refuses_histories_past_its_indexes(lib):
+    def call(ld):
+        return lib.dflash_logits_adjust(1, 2, 100, 1, P, 100, ctypes.c_void_p(4096), 100, None, P, ld, P, None, None, None,
+                                        None, None, None, 0, None, None, 0, None, 0, None)
+    for ld in ((1 << 30) + 1, (1 << 31) - 1):
+        assert call(ld) == 1 and b"history" in lib.dflash_last_error()
+    assert call(1 << 30) == 1 and b"null" in lib.dflash_last_error()       # (the row offsets)
