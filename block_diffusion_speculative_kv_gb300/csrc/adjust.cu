@@ -66,13 +66,13 @@ __device__ __forceinline__ int first_group(const AdjustParams& p, int r) {
 
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowTokens = 512;   // of a request's rows in a stretch; more are looked up again for each row
-constexpr int kPath = 64;         // a row's own tokens in a warp's part of a stretch; more for each element
+constexpr int kPath = 64;         // a row's own tokens in a warp's part of a stretch; more 32 at a time
 
 // kDeep: 16-byte pieces of a row that a lane has at a time.
 template <typename T, int C, int kDeep>
 struct Stretch {
   static constexpr int V = Piece<T>::V, kPart = 32 * kDeep * V, kParts = C / kPart, kWords = C / 32 + 2;
-  static_assert(C % kPart == 0 && C / 32 <= kThreads - 2);
+  static_assert(C % kPart == 0 && C / 32 <= kThreads - 2 && kPart <= 1024 && kPath >= 32);
   uint4 buffer[kWarps][32 * kDeep];                        // a part of a row, a warp's
   uint32_t count[C + V];                                   // times generated; the top bit: in the prompt
   uint32_t bias[C + V];                                    // 1 + place in the list of biases
@@ -255,13 +255,17 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
       // (from the list, or, if there are more, from all rows' tokens: only a tree has so many)
       int own = 0;
       const bool all = listed > kRowTokens;
-      for (int e0 = 0, of = all ? n : listed; e0 < of; e0 += 32) {
-        const int e = e0 + lane, j = all || e >= of ? e : s.row[e];
+      const int of = all ? n : listed;
+      auto own_at = [&](int e) {                           // entry e's place in the part, or -1
+        const int j = all || e >= of ? e : s.row[e];
         const int a = e >= of ? -1 : (all ? static_cast<int>(from(__ldg(p.tok + row0 + e))) : s.token[e]) - a0;
-        const bool on = a >= 0 && a < kPart && sees(i, j);
-        const uint32_t who = __ballot_sync(0xffffffffu, on);
+        return a >= 0 && a < kPart && sees(i, j) ? a : -1;
+      };
+      for (int e0 = 0; e0 < of; e0 += 32) {
+        const int a = own_at(e0 + lane);
+        const uint32_t who = __ballot_sync(0xffffffffu, a >= 0);
         const int at = own + __popc(who & ((1u << lane) - 1u));
-        if (on) {
+        if (a >= 0) {
           atomicOr(&s.path[warp][a >> 5], 1u << (a & 31));
           if (at < kPath) s.entry[warp][at] = static_cast<uint16_t>(a);
         }
@@ -280,11 +284,11 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
           if (c) y = y - phi * static_cast<float>(c) - pi;
           value[a] = from_f32<T>(y);
         };
+        for (int e = r0 + lane; e < r1; e += 32) {
+          const int a = s.list[e] - a0;
+          if (!((s.path[warp][a >> 5] >> (a & 31)) & 1u)) fix(a, 0);
+        }
         if (own <= kPath) {
-          for (int e = r0 + lane; e < r1; e += 32) {
-            const int a = s.list[e] - a0;
-            if (!((s.path[warp][a >> 5] >> (a & 31)) & 1u)) fix(a, 0);
-          }
           for (int e = lane; e < own; e += 32) {
             const int a = s.entry[warp][e];
             uint32_t more = 0;
@@ -296,12 +300,31 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
               }
             if (first) fix(a, more);
           }
-        } else {                                           // too many to list
-          for (int a = lane; a < kPart; a += 32) {
+        } else {
+          // Too many to list: 32 of the path's different tokens at a time, ascending, one to a
+          // lane, which counts it as all entries pass.  (A lane has a word of the path's bits.)
+          uint32_t word = lane < kPart / 32 ? s.path[warp][lane] : 0u;
+          int upto = __popc(word);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+          }
+          const int distinct = __shfl_sync(0xffffffffu, upto, 31);
+          int at = upto - __popc(word);
+          for (int d0 = 0; d0 < distinct; d0 += 32) {
+            __syncwarp();
+            for (; word && at < d0 + 32; word &= word - 1)
+              s.entry[warp][at++ - d0] = static_cast<uint16_t>(lane * 32 + __ffs(word) - 1);
+            __syncwarp();
+            const int mine = d0 + lane < distinct ? s.entry[warp][lane] : -1;
             uint32_t more = 0;
-            for (int j = p.mask ? 0 : i0; j < (p.mask ? n : i + 1); ++j)
-              if (__ldg(p.tok + row0 + j) == t0 + a && sees(i, j)) ++more;
-            if (t0 + a >= 0 && t0 + a < p.vocab) fix(a, more);
+            for (int e0 = 0; e0 < of; e0 += 32) {
+              const int a = own_at(e0 + lane);
+              for (uint32_t who = __ballot_sync(0xffffffffu, a >= 0); who; who &= who - 1)
+                more += __shfl_sync(0xffffffffu, a, __ffs(who) - 1) == mine;
+            }
+            if (mine >= 0) fix(mine, more);
           }
         }
         __syncwarp();

@@ -305,3 +305,24 @@ def test_adjust_alone_and_in_a_batch_agree(dtype):
         got = _run(last)
         torch.cuda.synchronize()
         assert torch.equal(got[0], out[b - 1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n,span,few", [(257, 900, 1), (257, 40, 1), (600, 3000, 1), (200, 1000, 40), (65, 64, 1)])
+def test_adjust_long_paths_through_common_tokens(dtype, n, span, few):
+    """Masks that are chains, so that rows have up to n tokens of their own close together,
+    some many times; one request, and many of few rows beside it."""
+    rng = np.random.default_rng(n + span)
+    rows = [n] + [1] * (few - 1) * 9
+    d = _case(rows, 5003, dtype, [700] * len(rows), True, 20, True, seed=1, low=0.1, pad=1)
+    d["mask"] = np.zeros((n + len(rows), (n + 31) // 32), dtype=np.uint32)
+    for i in range(n):
+        bits = np.arange(32 * d["mask"].shape[1]) <= i
+        d["mask"][i] = np.packbits(bits, bitorder="little").view(np.uint32)
+    d["mask"][n:, 0] = 1
+    d["tok"] = rng.integers(-1, span, size=len(d["tok"])).astype(np.int32)
+    out = _run(d)
+    again = _run(d)
+    torch.cuda.synchronize()
+    _check(d, out)
+    assert torch.equal(out, again)
