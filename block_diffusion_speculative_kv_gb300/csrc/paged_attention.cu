@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(kThreadsS, kPerSmS) paged_attn_small_kernel(co
       if ((lane & 3) == 0) sMl[warp * 16 + ra + 8 * h] = make_float2(m[h], l[h]);
     }
     __syncthreads();
-    paged_finish_small<HD, kRowsS, S::kLd, kThreadsS, S::kRing, GeoS>(p, c, pc, total, end, rho0, live, sO, sMl,
-                                                                      smem, sLast);
+    paged_finish_small<HD, kRowsS, S::kLd, kThreadsS, S::kRing, kPerSmS, GeoS>(p, c, pc, total, end, rho0, live, sO,
+                                                                         sMl, smem, sLast);
     __syncthreads();                                     // the ring is free again
   }
 }
@@ -1129,6 +1129,8 @@ dflash_status dflash_paged_attention(const dflash_pages* pages, int n_req, int n
   DFL_REQUIRE(row_off && pos0 && q && out, "paged attention: null pointer argument");
   DFL_REQUIRE(((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0,
               "paged attention: q and out must be 16-byte aligned");
+  if (num_sms() > kMostSms)
+    return set_error(DFLASH_ERR_UNSUPPORTED, "paged attention: more than %d SMs", kMostSms);
   const PagedWs w = paged_ws(num_sms(), hd);
   if (!ws || ws_bytes < w.bytes)
     return set_error(DFLASH_ERR_WORKSPACE, "paged attention workspace needs %zu bytes, got %zu",

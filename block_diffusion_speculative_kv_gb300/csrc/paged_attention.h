@@ -322,17 +322,22 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 // 2048 slots 10.0 / 9.9 / 9.6 us, four rows 15.6 / 15.5 / 14.1, one over 500 9.0 / 9.2 / 9.3).
 constexpr int kJoin = 20;
 
+// SMs that the join of few rows has room for (the calls refuse more), and the bytes it takes.
+constexpr int kMostSms = 160;
+constexpr int paged_pairs(int rows, int per_sm) { return rows * static_cast<int>(sizeof(float2)) * per_sm * kMostSms; }
+
 // The end of a piece of a tile of few rows: the states of its four warps, sO [4][ROWS][LD]
 // unnormalised and sMl [4][ROWS] (max, sum), of which `live` rows count, become rows of
 // out; or, where shares' borders cut the tile, a part of it, and the last of its CTAs to
 // arrive joins the parts, in key order.  scratch: SCRATCH bytes, free once sO has been
-// read.  They hold (max, sum) of the first parts; a long tile has one for each CTA of the
-// grid, and what does not fit is read where it lies.  Block-collective; sLast: one int.
-template <int HD, int ROWS, int LD, int THREADS, int SCRATCH, typename Geo>
+// read: a pair for each row of as many parts as there may be CTAs, PER_SM to an SM (a long
+// request's tile falls into a part for each).  Block-collective; sLast: one int.
+template <int HD, int ROWS, int LD, int THREADS, int SCRATCH, int PER_SM, typename Geo>
 __device__ __forceinline__ void paged_finish_small(const PagedAttnParams& p, const PagedCursor& c,
                                                    const PagedPiece& pc, long long total, long long end, int rho0,
                                                    int live, const float* sO, const float2* sMl, void* scratch,
                                                    int* sLast) {
+  static_assert(SCRATCH >= paged_pairs(ROWS, PER_SM), "the join's scratch");
   const PagedReq& rq = c.rq;
   const int tid = threadIdx.x, head0 = c.g * p.heads.G;
   // a thread takes four columns of a row: HD / 4 neighbours make a row
@@ -387,53 +392,35 @@ __device__ __forceinline__ void paged_finish_small(const PagedAttnParams& p, con
       if (tid == 0) p.arrive[c0] = 0;                  // for the next call
       // the pieces' (max, sum) first, all at once, into the idle ring
       float2* sPart = reinterpret_cast<float2*>(scratch);
-      constexpr int kHeld = SCRATCH / (ROWS * static_cast<int>(sizeof(float2)));
-      static_assert(kHeld >= 1, "the scratch holds a part");
-      const int parts = c1 - c0 + 1, held = min(parts, kHeld);
-      auto ml_of = [&](int k, int row) {
-        const int cc = c0 + k;
-        return __ldcg(p.part_ml + ((size_t)cc * 2 + (cc == c0)) * ROWS + row);
-      };
-      for (int i = tid; i < held * ROWS; i += THREADS)
-        sPart[i] = i % ROWS < live ? ml_of(i / ROWS, i % ROWS) : make_float2(-CUDART_INF_F, 0.f);
+      const int parts = c1 - c0 + 1;
+      for (int i = tid; i < parts * ROWS; i += THREADS) {
+        const int cc = c0 + i / ROWS;
+        sPart[i] = i % ROWS < live
+                       ? __ldcg(p.part_ml + ((size_t)cc * 2 + (cc == c0)) * ROWS + i % ROWS)
+                       : make_float2(-CUDART_INF_F, 0.f);
+      }
       __syncthreads();
       for (int i = tid; i < items; i += THREADS) {
         const int row = i / (HD / 4), col = i % (HD / 4) * 4;
         float M = -CUDART_INF_F, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < held; ++k) M = fmaxf(M, sPart[k * ROWS + row].x);
-#pragma unroll 8
-        for (int k = held; k < parts; ++k) M = fmaxf(M, ml_of(k, row).x);
-        auto part = [&](int k) {
-          const int cc = c0 + k;
-          return __ldcg(reinterpret_cast<const float4*>(
-              p.part_o + (((size_t)cc * 2 + (cc == c0)) * ROWS + row) * HD + col));
-        };
-        auto join = [&](const float2& ml, const float4& v) {
-          if (ml.y == 0.f) return;
-          const float f = ex2(ml.x - M);
-          L += f * ml.y;
-          add(acc, f, v);
-        };
-        for (int k0 = 0; k0 < held; k0 += kJoin) {     // their loads in flight
+        for (int k = 0; k < parts; ++k) M = fmaxf(M, sPart[k * ROWS + row].x);
+        for (int k0 = 0; k0 < parts; k0 += kJoin) {    // their loads in flight
           float4 v[kJoin];
 #pragma unroll
-          for (int k = 0; k < kJoin; ++k) v[k] = part(min(k0 + k, held - 1));
-#pragma unroll
-          for (int k = 0; k < kJoin; ++k)
-            if (k0 + k < held) join(sPart[(k0 + k) * ROWS + row], v[k]);
-        }
-        for (int k0 = held; k0 < parts; k0 += kJoin / 2) {
-          float2 ml[kJoin / 2];
-          float4 v[kJoin / 2];
-#pragma unroll
-          for (int k = 0; k < kJoin / 2; ++k) {
-            ml[k] = ml_of(min(k0 + k, parts - 1), row);
-            v[k] = part(min(k0 + k, parts - 1));
+          for (int k = 0; k < kJoin; ++k) {
+            const int cc = c0 + min(k0 + k, parts - 1);
+            v[k] = __ldcg(reinterpret_cast<const float4*>(
+                p.part_o + (((size_t)cc * 2 + (cc == c0)) * ROWS + row) * HD + col));
           }
 #pragma unroll
-          for (int k = 0; k < kJoin / 2; ++k)
-            if (k0 + k < parts) join(ml[k], v[k]);
+          for (int k = 0; k < kJoin; ++k) {
+            const float2 ml = sPart[min(k0 + k, parts - 1) * ROWS + row];
+            if (k0 + k >= parts || ml.y == 0.f) continue;
+            const float f = ex2(ml.x - M);
+            L += f * ml.y;
+            add(acc, f, v[k]);
+          }
         }
         write(row, col, acc, L);
       }

@@ -119,8 +119,10 @@ template <int HD, int NT>
 struct Small {
   static constexpr int kTile = 16 * HD;                           // a block of K or V
   static constexpr int kRing = 4 * kStagesS * 2 * kTile;
-  static constexpr int kRows = 8 * NT, kLd = HD + 8;
-  static constexpr int kMl = kRing, kBar = kMl + 4 * kRows * 8, kBytes = kBar + 4 * kStagesS * 8 + 16;
+  static constexpr int kRows = 8 * NT, kLd = HD + 8, kPairs = paged_pairs(kRows, kPerSmS);
+  static constexpr int kMl = kRing > kPairs ? kRing : kPairs;     // (the join's pairs lie over the ring)
+  static constexpr int kBar = kMl + 4 * kRows * 8, kBytes = kBar + 4 * kStagesS * 8 + 16;
+  static_assert(kPerSmS * (kBytes + 1024) <= 228 * 1024, "shared memory of an SM");
   static_assert(4 * kRows * kLd * 4 <= kRing, "the warps' states meet in the idle ring");
 };
 
@@ -463,8 +465,8 @@ paged_attn_small_e4m3_kernel(const __grid_constant__ PagedE4M3Maps maps, const P
         if (ra == 0) sMl[warp * S::kRows + row] = make_float2(m[nt][h], l[nt][h]);
       }
     __syncthreads();
-    paged_finish_small<HD, S::kRows, S::kLd, kThreadsS, S::kRing, Geo>(p, c, pc, total, end, rho0, live, sO, sMl,
-                                                                       smem, sLast);
+    paged_finish_small<HD, S::kRows, S::kLd, kThreadsS, S::kMl, kPerSmS, Geo>(p, c, pc, total, end, rho0, live, sO, sMl,
+                                                                              smem, sLast);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();                                     // the ring is free again
   }
@@ -1454,6 +1456,8 @@ dflash_status dflash_paged_attention_e4m3(const dflash_pages_e4m3* pages, int n_
   DFL_REQUIRE(row_off && pos0 && q && out, "paged attention e4m3: null pointer argument");
   DFL_REQUIRE(((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0,
               "paged attention e4m3: q and out must be 16-byte aligned");
+  if (num_sms() > kMostSms)
+    return set_error(DFLASH_ERR_UNSUPPORTED, "paged attention e4m3: more than %d SMs", kMostSms);
   const PagedWs w = paged_ws(num_sms(), hd);
   if (!ws || ws_bytes < w.bytes)
     return set_error(DFLASH_ERR_WORKSPACE, "paged attention e4m3 workspace needs %zu bytes, got %zu",

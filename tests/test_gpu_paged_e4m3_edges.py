@@ -36,7 +36,7 @@ def _parts(slots, tiles, sms):
     ([16], [100000], 1, 1, 64, 256, False, True),
 ])
 def test_attention_of_long_requests(rows, ctx, n_q, n_kv, hd, page, tree, wide):
-    """More parts to a tile than the shared memory of the CTA that joins them holds
+    """More parts to a tile than the loading ring of the CTA that joins them has room for
     (max, sum) pairs of: 24 KB with heads of 64, 48 KB with 128."""
     tile = 16 if wide else 8
     sms = torch.cuda.get_device_properties(0).multi_processor_count
