@@ -86,6 +86,28 @@ struct Stretch {
   uint16_t entry[kWarps][kPath];
 };
 
+// How often the token at place `mine` of a part is in row i's path, a lane to a place: of the
+// `of` listed rows' tokens, or of all rows' (tok).  Places [0, part) of the part begin at token
+// t0 and place a0 of the stretch.  Warp-collective.  (Rare, and a function of its own: inlined,
+// it cost the tree of 257 fp32 nodes 60 us against 56.)
+__device__ __noinline__ uint32_t times_in_path(const int* row, const uint16_t* token, const int32_t* tok, int of, int t0,
+                                               int a0, int part, const uint32_t* mask, int words, int i, int mine, int lane) {
+  uint32_t times = 0;
+  for (int e0 = 0; e0 < of; e0 += 32) {
+    const int e = e0 + lane;
+    int a = -1;
+    if (e < of) {
+      const int j = tok ? e : row[e];
+      a = tok ? static_cast<int>(static_cast<unsigned>(__ldg(tok + e)) - static_cast<unsigned>(t0)) : token[e] - a0;
+      const bool on = mask ? (j >> 5) < words && ((__ldg(mask + (j >> 5)) >> (j & 31)) & 1u) : j <= i;
+      if (a < 0 || a >= part || !on) a = -1;
+    }
+    for (uint32_t who = __ballot_sync(0xffffffffu, a >= 0); who; who &= who - 1)
+      times += __shfl_sync(0xffffffffu, a, __ffs(who) - 1) == mine;
+  }
+  return times;
+}
+
 template <typename T, int C, int kDeep, int ROWS>
 __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_kernel(const AdjustParams p) {
   // Pieces lie on 16-byte boundaries, so a row's first one may begin up to V - 1 tokens
@@ -255,17 +277,13 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
       // (from the list, or, if there are more, from all rows' tokens: only a tree has so many)
       int own = 0;
       const bool all = listed > kRowTokens;
-      const int of = all ? n : listed;
-      auto own_at = [&](int e) {                           // entry e's place in the part, or -1
-        const int j = all || e >= of ? e : s.row[e];
+      for (int e0 = 0, of = all ? n : listed; e0 < of; e0 += 32) {
+        const int e = e0 + lane, j = all || e >= of ? e : s.row[e];
         const int a = e >= of ? -1 : (all ? static_cast<int>(from(__ldg(p.tok + row0 + e))) : s.token[e]) - a0;
-        return a >= 0 && a < kPart && sees(i, j) ? a : -1;
-      };
-      for (int e0 = 0; e0 < of; e0 += 32) {
-        const int a = own_at(e0 + lane);
-        const uint32_t who = __ballot_sync(0xffffffffu, a >= 0);
+        const bool on = a >= 0 && a < kPart && sees(i, j);
+        const uint32_t who = __ballot_sync(0xffffffffu, on);
         const int at = own + __popc(who & ((1u << lane) - 1u));
-        if (a >= 0) {
+        if (on) {
           atomicOr(&s.path[warp][a >> 5], 1u << (a & 31));
           if (at < kPath) s.entry[warp][at] = static_cast<uint16_t>(a);
         }
@@ -284,11 +302,14 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
           if (c) y = y - phi * static_cast<float>(c) - pi;
           value[a] = from_f32<T>(y);
         };
-        for (int e = r0 + lane; e < r1; e += 32) {
-          const int a = s.list[e] - a0;
-          if (!((s.path[warp][a >> 5] >> (a & 31)) & 1u)) fix(a, 0);
-        }
+        auto listed_ones = [&]() {                         // that are not in the path
+          for (int e = r0 + lane; e < r1; e += 32) {
+            const int a = s.list[e] - a0;
+            if (!((s.path[warp][a >> 5] >> (a & 31)) & 1u)) fix(a, 0);
+          }
+        };
         if (own <= kPath) {
+          listed_ones();
           for (int e = lane; e < own; e += 32) {
             const int a = s.entry[warp][e];
             uint32_t more = 0;
@@ -303,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
         } else {
           // Too many to list: 32 of the path's different tokens at a time, ascending, one to a
           // lane, which counts it as all entries pass.  (A lane has a word of the path's bits.)
+          listed_ones();
           uint32_t word = lane < kPart / 32 ? s.path[warp][lane] : 0u;
           int upto = __popc(word);
 #pragma unroll
@@ -318,12 +340,9 @@ __global__ void __launch_bounds__(kThreads, kDeep > 4 ? 3 : 4) logits_adjust_ker
               s.entry[warp][at++ - d0] = static_cast<uint16_t>(lane * 32 + __ffs(word) - 1);
             __syncwarp();
             const int mine = d0 + lane < distinct ? s.entry[warp][lane] : -1;
-            uint32_t more = 0;
-            for (int e0 = 0; e0 < of; e0 += 32) {
-              const int a = own_at(e0 + lane);
-              for (uint32_t who = __ballot_sync(0xffffffffu, a >= 0); who; who &= who - 1)
-                more += __shfl_sync(0xffffffffu, a, __ffs(who) - 1) == mine;
-            }
+            const uint32_t more = times_in_path(s.row, s.token, all ? p.tok + row0 : nullptr, all ? n : listed, base + a0, a0,
+                                                kPart, p.mask ? p.mask + (size_t)(row0 + i) * p.mask_ld : nullptr, words, i,
+                                                mine, lane);
             if (mine >= 0) fix(mine, more);
           }
         }
