@@ -12,14 +12,19 @@
 // A CTA takes one stretch of the vocabulary for several rows of one request: it counts
 // the request's history in that stretch once, in shared memory, makes a sorted list of
 // the tokens that occurred or have a bias, and lists the rows' own tokens that lie there.
-// Then every warp works for itself, without another barrier: it brings 2 KB of a row,
-// picks from the list what the row's path holds, changes the listed tokens, a lane to a
-// token, in a buffer of its own, and writes the 2 KB.  A history of 8192 tokens touches one
-// token in 35, one of almost every 128 neighbours: changed where they are, in the
+// Then every warp works for itself, without another barrier: it brings a part of a row, 1, 2 or
+// 4 KB (kDeep 2, 4, 8), picks from the list what the row's path holds, changes the listed tokens,
+// a lane to a token, in a buffer of its own, and writes the part.  A history of 8192 tokens touches
+// one token in 35, one of almost every 128 neighbours: changed where they are, in the
 // registers of the lanes that have them, they made the warps' instructions the limit (480
-// bf16 rows of 151936: 159 us).  Now those take 76 us (4.0 TB/s; a copy 46), 257 fp32 nodes of a
-// tree 56 (5.6 TB/s), where waiting for rows bounds them; 256 bf16 requests of one row
-// after 2048 tokens each 83, half of that the histories' instructions.
+// bf16 rows of 151936: 159 us).  Now those take 76 us by 2 KB (4.0 TB/s; a copy 46), 257 fp32 nodes
+// of a tree 56 by 4 KB (5.6 TB/s), where waiting for rows bounds them; 256 bf16 requests of one
+// row after 2048 tokens each 83 by 1 KB, half of that the histories' instructions.
+//
+// Each stretch of each group of rows goes through its request's history, so time grows with
+// history times vocabulary.  Histories of 0 / 8192 / 32768 / 131072 tokens, us, bf16: 32 requests
+// of 15 rows 56 / 72 / 109 / 230, 256 of one row 63 / 113 / 234 / 757, one row 6 / 12 / 23 / 63,
+// one request of 257 rows 33 / 44 / 62 / 125: past about 30000 tokens they decide.
 #include <math_constants.h>
 
 #include "common.cuh"

@@ -109,7 +109,8 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // HBM bounds it: 32 single tokens over 512 .. 8192 slots take 57 us, 5.5 TB/s of 6.8 (of the
 // 16-bit cache 100), the tail of shares and the chain of conversions, MMAs and exponentials
 // in each warp the rest.  CTAs an SM and stages, us: 2 and 6 64, 3 and 4 58, 4 and 3 60, 3 and
-// 3 57.  One request over 2048 slots takes 11 (launch, plan, two steps, join).
+// 3 57.  One request over 2048 slots takes 11 (launch, plan, two steps, join; the 16-bit cache
+// 10), over 8192 17 (15), over 65536 37 (52), over 131072 53 (90).
 constexpr int kStepS = 64, kStagesS = 3, kThreadsS = 128, kPerSmS = 3;
 
 template <int NT>
@@ -528,7 +529,8 @@ dflash_status launch_small(const PagedE4M3Params& p, const dflash_pages_e4m3& pa
 // barrier (351, 108: MMAs 64 keys wide read q twice as often).
 constexpr int kStepT = 128;
 // Registers with NG = 2: the launch's 96 for each of five warpgroups, of which the four of
-// the softmax take 104 and the other one keeps 64.
+// the softmax take 104 and the other one keeps 64.  The compiler plans for 96 and spills 394
+// bytes (572 read back) in a kernel; NG = 1, with 128, spills none.
 constexpr int kRegsSoftmax = 104, kRegsOther = 64;
 static_assert(4 * kRegsSoftmax + kRegsOther <= 5 * 96, "register split");
 
